@@ -24,6 +24,7 @@ SL_SLICE_OUT, SL_SLICE_IN = 0, 1
 SL_LAYOUT_NATURAL, SL_LAYOUT_SIGMA = 0, 1
 SL_EPI_NONE, SL_EPI_SWIGLU = 0, 1
 SL_LORA_FWD, SL_LORA_BWD = 0, 1
+SL_ROPE_HALVES, SL_ROPE_PAIRS = 0, 1
 
 EXPORTED = ("sl_status_string", "sl_version", "sl_keep_count", "sl_workspace_init", "sl_read_device_flag",
             "sl_svd_estimate", "sl_select_channels", "sl_lora_fwd_bwd", "sl_sparse_linear_fwd",
@@ -32,7 +33,9 @@ EXPORTED = ("sl_status_string", "sl_version", "sl_keep_count", "sl_workspace_ini
             "sl_svd_scores_from_partials", "sl_select_heads", "sl_wanda_scores", "sl_rmsnorm_fwd", "sl_rmsnorm_bwd",
             "sl_add_rows", "sl_adamw_step", "sl_gather_rows_batch", "sl_set_pair_tile_rows",
             "sl_debug_bounds_enabled", "sl_read_debug_flag", "sl_attention_fwd", "sl_attention_bwd",
-            "sl_lora_fwd_estimate", "sl_svd_scores_from_z", "sl_permute_rows_sigma")
+            "sl_lora_fwd_estimate", "sl_svd_scores_from_z", "sl_permute_rows_sigma", "sl_qk_norm_rope_fwd",
+            "sl_qk_norm_rope_bwd", "sl_attention_plan_bytes", "sl_attention_plan", "sl_attention_masked_fwd",
+            "sl_attention_masked_bwd", "sl_token_logprobs_fwd", "sl_token_logprobs_bwd")
 
 
 class SlWorkspaceC(ctypes.Structure):
@@ -145,11 +148,27 @@ def load(path):
                                    POINTER(SlWorkspaceC), P]
     L.sl_attention_bwd.argtypes = [P, P, P, P, P, P, c_int64, c_int64, c_int32, c_int32, c_int32, c_int32, c_int32,
                                    P, P, P, POINTER(SlWorkspaceC), P]
+    L.sl_qk_norm_rope_fwd.argtypes = [P, c_int64, P, c_int64, P, P, c_int32, c_int32, P, P, c_float, c_int64, c_int32,
+                                      c_int32, c_int32, P, c_int64, P, c_int64, P]
+    L.sl_qk_norm_rope_bwd.argtypes = [P, c_int64, P, c_int64, P, c_int64, P, c_int64, P, P, c_int32, c_int32, P, P,
+                                      c_float, c_int64, c_int32, c_int32, c_int32, P, c_int64, P, c_int64, P, P,
+                                      POINTER(SlWorkspaceC), P]
+    L.sl_attention_plan_bytes.restype = c_int64
+    L.sl_attention_plan_bytes.argtypes = [c_int32, c_int32]
+    L.sl_attention_plan.argtypes = [P, P, c_int32, c_int32, P, c_int64, P]
+    L.sl_attention_masked_fwd.argtypes = [P, c_int64, P, c_int64, P, c_int64, c_int32, c_int32, c_int32, c_int32,
+                                          c_int32, c_float, c_float, P, P, c_int64, P, c_int64, P,
+                                          POINTER(SlWorkspaceC), P]
+    L.sl_attention_masked_bwd.argtypes = [P, c_int64, P, c_int64, P, c_int64, P, c_int64, P, c_int32,
+                                          c_int32, c_int32, c_int32, c_int32, c_float, c_float, P, P, c_int64, P,
+                                          c_int64, P, c_int64, P, c_int64, POINTER(SlWorkspaceC), P]
+    L.sl_token_logprobs_fwd.argtypes = [c_int32, P, c_int64, c_int64, c_int64, P, P, P, P, c_int32, P, P, P]
+    L.sl_token_logprobs_bwd.argtypes = [c_int32, P, c_int64, c_int64, c_int64, P, P, P, P, P, P, c_int64, P]
     L.sl_read_debug_flag.argtypes = [POINTER(c_int32), P]
     L.sl_set_pair_tile_rows.argtypes = [c_int32]
     for n in EXPORTED:
         if n not in ("sl_status_string", "sl_version", "sl_keep_count", "sl_svd_partials_count",
-                     "sl_debug_bounds_enabled"):
+                     "sl_debug_bounds_enabled", "sl_attention_plan_bytes"):
             getattr(L, n).restype = c_int32
     return L
 
@@ -424,6 +443,166 @@ def sl_attention_bwd(ws: Workspace, q, k, v, o, d_o, lse, n_seq, n_q_heads, n_kv
     ws.call("sl_attention_bwd", _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(d_o), _ptr(lse), q.stride(0), k.stride(0),
             int(n_seq), q.shape[0] // int(n_seq), int(n_q_heads), int(n_kv_heads), int(head_dim), _ptr(dq), _ptr(dk),
             _ptr(dv))
+
+
+def _need(fn, ok):
+    """An argument that the library could not check itself (a tensor's type, shape, device or strides)."""
+    if not ok:
+        raise SparseLoRAError(fn, SL_ERR_INVALID_ARG)
+
+
+def _rows(fn, t, shape, dtype, dev):
+    """`t` as rows for the library: its address and leading dimension. 2-D, of this type and shape, on the
+    current device, its rows contiguous (a row may be a slice of a longer one)."""
+    _need(fn, t.dtype == dtype and t.shape == shape and t.stride(1) == 1 and t.get_device() == dev)
+    # the stride of a single row says nothing
+    return t.data_ptr(), (t.stride(0) if shape[0] > 1 else -(-shape[1] // 8) * 8)
+
+
+def _flat(fn, t, n, dtype, dev):
+    """The address of a dense tensor of n elements (None stays None)."""
+    if t is None:
+        return None
+    _need(fn, t.dtype == dtype and t.numel() == n and t.is_contiguous() and t.get_device() == dev)
+    return t.data_ptr()
+
+
+def _device(fn, t):
+    """The index of t's device, which has to be the current one (the calls go to its current stream)."""
+    dev = t.get_device()
+    _need(fn, dev >= 0 and dev == torch.cuda.current_device())
+    return dev
+
+
+def _raw_stream(dev):
+    return torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _rope_args(fn, q, k, positions, inv_freq, head_dim, gq, gk, eps, style, dev):
+    _need(fn, head_dim > 0 and q.dim() == 2 and k.dim() == 2 and q.shape[0] == k.shape[0]
+          and q.shape[1] % head_dim == 0 and k.shape[1] % head_dim == 0)
+    T, rot = q.shape[0], 0 if inv_freq is None else 2 * inv_freq.numel()
+    return ((_flat(fn, positions, T, torch.int32, dev), _flat(fn, inv_freq, rot // 2, torch.float32, dev), rot, style,
+             _flat(fn, gq, head_dim, torch.bfloat16, dev), _flat(fn, gk, head_dim, torch.bfloat16, dev), eps, T,
+             q.shape[1] // head_dim, k.shape[1] // head_dim, head_dim))
+
+
+def sl_qk_norm_rope_fwd(q, k, positions, inv_freq, head_dim, yq, yk, gq=None, gk=None, eps=1e-6,
+                        style=SL_ROPE_HALVES):
+    """Per-head RMSNorm (with gains gq, gk [head_dim]; None: no norm) and rotation of q and k [T, heads *
+    head_dim] at int32 positions [T] with the frequencies inv_freq [rot_dim / 2] (None: no rotation)."""
+    fn, bf = "sl_qk_norm_rope_fwd", torch.bfloat16
+    dev = _device(fn, q)
+    rest = _rope_args(fn, q, k, positions, inv_freq, head_dim, gq, gk, eps, style, dev)
+    _check(fn, lib().sl_qk_norm_rope_fwd(*_rows(fn, q, q.shape, bf, dev), *_rows(fn, k, k.shape, bf, dev), *rest,
+                                         *_rows(fn, yq, q.shape, bf, dev), *_rows(fn, yk, k.shape, bf, dev),
+                                         _raw_stream(dev)))
+
+
+def sl_qk_norm_rope_bwd(ws: Workspace, dyq, dyk, q, k, positions, inv_freq, head_dim, dq, dk, gq=None, gk=None,
+                        eps=1e-6, style=SL_ROPE_HALVES, dgq=None, dgk=None):
+    """Gradients of sl_qk_norm_rope_fwd at its inputs q and k (not read without gains), and at the gains (fp32)
+    where dgq, dgk are given."""
+    fn, bf = "sl_qk_norm_rope_bwd", torch.bfloat16
+    dev = _device(fn, dyq)
+    rest = _rope_args(fn, dyq, dyk, positions, inv_freq, head_dim, gq, gk, eps, style, dev)
+    xs = (None, 0, None, 0)
+    if gq is not None:
+        _need(fn, q is not None and k is not None)
+        xs = (*_rows(fn, q, dyq.shape, bf, dev), *_rows(fn, k, dyk.shape, bf, dev))
+    ws.call(fn, *_rows(fn, dyq, dyq.shape, bf, dev), *_rows(fn, dyk, dyk.shape, bf, dev), *xs, *rest,
+            *_rows(fn, dq, dyq.shape, bf, dev), *_rows(fn, dk, dyk.shape, bf, dev),
+            _flat(fn, dgq, head_dim, torch.float32, dev), _flat(fn, dgk, head_dim, torch.float32, dev))
+
+
+def sl_attention_plan_bytes(n_seq: int, seq_len: int) -> int:
+    return int(lib().sl_attention_plan_bytes(int(n_seq), int(seq_len)))
+
+
+def attention_plan_buffer(n_seq: int, seq_len: int, device="cuda"):
+    """A buffer for sl_attention_plan of these sizes."""
+    n = sl_attention_plan_bytes(n_seq, seq_len)
+    if n <= 0:
+        raise SparseLoRAError("sl_attention_plan_bytes", SL_ERR_SHAPE)
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def sl_attention_plan(row_lo, row_hi, n_seq, plan, seq_len=None):
+    """The plan of a batch of n_seq equal-length sequences whose token t sees keys [row_lo[t], row_hi[t]) of its own
+    sequence (int32 [n_seq * seq_len]; None: 0, or position + 1; seq_len is needed when both are)."""
+    fn = "sl_attention_plan"
+    dev = _device(fn, plan)
+    rows = row_lo if row_lo is not None else row_hi
+    _need(fn, n_seq > 0 and (seq_len is not None if rows is None else rows.numel() % n_seq == 0))
+    T = n_seq * seq_len if rows is None else rows.numel()
+    _need(fn, seq_len is None or T == n_seq * seq_len)
+    _check(fn, lib().sl_attention_plan(_flat(fn, row_lo, T, torch.int32, dev), _flat(fn, row_hi, T, torch.int32, dev),
+                                       n_seq, T // n_seq, _flat(fn, plan, plan.numel(), torch.uint8, dev),
+                                       plan.numel(), _raw_stream(dev)))
+
+
+def _masked_args(fn, q, k, n_seq, n_q_heads, n_kv_heads, head_dim):
+    T = q.shape[0]
+    _need(fn, n_seq > 0 and T % n_seq == 0)
+    return (T, n_q_heads * head_dim), (T, n_kv_heads * head_dim)
+
+
+def sl_attention_masked_fwd(ws: Workspace, q, k, v, n_seq, n_q_heads, n_kv_heads, head_dim, plan, o, lse, softcap=0.0,
+                            slopes=None, scale=0.0):
+    """Attention over the plan's intervals of keys, with scores capped by softcap * tanh(. / softcap) (0: not) and
+    lowered by slopes[head] * distance (None: not); o and the rows' log-sum-exp lse [n_q_heads, T]."""
+    fn, bf, f32 = "sl_attention_masked_fwd", torch.bfloat16, torch.float32
+    dev = _device(fn, q)
+    sq, sk = _masked_args(fn, q, k, n_seq, n_q_heads, n_kv_heads, head_dim)
+    ws.call(fn, *_rows(fn, q, sq, bf, dev), *_rows(fn, k, sk, bf, dev), *_rows(fn, v, sk, bf, dev), n_seq,
+            sq[0] // n_seq, n_q_heads, n_kv_heads, head_dim, scale, softcap, _flat(fn, slopes, n_q_heads, f32, dev),
+            _flat(fn, plan, plan.numel(), torch.uint8, dev), plan.numel(), *_rows(fn, o, sq, bf, dev),
+            _flat(fn, lse, n_q_heads * sq[0], f32, dev))
+
+
+def sl_attention_masked_bwd(ws: Workspace, q, k, v, o, d_o, lse, n_seq, n_q_heads, n_kv_heads, head_dim, plan, dq, dk,
+                            dv, softcap=0.0, slopes=None, scale=0.0):
+    """Gradients of sl_attention_masked_fwd at q, k and v, from its lse and the gradient d_o at o. The call reads like
+    sl_attention_bwd's; o itself is not used and may be None."""
+    fn, bf, f32 = "sl_attention_masked_bwd", torch.bfloat16, torch.float32
+    dev = _device(fn, q)
+    sq, sk = _masked_args(fn, q, k, n_seq, n_q_heads, n_kv_heads, head_dim)
+    ws.call(fn, *_rows(fn, q, sq, bf, dev), *_rows(fn, k, sk, bf, dev), *_rows(fn, v, sk, bf, dev),
+            *_rows(fn, d_o, sq, bf, dev), _flat(fn, lse, n_q_heads * sq[0], f32, dev), n_seq,
+            sq[0] // n_seq, n_q_heads, n_kv_heads, head_dim, scale, softcap, _flat(fn, slopes, n_q_heads, f32, dev),
+            _flat(fn, plan, plan.numel(), torch.uint8, dev), plan.numel(), *_rows(fn, dq, sq, bf, dev),
+            *_rows(fn, dk, sk, bf, dev), *_rows(fn, dv, sk, bf, dev))
+
+
+def _logits(fn, t, shape, dtype, dev):
+    _need(fn, t.dim() == 2 and dtype in (torch.bfloat16, torch.float32))
+    return _rows(fn, t, shape, dtype, dev)
+
+
+def sl_token_logprobs_fwd(logits, targets, logp, stats, entropy=None, top_ids=None, top_logp=None):
+    """logp [N] of the int32 targets [N] (outside [0, V): none, 0) under logits [N, V] (bf16 or fp32), stats [N, 2] for
+    the backward, and optionally the rows' entropy [N] and the k most likely tokens top_ids, top_logp [N, k]."""
+    fn, f32 = "sl_token_logprobs_fwd", torch.float32
+    dev = _device(fn, logits)
+    N, V = logits.shape
+    k = 0 if top_ids is None else top_ids.shape[1]
+    _check(fn, lib().sl_token_logprobs_fwd(
+        SL_DT_F32 if logits.dtype == f32 else SL_DT_BF16, *_logits(fn, logits, logits.shape, logits.dtype, dev), N, V,
+        _flat(fn, targets, N, torch.int32, dev), _flat(fn, logp, N, f32, dev), _flat(fn, stats, 2 * N, f32, dev),
+        _flat(fn, entropy, N, f32, dev), k, _flat(fn, top_ids, N * k, torch.int32, dev),
+        _flat(fn, top_logp, N * k, f32, dev), _raw_stream(dev)))
+
+
+def sl_token_logprobs_bwd(logits, targets, stats, g_logp, dlogits, g_entropy=None, entropy=None):
+    """dlogits (the logits' type; may be the logits) from the gradients g_logp [N] at logp and g_entropy [N] at entropy."""
+    fn, f32 = "sl_token_logprobs_bwd", torch.float32
+    dev = _device(fn, logits)
+    N, V = logits.shape
+    _check(fn, lib().sl_token_logprobs_bwd(
+        SL_DT_F32 if logits.dtype == f32 else SL_DT_BF16, *_logits(fn, logits, logits.shape, logits.dtype, dev), N, V,
+        _flat(fn, targets, N, torch.int32, dev), _flat(fn, stats, 2 * N, f32, dev), _flat(fn, g_logp, N, f32, dev),
+        _flat(fn, g_entropy, N, f32, dev), _flat(fn, entropy, N, f32, dev),
+        *_logits(fn, dlogits, logits.shape, logits.dtype, dev), _raw_stream(dev)))
 
 
 def sl_set_pair_tile_rows(rows: int):

@@ -1275,6 +1275,191 @@ sl_status sl_attention_bwd(const void* q, const void* k, const void* v, const vo
   return rc == 0 ? SL_OK : (rc == 2 ? SL_ERR_ALIGNMENT : SL_ERR_CUDA);
 }
 
+// ------------------------------------------------------------------ attention over intervals of keys
+namespace {
+bool plan_sizes_ok(int32_t n_seq, int32_t seq_len) {
+  return n_seq >= 1 && seq_len >= 1 && seq_len <= (1 << 20) && (int64_t)n_seq * seq_len <= (int64_t)1 << 30;
+}
+sl_status masked_args(int32_t n_seq, int32_t seq_len, int32_t hq, int32_t hkv, int32_t hd, float scale, float cap,
+                      const void* plan, int64_t plan_bytes) {
+  if (!plan_sizes_ok(n_seq, seq_len) || hq < 1 || hkv < 1 || hq % hkv || hd < 8 || hd > 128 || hd % 8 || hq > 65535)
+    return SL_ERR_SHAPE;
+  if (((int64_t)seq_len + 127) / 128 * n_seq * hq > 0x7fffffff) return SL_ERR_SHAPE;
+  if (!(scale >= 0.f && scale < INFINITY) || !(cap >= 0.f && cap < INFINITY)) return SL_ERR_SHAPE;
+  if (plan_bytes < attention_plan_bytes(n_seq, seq_len)) return SL_ERR_SHAPE;
+  return al16(plan) ? SL_OK : SL_ERR_ALIGNMENT;
+}
+}  // namespace
+
+int64_t sl_attention_plan_bytes(int32_t n_seq, int32_t seq_len) {
+  return plan_sizes_ok(n_seq, seq_len) ? attention_plan_bytes(n_seq, seq_len) : 0;
+}
+
+sl_status sl_attention_plan(const int32_t* row_lo, const int32_t* row_hi, int32_t n_seq, int32_t seq_len, void* plan,
+                            int64_t plan_bytes, sl_stream stream) {
+  if (!plan) return SL_ERR_INVALID_ARG;
+  if (!plan_sizes_ok(n_seq, seq_len) || plan_bytes < attention_plan_bytes(n_seq, seq_len)) return SL_ERR_SHAPE;
+  if (!al16(plan) || (reinterpret_cast<uintptr_t>(row_lo) & 3) || (reinterpret_cast<uintptr_t>(row_hi) & 3))
+    return SL_ERR_ALIGNMENT;
+  return from_kernel(attention_plan(row_lo, row_hi, n_seq, seq_len, plan, cs(stream)));
+}
+
+sl_status sl_attention_masked_fwd(const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v, int64_t ldv,
+                                  int32_t n_seq, int32_t seq_len, int32_t n_q_heads, int32_t n_kv_heads,
+                                  int32_t head_dim, float scale, float softcap, const float* slopes, const void* plan,
+                                  int64_t plan_bytes, void* o, int64_t ldo, float* lse, sl_workspace* ws,
+                                  sl_stream stream) {
+  if (!q || !k || !v || !plan || !o || !lse) return SL_ERR_INVALID_ARG;
+  if (sl_status st = masked_args(n_seq, seq_len, n_q_heads, n_kv_heads, head_dim, scale, softcap, plan, plan_bytes))
+    return st;
+  const int64_t nq = (int64_t)n_q_heads * head_dim, nk = (int64_t)n_kv_heads * head_dim;
+  if (!rows_ok(q, ldq, nq) || !rows_ok(k, ldk, nk) || !rows_ok(v, ldv, nk) || !rows_ok(o, ldo, nq) || !al16(lse))
+    return SL_ERR_ALIGNMENT;
+  if (sl_status st = ws_check(ws, kWorkspaceHeaderBytes)) return st;
+  MaskedArgs a = {};
+  a.q = q, a.k = k, a.v = v, a.ldq = ldq, a.ldk = ldk, a.ldv = ldv, a.o = o, a.ldo = ldo, a.lse = lse, a.plan = plan;
+  a.n_seq = n_seq, a.S = seq_len, a.hq = n_q_heads, a.hkv = n_kv_heads, a.hd = head_dim;
+  a.scale = scale, a.cap = softcap, a.slopes = slopes, a.err = err_word(ws);
+  const int rc = attention_masked_fwd(a, cs(stream));
+  return rc == 0 ? SL_OK : (rc == 2 ? SL_ERR_ALIGNMENT : SL_ERR_CUDA);
+}
+
+sl_status sl_attention_masked_bwd(const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v, int64_t ldv,
+                                  const void* d_o, int64_t lddo, const float* lse, int32_t n_seq, int32_t seq_len, int32_t n_q_heads, int32_t n_kv_heads,
+                                  int32_t head_dim, float scale, float softcap, const float* slopes, const void* plan,
+                                  int64_t plan_bytes, void* dq, int64_t lddq, void* dk, int64_t lddk, void* dv,
+                                  int64_t lddv, sl_workspace* ws, sl_stream stream) {
+  if (!q || !k || !v || !d_o || !lse || !plan || !dq || !dk || !dv) return SL_ERR_INVALID_ARG;
+  if (sl_status st = masked_args(n_seq, seq_len, n_q_heads, n_kv_heads, head_dim, scale, softcap, plan, plan_bytes))
+    return st;
+  const int64_t nq = (int64_t)n_q_heads * head_dim, nk = (int64_t)n_kv_heads * head_dim;
+  if (!rows_ok(q, ldq, nq) || !rows_ok(k, ldk, nk) || !rows_ok(v, ldv, nk) || !rows_ok(d_o, lddo, nq) || !rows_ok(dq, lddq, nq) || !rows_ok(dk, lddk, nk) || !rows_ok(dv, lddv, nk) ||
+      !al16(lse))
+    return SL_ERR_ALIGNMENT;
+  const size_t scratch = attention_bwd_scratch(n_seq, seq_len, n_q_heads, head_dim);
+  Carver c(nullptr);
+  c.take<uint8_t>(scratch);
+  if (sl_status st = ws_check(ws, c.off)) return st;
+  Carver c2(ws->ptr);
+  MaskedArgs a = {};
+  a.q = q, a.k = k, a.v = v, a.ldq = ldq, a.ldk = ldk, a.ldv = ldv;
+  a.lse = lse, a.plan = plan, a.d_o = d_o, a.lddo = lddo;
+  a.dq = dq, a.dk = dk, a.dv = dv, a.lddq = lddq, a.lddk = lddk, a.lddv = lddv;
+  a.n_seq = n_seq, a.S = seq_len, a.hq = n_q_heads, a.hkv = n_kv_heads, a.hd = head_dim;
+  a.scale = scale, a.cap = softcap, a.slopes = slopes, a.err = err_word(ws), a.scratch = c2.take<uint8_t>(scratch);
+  const int rc = attention_masked_bwd(a, cs(stream));
+  return rc == 0 ? SL_OK : (rc == 2 ? SL_ERR_ALIGNMENT : SL_ERR_CUDA);
+}
+
+// ------------------------------------------------------------------ q/k norm and rotation
+namespace {
+sl_status rotary_args(const int32_t* positions, const float* inv_freq, int32_t rot_dim, int32_t style,
+                      const void* gamma_q, const void* gamma_k, float eps, int64_t n_tok, int32_t hq, int32_t hkv,
+                      int32_t hd) {
+  if (rot_dim > 0 && (!positions || !inv_freq)) return SL_ERR_INVALID_ARG;
+  if (!gamma_q != !gamma_k || (style != SL_ROPE_HALVES && style != SL_ROPE_PAIRS)) return SL_ERR_INVALID_ARG;
+  if (rot_dim == 0 && !gamma_q) return SL_ERR_INVALID_ARG;  // nothing to do
+  if (n_tok < 1 || n_tok > (int64_t)1 << 31 || hq < 1 || hkv < 1 || hq > 4096 || hkv > 4096 || hd < 8 || hd > 256 ||
+      hd % 8 || rot_dim < 0 || rot_dim > hd || rot_dim % 8 || !(eps >= 0.f))
+    return SL_ERR_SHAPE;
+  if ((reinterpret_cast<uintptr_t>(positions) & 3) || (reinterpret_cast<uintptr_t>(inv_freq) & 3) ||
+      !al16(gamma_q) || !al16(gamma_k))
+    return SL_ERR_ALIGNMENT;
+  return SL_OK;
+}
+}  // namespace
+
+sl_status sl_qk_norm_rope_fwd(const void* q, int64_t ldq, const void* k, int64_t ldk, const int32_t* positions,
+                              const float* inv_freq, int32_t rot_dim, int32_t style, const void* gamma_q,
+                              const void* gamma_k, float eps, int64_t n_tok, int32_t n_q_heads, int32_t n_kv_heads,
+                              int32_t head_dim, void* yq, int64_t ldyq, void* yk, int64_t ldyk, sl_stream stream) {
+  if (!q || !k || !yq || !yk) return SL_ERR_INVALID_ARG;
+  if (sl_status st = rotary_args(positions, inv_freq, rot_dim, style, gamma_q, gamma_k, eps, n_tok, n_q_heads,
+                                 n_kv_heads, head_dim))
+    return st;
+  const int64_t nq = (int64_t)n_q_heads * head_dim, nk = (int64_t)n_kv_heads * head_dim;
+  if (!rows_ok(q, ldq, nq) || !rows_ok(k, ldk, nk) || !rows_ok(yq, ldyq, nq) || !rows_ok(yk, ldyk, nk))
+    return SL_ERR_ALIGNMENT;
+  RotaryArgs a = {};
+  a.xq = q, a.xk = k, a.ldxq = ldq, a.ldxk = ldk, a.oq = yq, a.ok = yk, a.ldoq = ldyq, a.ldok = ldyk;
+  a.pos = positions, a.inv_freq = inv_freq, a.gq = gamma_q, a.gk = gamma_k, a.eps = eps, a.n_tok = n_tok;
+  a.hq = n_q_heads, a.hkv = n_kv_heads, a.hd = head_dim, a.rot = rot_dim, a.pairs = style == SL_ROPE_PAIRS;
+  return from_kernel(rotary(a, cs(stream)));
+}
+
+sl_status sl_qk_norm_rope_bwd(const void* dyq, int64_t lddyq, const void* dyk, int64_t lddyk, const void* q,
+                              int64_t ldq, const void* k, int64_t ldk, const int32_t* positions,
+                              const float* inv_freq, int32_t rot_dim, int32_t style, const void* gamma_q,
+                              const void* gamma_k, float eps, int64_t n_tok, int32_t n_q_heads, int32_t n_kv_heads,
+                              int32_t head_dim, void* dq, int64_t lddq, void* dk, int64_t lddk, float* dgamma_q,
+                              float* dgamma_k, sl_workspace* ws, sl_stream stream) {
+  if (!dyq || !dyk || !dq || !dk || (gamma_q && (!q || !k)) || (!gamma_q && (dgamma_q || dgamma_k)))
+    return SL_ERR_INVALID_ARG;
+  if (sl_status st = rotary_args(positions, inv_freq, rot_dim, style, gamma_q, gamma_k, eps, n_tok, n_q_heads,
+                                 n_kv_heads, head_dim))
+    return st;
+  const int64_t nq = (int64_t)n_q_heads * head_dim, nk = (int64_t)n_kv_heads * head_dim;
+  if (!rows_ok(dyq, lddyq, nq) || !rows_ok(dyk, lddyk, nk) || !rows_ok(dq, lddq, nq) || !rows_ok(dk, lddk, nk) ||
+      (gamma_q && (!rows_ok(q, ldq, nq) || !rows_ok(k, ldk, nk))))
+    return SL_ERR_ALIGNMENT;
+  RotaryArgs a = {};
+  if (dgamma_q || dgamma_k) {
+    const size_t floats = (size_t)rotary_partial_floats(n_tok, head_dim);
+    Carver c(nullptr);
+    c.take<float>(floats);
+    if (sl_status st = ws_check(ws, c.off)) return st;
+    Carver c2(ws->ptr);
+    a.partial = c2.take<float>(floats);
+  }
+  a.xq = q, a.xk = k, a.ldxq = ldq, a.ldxk = ldk, a.dyq = dyq, a.dyk = dyk, a.lddq = lddyq, a.lddk = lddyk;
+  a.oq = dq, a.ok = dk, a.ldoq = lddq, a.ldok = lddk;
+  a.pos = positions, a.inv_freq = inv_freq, a.gq = gamma_q, a.gk = gamma_k, a.eps = eps, a.n_tok = n_tok;
+  a.hq = n_q_heads, a.hkv = n_kv_heads, a.hd = head_dim, a.rot = rot_dim, a.pairs = style == SL_ROPE_PAIRS;
+  a.dgq = dgamma_q, a.dgk = dgamma_k;
+  return from_kernel(rotary(a, cs(stream)));
+}
+
+// ------------------------------------------------------------------ token log probabilities
+namespace {
+bool logits_ok(const void* p, int64_t ld, int64_t vocab, sl_dtype t) {
+  return al16(p) && ld >= vocab && ld % (t == SL_DT_F32 ? 4 : 8) == 0;
+}
+bool logprob_sizes_ok(int64_t rows, int64_t vocab) {
+  return rows >= 1 && vocab >= 1 && rows <= (1 << 28) && vocab <= (1 << 24);
+}
+}  // namespace
+
+sl_status sl_token_logprobs_fwd(sl_dtype dtype, const void* logits, int64_t ld, int64_t n_rows, int64_t vocab,
+                                const int32_t* targets, float* logp, float* stats, float* entropy, int32_t top_k,
+                                int32_t* top_ids, float* top_logp, sl_stream stream) {
+  if (!logits || !targets || !logp || !stats || (dtype != SL_DT_BF16 && dtype != SL_DT_F32)) return SL_ERR_INVALID_ARG;
+  if (top_k > 0 && (!top_ids || !top_logp)) return SL_ERR_INVALID_ARG;
+  if (!logprob_sizes_ok(n_rows, vocab) || top_k < 0 || top_k > 32 || top_k > vocab) return SL_ERR_SHAPE;
+  if (!logits_ok(logits, ld, vocab, dtype) || (reinterpret_cast<uintptr_t>(stats) & 7)) return SL_ERR_ALIGNMENT;
+  LogprobArgs a = {};
+  a.z = logits, a.fp32 = dtype == SL_DT_F32, a.ld = ld, a.rows = n_rows, a.vocab = vocab, a.target = targets;
+  a.logp = logp, a.stats = stats, a.entropy = entropy, a.k = top_k, a.top_ids = top_ids, a.top_logp = top_logp;
+  return from_kernel(token_logprobs_fwd(a, cs(stream)));
+}
+
+sl_status sl_token_logprobs_bwd(sl_dtype dtype, const void* logits, int64_t ld, int64_t n_rows, int64_t vocab,
+                                const int32_t* targets, const float* stats, const float* g_logp,
+                                const float* g_entropy, const float* entropy, void* dlogits, int64_t ldd,
+                                sl_stream stream) {
+  if (!logits || !targets || !stats || !g_logp || !dlogits || (g_entropy && !entropy) ||
+      (dtype != SL_DT_BF16 && dtype != SL_DT_F32))
+    return SL_ERR_INVALID_ARG;
+  if (!logprob_sizes_ok(n_rows, vocab)) return SL_ERR_SHAPE;
+  if (!logits_ok(logits, ld, vocab, dtype) || !logits_ok(dlogits, ldd, vocab, dtype) ||
+      (reinterpret_cast<uintptr_t>(stats) & 7))
+    return SL_ERR_ALIGNMENT;
+  LogprobArgs a = {};
+  a.z = logits, a.fp32 = dtype == SL_DT_F32, a.ld = ld, a.rows = n_rows, a.vocab = vocab, a.target = targets;
+  a.stats = const_cast<float*>(stats), a.g_logp = g_logp, a.g_entropy = g_entropy;
+  a.entropy = const_cast<float*>(entropy), a.dz = dlogits, a.ldd = ldd;
+  return from_kernel(token_logprobs_bwd(a, cs(stream)));
+}
+
 sl_status sl_set_pair_tile_rows(int32_t rows) {
   if (rows != 0 && rows != 128 && rows != 256 && rows != 512) return SL_ERR_INVALID_ARG;
   set_forced_pair_mh(rows == 128 ? -1 : rows / 256);

@@ -1,0 +1,1292 @@
+// Grouped-query attention in which each query sees an interval of its sequence's keys, with capped
+// scores and a bias that falls with the distance, forward and backward, on the tcgen05 tensor cores:
+//   t_ij = cap tanh(scale q_i k_j / cap) (or scale q_i k_j) - slope_h |i - j|,  lo_i <= j < hi_i;
+//   P = softmax_j(t), o_i = sum_j P_ij v_j, lse_i = log sum_j e^(t_ij); a row that sees nothing: o = 0, lse = -inf.
+//   Backward with dP = do v, D_i = sum_j P_ij dP_ij: dS = P (dP - D) (1 - tanh^2), dq = scale dS k, dk = scale dS^T q,
+//   dv = P^T do.
+// Intervals say causal, packed documents, prefixes, windows and padding alike, and their extremes over
+// 128-row tiles say which tiles of keys a tile of queries needs at all and which need no mask. That is the plan
+// (attention_plan): made once for a batch and read by every layer's forward and backward.
+#include <cuda_bf16.h>
+#include <type_traits>
+
+#include <algorithm>
+#include <atomic>
+#include <cmath>
+
+#include "sl_attn.cuh"
+
+namespace sl {
+
+namespace {
+
+constexpr int kSoftThreads = 256;                   // forward: warps 2..9 softmax / epilogue
+constexpr int kAttnThreads = 64 + kSoftThreads;     // warp 0 TMA, warp 1 MMA + TMEM
+constexpr int kBwdComputeThreads = 256;                   // backward: warps 2..9
+constexpr int kAttnBwdThreads = 64 + kBwdComputeThreads;  // warp 0 TMA, warp 1 MMA + TMEM
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// ------------------------------------------------------------------------------------------- plan
+
+constexpr int kPlanHeader = 16;          // int32 words
+constexpr int32_t kPlanMagic = 0x534c504c;
+
+struct Plan {
+  const int32_t* header;   // magic, n_seq, S
+  const int32_t *lo, *hi;  // [T], within [0, S]; a row that sees nothing has lo = hi = 0
+  // [n_seq * n_t], n_t = ceil(S / 128). q_range: key tiles [x, y) that any row of the query tile sees (never
+  // empty: [0, 1) when none does), and [z, w) that all of its rows see whole; k_range: query tiles [x, y) that
+  // see any of the key tile (never empty)
+  const int4* q_range;
+  const int2* k_range;
+  const int32_t *q_order, *k_order;  // tiles (sequence * n_t + tile), the longest ranges first
+};
+
+int64_t plan_tiles(int n_seq, int S) { return (int64_t)n_seq * ((S + kTile - 1) / kTile); }
+
+// Carves a plan out of a buffer (16-byte aligned) and returns its bytes.
+int64_t carve_plan(void* buf, int n_seq, int S, Plan* out) {
+  const int64_t T = (int64_t)n_seq * S, nt = plan_tiles(n_seq, S);
+  uint8_t* b = static_cast<uint8_t*>(buf);
+  int64_t off = 0;
+  auto take = [&](int64_t bytes) {
+    uint8_t* p = b ? b + off : nullptr;
+    off += (bytes + 15) & ~int64_t(15);
+    return p;
+  };
+  Plan p;
+  p.header = reinterpret_cast<int32_t*>(take(kPlanHeader * 4));
+  p.lo = reinterpret_cast<int32_t*>(take(T * 4));
+  p.hi = reinterpret_cast<int32_t*>(take(T * 4));
+  p.q_range = reinterpret_cast<int4*>(take(nt * 16));
+  p.k_range = reinterpret_cast<int2*>(take(nt * 8));
+  p.q_order = reinterpret_cast<int32_t*>(take(nt * 4));
+  p.k_order = reinterpret_cast<int32_t*>(take(nt * 4));
+  if (out) *out = p;
+  return off;
+}
+
+// Whether the buffer holds a plan of these sizes (else the error word is set and nothing is computed).
+__device__ __forceinline__ bool plan_fits(const Plan& p, int n_seq, int S, int* err) {
+  const bool ok = p.header[0] == kPlanMagic && p.header[1] == n_seq && p.header[2] == S;
+  if (!ok && threadIdx.x == 0 && blockIdx.x == 0) record_error(err, DEV_BAD_PLAN);
+  return ok;
+}
+
+constexpr int kPlanThreads = 1024;
+
+// Rows of the tiles (sequence * n_t + tile) first, first + step, ...: a warp per tile.
+__device__ void plan_rows(const Plan& p, const int32_t* row_lo, const int32_t* row_hi, int n_seq, int S, int64_t first,
+                          int64_t step) {
+  const int n_t = (S + kTile - 1) / kTile, lane = threadIdx.x & 31;
+  int32_t *lo = const_cast<int32_t*>(p.lo), *hi = const_cast<int32_t*>(p.hi);
+  for (int64_t at = first; at < (int64_t)n_seq * n_t; at += step) {
+    const int t = (int)(at % n_t);
+    const int64_t b = at / n_t;
+    int l_min = S, l_max = 0, h_min = S, h_max = 0;
+    bool any_empty = false;
+    for (int r = lane; r < kTile; r += 32) {
+      const int q = t * kTile + r;
+      if (q >= S) continue;
+      const int64_t row = b * S + q;
+      int l = max(0, row_lo ? row_lo[row] : 0), h = min(S, row_hi ? row_hi[row] : q + 1);
+      if (l >= h) {
+        l = h = 0;
+        any_empty = true;
+      } else {
+        l_min = min(l_min, l);
+        l_max = max(l_max, l);
+        h_min = min(h_min, h);
+        h_max = max(h_max, h);
+      }
+      lo[row] = l;
+      hi[row] = h;
+    }
+    l_min = __reduce_min_sync(0xffffffffu, l_min);
+    l_max = __reduce_max_sync(0xffffffffu, l_max);
+    h_min = __reduce_min_sync(0xffffffffu, h_min);
+    h_max = __reduce_max_sync(0xffffffffu, h_max);
+    any_empty = __any_sync(0xffffffffu, any_empty);
+    if (lane == 0) {
+      int4 v = h_max == 0 ? make_int4(0, 1, 0, 0)
+                          : make_int4(l_min / kTile, (h_max + kTile - 1) / kTile, (l_max + kTile - 1) / kTile, h_min / kTile);
+      if (any_empty) v.z = v.w = 0;
+      const_cast<int4*>(p.q_range)[at] = v;
+      const_cast<int2*>(p.k_range)[at] = make_int2(n_t, 0);
+    }
+  }
+}
+
+// Tiles by the lengths of their ranges, the longest first (equal ones in no set order: the order only
+// says when a unit starts). hist: n_t + 2 counters.
+template <typename R>
+__device__ void plan_order(const R* range, int64_t n, int n_t, int32_t* order, int32_t* hist, int32_t* carry) {
+  for (int i = threadIdx.x; i < n_t + 2; i += kPlanThreads) hist[i] = 0;
+  __syncthreads();
+  for (int64_t at = threadIdx.x; at < n; at += kPlanThreads) atomicAdd(&hist[n_t - (range[at].y - range[at].x)], 1);
+  __syncthreads();
+  // exclusive sums, 1024 counters at a time
+  if (threadIdx.x == 0) *carry = 0;
+  __syncthreads();
+  __shared__ int32_t warp_sum[32];
+  for (int base = 0; base < n_t + 2; base += kPlanThreads) {
+    const int i = base + threadIdx.x, lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int v = i < n_t + 2 ? hist[i] : 0;
+    int inc = v;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += u;
+    }
+    if (lane == 31) warp_sum[w] = inc;
+    __syncthreads();
+    int before = *carry;
+    for (int k = 0; k < w; ++k) before += warp_sum[k];
+    if (i < n_t + 2) hist[i] = before + inc - v;
+    __syncthreads();
+    if (threadIdx.x == kPlanThreads - 1) *carry = before + inc;
+    __syncthreads();
+  }
+  for (int64_t at = threadIdx.x; at < n; at += kPlanThreads)
+    order[atomicAdd(&hist[n_t - (range[at].y - range[at].x)], 1)] = (int32_t)at;
+  __syncthreads();
+}
+
+// Key tiles' ranges from the query tiles', and both orders (one block).
+__device__ void plan_tiles_and_order(const Plan& p, int n_seq, int S, int32_t* hist, int32_t* carry) {
+  const int n_t = (S + kTile - 1) / kTile;
+  const int64_t n = (int64_t)n_seq * n_t;
+  int2* kr = const_cast<int2*>(p.k_range);
+  for (int64_t at = threadIdx.x; at < n; at += kPlanThreads) {
+    const int4 v = p.q_range[at];
+    const int t = (int)(at % n_t);
+    const int64_t seq0 = at - t;
+    for (int j = v.x; j < v.y; ++j) {
+      atomicMin(&kr[seq0 + j].x, t);
+      atomicMax(&kr[seq0 + j].y, t + 1);
+    }
+  }
+  __syncthreads();
+  for (int64_t at = threadIdx.x; at < n; at += kPlanThreads)
+    if (kr[at].y == 0) kr[at] = make_int2(0, 1);
+  __syncthreads();
+  plan_order(p.q_range, n, n_t, const_cast<int32_t*>(p.q_order), hist, carry);
+  plan_order(p.k_range, n, n_t, const_cast<int32_t*>(p.k_order), hist, carry);
+  if (threadIdx.x < 3) const_cast<int32_t*>(p.header)[threadIdx.x] = threadIdx.x == 0 ? kPlanMagic : threadIdx.x == 1 ? n_seq : S;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) plan_rows_kernel(Plan p, const int32_t* lo, const int32_t* hi, int n_seq, int S) {
+  pdl_wait();
+  const int64_t warp = ((int64_t)blockIdx.x * kPlanThreads + threadIdx.x) >> 5;
+  plan_rows(p, lo, hi, n_seq, S, warp, (int64_t)gridDim.x * (kPlanThreads / 32));
+}
+
+// rows: also the rows (a plan of few tiles is one launch)
+__global__ void __launch_bounds__(kPlanThreads) plan_tiles_kernel(Plan p, const int32_t* lo, const int32_t* hi, int n_seq, int S,
+                                                                  bool rows) {
+  extern __shared__ int32_t hist[];
+  __shared__ int32_t carry;
+  pdl_wait();
+  if (rows) {
+    plan_rows(p, lo, hi, n_seq, S, threadIdx.x >> 5, kPlanThreads / 32);
+    __syncthreads();
+  }
+  plan_tiles_and_order(p, n_seq, S, hist, &carry);
+}
+
+// ----------------------------------------------------------------------------------------- scores
+
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// tanh(u) from e^(2u) = 2^(u'), u' = 2 log2(e) u: 1 - 2 / (2^u' + 1). The error is about 1e-7 of 1 at every u
+// (2^u' = inf gives 1, 2^u' = 0 gives -1); tanh.approx would be off by 5e-4 of the value.
+__device__ __forceinline__ float tanh_2(float u2) { return fmaf(-2.f, rcp(ex2(u2) + 1.f), 1.f); }
+
+// The score in powers of two from the raw product s. CAP: mul = 2 log2(e) scale / cap, cap_log2 = cap
+// log2(e); else mul = log2(e) scale. away: the distance, of either sign.
+template <bool CAP, bool BIAS>
+__device__ __forceinline__ float score(float s, float mul, float cap_log2, float slope, float away) {
+  float y = CAP ? cap_log2 * tanh_2(s * mul) : s * mul;
+  if (BIAS) y = fmaf(-slope, fabsf(away), y);
+  return y;
+}
+template <bool CAP, bool BIAS>
+__device__ __forceinline__ float score_grad(float s, float mul, float cap_log2, float slope, float away, float& grad) {
+  if (!CAP) return score<CAP, BIAS>(s, mul, cap_log2, slope, away);
+  const float t = tanh_2(s * mul);
+  grad = fmaf(-t, t, 1.f);
+  const float y = cap_log2 * t;
+  return BIAS ? fmaf(-slope, fabsf(away), y) : y;
+}
+
+struct MaskedFwdParams {
+  CUtensorMap qmap, kmap, vmap;  // [head_dim, heads, seq_len, n_seq], boxes 64 x 1 x 128 x 1
+  CUtensorMap omap;              // the same view of o (bulk stores of the output tile)
+  Plan plan;
+  const float* slopes;           // [hq]
+  float* lse;                    // [n_q_heads][n_seq * seq_len]
+  int32_t n_seq, S, hq, hkv, hd, nd;
+  float mul, cap_log2;           // see score()
+  int* err;
+};
+
+struct MaskedDeltaParams {
+  CUtensorMap qmap, kmap, vmap, domap;
+  Plan plan;
+  const float* slopes;
+  const float* lse;              // [hq][T]
+  float* delta;                  // [hq][T]
+  float* dq_acc;                 // [T][hq * hd]
+  int32_t n_seq, S, hq, hkv, hd, nd;
+  float mul, cap_log2;
+  int* err;
+};
+
+struct MaskedBwdParams {
+  CUtensorMap qmap, kmap, vmap, domap;
+  CUtensorMap dqmap;             // dq_acc as [head_dim, hq, seq_len, n_seq] fp32, boxes 32 x 1 x 32 x 1
+  Plan plan;
+  const float* slopes;
+  const float* lse;              // [hq][T]
+  const float* delta;            // [hq][T]: D per query row
+  __nv_bfloat16* dk;
+  __nv_bfloat16* dv;
+  int64_t lddk, lddv;
+  int32_t n_seq, S, hq, hkv, hd, nd;
+  float scale, mul, cap_log2;
+  int* err;
+};
+
+// Barrier of the forward's softmax warps that also returns whether `ok` holds in all of them.
+__device__ __forceinline__ bool bar_and_soft(bool ok) {
+  uint32_t all;
+  asm volatile(
+      "{\n\t.reg .pred q, a;\n\t"
+      "setp.ne.u32 q, %1, 0;\n\t"
+      "bar.red.and.pred a, 1, 256, q;\n\t"
+      "selp.u32 %0, 1, 0, a;\n\t}"
+      : "=r"(all)
+      : "r"((uint32_t)ok)
+      : "memory");
+  return all != 0;
+}
+// Barrier of the backward's compute warps that also returns whether `ok` holds in all of them.
+__device__ __forceinline__ bool bar_and_bwd(bool ok) {
+  uint32_t all;
+  asm volatile(
+      "{\n\t.reg .pred q, a;\n\t"
+      "setp.ne.u32 q, %1, 0;\n\t"
+      "bar.red.and.pred a, 1, 256, q;\n\t"
+      "selp.u32 %0, 1, 0, a;\n\t}"
+      : "=r"(all)
+      : "r"((uint32_t)ok)
+      : "memory");
+  return all != 0;
+}
+
+// ------------------------------------------------------------------------------------ forward
+
+template <bool CAP, bool BIAS>
+__global__ void __launch_bounds__(kAttnThreads, 1) masked_fwd_kernel(const __grid_constant__ MaskedFwdParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int nd = p.nd;
+  uint8_t* sq = smem;                          // Q: nd chunks (room for 2)
+  uint8_t* skv = sq + 2 * kChunk;              // stage s: K (nd chunks) then V (nd chunks)
+  uint8_t* sp = skv + 2 * 2 * nd * kChunk;     // P: 2 chunks (128 keys)
+  uint8_t* sob = sp + 2 * kChunk;              // O staging tile for the bulk stores: 2 chunks
+  float* s_l = reinterpret_cast<float*>(sob + 2 * kChunk);  // [2][128]: the two halves' row sums
+  uint64_t* bars = reinterpret_cast<uint64_t*>(s_l + 256);
+  uint64_t* q_full = bars;
+  uint64_t* q_empty = bars + 1;   // Q of a query tile is free once its last S has read it
+  uint64_t* k_full = bars + 2;    // [2]
+  uint64_t* k_empty = bars + 4;   // [2]: K of a stage is free once S has read it
+  uint64_t* v_full = bars + 6;    // [2]
+  uint64_t* v_empty = bars + 8;   // [2]: V of a stage is free once P V has read it
+  uint64_t* s_full = bars + 10;   // [2]
+  uint64_t* s_free = bars + 12;   // [2]
+  uint64_t* p_full = bars + 14;
+  uint64_t* pv_done = bars + 15;
+  uint64_t* o_free = bars + 16;   // [2]: an O accumulator is free once the epilogue has read it
+  uint64_t* drain = bars + 18;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 19);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // Persistent CTAs: unit u = (tile of queries in the plan's order, query head); CTA c takes units
+  // c, c + grid, ... Every role walks the same units; K/V stages, S buffers and P follow one tile
+  // counter over all of a CTA's units, the two O accumulators alternate by unit. A unit's key tiles
+  // are j0 .. j1 - 1 (at least one, so that a tile whose rows see nothing takes the same path).
+  const int n_qt = (p.S + kTile - 1) / kTile;
+  const int n_units = n_qt * p.n_seq * p.hq;
+  const int hpg = p.hq / p.hkv;
+  auto unit = [&](int u, int& qt, int& h, int& b, int& j0, int& j1) {
+    const int at = p.plan.q_order[u / p.hq];
+    const int4 range = p.plan.q_range[at];
+    qt = at % n_qt;
+    b = at / n_qt;
+    h = u % p.hq;
+    j0 = range.x;
+    j1 = range.y;
+  };
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&k_full[s], 1);
+      mbar_init(&k_empty[s], 1);
+      mbar_init(&v_full[s], 1);
+      mbar_init(&v_empty[s], 1);
+      mbar_init(&s_full[s], 1);
+      mbar_init(&s_free[s], kSoftThreads);
+      mbar_init(&o_free[s], kSoftThreads);
+    }
+    mbar_init(p_full, kSoftThreads);
+    mbar_init(pv_done, 1);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;  // S buffers at columns 0 and 128, O accumulators at 256 and 384
+  pdl_wait();
+  const bool plan_ok = plan_fits(p.plan, p.n_seq, p.S, p.err);
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // Loads in order: Q of a unit right before K of its first key tile (once the previous unit's
+      // last S has read Q), K of tile t + 1 ahead of V of tile t.
+      auto load_kv = [&](int t, bool is_v, int g, int kv, int b) -> bool {
+        const int s = t & 1;
+        uint64_t* empty = is_v ? &v_empty[s] : &k_empty[s];
+        uint64_t* full = is_v ? &v_full[s] : &k_full[s];
+        if (!mbar_wait(empty, ((t >> 1) & 1) ^ 1, abort_flag, p.err, DEV_TIMEOUT_PRODUCER)) return false;
+        mbar_arrive_expect_tx(full, nd * kChunk);
+        uint8_t* st = skv + s * 2 * nd * kChunk + (is_v ? nd * kChunk : 0);
+        for (int c = 0; c < nd; ++c)
+          tma_load_4d(st + c * kChunk, is_v ? &p.vmap : &p.kmap, full, 64 * c, g, kv * kTile, b);
+        return true;
+      };
+      int nq = 0, nk = 0, nv = 0;  // Q, K and V tiles issued
+      int pg = 0, pkv = 0, pb = 0;   // the tile whose V is still to load (tile nv when nk > nv)
+      bool ok = true;
+      for (int u = blockIdx.x, i = 0; ok && plan_ok && u < n_units; u += gridDim.x, ++i) {
+        int qt, h, b, j0, j1;
+        unit(u, qt, h, b, j0, j1);
+        const int g = h / hpg;
+        for (int j = j0; j < j1; ++j) {
+          if (j == j0) {
+            // the previous unit's last V first (its P V does not wait for this unit), then Q
+            if (nk > nv) {
+              if (!load_kv(nv, true, pg, pkv, pb)) { ok = false; break; }
+              ++nv;
+            }
+            if (i > 0 && !mbar_wait(q_empty, (i - 1) & 1, abort_flag, p.err, DEV_TIMEOUT_PRODUCER)) { ok = false; break; }
+            mbar_arrive_expect_tx(q_full, nd * kChunk);
+            for (int c = 0; c < nd; ++c) tma_load_4d(sq + c * kChunk, &p.qmap, q_full, 64 * c, h, qt * kTile, b);
+            ++nq;
+          }
+          if (!load_kv(nk, false, g, j, b)) { ok = false; break; }
+          ++nk;
+          if (j > j0) {
+            if (!load_kv(nv, true, pg, pkv, pb)) { ok = false; break; }
+            ++nv;
+          }
+          pg = g;
+          pkv = j;
+          pb = b;
+        }
+      }
+      if (ok && nk > nv && load_kv(nv, true, pg, pkv, pb)) ++nv;
+      // every copy lands before the CTA may exit
+      if (nq > 0) mbar_wait(q_full, (nq - 1) & 1, nullptr, p.err, DEV_TIMEOUT_DRAIN);
+      for (int t = max(0, nk - 2); t < nk; ++t) mbar_wait(&k_full[t & 1], (t >> 1) & 1, nullptr, p.err, DEV_TIMEOUT_DRAIN);
+      for (int t = max(0, nv - 2); t < nv; ++t) mbar_wait(&v_full[t & 1], (t >> 1) & 1, nullptr, p.err, DEV_TIMEOUT_DRAIN);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t id_s = idesc_bf16(128, 128, 0, 0);          // S = Q K^T: both K-major over d
+      const uint32_t id_pv = idesc_bf16(128, 64 * nd, 0, 1);     // O += P V: P K-major, V MN-major
+      const uint32_t aq = smem_u32(sq), ap = smem_u32(sp);
+      // P V of tile t (the first or a later key tile of the CTA's unit i) into the unit's O accumulator
+      auto issue_pv = [&](int t, int i, bool first) -> bool {
+        if (!mbar_wait(p_full, t & 1, abort_flag, p.err, DEV_TIMEOUT_MMA)) return false;
+        if (!mbar_wait(&v_full[t & 1], (t >> 1) & 1, abort_flag, p.err, DEV_TIMEOUT_MMA)) return false;
+        // the first P V of a unit overwrites its accumulator: the epilogue of unit i - 2 has read it
+        if (first && i >= 2 && !mbar_wait(&o_free[i & 1], ((i >> 1) & 1) ^ 1, abort_flag, p.err, DEV_TIMEOUT_MMA))
+          return false;
+        tc_fence_after();
+        const uint32_t bv = smem_u32(skv + (t & 1) * 2 * nd * kChunk + nd * kChunk);
+        for (int k = 0; k < 8; ++k)
+          umma_bf16(tmem + 256 + 128 * (i & 1), kmajor_desc(ap, k), mnmajor_desc(bv, k), id_pv, (!first || k > 0) ? 1u : 0u);
+        umma_commit(pv_done);
+        umma_commit(&v_empty[t & 1]);
+        return true;
+      };
+      bool ok = true;
+      int t = 0;
+      for (int u = blockIdx.x, i = 0; ok && plan_ok && u < n_units; u += gridDim.x, ++i) {
+        int qt, h, b, j0, j1;
+        unit(u, qt, h, b, j0, j1);
+        if (!mbar_wait(q_full, i & 1, abort_flag, p.err, DEV_TIMEOUT_MMA)) { ok = false; break; }
+        for (int j = j0; j < j1; ++j, ++t) {
+          const int s = t & 1;
+          if (!mbar_wait(&k_full[s], (t >> 1) & 1, abort_flag, p.err, DEV_TIMEOUT_MMA)) { ok = false; break; }
+          if (t >= 2 && !mbar_wait(&s_free[s], ((t - 2) >> 1) & 1, abort_flag, p.err, DEV_TIMEOUT_MMA)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t bk = smem_u32(skv + s * 2 * nd * kChunk);
+          for (int k = 0; k < 4 * nd; ++k)
+            umma_bf16(tmem + 128 * s, kmajor_desc(aq, k), kmajor_desc(bk, k), id_s, k > 0 ? 1u : 0u);
+          umma_commit(&s_full[s]);
+          umma_commit(&k_empty[s]);
+          if (j == j1 - 1) umma_commit(q_empty);
+          if (j > j0 && !issue_pv(t - 1, i, j - 1 == j0)) { ok = false; break; }
+        }
+        // this unit's last P V before the next unit's first S: the epilogue needs it first
+        if (ok && !issue_pv(t - 1, i, j1 - 1 == j0)) ok = false;
+      }
+      umma_commit(drain);
+      mbar_wait(drain, 0, nullptr, p.err, DEV_TIMEOUT_DRAIN);
+    }
+  } else {
+    // Eight softmax warps: warp w holds query rows 32 (w % 4) .. + 31 (its TMEM lanes) and one half
+    // of the key columns of each S tile (exponentials, P) and of O (rescale, output). Both halves
+    // read the whole S row for its maximum, so they keep the same running maximum without an
+    // exchange; their partial row sums meet once per unit, at its end.
+    const int cw = warp - 2;
+    const int quarter = warp & 3;
+    const int half = cw >> 2;
+    const int r = quarter * 32 + lane;               // query row in the tile = TMEM lane
+    const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
+    const int own0 = 64 * half, oth0 = 64 - own0;    // first key column of this half / the other
+    const bool storer = cw == 0 && lane == 0;        // issues the output tile's bulk stores
+    bool ok = true;
+    int t = 0;
+    for (int u = blockIdx.x, i = 0; plan_ok && u < n_units; u += gridDim.x, ++i) {
+      int qt, h, b, j0, j1;
+      unit(u, qt, h, b, j0, j1);
+      const int qpos = qt * kTile + r;               // position in the sequence
+      // the keys [lo, hi) that this row sees (rows past the sequence: none)
+      const int64_t row_at = (int64_t)b * p.S + qpos;
+      const int lo = qpos < p.S ? p.plan.lo[row_at] : 0, hi = qpos < p.S ? p.plan.hi[row_at] : 0;
+      const float slope = BIAS ? p.slopes[h] * kLog2e : 0.f;
+      const uint32_t o_tm = tmem + lane_off + 256 + 128 * (i & 1);
+      float m = -INFINITY, l = 0.f;                  // l: this half's share of the row sum
+      for (int j = j0; j < j1 && ok; ++j, ++t) {
+        const int s = t & 1;
+        if (!__all_sync(0xffffffffu, mbar_wait(&s_full[s], (t >> 1) & 1, abort_flag, p.err, DEV_TIMEOUT_EPILOGUE))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        uint32_t so[2][32], sx[2][32];               // this half's columns, the other half's
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          tmem_ld32(tmem + lane_off + 128 * s + own0 + 32 * c, so[c]);
+          tmem_ld32(tmem + lane_off + 128 * s + oth0 + 32 * c, sx[c]);
+        }
+        tmem_ld_wait();
+        tc_fence_before();
+        mbar_arrive(&s_free[s]);
+        // scores in powers of two: capped, biased, and -inf where the row does not see the key
+        const int kbase = j * kTile;
+        const int kmin = lo - kbase, kmax = hi - 1 - kbase;  // visible columns of this tile
+        const bool whole = kmin <= 0 && kmax >= kTile - 1;
+        const float away = (float)(qpos - kbase);
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const int co = own0 + 32 * c + e, cx = oth0 + 32 * c + e;
+            float yo = score<CAP, BIAS>(__uint_as_float(so[c][e]), p.mul, p.cap_log2, slope, away - (float)co);
+            float yx = score<CAP, BIAS>(__uint_as_float(sx[c][e]), p.mul, p.cap_log2, slope, away - (float)cx);
+            if (!whole) {
+              if (co < kmin || co > kmax) yo = -INFINITY;
+              if (cx < kmin || cx > kmax) yx = -INFINITY;
+            }
+            so[c][e] = __float_as_uint(yo);
+            sx[c][e] = __float_as_uint(yx);
+          }
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            mx[e & 3] = fmaxf(mx[e & 3], fmaxf(__uint_as_float(so[c][e]), __uint_as_float(sx[c][e])));
+        const float mj = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        // The running maximum moves only when a row's maximum grows by more than 2^8 in the
+        // exponential's scale: the exponentials then stay below 256 and O and l keep one common
+        // reference, so O is rescaled in TMEM rarely (after the first tiles almost never).
+        const float m_cand = fmaxf(m, mj);
+        const bool grow = m == -INFINITY || m_cand - m > 8.0f;
+        const float m_new = grow ? m_cand : m;
+        const float mb = m_new == -INFINITY ? 0.f : m_new;  // a row that has seen nothing yet
+        const float corr = (m == -INFINITY) ? 0.f : (grow ? ex2(m - mb) : 1.f);
+        float rs[4] = {0.f, 0.f, 0.f, 0.f};
+        uint32_t pw[2][16];
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const float e0 = ex2(__uint_as_float(so[c][e]) - mb);
+            const float e1 = ex2(__uint_as_float(so[c][e + 1]) - mb);
+            rs[(e >> 1) & 3] += e0 + e1;
+            pw[c][e / 2] = pack2(e0, e1);
+          }
+        l = l * corr + ((rs[0] + rs[1]) + (rs[2] + rs[3]));
+        if (j > j0) {
+          // the previous P V has landed in O (and read P): rescale this half of O when the maximum
+          // grew (the first key tile of a unit: the previous unit's epilogue waited for its last P V)
+          if (!__all_sync(0xffffffffu, mbar_wait(pv_done, (t - 1) & 1, abort_flag, p.err, DEV_TIMEOUT_EPILOGUE))) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          if (__any_sync(0xffffffffu, corr != 1.f)) {
+            for (int c = 2 * half; c < 2 * half + 2 && c < 2 * nd; ++c) {
+              uint32_t ov[32];
+              __syncwarp();
+              tmem_ld32(o_tm + 32 * c, ov);
+              tmem_ld_wait_regs(ov);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * corr);
+              tmem_st32(o_tm + 32 * c, ov);
+            }
+            tmem_st_wait();
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < 2; ++c) st_swizzled_row32(sp, r, own0 + 32 * c, pw[c]);
+        fence_proxy_async_smem();
+        tc_fence_before();
+        mbar_arrive(p_full);
+        m = m_new;
+      }
+      // this unit's last P V (tile t - 1) has landed
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(pv_done, (t - 1) & 1, abort_flag, p.err, DEV_TIMEOUT_EPILOGUE));
+      // the previous unit's bulk stores have read the staging tile (rewritten below)
+      if (storer) bulk_wait_read<0>();
+      s_l[half * 128 + r] = l;
+      // every softmax thread reaches both barriers of every unit (the loops only break)
+      ok = bar_and_soft(ok);
+      if (ok) {
+        // O / l as bf16 into the staging tile, laid out like a loaded tile (128-byte swizzle,
+        // 64-column chunks), then out by bulk tensor stores (rows past the sequence and columns
+        // past head_dim are not written); the accumulator is released as soon as it is read
+        tc_fence_after();
+        const float lt = s_l[r] + s_l[128 + r];
+        const float inv = lt == 0.f ? 0.f : 1.f / lt;  // a row that sees nothing: o = 0
+        for (int c = 2 * half; c < 2 * half + 2 && c < 2 * nd; ++c) {
+          uint32_t ov[32];
+          __syncwarp();
+          tmem_ld32(o_tm + 32 * c, ov);
+          tmem_ld_wait_regs(ov);
+          uint32_t w[16];
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) w[e / 2] = pack2(__uint_as_float(ov[e]) * inv, __uint_as_float(ov[e + 1]) * inv);
+          st_swizzled_row32(sob, r, 32 * c, w);
+        }
+        tc_fence_before();
+        mbar_arrive(&o_free[i & 1]);
+        fence_proxy_async_smem();
+        if (qpos < p.S && half == 0) p.lse[(int64_t)h * p.n_seq * p.S + (int64_t)b * p.S + qpos] = lt == 0.f ? -INFINITY : m * kLn2 + logf(lt);
+      }
+      ok = bar_and_soft(ok);
+      if (!ok) break;
+      if (storer) {
+        for (int c = 0; c < nd; ++c) tma_store_4d(&p.omap, sob + c * kChunk, 64 * c, h, qt * kTile, b);
+        bulk_commit();
+      }
+    }
+    if (storer) bulk_wait_all();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) {
+    __syncwarp();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// --------------------------------------------------------------------------- backward pieces
+
+// D_i = sum_j P_ij dP_ij = dO_i . o_i for every query row and head, and the dQ accumulator's rows set to zero
+// (the backward adds into them). From P and dP in fp32 and not from the stored o: that one is rounded to bf16, and
+// its error, the same for all keys of a row, is as large as all other roundings of dq and dk together where a row's
+// weight lies on few keys (relative error of dq over 4e-3 with 8 keys, against 2.3e-3).
+// Persistent CTAs over the same units as the forward. Warp 0 loads Q, dO and a two-stage ring of (K, V); warp 1 issues
+// S = Q K^T and dP = dO V^T into two alternating pairs of TMEM buffers; warps 2-9 read both, half of the columns
+// each, and sum exp(S - lse) dP per row: nothing waits for the softmax, so the products run ahead.
+template <bool CAP, bool BIAS>
+__global__ void __launch_bounds__(kAttnThreads, 1) masked_delta_kernel(const __grid_constant__ MaskedDeltaParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int nd = p.nd;
+  uint8_t* sq = smem;                       // Q, then dO: nd chunks each
+  uint8_t* skv = sq + 2 * nd * kChunk;      // stage s: K, then V
+  float* s_part = reinterpret_cast<float*>(smem + 12 * kChunk);  // [128]: the second half's sums
+  uint64_t* bars = reinterpret_cast<uint64_t*>(s_part + 128);
+  uint64_t* q_full = bars;
+  uint64_t* q_empty = bars + 1;
+  uint64_t* kv_full = bars + 2;    // [2]
+  uint64_t* kv_empty = bars + 4;   // [2]
+  uint64_t* s_full = bars + 6;     // [2]
+  uint64_t* s_free = bars + 8;     // [2]
+  uint64_t* drain = bars + 10;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 11);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int n_qt = (p.S + kTile - 1) / kTile;
+  const int n_units = n_qt * p.n_seq * p.hq;
+  const int hpg = p.hq / p.hkv;
+  auto unit = [&](int u, int& qt, int& h, int& b, int& j0, int& j1) {
+    const int at = p.plan.q_order[u / p.hq];
+    const int4 range = p.plan.q_range[at];
+    qt = at % n_qt;
+    b = at / n_qt;
+    h = u % p.hq;
+    j0 = range.x;
+    j1 = range.y;
+  };
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&kv_full[s], 1);
+      mbar_init(&kv_empty[s], 1);
+      mbar_init(&s_full[s], 1);
+      mbar_init(&s_free[s], kSoftThreads);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;  // buffer s: S at 256 s, dP at 256 s + 128
+  pdl_wait();
+  const bool plan_ok = plan_fits(p.plan, p.n_seq, p.S, p.err);
+  if (warp == 0) {
+    if (lane == 0) {
+      int nq = 0, t = 0;
+      bool ok = plan_ok;
+      for (int u = blockIdx.x, i = 0; ok && u < n_units; u += gridDim.x, ++i) {
+        int qt, h, b, j0, j1;
+        unit(u, qt, h, b, j0, j1);
+        if (i > 0 && !mbar_wait(q_empty, (i - 1) & 1, abort_flag, p.err, DEV_TIMEOUT_PRODUCER)) break;
+        mbar_arrive_expect_tx(q_full, 2 * nd * kChunk);
+        for (int c = 0; c < nd; ++c) {
+          tma_load_4d(sq + c * kChunk, &p.qmap, q_full, 64 * c, h, qt * kTile, b);
+          tma_load_4d(sq + (nd + c) * kChunk, &p.domap, q_full, 64 * c, h, qt * kTile, b);
+        }
+        ++nq;
+        for (int j = j0; j < j1; ++j, ++t) {
+          const int s = t & 1;
+          if (!mbar_wait(&kv_empty[s], ((t >> 1) & 1) ^ 1, abort_flag, p.err, DEV_TIMEOUT_PRODUCER)) { ok = false; break; }
+          mbar_arrive_expect_tx(&kv_full[s], 2 * nd * kChunk);
+          uint8_t* st = skv + s * 2 * nd * kChunk;
+          for (int c = 0; c < nd; ++c) {
+            tma_load_4d(st + c * kChunk, &p.kmap, &kv_full[s], 64 * c, h / hpg, j * kTile, b);
+            tma_load_4d(st + (nd + c) * kChunk, &p.vmap, &kv_full[s], 64 * c, h / hpg, j * kTile, b);
+          }
+        }
+      }
+      // every copy lands before the CTA may exit
+      if (nq > 0) mbar_wait(q_full, (nq - 1) & 1, nullptr, p.err, DEV_TIMEOUT_DRAIN);
+      for (int k = max(0, t - 2); k < t; ++k) mbar_wait(&kv_full[k & 1], (k >> 1) & 1, nullptr, p.err, DEV_TIMEOUT_DRAIN);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t id = idesc_bf16(128, 128, 0, 0);
+      const uint32_t aq = smem_u32(sq), ado = aq + nd * kChunk;
+      bool ok = plan_ok;
+      int t = 0;
+      for (int u = blockIdx.x, i = 0; ok && u < n_units; u += gridDim.x, ++i) {
+        int qt, h, b, j0, j1;
+        unit(u, qt, h, b, j0, j1);
+        if (!mbar_wait(q_full, i & 1, abort_flag, p.err, DEV_TIMEOUT_MMA)) break;
+        for (int j = j0; j < j1; ++j, ++t) {
+          const int s = t & 1;
+          if (!mbar_wait(&kv_full[s], (t >> 1) & 1, abort_flag, p.err, DEV_TIMEOUT_MMA) ||
+              (t >= 2 && !mbar_wait(&s_free[s], ((t - 2) >> 1) & 1, abort_flag, p.err, DEV_TIMEOUT_MMA))) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t bk = smem_u32(skv + s * 2 * nd * kChunk), bv = bk + nd * kChunk;
+          for (int k = 0; k < 4 * nd; ++k)
+            umma_bf16(tmem + 256 * s, kmajor_desc(aq, k), kmajor_desc(bk, k), id, k > 0 ? 1u : 0u);
+          for (int k = 0; k < 4 * nd; ++k)
+            umma_bf16(tmem + 256 * s + 128, kmajor_desc(ado, k), kmajor_desc(bv, k), id, k > 0 ? 1u : 0u);
+          umma_commit(&s_full[s]);
+          umma_commit(&kv_empty[s]);
+          if (j == j1 - 1) umma_commit(q_empty);
+        }
+      }
+      umma_commit(drain);
+      mbar_wait(drain, 0, nullptr, p.err, DEV_TIMEOUT_DRAIN);
+    }
+  } else {
+    const int quarter = warp & 3, half = (warp - 2) >> 2;
+    const int r = quarter * 32 + lane;
+    const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
+    bool ok = plan_ok;
+    int t = 0;
+    for (int u = blockIdx.x; plan_ok && u < n_units; u += gridDim.x) {
+      int qt, h, b, j0, j1;
+      unit(u, qt, h, b, j0, j1);
+      const int qpos = qt * kTile + r;
+      const bool in = qpos < p.S;
+      const int64_t row = (int64_t)b * p.S + qpos, T = (int64_t)p.n_seq * p.S;
+      const int lo = in ? p.plan.lo[row] : 0, hi = in ? p.plan.hi[row] : 0;
+      const float lse = lo < hi ? p.lse[(int64_t)h * T + row] * kLog2e : 0.f;
+      const float slope = BIAS ? p.slopes[h] * kLog2e : 0.f;
+      // the accumulator's rows of this unit: 128 x hd fp32, a row per 16 threads
+      for (int k = threadIdx.x - 64; k < 128 * (p.hd / 4); k += kSoftThreads) {
+        const int rr = qt * kTile + k / (p.hd / 4), c = k % (p.hd / 4) * 4;
+        if (rr < p.S)
+          *reinterpret_cast<float4*>(p.dq_acc + (((int64_t)b * p.S + rr) * p.hq + h) * p.hd + c) = make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      float sum[2] = {0.f, 0.f};
+      for (int j = j0; j < j1 && ok; ++j, ++t) {
+        const int s = t & 1;
+        ok = __all_sync(0xffffffffu, mbar_wait(&s_full[s], (t >> 1) & 1, abort_flag, p.err, DEV_TIMEOUT_EPILOGUE));
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t sv[2][32], dv[2][32];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          tmem_ld32(tmem + lane_off + 256 * s + 64 * half + 32 * c, sv[c]);
+          tmem_ld32(tmem + lane_off + 256 * s + 128 + 64 * half + 32 * c, dv[c]);
+        }
+        tmem_ld_wait_regs(sv[0]);
+        regs_after_wait(sv[1]);
+        regs_after_wait(dv[0]);
+        regs_after_wait(dv[1]);
+        tc_fence_before();
+        mbar_arrive(&s_free[s]);
+        const int c0 = j * kTile + 64 * half;  // key of this thread's first column
+        const bool whole = lo <= c0 && c0 + 64 <= hi;
+        const float away = (float)(qpos - c0);
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const int col = 32 * c + e;
+            float pe = ex2(score<CAP, BIAS>(__uint_as_float(sv[c][e]), p.mul, p.cap_log2, slope, away - (float)col) - lse);
+            if (!whole && (c0 + col < lo || c0 + col >= hi)) pe = 0.f;
+            sum[e & 1] = fmaf(pe, __uint_as_float(dv[c][e]), sum[e & 1]);
+          }
+      }
+      if (half == 1) s_part[r] = sum[0] + sum[1];
+      ok = bar_and_soft(ok);
+      if (ok && half == 0 && in) p.delta[(int64_t)h * T + row] = sum[0] + sum[1] + s_part[r];
+      ok = bar_and_soft(ok);  // s_part is read before the next unit writes it
+      if (!ok) break;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) {
+    __syncwarp();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// dq[t * ldq + c] = bf16(acc[t * n + c]) for a [T, n] fp32 accumulator (n % 4 == 0), four
+// columns per thread.
+__global__ void masked_dq_cast_kernel(const float* __restrict__ acc, int64_t T, int64_t n, __nv_bfloat16* __restrict__ dq,
+                                    int64_t ldq) {
+  pdl_wait();
+  const int64_t i = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * 4;
+  if (i >= T * n) return;
+  const int64_t t = i / n, c = i % n;
+  const float4 v = *reinterpret_cast<const float4*>(acc + i);
+  *reinterpret_cast<uint2*>(dq + t * ldq + c) = make_uint2(pack2(v.x, v.y), pack2(v.z, v.w));
+}
+
+// ----------------------------------------------------------------------------------- backward
+
+template <bool CAP, bool BIAS>
+__global__ void __launch_bounds__(kAttnBwdThreads, 1) masked_bwd_kernel(const __grid_constant__ MaskedBwdParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int nd = p.nd;
+  uint8_t* sk = smem;                  // K_j: nd chunks
+  uint8_t* sv = sk + nd * kChunk;      // V_j
+  uint8_t* sq = sv + nd * kChunk;      // Q_i
+  uint8_t* sdo = sq + nd * kChunk;     // dO_i
+  uint8_t* spt = sdo + nd * kChunk;    // P^T: 2 chunks (128 queries)
+  uint8_t* sdst = spt + 2 * kChunk;    // dS^T: 2 chunks
+  // P^T and dS^T also hold the dQ boxes (32 query rows x 32 fp32 per warp and box, 128-byte
+  // swizzle) once the MMAs of an iteration have read them
+  float* s_lse = reinterpret_cast<float*>(sdst + 2 * kChunk);  // [2][128] by iteration parity
+  float* s_delta = s_lse + 256;                                // [2][128]
+  int2* s_see = reinterpret_cast<int2*>(s_delta + 256);         // [2][128]: keys that each query sees
+  uint64_t* bars = reinterpret_cast<uint64_t*>(s_see + 256);
+  uint64_t* kv_full = bars;
+  uint64_t* q_full = bars + 1;
+  uint64_t* q_empty = bars + 2;
+  uint64_t* do_full = bars + 3;
+  uint64_t* do_empty = bars + 4;
+  uint64_t* s_full = bars + 5;
+  uint64_t* p_full = bars + 6;
+  uint64_t* mma2_done = bars + 7;
+  uint64_t* dq_free = bars + 8;
+  uint64_t* drain = bars + 9;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 10);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int n_t = (p.S + kTile - 1) / kTile;
+  const int g = blockIdx.x % p.hkv;
+  const int hpg = p.hq / p.hkv;
+  const int64_t T = (int64_t)p.n_seq * p.S;
+  if (threadIdx.x == 0) {
+    mbar_init(kv_full, 1);
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
+    mbar_init(do_full, 1);
+    mbar_init(do_empty, 1);
+    mbar_init(s_full, 1);
+    mbar_init(p_full, kBwdComputeThreads);
+    mbar_init(mma2_done, 1);
+    mbar_init(dq_free, kBwdComputeThreads);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  // TMEM: S^T, then dQ, at 0; dP^T at 128; dV at 256; dK at 256 + 64 nd
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t t_dv = 256, t_dk = 256 + 64 * nd;
+  pdl_wait();
+  // (key tile, sequence) in the plan's order, and the query tiles q0 .. q1 - 1 that see any of it (at
+  // least one, so that a tile that nobody sees takes the same path and gets zeros)
+  const bool plan_ok = plan_fits(p.plan, p.n_seq, p.S, p.err);
+  const int at_tile = plan_ok ? p.plan.k_order[blockIdx.x / p.hkv] : 0;
+  const int kt = at_tile % n_t, b = at_tile / n_t;
+  const int q0 = plan_ok ? p.plan.k_range[at_tile].x : 0, q1 = plan_ok ? p.plan.k_range[at_tile].y : 0;
+  const int n_it = hpg * (q1 - q0);  // (query head of the group, query tile)
+
+  auto it_head = [&](int it) { return g * hpg + it % hpg; };
+  auto it_qtile = [&](int it) { return q0 + it / hpg; };
+
+  if (!plan_ok) {
+    // nothing was issued
+  } else if (warp == 0) {
+    if (lane == 0) {
+      mbar_arrive_expect_tx(kv_full, 2 * nd * kChunk);
+      for (int c = 0; c < nd; ++c) {
+        tma_load_4d(sk + c * kChunk, &p.kmap, kv_full, 64 * c, g, kt * kTile, b);
+        tma_load_4d(sv + c * kChunk, &p.vmap, kv_full, 64 * c, g, kt * kTile, b);
+      }
+      // dO and Q have one buffer each and separate barriers: dO_(i+1) loads as soon as dV_i has
+      // read dO_i, Q_(i+1) once dK_i has read Q_i
+      int issued_do = 0, issued_q = 0;
+      for (int it = 0; it < n_it; ++it) {
+        const int h = it_head(it), qt = it_qtile(it);
+        if (it > 0 && !mbar_wait(do_empty, (it - 1) & 1, abort_flag, p.err, DEV_TIMEOUT_PRODUCER)) break;
+        mbar_arrive_expect_tx(do_full, nd * kChunk);
+        for (int c = 0; c < nd; ++c) tma_load_4d(sdo + c * kChunk, &p.domap, do_full, 64 * c, h, qt * kTile, b);
+        issued_do = it + 1;
+        if (it > 0 && !mbar_wait(q_empty, (it - 1) & 1, abort_flag, p.err, DEV_TIMEOUT_PRODUCER)) break;
+        mbar_arrive_expect_tx(q_full, nd * kChunk);
+        for (int c = 0; c < nd; ++c) tma_load_4d(sq + c * kChunk, &p.qmap, q_full, 64 * c, h, qt * kTile, b);
+        issued_q = it + 1;
+      }
+      mbar_wait(kv_full, 0, nullptr, p.err, DEV_TIMEOUT_DRAIN);
+      if (issued_do > 0) mbar_wait(do_full, (issued_do - 1) & 1, nullptr, p.err, DEV_TIMEOUT_DRAIN);
+      if (issued_q > 0) mbar_wait(q_full, (issued_q - 1) & 1, nullptr, p.err, DEV_TIMEOUT_DRAIN);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t id_kq = idesc_bf16(128, 128, 0, 0);       // S^T = K Q^T, dP^T = V dO^T
+      const uint32_t id_kd = idesc_bf16(128, 64 * nd, 0, 1);   // dV += P^T dO, dK += dS^T Q
+      const uint32_t id_qd = idesc_bf16(128, 64 * nd, 1, 1);   // dQ = dS K (dS read MN-major from dS^T)
+      const uint32_t ak = smem_u32(sk), av = smem_u32(sv), bq = smem_u32(sq), bdo = smem_u32(sdo);
+      const uint32_t apt = smem_u32(spt), adst = smem_u32(sdst);
+      bool ok = mbar_wait(kv_full, 0, abort_flag, p.err, DEV_TIMEOUT_MMA);
+      for (int it = 0; ok && it < n_it; ++it) {
+        // dP^T (columns 128..255) needs only dO: it may run while the previous dQ is drained
+        if (!mbar_wait(do_full, it & 1, abort_flag, p.err, DEV_TIMEOUT_MMA)) { ok = false; break; }
+        tc_fence_after();
+        for (int t = 0; t < 4 * nd; ++t)
+          umma_bf16(tmem + 128, kmajor_desc(av, t), kmajor_desc(bdo, t), id_kq, t > 0 ? 1u : 0u);
+        if (!mbar_wait(q_full, it & 1, abort_flag, p.err, DEV_TIMEOUT_MMA)) { ok = false; break; }
+        if (it > 0 && !mbar_wait(dq_free, (it - 1) & 1, abort_flag, p.err, DEV_TIMEOUT_MMA)) { ok = false; break; }
+        tc_fence_after();
+        for (int t = 0; t < 4 * nd; ++t)
+          umma_bf16(tmem, kmajor_desc(ak, t), kmajor_desc(bq, t), id_kq, t > 0 ? 1u : 0u);
+        umma_commit(s_full);
+        if (!mbar_wait(p_full, it & 1, abort_flag, p.err, DEV_TIMEOUT_MMA)) { ok = false; break; }
+        tc_fence_after();
+        for (int t = 0; t < 8; ++t)
+          umma_bf16(tmem + t_dv, kmajor_desc(apt, t), mnmajor_desc(bdo, t), id_kd, (it > 0 || t > 0) ? 1u : 0u);
+        umma_commit(do_empty);
+        for (int t = 0; t < 8; ++t)
+          umma_bf16(tmem + t_dk, kmajor_desc(adst, t), mnmajor_desc(bq, t), id_kd, (it > 0 || t > 0) ? 1u : 0u);
+        umma_commit(q_empty);
+        for (int t = 0; t < 8; ++t)
+          umma_bf16(tmem, mnmajor_desc(adst, t), mnmajor_desc(ak, t), id_qd, t > 0 ? 1u : 0u);
+        umma_commit(mma2_done);
+      }
+      umma_commit(drain);
+      mbar_wait(drain, 0, nullptr, p.err, DEV_TIMEOUT_DRAIN);
+    }
+  } else {
+    // Eight compute warps: warp w reads TMEM lanes 32 (w % 4) .. + 31 and handles one half of the
+    // columns (query columns of S^T / dP^T, head-dimension columns of dQ, dK or dV).
+    const int cw = warp - 2;
+    const int quarter = warp & 3;
+    const int half = cw >> 2;
+    const int r = quarter * 32 + lane;           // key row of the tile (S^T, dP^T, dV, dK) or query row (dQ)
+    const int kpos = kt * kTile + r;
+    const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
+    const float log2e = kLog2e;
+    // This warp's dQ boxes: head-dimension columns 64 half .. + 31 over its rows of P^T chunk `half`,
+    // columns 64 half + 32 .. + 63 over its rows of dS^T chunk `half`: the same shared memory the
+    // warp itself rewrites next (P^T and dS^T rows r, columns 64 half .. + 63), so one wait of its
+    // own bulk reads orders the two.
+    uint8_t* box0 = spt + half * kChunk + quarter * 32 * 128;
+    uint8_t* box1 = sdst + half * kChunk + quarter * 32 * 128;
+    // LSE and delta of a query tile are staged in shared memory (two buffers by iteration parity),
+    // read from global memory one iteration ahead
+    float n_lse = 0.f, n_delta = 0.f;
+    int2 n_see = make_int2(0, 0);
+    auto fetch = [&](int it) {
+      const int qp = it_qtile(it) * kTile + r;
+      const int64_t at = (int64_t)it_head(it) * T + (int64_t)b * p.S + qp;
+      n_lse = qp < p.S ? p.lse[at] * log2e : 0.f;
+      n_delta = qp < p.S ? p.delta[at] : 0.f;
+      const int64_t row = (int64_t)b * p.S + qp;
+      n_see = qp < p.S ? make_int2(p.plan.lo[row], p.plan.hi[row]) : make_int2(0, 0);
+      if (n_see.x >= n_see.y) n_lse = 0.f;  // a row that sees nothing (its lse is -inf): masked below
+    };
+    if (half == 0 && n_it > 0) fetch(0);
+    bool ok = true;
+    for (int it = 0; it < n_it; ++it) {
+      const int h = it_head(it), qt = it_qtile(it);
+      float* lse_it = s_lse + (it & 1) * 128;
+      float* delta_it = s_delta + (it & 1) * 128;
+      int2* see_it = s_see + (it & 1) * 128;
+      if (half == 0) {
+        lse_it[r] = n_lse;
+        delta_it[r] = n_delta;
+        see_it[r] = n_see;
+      }
+      // this iteration's LSE and delta are visible; `ok` is the same in every compute thread
+      ok = bar_and_bwd(ok);
+      if (!ok) break;
+      if (half == 0 && it + 1 < n_it) fetch(it + 1);
+      ok = __all_sync(0xffffffffu, mbar_wait(s_full, it & 1, abort_flag, p.err, DEV_TIMEOUT_EPILOGUE));
+      if (ok) {
+        tc_fence_after();
+        // this warp's previous dQ reductions have read its boxes (rewritten below)
+        if (lane == 0) bulk_wait_read<0>();
+        __syncwarp();
+        // a query tile all of whose rows see all of this key tile needs no masks
+        const int4 q_see = p.plan.q_range[b * n_t + qt];
+        const bool whole = q_see.z <= kt && kt < q_see.w;
+        const float slope = BIAS ? p.slopes[h] * log2e : 0.f;
+        const float away = (float)(qt * kTile - kpos);
+        auto soft_chunk = [&](int c, auto masked) {
+          uint32_t st[32], dp[32];
+          __syncwarp();
+          tmem_ld32(tmem + lane_off + 32 * c, st);
+          tmem_ld32(tmem + lane_off + 128 + 32 * c, dp);
+          tmem_ld_wait_regs(st);
+          regs_after_wait(dp);
+          uint32_t pw[16], dw[16];
+#pragma unroll
+          for (int i = 0; i < 32; i += 4) {
+            const float4 l4 = *reinterpret_cast<const float4*>(lse_it + 32 * c + i);
+            const float4 d4 = *reinterpret_cast<const float4*>(delta_it + 32 * c + i);
+            const float lv[4] = {l4.x, l4.y, l4.z, l4.w}, dl[4] = {d4.x, d4.y, d4.z, d4.w};
+            float pv[4], dv4[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int col = 32 * c + i + e;
+              float grad;  // d (capped score) / d (score)
+              const float y = score_grad<CAP, BIAS>(__uint_as_float(st[i + e]), p.mul, p.cap_log2, slope,
+                                                    away + (float)col, grad);
+              float pe = ex2(y - lv[e]);
+              if (decltype(masked)::value) {
+                const int2 see = see_it[col];
+                pe = (see.x <= kpos && kpos < see.y) ? pe : 0.f;
+              }
+              pv[e] = pe;
+              dv4[e] = pe * (__uint_as_float(dp[i + e]) - dl[e]);
+              if (CAP) dv4[e] *= grad;
+            }
+            pw[i / 2] = pack2(pv[0], pv[1]);
+            pw[i / 2 + 1] = pack2(pv[2], pv[3]);
+            dw[i / 2] = pack2(dv4[0], dv4[1]);
+            dw[i / 2 + 1] = pack2(dv4[2], dv4[3]);
+          }
+          st_swizzled_row32(spt, r, 32 * c, pw);
+          st_swizzled_row32(sdst, r, 32 * c, dw);
+        };
+        for (int c = 2 * half; c < 2 * half + 2; ++c) {
+          if (whole) soft_chunk(c, std::false_type{});
+          else soft_chunk(c, std::true_type{});
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        mbar_arrive(p_full);
+        ok = __all_sync(0xffffffffu, mbar_wait(mma2_done, it & 1, abort_flag, p.err, DEV_TIMEOUT_EPILOGUE));
+      }
+      if (ok) {
+        // dQ of this (head, query tile), lane r = query row qt * 128 + r: out of TMEM (which the next
+        // S^T may then overwrite), scaled into this warp's boxes, added to the accumulator by bulk
+        // reductions of 32 rows x 32 columns
+        tc_fence_after();
+        uint32_t v0[32], v1[32];
+        __syncwarp();
+        tmem_ld32(tmem + lane_off + 64 * half, v0);
+        tmem_ld32(tmem + lane_off + 64 * half + 32, v1);
+        tmem_ld_wait_regs(v0);
+        regs_after_wait(v1);
+        tc_fence_before();
+        mbar_arrive(dq_free);
+        st_dq_box_row(box0, lane, v0, p.scale);
+        st_dq_box_row(box1, lane, v1, p.scale);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0 && 64 * half < p.hd) {
+          tma_reduce_add_4d(&p.dqmap, box0, 64 * half, h, qt * kTile + 32 * quarter, b);
+          if (64 * half + 32 < p.hd) tma_reduce_add_4d(&p.dqmap, box1, 64 * half + 32, h, qt * kTile + 32 * quarter, b);
+          bulk_commit();
+        }
+      }
+    }
+    // the reductions have completed before the CTA ends (and before its shared memory is reused)
+    if (lane == 0) bulk_wait_all();
+    // dK (half 1), dV (half 0) of this key tile: the MMAs of the last iteration have completed
+    // (mma2_done); every lane takes part in the (warp-collective) loads, rows past the sequence
+    // store nothing
+    if (ok) {
+      tc_fence_after();
+      const bool kok = kpos < p.S;
+      const int64_t row = (int64_t)b * p.S + kpos;
+      const int which = half;
+      __nv_bfloat16* out = (which ? p.dk + row * p.lddk : p.dv + row * p.lddv) + (int64_t)g * p.hd;
+      const float mul = which ? p.scale : 1.f;
+      for (int c = 0; c < 2 * nd; ++c) {
+        uint32_t v[32];
+        __syncwarp();
+        tmem_ld32(tmem + lane_off + (which ? t_dk : t_dv) + 32 * c, v);
+        tmem_ld_wait_regs(v);
+        if (!kok || 32 * c >= p.hd) continue;
+        uint32_t w[16];
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) w[i / 2] = pack2(__uint_as_float(v[i]) * mul, __uint_as_float(v[i + 1]) * mul);
+        uint4* dst = reinterpret_cast<uint4*>(out + 32 * c);
+        const int nv = min(32, p.hd - 32 * c) / 8;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (q < nv) dst[q] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) {
+    __syncwarp();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ---------------------------------------------------------------------------------- host side
+
+// Shared memory of a launch: sized for head_dim 128 whatever the head dimension, which also keeps
+// one CTA per SM (each CTA allocates all 512 TMEM columns).
+int fwd_smem() { return 1024 + 2 * kChunk + 8 * kChunk + 2 * kChunk + 2 * kChunk + 1024 + 256; }
+int bwd_smem() { return 1024 + 8 * kChunk + 4 * kChunk + 2 * 256 * 4 + 256 * 8 + 256; }
+
+// Raises a kernel's shared-memory limit once per device.
+template <typename K>
+bool smem_limit(K kernel, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (done.load(std::memory_order_relaxed) & bit) return true;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+  done.fetch_or(bit, std::memory_order_relaxed);
+  return true;
+}
+
+int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return 0;
+  return n;
+}
+
+template <bool CAP, bool BIAS>
+int fwd_launch(const MaskedFwdParams& p, cudaStream_t s) {
+  static std::atomic<uint64_t> done{0};
+  if (!smem_limit(masked_fwd_kernel<CAP, BIAS>, fwd_smem(), done)) return 5;
+  const int n_sm = sm_count();
+  if (n_sm <= 0) return 5;
+  const int64_t n_units = plan_tiles(p.n_seq, p.S) * p.hq;
+  launch_kernel(masked_fwd_kernel<CAP, BIAS>, (unsigned)std::min<int64_t>(n_units, n_sm), kAttnThreads, fwd_smem(), s, p);
+  if (launch_failed("sl_attention_masked")) return 5;
+  note_launch();
+  return 0;
+}
+
+int delta_smem() { return 1024 + 12 * kChunk + 512 + 256; }
+
+template <bool CAP, bool BIAS>
+int delta_launch(const MaskedDeltaParams& p, cudaStream_t s) {
+  static std::atomic<uint64_t> done{0};
+  if (!smem_limit(masked_delta_kernel<CAP, BIAS>, delta_smem(), done)) return 5;
+  const int n_sm = sm_count();
+  if (n_sm <= 0) return 5;
+  const int64_t n_units = plan_tiles(p.n_seq, p.S) * p.hq;
+  launch_kernel(masked_delta_kernel<CAP, BIAS>, (unsigned)std::min<int64_t>(n_units, n_sm), kAttnThreads, delta_smem(), s, p);
+  if (launch_failed("sl_attention_masked")) return 5;
+  note_launch();
+  return 0;
+}
+
+template <bool CAP, bool BIAS>
+int bwd_launch(const MaskedBwdParams& p, cudaStream_t s) {
+  static std::atomic<uint64_t> done{0};
+  if (!smem_limit(masked_bwd_kernel<CAP, BIAS>, bwd_smem(), done)) return 5;
+  launch_kernel(masked_bwd_kernel<CAP, BIAS>, (unsigned)(plan_tiles(p.n_seq, p.S) * p.hkv), kAttnBwdThreads, bwd_smem(), s, p);
+  if (launch_failed("sl_attention_masked")) return 5;
+  note_launch();
+  return 0;
+}
+
+// mul and cap_log2 of score()
+void score_constants(const MaskedArgs& a, float* scale, float* mul, float* cap_log2) {
+  const double sc = a.scale > 0.f ? (double)a.scale : 1.0 / std::sqrt((double)a.hd);
+  *scale = (float)sc;
+  *mul = (float)(a.cap > 0.f ? 2.0 * 1.4426950408889634 * sc / a.cap : 1.4426950408889634 * sc);
+  *cap_log2 = (float)(a.cap * 1.4426950408889634);
+}
+
+}  // namespace
+
+int64_t attention_plan_bytes(int n_seq, int S) { return carve_plan(nullptr, n_seq, S, nullptr); }
+
+int attention_plan(const int32_t* row_lo, const int32_t* row_hi, int n_seq, int S, void* plan, cudaStream_t s) {
+  Plan p;
+  carve_plan(plan, n_seq, S, &p);
+  const int64_t tiles = plan_tiles(n_seq, S);
+  // up to 64 tiles one block does it all; more: the rows over many blocks first
+  const bool one = tiles <= 64;
+  if (!one) {
+    launch_kernel(plan_rows_kernel, (unsigned)std::min<int64_t>((tiles + 31) / 32, 148), kPlanThreads, 0, s, p, row_lo,
+                  row_hi, n_seq, S);
+    if (launch_failed("sl_attention_plan")) return 5;
+    note_launch();
+  }
+  const size_t smem = ((size_t)(S + kTile - 1) / kTile + 2) * 4;
+  launch_kernel(plan_tiles_kernel, 1u, kPlanThreads, smem, s, p, row_lo, row_hi, n_seq, S, one);
+  if (launch_failed("sl_attention_plan")) return 5;
+  note_launch();
+  return 0;
+}
+
+int attention_masked_fwd(const MaskedArgs& a, cudaStream_t s) {
+  MaskedFwdParams p;
+  memset(&p, 0, sizeof(p));
+  if (!head_map(&p.qmap, a.q, a.ldq, a.n_seq, a.S, a.hq, a.hd) || !head_map(&p.kmap, a.k, a.ldk, a.n_seq, a.S, a.hkv, a.hd) ||
+      !head_map(&p.vmap, a.v, a.ldv, a.n_seq, a.S, a.hkv, a.hd) || !head_map(&p.omap, a.o, a.ldo, a.n_seq, a.S, a.hq, a.hd))
+    return 2;
+  carve_plan(const_cast<void*>(a.plan), a.n_seq, a.S, &p.plan);
+  p.slopes = a.slopes;
+  p.lse = const_cast<float*>(a.lse);
+  p.n_seq = a.n_seq;
+  p.S = a.S;
+  p.hq = a.hq;
+  p.hkv = a.hkv;
+  p.hd = a.hd;
+  p.nd = (a.hd + 63) / 64;
+  float scale;
+  score_constants(a, &scale, &p.mul, &p.cap_log2);
+  p.err = a.err;
+  if (a.cap > 0.f) return a.slopes ? fwd_launch<true, true>(p, s) : fwd_launch<true, false>(p, s);
+  return a.slopes ? fwd_launch<false, true>(p, s) : fwd_launch<false, false>(p, s);
+}
+
+int attention_masked_bwd(const MaskedArgs& a, cudaStream_t s) {
+  MaskedBwdParams p;
+  memset(&p, 0, sizeof(p));
+  if (!head_map(&p.qmap, a.q, a.ldq, a.n_seq, a.S, a.hq, a.hd) || !head_map(&p.kmap, a.k, a.ldk, a.n_seq, a.S, a.hkv, a.hd) ||
+      !head_map(&p.vmap, a.v, a.ldv, a.n_seq, a.S, a.hkv, a.hd) || !head_map(&p.domap, a.d_o, a.lddo, a.n_seq, a.S, a.hq, a.hd))
+    return 2;
+  const int64_t T = (int64_t)a.n_seq * a.S;
+  float* dq_acc = static_cast<float*>(a.scratch);
+  float* delta = reinterpret_cast<float*>(static_cast<uint8_t*>(a.scratch) + ((T * a.hq * a.hd * 4 + 255) & ~int64_t(255)));
+  if (!dq_acc_map(&p.dqmap, dq_acc, a.n_seq, a.S, a.hq, a.hd)) return 2;
+  carve_plan(const_cast<void*>(a.plan), a.n_seq, a.S, &p.plan);
+  p.slopes = a.slopes;
+  p.lse = a.lse;
+  p.delta = delta;
+  p.dk = static_cast<__nv_bfloat16*>(a.dk);
+  p.dv = static_cast<__nv_bfloat16*>(a.dv);
+  p.lddk = a.lddk;
+  p.lddv = a.lddv;
+  p.n_seq = a.n_seq;
+  p.S = a.S;
+  p.hq = a.hq;
+  p.hkv = a.hkv;
+  p.hd = a.hd;
+  p.nd = (a.hd + 63) / 64;
+  score_constants(a, &p.scale, &p.mul, &p.cap_log2);
+  p.err = a.err;
+  MaskedDeltaParams d;
+  memset(&d, 0, sizeof(d));
+  d.qmap = p.qmap, d.kmap = p.kmap, d.vmap = p.vmap, d.domap = p.domap;
+  d.plan = p.plan, d.slopes = p.slopes, d.lse = p.lse, d.delta = delta, d.dq_acc = dq_acc;
+  d.n_seq = p.n_seq, d.S = p.S, d.hq = p.hq, d.hkv = p.hkv, d.hd = p.hd, d.nd = p.nd;
+  d.mul = p.mul, d.cap_log2 = p.cap_log2, d.err = p.err;
+  int rc = a.cap > 0.f ? (a.slopes ? delta_launch<true, true>(d, s) : delta_launch<true, false>(d, s))
+                       : (a.slopes ? delta_launch<false, true>(d, s) : delta_launch<false, false>(d, s));
+  if (rc) return rc;
+  rc = a.cap > 0.f ? (a.slopes ? bwd_launch<true, true>(p, s) : bwd_launch<true, false>(p, s))
+                             : (a.slopes ? bwd_launch<false, true>(p, s) : bwd_launch<false, false>(p, s));
+  if (rc) return rc;
+  // dQ: the dense [T, hq hd] accumulator to bf16 rows
+  const int64_t n = (int64_t)a.hq * a.hd;
+  launch_kernel(masked_dq_cast_kernel, (unsigned)((T * n / 4 + 255) / 256), 256, 0, s, (const float*)dq_acc, T, n,
+                static_cast<__nv_bfloat16*>(a.dq), a.lddq);
+  if (launch_failed("sl_attention_masked")) return 5;
+  note_launch();
+  return 0;
+}
+
+}  // namespace sl

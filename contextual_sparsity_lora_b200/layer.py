@@ -11,21 +11,32 @@ RMSNorm, the residual adds, every projection and the causal grouped-query attent
 in context-first order like the blocks' (sl_permute_rows moves q, k, v to sequence order for the
 attention core and its output back; when the attention block keeps its interfaces in the sigma
 layout, sl_permute_rows_sigma also restores or applies the channel order of the context rows in
-the same pass). No rotary positional encoding: the pages do not say how it
-meets channel sparsity (a rotation mixes channel pairs that the selection may split)."""
+the same pass). By default no rotary positional encoding: the pages do not say how it
+meets channel sparsity (a rotation mixes channel pairs that the selection may split).
+
+Options for batches as they are trained in earnest (each off by default): `rope` and `qk_norm` rotate and
+normalise q and k per head once their channels are back in natural order (sl_qk_norm_rope_fwd / _bwd), so
+the selection still acts on the projections' own channels; `plan`, `softcap` and `slopes` run the core
+over each token's interval of keys (packed documents, prefixes, windows, padding), with capped and
+distance-biased scores (sl_attention_masked_fwd / _bwd)."""
 from __future__ import annotations
 
 import torch
 
 from . import binding as B
 from .blocks import AttnProjBlock, FFNBlock
+from .packing import AttentionPlan
 
 
 class DecoderLayer:
-    def __init__(self, attn: AttnProjBlock, ffn: FFNBlock, gamma1, gamma2, perm, n_seq: int, eps: float = 1e-5):
+    def __init__(self, attn: AttnProjBlock, ffn: FFNBlock, gamma1, gamma2, perm, n_seq: int, eps: float = 1e-5,
+                 rope=None, qk_norm=None, plan: AttentionPlan | None = None, softcap: float = 0.0, slopes=None):
         """attn, ffn: the layer's projection blocks (same n_tok and n_ctx); gamma1, gamma2: frozen
         RMSNorm gains [D]; perm: int64 [n_tok], context-first position p holds sequence-order row
-        perm[p] (rows of n_seq sequences of equal length)."""
+        perm[p] (rows of n_seq sequences of equal length).
+        rope: (positions int32 [n_tok] in sequence order, inv_freq fp32 [rot_dim / 2], style
+        SL_ROPE_HALVES or SL_ROPE_PAIRS); qk_norm: frozen gains (gq, gk) [head_dim]; plan: which keys each
+        token sees; softcap, slopes [n_q_heads]: see sl_attention_masked_fwd (without a plan: causal)."""
         dev = attn.device
         self.attn, self.ffn = attn, ffn
         self.g1 = gamma1.to(device=dev, dtype=torch.bfloat16).contiguous()
@@ -52,6 +63,21 @@ class DecoderLayer:
         self.dq_nat, self.dk_nat, self.dv_nat = e(T, Dq), e(T, Dkv), e(T, Dkv)
         self.dq_cf, self.dk_cf, self.dv_cf = e(T, Dq), e(T, Dkv), e(T, Dkv)
         self.dx2, self.dx = e(T, D), e(T, D)
+        as_dev = lambda t, dt: None if t is None else torch.as_tensor(t).to(device=dev, dtype=dt).contiguous()
+        self.positions, self.inv_freq, self.rope_style = None, None, B.SL_ROPE_HALVES
+        if rope is not None:
+            self.positions, self.inv_freq = as_dev(rope[0], torch.int32), as_dev(rope[1], f32)
+            self.rope_style = rope[2] if len(rope) > 2 else B.SL_ROPE_HALVES
+        self.gq, self.gk = (None, None) if qk_norm is None else (as_dev(g, bf) for g in qk_norm)
+        self.turned = rope is not None or qk_norm is not None
+        # what the attention core reads: the rotated q and k (in place where the backward needs no input)
+        self.q_at, self.k_at = self.q_nat, self.k_nat
+        if qk_norm is not None:
+            self.q_at, self.k_at = e(T, Dq), e(T, Dkv)
+        self.softcap, self.slopes = float(softcap), as_dev(slopes, f32)
+        if plan is None and (self.softcap > 0 or slopes is not None):
+            plan = AttentionPlan(self.n_seq, self.S, dev)
+        self.plan = plan
         self.ws = B.Workspace(dev)  # the attention core's scratch (the dq accumulator) and error word
 
     def _to_seq(self, src, dst, name):
@@ -77,8 +103,15 @@ class DecoderLayer:
         q, k, v = at.forward_qkv(self.h1)
         for src, dst, name in ((q, self.q_nat, "q"), (k, self.k_nat, "k"), (v, self.v_nat, "v")):
             self._to_seq(src, dst, name)
-        B.sl_attention_fwd(self.ws, self.q_nat, self.k_nat, self.v_nat, self.n_seq, at.hq, at.hkv, at.hd, self.a_nat,
-                           self.lse)
+        if self.turned:
+            B.sl_qk_norm_rope_fwd(self.q_nat, self.k_nat, self.positions, self.inv_freq, at.hd, self.q_at, self.k_at,
+                                  self.gq, self.gk, self.eps, self.rope_style)
+        if self.plan is None:
+            B.sl_attention_fwd(self.ws, self.q_at, self.k_at, self.v_nat, self.n_seq, at.hq, at.hkv, at.hd, self.a_nat,
+                               self.lse)
+        else:
+            B.sl_attention_masked_fwd(self.ws, self.q_at, self.k_at, self.v_nat, self.n_seq, at.hq, at.hkv, at.hd,
+                                      self.plan.buf, self.a_nat, self.lse, self.softcap, self.slopes)
         self._to_cf(self.a_nat, self.a_cf, "o")
         o = at.forward_o(self.a_cf)
         # x2 = x + o (the residual stream) and h2 = RMSNorm(x2) in one pass
@@ -94,8 +127,17 @@ class DecoderLayer:
         B.sl_rmsnorm_bwd(dh2, self.x2, self.g2, self.rstd2, self.dx2, dres=dy)
         da_cf = at.backward_o(self.dx2)
         self._to_seq(da_cf, self.da_nat, "o")
-        B.sl_attention_bwd(self.ws, self.q_nat, self.k_nat, self.v_nat, self.a_nat, self.da_nat, self.lse, self.n_seq,
-                           at.hq, at.hkv, at.hd, self.dq_nat, self.dk_nat, self.dv_nat)
+        if self.plan is None:
+            B.sl_attention_bwd(self.ws, self.q_at, self.k_at, self.v_nat, self.a_nat, self.da_nat, self.lse, self.n_seq,
+                               at.hq, at.hkv, at.hd, self.dq_nat, self.dk_nat, self.dv_nat)
+        else:
+            B.sl_attention_masked_bwd(self.ws, self.q_at, self.k_at, self.v_nat, self.a_nat, self.da_nat, self.lse,
+                                      self.n_seq, at.hq, at.hkv, at.hd, self.plan.buf, self.dq_nat, self.dk_nat,
+                                      self.dv_nat, self.softcap, self.slopes)
+        if self.turned:
+            B.sl_qk_norm_rope_bwd(self.ws, self.dq_nat, self.dk_nat, self.q_nat, self.k_nat, self.positions,
+                                  self.inv_freq, at.hd, self.dq_nat, self.dk_nat, self.gq, self.gk, self.eps,
+                                  self.rope_style)
         for src, dst, name in ((self.dq_nat, self.dq_cf, "q"), (self.dk_nat, self.dk_cf, "k"),
                                (self.dv_nat, self.dv_cf, "v")):
             self._to_cf(src, dst, name)

@@ -8,8 +8,11 @@ Progressive Sparse Fine-Tuning" for the dense first steps):
 
 Per-layer keep ratios (attention q/k/v/o, FFN) come from a table; the first steps of a run are
 dense (progressive schedule). Every projection, RMSNorm, residual, the embedding gather and
-AdamW run in libsparselora's kernels; the attention core and the frozen LM head's product with
-its cross-entropy are torch library calls (like cuBLAS), outside the method's steps."""
+AdamW run in libsparselora's kernels; the frozen LM head's product and, by default, its
+cross-entropy are torch library calls (like cuBLAS), outside the method's steps. With
+loss="kernels" the cross-entropy and its gradient run in sl_token_logprobs_fwd / _bwd on the
+product's bf16 logits; score() gives log probabilities, entropies and top alternatives.
+Packed batches, rotation, q/k norms and capped or biased scores: see DecoderLayer's options."""
 from __future__ import annotations
 
 import math
@@ -19,6 +22,7 @@ import torch
 from . import binding as B
 from .blocks import AttnProjBlock, FFNBlock
 from .layer import DecoderLayer
+from .packing import AttentionPlan
 
 
 def llama3_8b_math10k_keep(n_layers: int = 32):
@@ -62,12 +66,17 @@ def cosine_lr(step: int, n_steps: int, peak: float, warmup_frac: float = 0.04) -
 
 class SparseLoRAModel:
     def __init__(self, frozen, loras, gammas, keep, perm, n_ctx, n_seq, heads, est_k, lora_scale, device="cuda",
-                 eps=1e-5):
+                 eps=1e-5, rope=None, qk_norms=None, plan: AttentionPlan | None = None, softcap: float = 0.0,
+                 slopes=None, loss: str = "library"):
         """frozen: dict with "embed" [V, D], "lm_head" [V, D], "gamma_f" [D] and the projection
         weights "q","k","v","o","gate","up","down" (SpectralWeight-like: .W, .W_A, .W_B), shared by
         every layer or a list of such dicts (one per layer); loras: per layer a dict of (A, B);
         gammas: per layer (g1, g2); keep: per layer (attn_keep, ffn_keep); perm: context-first
-        row order of the batch (n_seq sequences); heads: (n_q_heads, n_kv_heads, head_dim)."""
+        row order of the batch (n_seq sequences); heads: (n_q_heads, n_kv_heads, head_dim).
+        rope, plan, softcap, slopes: DecoderLayer's options, the same for every layer; qk_norms: per
+        layer (gq, gk); loss: "library" or "kernels" (see above)."""
+        if loss not in ("library", "kernels"):
+            raise ValueError('loss is "library" or "kernels"')
         bf = torch.bfloat16
         self.device = device
         self.eps = eps
@@ -88,7 +97,8 @@ class SparseLoRAModel:
                                  hq, hkv, hd, T, n_ctx, keep[i][0], device, io_layout="sigma")
             ffn = FFNBlock(w["gate"], w["up"], w["down"], lo["gate"], lo["up"], lo["down"], lora_scale, est_k, T, n_ctx,
                            keep[i][1], device)
-            self.layers.append(DecoderLayer(attn, ffn, gammas[i][0], gammas[i][1], perm, n_seq, eps))
+            self.layers.append(DecoderLayer(attn, ffn, gammas[i][0], gammas[i][1], perm, n_seq, eps, rope,
+                                            None if qk_norms is None else qk_norms[i], plan, softcap, slopes))
         # fp32 master copies of every LoRA matrix and their AdamW moments, in the blocks' flat layout
         self.opt = []
         for lay in self.layers:
@@ -100,22 +110,73 @@ class SparseLoRAModel:
         self.hf, self.dhf, self.dx_top = e(T, self.D), e(T, self.D), e(T, self.D)
         self.rstd_f = e(T, dt=torch.float32)
         self.loss = torch.zeros((), dtype=torch.float32, device=device)
+        self.loss_kernels = loss == "kernels"
 
     def set_dense(self, on: bool):
         for lay in self.layers:
             lay.attn.set_dense(on)
             lay.ffn.set_dense(on)
 
-    def forward_backward(self, ids_cf, targets_out):
-        """ids_cf: int32 [T] token ids in context-first order; targets_out: int64 [T - C], the
-        next-token targets of the output rows (rows C..T-1 of the context-first order)."""
+    def _forward(self, ids_cf):
+        """The normalised output rows (rows C..T-1 of the context-first order) under the LM head."""
         B.sl_permute_rows(self.embed, ids_cf, self.x0)
         x = self.x0
         for lay in self.layers:
             x = lay.forward(x)
         self.x_top = x
         B.sl_rmsnorm_fwd(x, self.gamma_f, self.eps, self.hf, self.rstd_f)
-        h_out = self.hf[self.C:]
+        return self.hf[self.C:]
+
+    def _logits(self, h_out):
+        """bf16 [n_out, V] logits whose rows start on 16 bytes, as the token kernels want them."""
+        V = self.lm_head.shape[0]
+        logits = torch.empty(h_out.shape[0], -(-V // 8) * 8, dtype=torch.bfloat16, device=h_out.device)[:, :V]
+        return torch.matmul(h_out, self.lm_head.t(), out=logits) if logits.is_contiguous() else logits.copy_(
+            torch.matmul(h_out, self.lm_head.t()))
+
+    def score(self, ids_cf, targets_out, top_k: int = 0):
+        """(logp, entropy, top_ids, top_logp) of the output rows: log probabilities of targets_out (int [T - C];
+        negative: none, 0), entropies, and the top_k most likely tokens (None for top_k = 0). Forward only."""
+        logits = self._logits(self._forward(ids_cf))
+        n, dev = logits.shape[0], logits.device
+        logp, entropy = (torch.empty(n, device=dev) for _ in range(2))
+        ids = torch.empty(n, top_k, dtype=torch.int32, device=dev) if top_k else None
+        top = torch.empty(n, top_k, device=dev) if top_k else None
+        B.sl_token_logprobs_fwd(logits, targets_out.to(torch.int32), logp, torch.empty(n, 2, device=dev), entropy, ids, top)
+        return logp, entropy, ids, top
+
+    def _head_kernels(self, h_out, targets_out):
+        """Mean cross-entropy of the rows that have a target, and its gradient at the logits (in their place)."""
+        logits = self._logits(h_out)
+        n, dev = logits.shape[0], logits.device
+        targets = targets_out.to(torch.int32)
+        logp, stats = torch.empty(n, device=dev), torch.empty(n, 2, device=dev)
+        B.sl_token_logprobs_fwd(logits, targets, logp, stats)
+        has = ((targets >= 0) & (targets < logits.shape[1])).float()
+        g = has / -has.sum().clamp(min=1.0)
+        self.loss.copy_((logp * g).sum())
+        B.sl_token_logprobs_bwd(logits, targets, stats, g, logits)
+        return logits
+
+    def forward_backward(self, ids_cf, targets_out):
+        """ids_cf: int32 [T] token ids in context-first order; targets_out: int64 [T - C], the
+        next-token targets of the output rows (rows C..T-1 of the context-first order; with
+        loss="kernels" a negative one leaves its row out)."""
+        h_out = self._forward(ids_cf)
+        x = self.x_top
+        if self.loss_kernels:
+            dlogits = self._head_kernels(h_out, targets_out)
+        else:
+            dlogits = self._head_library(h_out, targets_out)
+        self.dhf.zero_()
+        self.dhf[self.C:] = torch.matmul(dlogits, self.lm_head)
+        B.sl_rmsnorm_bwd(self.dhf, x, self.gamma_f, self.rstd_f, self.dx_top)
+        dx = self.dx_top
+        for lay in reversed(self.layers):
+            dx = lay.backward(dx)
+        return self.loss
+
+    def _head_library(self, h_out, targets_out):
         logits = torch.matmul(h_out, self.lm_head.t()).float()
         n_out = logits.shape[0]
         lse = torch.logsumexp(logits, dim=1)
@@ -123,13 +184,7 @@ class SparseLoRAModel:
         dlogits = torch.softmax(logits, dim=1)
         dlogits[torch.arange(n_out, device=logits.device), targets_out] -= 1.0
         dlogits /= n_out
-        self.dhf.zero_()
-        self.dhf[self.C:] = torch.matmul(dlogits.to(torch.bfloat16), self.lm_head)
-        B.sl_rmsnorm_bwd(self.dhf, x, self.gamma_f, self.rstd_f, self.dx_top)
-        dx = self.dx_top
-        for lay in reversed(self.layers):
-            dx = lay.backward(dx)
-        return self.loss
+        return dlogits.to(torch.bfloat16)
 
     def optimizer_step(self, step: int, lr: float, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.0):
         for blk, master, m, v in self.opt:

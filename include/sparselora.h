@@ -88,6 +88,7 @@ typedef enum { SL_SLICE_OUT = 0, SL_SLICE_IN = 1 } sl_slice;
 typedef enum { SL_LAYOUT_NATURAL = 0, SL_LAYOUT_SIGMA = 1 } sl_layout;
 typedef enum { SL_EPI_NONE = 0, SL_EPI_SWIGLU = 1 } sl_epilogue;
 typedef enum { SL_LORA_FWD = 0, SL_LORA_BWD = 1 } sl_lora_mode;
+typedef enum { SL_ROPE_HALVES = 0, SL_ROPE_PAIRS = 1 } sl_rope_style;
 
 /* Caller-owned scratch memory. When ptr is NULL or bytes < the size a call needs, the
  * call stores the size in `needed` and returns SL_ERR_WORKSPACE without launching.
@@ -415,6 +416,98 @@ SL_API sl_status sl_attention_bwd(const void* q, const void* k, const void* v, c
                                   const float* lse, int64_t ldq, int64_t ldkv, int32_t n_seq, int32_t seq_len,
                                   int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim, void* dq, void* dk,
                                   void* dv, sl_workspace* ws, sl_stream stream);
+
+/* Per-head RMSNorm of q and k and the position rotation, in one pass over both (between the q and k
+ * projections and the attention core). For a head's row x of head_dim elements at position p:
+ *   n = x / sqrt(mean(x^2) + eps) * gamma (n = x without gains), then for i < rot_dim / 2, with (a, b) =
+ *   (i, i + rot_dim / 2) for SL_ROPE_HALVES or (2 i, 2 i + 1) for SL_ROPE_PAIRS and t = p * inv_freq[i]:
+ *   y[a] = n[a] cos t - n[b] sin t, y[b] = n[b] cos t + n[a] sin t; elements from rot_dim on: y = n.
+ *   q, yq, dyq, dq: bf16 [n_tok, n_q_heads * head_dim]; k, yk, dyk, dk: bf16 [n_tok, n_kv_heads *
+ *     head_dim]; each with its leading dimension (a multiple of 8, 16-byte aligned base).
+ *   positions: int32 [n_tok], of any sign; inv_freq: fp32 [rot_dim / 2]; both may be NULL with rot_dim =
+ *     0 (norm only). t is reduced exactly (64-bit fractions of a turn), at any position.
+ *   gamma_q, gamma_k: bf16 [head_dim], both or neither (NULL: no norm, rotation only).
+ * The backward takes the forward's inputs q and k (not read, may be NULL, without gains) and writes
+ *   dq, dk and, where given, dgamma_q, dgamma_k (fp32 [head_dim], sums over tokens and heads in a
+ *   fixed order; workspace: up to 1184 * 2 * head_dim floats past the header, ws may be NULL without
+ *   them).
+ * An output may be its input (same pointer and leading dimension: yq = q, dq = dyq); no other overlap. fp32
+ * arithmetic, each output rounded once. head_dim in [8, 256], a multiple of 8; rot_dim a multiple of 8
+ * up to head_dim. */
+SL_API sl_status sl_qk_norm_rope_fwd(const void* q, int64_t ldq, const void* k, int64_t ldk, const int32_t* positions,
+                                     const float* inv_freq, int32_t rot_dim, int32_t style, const void* gamma_q,
+                                     const void* gamma_k, float eps, int64_t n_tok, int32_t n_q_heads,
+                                     int32_t n_kv_heads, int32_t head_dim, void* yq, int64_t ldyq, void* yk,
+                                     int64_t ldyk, sl_stream stream);
+SL_API sl_status sl_qk_norm_rope_bwd(const void* dyq, int64_t lddyq, const void* dyk, int64_t lddyk, const void* q,
+                                     int64_t ldq, const void* k, int64_t ldk, const int32_t* positions,
+                                     const float* inv_freq, int32_t rot_dim, int32_t style, const void* gamma_q,
+                                     const void* gamma_k, float eps, int64_t n_tok, int32_t n_q_heads,
+                                     int32_t n_kv_heads, int32_t head_dim, void* dq, int64_t lddq, void* dk,
+                                     int64_t lddk, float* dgamma_q, float* dgamma_k, sl_workspace* ws,
+                                     sl_stream stream);
+
+/* Attention in which each query sees an interval of its sequence's keys: packed documents, prefixes
+ * that see themselves whole, sliding windows, padding, and any mix of them.
+ *   sl_attention_plan makes the plan of a batch from the rows' intervals: token t of n_seq * seq_len sees
+ *     keys [row_lo[t], row_hi[t]) of its own sequence (positions within the sequence; int32; values outside
+ *     [0, seq_len] are clipped; lo >= hi: the row sees nothing). row_lo NULL: 0; row_hi NULL: causal
+ *     (position + 1). plan: a 16-byte aligned buffer of sl_attention_plan_bytes(n_seq, seq_len) bytes (0
+ *     for sizes out of range); it keeps the intervals, so row_lo and row_hi are not needed later, and serves any
+ *     number of layers, heads and calls, forward and backward, on streams ordered after it.
+ *   sl_attention_masked_fwd: t_ij = scale q_i . k_j; with softcap > 0: t_ij = softcap tanh(t_ij / softcap); with
+ *     slopes (fp32 [n_q_heads]): t_ij -= slopes[h] |i - j|; P = softmax over the keys that row i sees; o = P v;
+ *     lse (fp32 [n_q_heads][T]) = log sum_j e^(t_ij). A row that sees nothing: o = 0, lse = -inf.
+ *     scale = 0 means 1 / sqrt(head_dim); softcap = 0 means no cap. Heads as in sl_attention_fwd.
+ *   sl_attention_masked_bwd: dq, dk, dv of the loss whose gradient at o is d_o, from the forward's lse (the
+ *     rounded o is not used: the rows' sums of P dP are formed again in fp32; the slopes are constants). Rows that see nothing give and get zeros. dq is summed across key
+ *     tiles in fp32 reductions whose order varies between runs (its last bits may differ); dk and dv are
+ *     run-to-run identical. Workspace as sl_attention_bwd (the forward needs only the header).
+ * q, o, d_o, dq: bf16 [T, n_q_heads * head_dim]; k, v, dk, dv: bf16 [T, n_kv_heads * head_dim], each with its
+ * own leading dimension (slices of one projection's output need no copy). Values have to be finite in every
+ * row, those that nobody sees too (a product of tiles multiplies them by zero). head_dim in [8, 128], a
+ * multiple of 8; seq_len <= 2^20; n_q_heads a multiple of n_kv_heads; pointers 16-byte aligned, leading
+ * dimensions multiples of 8. Errors: SL_ERR_INVALID_ARG (null pointer), SL_ERR_SHAPE (a size, scale or cap out of
+ * range, a plan buffer too small), SL_ERR_ALIGNMENT, SL_ERR_WORKSPACE. A buffer that holds no plan of the
+ * call's sizes is seen on the device: nothing is computed, and the workspace's error word says so. */
+SL_API int64_t sl_attention_plan_bytes(int32_t n_seq, int32_t seq_len);
+SL_API sl_status sl_attention_plan(const int32_t* row_lo, const int32_t* row_hi, int32_t n_seq, int32_t seq_len,
+                                   void* plan, int64_t plan_bytes, sl_stream stream);
+SL_API sl_status sl_attention_masked_fwd(const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v,
+                                         int64_t ldv, int32_t n_seq, int32_t seq_len, int32_t n_q_heads,
+                                         int32_t n_kv_heads, int32_t head_dim, float scale, float softcap,
+                                         const float* slopes, const void* plan, int64_t plan_bytes, void* o,
+                                         int64_t ldo, float* lse, sl_workspace* ws, sl_stream stream);
+SL_API sl_status sl_attention_masked_bwd(const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v,
+                                         int64_t ldv, const void* d_o, int64_t lddo, const float* lse, int32_t n_seq, int32_t seq_len, int32_t n_q_heads,
+                                         int32_t n_kv_heads, int32_t head_dim, float scale, float softcap,
+                                         const float* slopes, const void* plan, int64_t plan_bytes, void* dq,
+                                         int64_t lddq, void* dk, int64_t lddk, void* dv, int64_t lddv,
+                                         sl_workspace* ws, sl_stream stream);
+
+/* Log probabilities of given tokens, entropy and top alternatives of rows of logits, and their gradient
+ * (the loss at the LM head, and the scores of a generation).
+ *   logits: bf16 or fp32 [n_rows, vocab] (ld elements, 16-byte aligned rows); targets: int32 [n_rows]; a target
+ *     outside [0, vocab) names no token: its logp is 0 and has no gradient.
+ *   sl_token_logprobs_fwd: logp[r] = z_t - log sum_j e^(z_j); stats[r] = two floats for the backward, with
+ *     log sum_j e^(z_j) = ln 2 (stats[r][0] + stats[r][1]); entropy[r] (optional) = -sum_j p_j log p_j;
+ *     with top_k > 0 (<= 32, <= vocab): top_ids[r], top_logp[r] ([n_rows, top_k], dense): the tokens of the largest
+ *     logits, largest first, equal ones by the lower index, NaN below every number.
+ *   sl_token_logprobs_bwd: dlogits (the logits' type, leading dimension ldd; may be the logits themselves) of
+ *     the loss whose gradients are g_logp[r] at logp and, optionally, g_entropy[r] at entropy (then entropy is
+ *     the forward's): dz_j = g_logp ([j = t] - p_j) - g_entropy p_j (log p_j + entropy). A row whose gradients
+ *     are both 0 (or that has no target and no g_entropy) gets zeros. Columns from vocab to ldd are left as they were.
+ * Logits below -1e37 count as -inf (probability 0, no gradient). A row with nothing above that: logp = -inf (0 without
+ * a target), entropy 0, top_logp = -inf, no gradient. A row with NaN, +inf or a logit above 1e37: NaN results. Sums in
+ * fp32 in a fixed order (run-to-run identical). Errors: SL_ERR_INVALID_ARG, SL_ERR_SHAPE (vocab up to 2^24,
+ * with top_k up to 6553600 fp32 or 13107200 bf16 columns), SL_ERR_ALIGNMENT. */
+SL_API sl_status sl_token_logprobs_fwd(sl_dtype dtype, const void* logits, int64_t ld, int64_t n_rows, int64_t vocab,
+                                       const int32_t* targets, float* logp, float* stats, float* entropy,
+                                       int32_t top_k, int32_t* top_ids, float* top_logp, sl_stream stream);
+SL_API sl_status sl_token_logprobs_bwd(sl_dtype dtype, const void* logits, int64_t ld, int64_t n_rows, int64_t vocab,
+                                       const int32_t* targets, const float* stats, const float* g_logp,
+                                       const float* g_entropy, const float* entropy, void* dlogits, int64_t ldd,
+                                       sl_stream stream);
 
 /* Tile height of the CTA-pair tensor-core GEMM that runs the sliced products (a4, a5):
  * rows = 256 (each pair of SMs computes 256 x 256 output tiles with two accumulators, so a
