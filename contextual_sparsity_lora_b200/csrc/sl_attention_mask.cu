@@ -20,8 +20,9 @@ namespace sl {
 
 namespace {
 
-constexpr int kSoftThreads = 256;                   // forward: warps 2..9 softmax / epilogue
+constexpr int kSoftThreads = 256;                   // delta: warps 2..9
 constexpr int kAttnThreads = 64 + kSoftThreads;     // warp 0 TMA, warp 1 MMA + TMEM
+constexpr int kFwdThreads = 384;                    // warp 0 TMA, warp 1 MMA, warps 4..11 softmax
 constexpr int kBwdComputeThreads = 256;                   // backward: warps 2..9
 constexpr int kAttnBwdThreads = 64 + kBwdComputeThreads;  // warp 0 TMA, warp 1 MMA + TMEM
 constexpr float kLog2e = 1.4426950408889634f;
@@ -40,7 +41,8 @@ struct Plan {
   // see any of the key tile (never empty)
   const int4* q_range;
   const int2* k_range;
-  const int32_t *q_order, *k_order;  // tiles (sequence * n_t + tile), the longest ranges first
+  const int2* q2_range;  // key tiles of query tiles 2 i and 2 i + 1 together (sequence * ceil(n_t / 2) + i)
+  const int32_t *q_order, *k_order, *q2_order;  // tiles (sequence * n_t + tile) and pairs, the longest ranges first
 };
 
 int64_t plan_tiles(int n_seq, int S) { return (int64_t)n_seq * ((S + kTile - 1) / kTile); }
@@ -63,6 +65,9 @@ int64_t carve_plan(void* buf, int n_seq, int S, Plan* out) {
   p.k_range = reinterpret_cast<int2*>(take(nt * 8));
   p.q_order = reinterpret_cast<int32_t*>(take(nt * 4));
   p.k_order = reinterpret_cast<int32_t*>(take(nt * 4));
+  const int64_t n2 = (int64_t)n_seq * (((S + kTile - 1) / kTile + 1) / 2);
+  p.q2_range = reinterpret_cast<int2*>(take(n2 * 8));
+  p.q2_order = reinterpret_cast<int32_t*>(take(n2 * 4));
   if (out) *out = p;
   return off;
 }
@@ -169,7 +174,20 @@ __device__ void plan_tiles_and_order(const Plan& p, int n_seq, int S, int32_t* h
   __syncthreads();
   for (int64_t at = threadIdx.x; at < n; at += kPlanThreads)
     if (kr[at].y == 0) kr[at] = make_int2(0, 1);
+  const int n_t2 = (n_t + 1) / 2;
+  const int64_t n2 = (int64_t)n_seq * n_t2;
+  for (int64_t at = threadIdx.x; at < n2; at += kPlanThreads) {
+    const int i = (int)(at % n_t2);
+    const int4 a = p.q_range[at / n_t2 * n_t + 2 * i];
+    int2 v = make_int2(a.x, a.y);
+    if (2 * i + 1 < n_t) {
+      const int4 c = p.q_range[at / n_t2 * n_t + 2 * i + 1];
+      v = make_int2(min(v.x, c.x), max(v.y, c.y));
+    }
+    const_cast<int2*>(p.q2_range)[at] = v;
+  }
   __syncthreads();
+  plan_order(p.q2_range, n2, n_t, const_cast<int32_t*>(p.q2_order), hist, carry);
   plan_order(p.q_range, n, n_t, const_cast<int32_t*>(p.q_order), hist, carry);
   plan_order(p.k_range, n, n_t, const_cast<int32_t*>(p.k_order), hist, carry);
   if (threadIdx.x < 3) const_cast<int32_t*>(p.header)[threadIdx.x] = threadIdx.x == 0 ? kPlanMagic : threadIdx.x == 1 ? n_seq : S;
@@ -202,35 +220,51 @@ __device__ __forceinline__ float rcp(float x) {
   return y;
 }
 
-// tanh(u) from e^(2u) = 2^(u'), u' = 2 log2(e) u: 1 - 2 / (2^u' + 1). The error is about 1e-7 of 1 at every u
-// (2^u' = inf gives 1, 2^u' = 0 gives -1); tanh.approx would be off by 5e-4 of the value.
-__device__ __forceinline__ float tanh_2(float u2) { return fmaf(-2.f, rcp(ex2(u2) + 1.f), 1.f); }
-
-// The score in powers of two from the raw product s. CAP: mul = 2 log2(e) scale / cap, cap_log2 = cap
-// log2(e); else mul = log2(e) scale. away: the distance, of either sign.
-template <bool CAP, bool BIAS>
-__device__ __forceinline__ float score(float s, float mul, float cap_log2, float slope, float away) {
-  float y = CAP ? cap_log2 * tanh_2(s * mul) : s * mul;
-  if (BIAS) y = fmaf(-slope, fabsf(away), y);
-  return y;
+// tanh of 32 raw products times mul (= scale / cap), in place. Up to 0.75 an odd polynomial (a least-maximum
+// fit of tanh(u) / u in u^2, relative error 3e-8, 1.6e-7 with fp32 arithmetic): 7 multiply-adds, and small
+// scores keep their relative exactness. Above, for the whole warp: 1 - 2 / (2^(2 log2(e) u) + 1), error
+// about 1e-7 of 1 (2^x = inf gives 1, 0 gives -1), on the exponential unit, which the softmax needs too.
+// tanh.approx would be off by 5e-4 of the value.
+__device__ __forceinline__ void tanh32(uint32_t (&v)[32], float mul) {
+  float top = 0.f;
+#pragma unroll
+  for (int e = 0; e < 32; ++e) top = fmaxf(top, fabsf(__uint_as_float(v[e])));
+  if (__any_sync(0xffffffffu, !(top * mul <= 0.75f))) {
+    const float mul2 = mul * (2.f * kLog2e);
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+      v[e] = __float_as_uint(fmaf(-2.f, rcp(ex2(__uint_as_float(v[e]) * mul2) + 1.f), 1.f));
+  } else {
+#pragma unroll
+    for (int e = 0; e < 32; ++e) {
+      const float u = __uint_as_float(v[e]) * mul, w = u * u;
+      float r = fmaf(w, -0.0047162557f, 0.019582905f);
+      r = fmaf(w, r, -0.053344428f);
+      r = fmaf(w, r, 0.13325407f);
+      r = fmaf(w, r, -0.33332959f);
+      v[e] = __float_as_uint(u * fmaf(w, r, 1.f));
+    }
+  }
 }
-template <bool CAP, bool BIAS>
-__device__ __forceinline__ float score_grad(float s, float mul, float cap_log2, float slope, float away, float& grad) {
-  if (!CAP) return score<CAP, BIAS>(s, mul, cap_log2, slope, away);
-  const float t = tanh_2(s * mul);
-  grad = fmaf(-t, t, 1.f);
-  const float y = cap_log2 * t;
+
+// The score in powers of two from a raw product (with a cap: its tanh) v: mul = log2(e) scale, or log2(e) cap. away:
+// the distance, of either sign.
+template <bool BIAS>
+__device__ __forceinline__ float score(uint32_t v, float mul, float slope, float away) {
+  const float y = __uint_as_float(v) * mul;
   return BIAS ? fmaf(-slope, fabsf(away), y) : y;
 }
 
 struct MaskedFwdParams {
   CUtensorMap qmap, kmap, vmap;  // [head_dim, heads, seq_len, n_seq], boxes 64 x 1 x 128 x 1
-  CUtensorMap omap;              // the same view of o (bulk stores of the output tile)
   Plan plan;
   const float* slopes;           // [hq]
+  __nv_bfloat16* o;
+  int64_t ldo;
   float* lse;                    // [n_q_heads][n_seq * seq_len]
   int32_t n_seq, S, hq, hkv, hd, nd;
-  float mul, cap_log2;           // see score()
+  int32_t n_units, pair_heads;   // pair_heads: the streams are two heads, else two query tiles
+  float mul, cap_mul;            // see score() and tanh32()
   int* err;
 };
 
@@ -242,7 +276,7 @@ struct MaskedDeltaParams {
   float* delta;                  // [hq][T]
   float* dq_acc;                 // [T][hq * hd]
   int32_t n_seq, S, hq, hkv, hd, nd;
-  float mul, cap_log2;
+  float mul, cap_mul;
   int* err;
 };
 
@@ -257,7 +291,7 @@ struct MaskedBwdParams {
   __nv_bfloat16* dv;
   int64_t lddk, lddv;
   int32_t n_seq, S, hq, hkv, hd, nd;
-  float scale, mul, cap_log2;
+  float scale, mul, cap_mul;
   int* err;
 };
 
@@ -290,63 +324,133 @@ __device__ __forceinline__ bool bar_and_bwd(bool ok) {
 
 // ------------------------------------------------------------------------------------ forward
 
+// Persistent CTAs, one per SM, over units of two streams that share their keys and values: two heads of a group at one
+// tile of 128 queries (an even number of heads per group: the streams see the same key tiles), else two
+// neighbouring query tiles of one head. Warp 0 loads each stream's Q and, for both, K and V (two stages each); warp 1
+// issues the products; warps 4-7 and 8-11 are the softmax of stream 0 and 1, a query row per thread (they take over the
+// registers that the first four warps give up). While one
+// stream's softmax runs, the tensor cores work for the other: O_x += P_x V of step t, then S_x = Q_x K^T of step t + 1, for
+// x = 0 and 1 in turn. P replaces S in TMEM (bf16, the first operand of P V), so it never passes through shared
+// memory, and since P V of step t stands before S of step t + 1 in the tensor pipe, a softmax that sees S
+// may rescale O without a further wait. TMEM: S_x / P_x at 128 x, O_x at 256 + 128 x.
+struct Unit {
+  int qt0, qt1, h0, h1, b, j0, j1;
+  __device__ __forceinline__ int qt(int x) const { return x ? qt1 : qt0; }
+  __device__ __forceinline__ int h(int x) const { return x ? h1 : h0; }
+};
+
+__device__ __forceinline__ Unit unit_of(const MaskedFwdParams& p, int u) {
+  Unit r;
+  if (p.pair_heads) {
+    const int n_qt = (p.S + kTile - 1) / kTile, half = p.hq >> 1;
+    const int at = p.plan.q_order[u / half];
+    const int4 range = p.plan.q_range[at];
+    r.b = at / n_qt;
+    r.qt0 = r.qt1 = at % n_qt;
+    r.h0 = 2 * (u % half);
+    r.h1 = r.h0 + 1;
+    r.j0 = range.x;
+    r.j1 = range.y;
+  } else {
+    const int n_t2 = ((p.S + kTile - 1) / kTile + 1) >> 1;
+    const int at = p.plan.q2_order[u / p.hq];
+    const int2 range = p.plan.q2_range[at];
+    r.b = at / n_t2;
+    r.qt0 = 2 * (at % n_t2);
+    r.qt1 = r.qt0 + 1;
+    r.h0 = r.h1 = u % p.hq;
+    r.j0 = range.x;
+    r.j1 = range.y;
+  }
+  return r;
+}
+
+// Steps of a CTA in order: (unit, key tile), the units being blockIdx.x, blockIdx.x + gridDim.x, ...
+struct Walk {
+  Unit un;
+  int u, i, j, t;  // unit, its number in this CTA, key tile, number of the step in this CTA
+  bool live;
+  __device__ __forceinline__ void start(const MaskedFwdParams& p, bool ok) {
+    u = blockIdx.x;
+    i = t = 0;
+    live = ok && u < p.n_units;
+    if (live) {
+      un = unit_of(p, u);
+      j = un.j0;
+    }
+  }
+  __device__ __forceinline__ bool first() const { return j == un.j0; }
+  __device__ __forceinline__ bool last() const { return j == un.j1 - 1; }
+  __device__ __forceinline__ void next(const MaskedFwdParams& p) {
+    ++t;
+    if (++j < un.j1) return;
+    u += gridDim.x;
+    ++i;
+    live = u < p.n_units;
+    if (live) {
+      un = unit_of(p, u);
+      j = un.j0;
+    }
+  }
+};
+
+// D[tmem] (+)= A[tmem] * B[smem desc]^T: A is 128 rows (lanes) of 16 bf16, two per 32-bit column.
+__device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                             uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Each thread of the warp writes 16 consecutive 32-bit columns of its TMEM lane.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
 template <bool CAP, bool BIAS>
-__global__ void __launch_bounds__(kAttnThreads, 1) masked_fwd_kernel(const __grid_constant__ MaskedFwdParams p) {
+__global__ void __launch_bounds__(kFwdThreads, 1) masked_fwd_kernel(const __grid_constant__ MaskedFwdParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int nd = p.nd;
-  uint8_t* sq = smem;                          // Q: nd chunks (room for 2)
-  uint8_t* skv = sq + 2 * kChunk;              // stage s: K (nd chunks) then V (nd chunks)
-  uint8_t* sp = skv + 2 * 2 * nd * kChunk;     // P: 2 chunks (128 keys)
-  uint8_t* sob = sp + 2 * kChunk;              // O staging tile for the bulk stores: 2 chunks
-  float* s_l = reinterpret_cast<float*>(sob + 2 * kChunk);  // [2][128]: the two halves' row sums
-  uint64_t* bars = reinterpret_cast<uint64_t*>(s_l + 256);
-  uint64_t* q_full = bars;
-  uint64_t* q_empty = bars + 1;   // Q of a query tile is free once its last S has read it
-  uint64_t* k_full = bars + 2;    // [2]
-  uint64_t* k_empty = bars + 4;   // [2]: K of a stage is free once S has read it
-  uint64_t* v_full = bars + 6;    // [2]
-  uint64_t* v_empty = bars + 8;   // [2]: V of a stage is free once P V has read it
-  uint64_t* s_full = bars + 10;   // [2]
-  uint64_t* s_free = bars + 12;   // [2]
-  uint64_t* p_full = bars + 14;
-  uint64_t* pv_done = bars + 15;
-  uint64_t* o_free = bars + 16;   // [2]: an O accumulator is free once the epilogue has read it
+  uint8_t* sq = smem;                     // Q of stream x: nd chunks at 2 x chunks
+  uint8_t* sk = smem + 4 * kChunk;        // [2] stages of K, 2 chunks each
+  uint8_t* sv = smem + 8 * kChunk;        // [2] stages of V
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + 12 * kChunk);
+  uint64_t* q_full = bars;         // [2] by stream
+  uint64_t* q_empty = bars + 2;    // [2]
+  uint64_t* k_full = bars + 4;     // [2] by stage
+  uint64_t* k_empty = bars + 6;    // [2]
+  uint64_t* v_full = bars + 8;     // [2]
+  uint64_t* v_empty = bars + 10;   // [2]
+  uint64_t* s_full = bars + 12;    // [2] by stream
+  uint64_t* p_full = bars + 14;    // [2]
+  uint64_t* o_full = bars + 16;    // [2]
   uint64_t* drain = bars + 18;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 19);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // Persistent CTAs: unit u = (tile of queries in the plan's order, query head); CTA c takes units
-  // c, c + grid, ... Every role walks the same units; K/V stages, S buffers and P follow one tile
-  // counter over all of a CTA's units, the two O accumulators alternate by unit. A unit's key tiles
-  // are j0 .. j1 - 1 (at least one, so that a tile whose rows see nothing takes the same path).
-  const int n_qt = (p.S + kTile - 1) / kTile;
-  const int n_units = n_qt * p.n_seq * p.hq;
   const int hpg = p.hq / p.hkv;
-  auto unit = [&](int u, int& qt, int& h, int& b, int& j0, int& j1) {
-    const int at = p.plan.q_order[u / p.hq];
-    const int4 range = p.plan.q_range[at];
-    qt = at % n_qt;
-    b = at / n_qt;
-    h = u % p.hq;
-    j0 = range.x;
-    j1 = range.y;
-  };
   if (threadIdx.x == 0) {
-    mbar_init(q_full, 1);
-    mbar_init(q_empty, 1);
     for (int s = 0; s < 2; ++s) {
+      mbar_init(&q_full[s], 1);
+      mbar_init(&q_empty[s], 1);
       mbar_init(&k_full[s], 1);
       mbar_init(&k_empty[s], 1);
       mbar_init(&v_full[s], 1);
       mbar_init(&v_empty[s], 1);
       mbar_init(&s_full[s], 1);
-      mbar_init(&s_free[s], kSoftThreads);
-      mbar_init(&o_free[s], kSoftThreads);
+      mbar_init(&p_full[s], 128);
+      mbar_init(&o_full[s], 1);
     }
-    mbar_init(p_full, kSoftThreads);
-    mbar_init(pv_done, 1);
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_barrier_init();
@@ -358,260 +462,206 @@ __global__ void __launch_bounds__(kAttnThreads, 1) masked_fwd_kernel(const __gri
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;  // S buffers at columns 0 and 128, O accumulators at 256 and 384
+  const uint32_t tmem = *tmem_slot;
   pdl_wait();
   const bool plan_ok = plan_fits(p.plan, p.n_seq, p.S, p.err);
 
-  if (warp == 0) {
-    if (lane == 0) {
-      // Loads in order: Q of a unit right before K of its first key tile (once the previous unit's
-      // last S has read Q), K of tile t + 1 ahead of V of tile t.
-      auto load_kv = [&](int t, bool is_v, int g, int kv, int b) -> bool {
-        const int s = t & 1;
-        uint64_t* empty = is_v ? &v_empty[s] : &k_empty[s];
-        uint64_t* full = is_v ? &v_full[s] : &k_full[s];
-        if (!mbar_wait(empty, ((t >> 1) & 1) ^ 1, abort_flag, p.err, DEV_TIMEOUT_PRODUCER)) return false;
-        mbar_arrive_expect_tx(full, nd * kChunk);
-        uint8_t* st = skv + s * 2 * nd * kChunk + (is_v ? nd * kChunk : 0);
-        for (int c = 0; c < nd; ++c)
-          tma_load_4d(st + c * kChunk, is_v ? &p.vmap : &p.kmap, full, 64 * c, g, kv * kTile, b);
-        return true;
-      };
-      int nq = 0, nk = 0, nv = 0;  // Q, K and V tiles issued
-      int pg = 0, pkv = 0, pb = 0;   // the tile whose V is still to load (tile nv when nk > nv)
-      bool ok = true;
-      for (int u = blockIdx.x, i = 0; ok && plan_ok && u < n_units; u += gridDim.x, ++i) {
-        int qt, h, b, j0, j1;
-        unit(u, qt, h, b, j0, j1);
-        const int g = h / hpg;
-        for (int j = j0; j < j1; ++j) {
-          if (j == j0) {
-            // the previous unit's last V first (its P V does not wait for this unit), then Q
-            if (nk > nv) {
-              if (!load_kv(nv, true, pg, pkv, pb)) { ok = false; break; }
-              ++nv;
-            }
-            if (i > 0 && !mbar_wait(q_empty, (i - 1) & 1, abort_flag, p.err, DEV_TIMEOUT_PRODUCER)) { ok = false; break; }
-            mbar_arrive_expect_tx(q_full, nd * kChunk);
-            for (int c = 0; c < nd; ++c) tma_load_4d(sq + c * kChunk, &p.qmap, q_full, 64 * c, h, qt * kTile, b);
-            ++nq;
+  if (warp < 4) {
+    // 384 threads start with 168 registers each: 72 here and 216 in the two softmax groups make the same sum
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp == 0 && lane == 0) {
+      Walk w;
+      int nq = 0, nk = 0, nv = 0;  // loads issued (Q: of both streams)
+      for (w.start(p, plan_ok); w.live; w.next(p)) {
+        const int g = w.un.h0 / hpg, s = w.t & 1;
+        if (w.first()) {
+          bool ok = true;
+          for (int x = 0; x < 2 && ok; ++x) {
+            if (w.i > 0) ok = mbar_wait(&q_empty[x], (w.i - 1) & 1, abort_flag, p.err, DEV_TIMEOUT_PRODUCER);
+            if (!ok) break;
+            mbar_arrive_expect_tx(&q_full[x], nd * kChunk);
+            for (int c = 0; c < nd; ++c)
+              tma_load_4d(sq + (2 * x + c) * kChunk, &p.qmap, &q_full[x], 64 * c, w.un.h(x), w.un.qt(x) * kTile, w.un.b);
+            if (x == 1) ++nq;
           }
-          if (!load_kv(nk, false, g, j, b)) { ok = false; break; }
-          ++nk;
-          if (j > j0) {
-            if (!load_kv(nv, true, pg, pkv, pb)) { ok = false; break; }
-            ++nv;
-          }
-          pg = g;
-          pkv = j;
-          pb = b;
+          if (!ok) break;
         }
+        if (!mbar_wait(&k_empty[s], ((w.t >> 1) & 1) ^ 1, abort_flag, p.err, DEV_TIMEOUT_PRODUCER)) break;
+        mbar_arrive_expect_tx(&k_full[s], nd * kChunk);
+        for (int c = 0; c < nd; ++c)
+          tma_load_4d(sk + (2 * s + c) * kChunk, &p.kmap, &k_full[s], 64 * c, g, w.j * kTile, w.un.b);
+        ++nk;
+        if (!mbar_wait(&v_empty[s], ((w.t >> 1) & 1) ^ 1, abort_flag, p.err, DEV_TIMEOUT_PRODUCER)) break;
+        mbar_arrive_expect_tx(&v_full[s], nd * kChunk);
+        for (int c = 0; c < nd; ++c)
+          tma_load_4d(sv + (2 * s + c) * kChunk, &p.vmap, &v_full[s], 64 * c, g, w.j * kTile, w.un.b);
+        ++nv;
       }
-      if (ok && nk > nv && load_kv(nv, true, pg, pkv, pb)) ++nv;
       // every copy lands before the CTA may exit
-      if (nq > 0) mbar_wait(q_full, (nq - 1) & 1, nullptr, p.err, DEV_TIMEOUT_DRAIN);
+      if (nq > 0)
+        for (int x = 0; x < 2; ++x) mbar_wait(&q_full[x], (nq - 1) & 1, nullptr, p.err, DEV_TIMEOUT_DRAIN);
       for (int t = max(0, nk - 2); t < nk; ++t) mbar_wait(&k_full[t & 1], (t >> 1) & 1, nullptr, p.err, DEV_TIMEOUT_DRAIN);
       for (int t = max(0, nv - 2); t < nv; ++t) mbar_wait(&v_full[t & 1], (t >> 1) & 1, nullptr, p.err, DEV_TIMEOUT_DRAIN);
-    }
-  } else if (warp == 1) {
-    if (lane == 0) {
-      const uint32_t id_s = idesc_bf16(128, 128, 0, 0);          // S = Q K^T: both K-major over d
-      const uint32_t id_pv = idesc_bf16(128, 64 * nd, 0, 1);     // O += P V: P K-major, V MN-major
-      const uint32_t aq = smem_u32(sq), ap = smem_u32(sp);
-      // P V of tile t (the first or a later key tile of the CTA's unit i) into the unit's O accumulator
-      auto issue_pv = [&](int t, int i, bool first) -> bool {
-        if (!mbar_wait(p_full, t & 1, abort_flag, p.err, DEV_TIMEOUT_MMA)) return false;
-        if (!mbar_wait(&v_full[t & 1], (t >> 1) & 1, abort_flag, p.err, DEV_TIMEOUT_MMA)) return false;
-        // the first P V of a unit overwrites its accumulator: the epilogue of unit i - 2 has read it
-        if (first && i >= 2 && !mbar_wait(&o_free[i & 1], ((i >> 1) & 1) ^ 1, abort_flag, p.err, DEV_TIMEOUT_MMA))
-          return false;
+    } else if (warp == 1 && lane == 0) {
+      const uint32_t id_s = idesc_bf16(128, 128, 0, 0);        // S = Q K^T: both K-major over d
+      const uint32_t id_pv = idesc_bf16(128, 64 * nd, 0, 1);   // O += P V: P in TMEM, V MN-major
+      auto issue_s = [&](const Walk& w, int x) -> bool {
+        const int s = w.t & 1;
+        if (w.first() && !mbar_wait(&q_full[x], w.i & 1, abort_flag, p.err, DEV_TIMEOUT_MMA)) return false;
+        if (x == 0 && !mbar_wait(&k_full[s], (w.t >> 1) & 1, abort_flag, p.err, DEV_TIMEOUT_MMA)) return false;
         tc_fence_after();
-        const uint32_t bv = smem_u32(skv + (t & 1) * 2 * nd * kChunk + nd * kChunk);
-        for (int k = 0; k < 8; ++k)
-          umma_bf16(tmem + 256 + 128 * (i & 1), kmajor_desc(ap, k), mnmajor_desc(bv, k), id_pv, (!first || k > 0) ? 1u : 0u);
-        umma_commit(pv_done);
-        umma_commit(&v_empty[t & 1]);
+        const uint32_t aq = smem_u32(sq + 2 * x * kChunk), bk = smem_u32(sk + 2 * s * kChunk);
+        for (int k = 0; k < 4 * nd; ++k)
+          umma_bf16(tmem + 128 * x, kmajor_desc(aq, k), kmajor_desc(bk, k), id_s, k > 0 ? 1u : 0u);
+        umma_commit(&s_full[x]);
+        if (w.last()) umma_commit(&q_empty[x]);
+        if (x == 1) umma_commit(&k_empty[s]);
         return true;
       };
-      bool ok = true;
-      int t = 0;
-      for (int u = blockIdx.x, i = 0; ok && plan_ok && u < n_units; u += gridDim.x, ++i) {
-        int qt, h, b, j0, j1;
-        unit(u, qt, h, b, j0, j1);
-        if (!mbar_wait(q_full, i & 1, abort_flag, p.err, DEV_TIMEOUT_MMA)) { ok = false; break; }
-        for (int j = j0; j < j1; ++j, ++t) {
-          const int s = t & 1;
-          if (!mbar_wait(&k_full[s], (t >> 1) & 1, abort_flag, p.err, DEV_TIMEOUT_MMA)) { ok = false; break; }
-          if (t >= 2 && !mbar_wait(&s_free[s], ((t - 2) >> 1) & 1, abort_flag, p.err, DEV_TIMEOUT_MMA)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t bk = smem_u32(skv + s * 2 * nd * kChunk);
-          for (int k = 0; k < 4 * nd; ++k)
-            umma_bf16(tmem + 128 * s, kmajor_desc(aq, k), kmajor_desc(bk, k), id_s, k > 0 ? 1u : 0u);
-          umma_commit(&s_full[s]);
-          umma_commit(&k_empty[s]);
-          if (j == j1 - 1) umma_commit(q_empty);
-          if (j > j0 && !issue_pv(t - 1, i, j - 1 == j0)) { ok = false; break; }
-        }
-        // this unit's last P V before the next unit's first S: the epilogue needs it first
-        if (ok && !issue_pv(t - 1, i, j1 - 1 == j0)) ok = false;
+      auto issue_pv = [&](const Walk& w, int x) -> bool {
+        const int s = w.t & 1;
+        if (!mbar_wait(&p_full[x], w.t & 1, abort_flag, p.err, DEV_TIMEOUT_MMA)) return false;
+        if (x == 0 && !mbar_wait(&v_full[s], (w.t >> 1) & 1, abort_flag, p.err, DEV_TIMEOUT_MMA)) return false;
+        tc_fence_after();
+        const uint32_t bv = smem_u32(sv + 2 * s * kChunk);
+        for (int k = 0; k < 8; ++k)
+          umma_bf16_ts(tmem + 256 + 128 * x, tmem + 128 * x + 8 * k, mnmajor_desc(bv, k), id_pv,
+                       (!w.first() || k > 0) ? 1u : 0u);
+        if (w.last()) umma_commit(&o_full[x]);
+        if (x == 1) umma_commit(&v_empty[s]);
+        return true;
+      };
+      Walk ws, wp;  // S runs a step ahead of P V
+      ws.start(p, plan_ok);
+      wp.start(p, plan_ok);
+      bool ok = ws.live && issue_s(ws, 0) && issue_s(ws, 1);
+      if (ok) ws.next(p);
+      for (; ok && wp.live; wp.next(p)) {
+        ok = issue_pv(wp, 0) && (!ws.live || issue_s(ws, 0)) && issue_pv(wp, 1) && (!ws.live || issue_s(ws, 1));
+        if (ws.live) ws.next(p);
       }
       umma_commit(drain);
       mbar_wait(drain, 0, nullptr, p.err, DEV_TIMEOUT_DRAIN);
     }
   } else {
-    // Eight softmax warps: warp w holds query rows 32 (w % 4) .. + 31 (its TMEM lanes) and one half
-    // of the key columns of each S tile (exponentials, P) and of O (rescale, output). Both halves
-    // read the whole S row for its maximum, so they keep the same running maximum without an
-    // exchange; their partial row sums meet once per unit, at its end.
-    const int cw = warp - 2;
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    const int x = (warp >> 2) - 1;                   // stream
     const int quarter = warp & 3;
-    const int half = cw >> 2;
     const int r = quarter * 32 + lane;               // query row in the tile = TMEM lane
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
-    const int own0 = 64 * half, oth0 = 64 - own0;    // first key column of this half / the other
-    const bool storer = cw == 0 && lane == 0;        // issues the output tile's bulk stores
-    bool ok = true;
+    const uint32_t s_tm = tmem + lane_off + 128 * x, o_tm = s_tm + 256;
+    bool ok = plan_ok;
     int t = 0;
-    for (int u = blockIdx.x, i = 0; plan_ok && u < n_units; u += gridDim.x, ++i) {
-      int qt, h, b, j0, j1;
-      unit(u, qt, h, b, j0, j1);
+    for (int u = blockIdx.x, i = 0; ok && u < p.n_units; u += gridDim.x, ++i) {
+      const Unit un = unit_of(p, u);
+      const int qt = un.qt(x), h = un.h(x);
       const int qpos = qt * kTile + r;               // position in the sequence
       // the keys [lo, hi) that this row sees (rows past the sequence: none)
-      const int64_t row_at = (int64_t)b * p.S + qpos;
+      const int64_t row_at = (int64_t)un.b * p.S + qpos;
       const int lo = qpos < p.S ? p.plan.lo[row_at] : 0, hi = qpos < p.S ? p.plan.hi[row_at] : 0;
       const float slope = BIAS ? p.slopes[h] * kLog2e : 0.f;
-      const uint32_t o_tm = tmem + lane_off + 256 + 128 * (i & 1);
-      float m = -INFINITY, l = 0.f;                  // l: this half's share of the row sum
-      for (int j = j0; j < j1 && ok; ++j, ++t) {
-        const int s = t & 1;
-        if (!__all_sync(0xffffffffu, mbar_wait(&s_full[s], (t >> 1) & 1, abort_flag, p.err, DEV_TIMEOUT_EPILOGUE))) {
-          ok = false;
-          break;
-        }
+      float m = -INFINITY, l = 0.f;
+      for (int j = un.j0; j < un.j1; ++j, ++t) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&s_full[x], t & 1, abort_flag, p.err, DEV_TIMEOUT_EPILOGUE));
+        if (!ok) break;
         tc_fence_after();
-        uint32_t so[2][32], sx[2][32];               // this half's columns, the other half's
+        uint32_t s[4][32];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          tmem_ld32(tmem + lane_off + 128 * s + own0 + 32 * c, so[c]);
-          tmem_ld32(tmem + lane_off + 128 * s + oth0 + 32 * c, sx[c]);
+        for (int c = 0; c < 4; ++c) tmem_ld32(s_tm + 32 * c, s[c]);
+        tmem_ld_wait_regs(s[0]);
+        regs_after_wait(s[1]);
+        regs_after_wait(s[2]);
+        regs_after_wait(s[3]);
+        if (CAP) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tanh32(s[c], p.cap_mul);
         }
-        tmem_ld_wait();
-        tc_fence_before();
-        mbar_arrive(&s_free[s]);
-        // scores in powers of two: capped, biased, and -inf where the row does not see the key
+        // With a bias the score itself is formed here (mul = 1 below), else scores stay raw products
         const int kbase = j * kTile;
+        if (BIAS) {
+          const float away = (float)(qpos - kbase);
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              s[c][e] = __float_as_uint(score<true>(s[c][e], p.mul, slope, away - (float)(32 * c + e)));
+        }
+        const float mul = BIAS ? 1.f : p.mul;
         const int kmin = lo - kbase, kmax = hi - 1 - kbase;  // visible columns of this tile
-        const bool whole = kmin <= 0 && kmax >= kTile - 1;
-        const float away = (float)(qpos - kbase);
+        if (__any_sync(0xffffffffu, kmin > 0 || kmax < kTile - 1)) {
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
+          for (int c = 0; c < 4; ++c)
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const int co = own0 + 32 * c + e, cx = oth0 + 32 * c + e;
-            float yo = score<CAP, BIAS>(__uint_as_float(so[c][e]), p.mul, p.cap_log2, slope, away - (float)co);
-            float yx = score<CAP, BIAS>(__uint_as_float(sx[c][e]), p.mul, p.cap_log2, slope, away - (float)cx);
-            if (!whole) {
-              if (co < kmin || co > kmax) yo = -INFINITY;
-              if (cx < kmin || cx > kmax) yx = -INFINITY;
-            }
-            so[c][e] = __float_as_uint(yo);
-            sx[c][e] = __float_as_uint(yx);
-          }
+            for (int e = 0; e < 32; ++e)
+              if (32 * c + e < kmin || 32 * c + e > kmax) s[c][e] = __float_as_uint(-INFINITY);
+        }
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
+        for (int c = 0; c < 4; ++c)
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            mx[e & 3] = fmaxf(mx[e & 3], fmaxf(__uint_as_float(so[c][e]), __uint_as_float(sx[c][e])));
-        const float mj = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-        // The running maximum moves only when a row's maximum grows by more than 2^8 in the
-        // exponential's scale: the exponentials then stay below 256 and O and l keep one common
-        // reference, so O is rescaled in TMEM rarely (after the first tiles almost never).
+          for (int e = 0; e < 32; e += 2)
+            mx[(e >> 1) & 3] = fmaxf(mx[(e >> 1) & 3], fmaxf(__uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1])));
+        const float mj = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * mul;
+        // The running maximum moves only when a row's maximum grows by more than 2^8: the exponentials then
+        // stay below 256 and O and l keep one common reference, so O is rescaled rarely.
         const float m_cand = fmaxf(m, mj);
         const bool grow = m == -INFINITY || m_cand - m > 8.0f;
         const float m_new = grow ? m_cand : m;
         const float mb = m_new == -INFINITY ? 0.f : m_new;  // a row that has seen nothing yet
         const float corr = (m == -INFINITY) ? 0.f : (grow ? ex2(m - mb) : 1.f);
-        float rs[4] = {0.f, 0.f, 0.f, 0.f};
-        uint32_t pw[2][16];
+        if (j > un.j0 && __any_sync(0xffffffffu, corr != 1.f)) {
+          for (int c = 0; c < 2 * nd; ++c) {
+            uint32_t ov[32];
+            tmem_ld32(o_tm + 32 * c, ov);
+            tmem_ld_wait_regs(ov);
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
+            for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * corr);
+            tmem_st32(o_tm + 32 * c, ov);
+          }
+        }
+        float rs[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t pw[16];
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
-            const float e0 = ex2(__uint_as_float(so[c][e]) - mb);
-            const float e1 = ex2(__uint_as_float(so[c][e + 1]) - mb);
+            const float e0 = ex2(fmaf(__uint_as_float(s[c][e]), mul, -mb));
+            const float e1 = ex2(fmaf(__uint_as_float(s[c][e + 1]), mul, -mb));
             rs[(e >> 1) & 3] += e0 + e1;
-            pw[c][e / 2] = pack2(e0, e1);
+            pw[e / 2] = pack2(e0, e1);
           }
+          tmem_st16(s_tm + 16 * c, pw);
+        }
         l = l * corr + ((rs[0] + rs[1]) + (rs[2] + rs[3]));
-        if (j > j0) {
-          // the previous P V has landed in O (and read P): rescale this half of O when the maximum
-          // grew (the first key tile of a unit: the previous unit's epilogue waited for its last P V)
-          if (!__all_sync(0xffffffffu, mbar_wait(pv_done, (t - 1) & 1, abort_flag, p.err, DEV_TIMEOUT_EPILOGUE))) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          if (__any_sync(0xffffffffu, corr != 1.f)) {
-            for (int c = 2 * half; c < 2 * half + 2 && c < 2 * nd; ++c) {
-              uint32_t ov[32];
-              __syncwarp();
-              tmem_ld32(o_tm + 32 * c, ov);
-              tmem_ld_wait_regs(ov);
-#pragma unroll
-              for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * corr);
-              tmem_st32(o_tm + 32 * c, ov);
-            }
-            tmem_st_wait();
-          }
-        }
-#pragma unroll
-        for (int c = 0; c < 2; ++c) st_swizzled_row32(sp, r, own0 + 32 * c, pw[c]);
-        fence_proxy_async_smem();
-        tc_fence_before();
-        mbar_arrive(p_full);
         m = m_new;
-      }
-      // this unit's last P V (tile t - 1) has landed
-      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(pv_done, (t - 1) & 1, abort_flag, p.err, DEV_TIMEOUT_EPILOGUE));
-      // the previous unit's bulk stores have read the staging tile (rewritten below)
-      if (storer) bulk_wait_read<0>();
-      s_l[half * 128 + r] = l;
-      // every softmax thread reaches both barriers of every unit (the loops only break)
-      ok = bar_and_soft(ok);
-      if (ok) {
-        // O / l as bf16 into the staging tile, laid out like a loaded tile (128-byte swizzle,
-        // 64-column chunks), then out by bulk tensor stores (rows past the sequence and columns
-        // past head_dim are not written); the accumulator is released as soon as it is read
-        tc_fence_after();
-        const float lt = s_l[r] + s_l[128 + r];
-        const float inv = lt == 0.f ? 0.f : 1.f / lt;  // a row that sees nothing: o = 0
-        for (int c = 2 * half; c < 2 * half + 2 && c < 2 * nd; ++c) {
-          uint32_t ov[32];
-          __syncwarp();
-          tmem_ld32(o_tm + 32 * c, ov);
-          tmem_ld_wait_regs(ov);
-          uint32_t w[16];
-#pragma unroll
-          for (int e = 0; e < 32; e += 2) w[e / 2] = pack2(__uint_as_float(ov[e]) * inv, __uint_as_float(ov[e + 1]) * inv);
-          st_swizzled_row32(sob, r, 32 * c, w);
-        }
+        tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(&o_free[i & 1]);
-        fence_proxy_async_smem();
-        if (qpos < p.S && half == 0) p.lse[(int64_t)h * p.n_seq * p.S + (int64_t)b * p.S + qpos] = lt == 0.f ? -INFINITY : m * kLn2 + logf(lt);
+        mbar_arrive(&p_full[x]);
       }
-      ok = bar_and_soft(ok);
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&o_full[x], i & 1, abort_flag, p.err, DEV_TIMEOUT_EPILOGUE));
       if (!ok) break;
-      if (storer) {
-        for (int c = 0; c < nd; ++c) tma_store_4d(&p.omap, sob + c * kChunk, 64 * c, h, qt * kTile, b);
-        bulk_commit();
+      // O / l as bf16, each thread its own row; the next unit's first P V waits for this softmax's next P
+      tc_fence_after();
+      const float inv = l == 0.f ? 0.f : 1.f / l;  // a row that sees nothing: o = 0
+      __nv_bfloat16* out = p.o + row_at * p.ldo + (int64_t)h * p.hd;
+      for (int c = 0; c < 2 * nd; ++c) {
+        uint32_t ov[32];
+        tmem_ld32(o_tm + 32 * c, ov);
+        tmem_ld_wait_regs(ov);
+        if (qpos >= p.S || 32 * c >= p.hd) continue;
+        const int nv = min(32, p.hd - 32 * c) / 8;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (q < nv)
+            *reinterpret_cast<uint4*>(out + 32 * c + 8 * q) = make_uint4(
+                pack2(__uint_as_float(ov[8 * q]) * inv, __uint_as_float(ov[8 * q + 1]) * inv),
+                pack2(__uint_as_float(ov[8 * q + 2]) * inv, __uint_as_float(ov[8 * q + 3]) * inv),
+                pack2(__uint_as_float(ov[8 * q + 4]) * inv, __uint_as_float(ov[8 * q + 5]) * inv),
+                pack2(__uint_as_float(ov[8 * q + 6]) * inv, __uint_as_float(ov[8 * q + 7]) * inv));
       }
+      tc_fence_before();
+      if (qpos < p.S) p.lse[(int64_t)h * p.n_seq * p.S + row_at] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
     }
-    if (storer) bulk_wait_all();
   }
   tc_fence_before();
   __syncthreads();
@@ -760,6 +810,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) masked_delta_kernel(const __g
       const int64_t row = (int64_t)b * p.S + qpos, T = (int64_t)p.n_seq * p.S;
       const int lo = in ? p.plan.lo[row] : 0, hi = in ? p.plan.hi[row] : 0;
       const float lse = lo < hi ? p.lse[(int64_t)h * T + row] * kLog2e : 0.f;
+      // a row that sees one key: P = 1 and D = dP to the bit, so that its dS is 0 and not a rounding's rest
+      const float single = hi - lo == 1 ? 0.f : 1.f;
       const float slope = BIAS ? p.slopes[h] * kLog2e : 0.f;
       // the accumulator's rows of this unit: 128 x hd fp32, a row per 16 threads
       for (int k = threadIdx.x - 64; k < 128 * (p.hd / 4); k += kSoftThreads) {
@@ -788,13 +840,17 @@ __global__ void __launch_bounds__(kAttnThreads, 1) masked_delta_kernel(const __g
         const int c0 = j * kTile + 64 * half;  // key of this thread's first column
         const bool whole = lo <= c0 && c0 + 64 <= hi;
         const float away = (float)(qpos - c0);
+        if (CAP) {
+          tanh32(sv[0], p.cap_mul);
+          tanh32(sv[1], p.cap_mul);
+        }
 #pragma unroll
         for (int c = 0; c < 2; ++c)
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
             const int col = 32 * c + e;
-            float pe = ex2(score<CAP, BIAS>(__uint_as_float(sv[c][e]), p.mul, p.cap_log2, slope, away - (float)col) - lse);
-            if (!whole && (c0 + col < lo || c0 + col >= hi)) pe = 0.f;
+            float pe = ex2((score<BIAS>(sv[c][e], p.mul, slope, away - (float)col) - lse));
+            if (!whole) pe = c0 + col < lo || c0 + col >= hi ? 0.f : single == 0.f ? 1.f : pe;
             sum[e & 1] = fmaf(pe, __uint_as_float(dv[c][e]), sum[e & 1]);
           }
       }
@@ -1024,6 +1080,7 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1) masked_bwd_kernel(const __
           tmem_ld32(tmem + lane_off + 128 + 32 * c, dp);
           tmem_ld_wait_regs(st);
           regs_after_wait(dp);
+          if (CAP) tanh32(st, p.cap_mul);
           uint32_t pw[16], dw[16];
 #pragma unroll
           for (int i = 0; i < 32; i += 4) {
@@ -1034,17 +1091,14 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1) masked_bwd_kernel(const __
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const int col = 32 * c + i + e;
-              float grad;  // d (capped score) / d (score)
-              const float y = score_grad<CAP, BIAS>(__uint_as_float(st[i + e]), p.mul, p.cap_log2, slope,
-                                                    away + (float)col, grad);
-              float pe = ex2(y - lv[e]);
+              float pe = ex2(score<BIAS>(st[i + e], p.mul, slope, away + (float)col) - lv[e]);
               if (decltype(masked)::value) {
                 const int2 see = see_it[col];
                 pe = (see.x <= kpos && kpos < see.y) ? pe : 0.f;
               }
               pv[e] = pe;
               dv4[e] = pe * (__uint_as_float(dp[i + e]) - dl[e]);
-              if (CAP) dv4[e] *= grad;
+              if (CAP) dv4[e] *= fmaf(-__uint_as_float(st[i + e]), __uint_as_float(st[i + e]), 1.f);
             }
             pw[i / 2] = pack2(pv[0], pv[1]);
             pw[i / 2 + 1] = pack2(pv[2], pv[3]);
@@ -1129,7 +1183,7 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1) masked_bwd_kernel(const __
 
 // Shared memory of a launch: sized for head_dim 128 whatever the head dimension, which also keeps
 // one CTA per SM (each CTA allocates all 512 TMEM columns).
-int fwd_smem() { return 1024 + 2 * kChunk + 8 * kChunk + 2 * kChunk + 2 * kChunk + 1024 + 256; }
+int fwd_smem() { return 1024 + 12 * kChunk + 256; }
 int bwd_smem() { return 1024 + 8 * kChunk + 4 * kChunk + 2 * 256 * 4 + 256 * 8 + 256; }
 
 // Raises a kernel's shared-memory limit once per device.
@@ -1157,8 +1211,7 @@ int fwd_launch(const MaskedFwdParams& p, cudaStream_t s) {
   if (!smem_limit(masked_fwd_kernel<CAP, BIAS>, fwd_smem(), done)) return 5;
   const int n_sm = sm_count();
   if (n_sm <= 0) return 5;
-  const int64_t n_units = plan_tiles(p.n_seq, p.S) * p.hq;
-  launch_kernel(masked_fwd_kernel<CAP, BIAS>, (unsigned)std::min<int64_t>(n_units, n_sm), kAttnThreads, fwd_smem(), s, p);
+  launch_kernel(masked_fwd_kernel<CAP, BIAS>, (unsigned)std::min(p.n_units, n_sm), kFwdThreads, fwd_smem(), s, p);
   if (launch_failed("sl_attention_masked")) return 5;
   note_launch();
   return 0;
@@ -1189,12 +1242,12 @@ int bwd_launch(const MaskedBwdParams& p, cudaStream_t s) {
   return 0;
 }
 
-// mul and cap_log2 of score()
-void score_constants(const MaskedArgs& a, float* scale, float* mul, float* cap_log2) {
+// scale, mul of score() and cap_mul of tanh32()
+void score_constants(const MaskedArgs& a, float* scale, float* mul, float* cap_mul) {
   const double sc = a.scale > 0.f ? (double)a.scale : 1.0 / std::sqrt((double)a.hd);
   *scale = (float)sc;
-  *mul = (float)(a.cap > 0.f ? 2.0 * 1.4426950408889634 * sc / a.cap : 1.4426950408889634 * sc);
-  *cap_log2 = (float)(a.cap * 1.4426950408889634);
+  *mul = (float)(1.4426950408889634 * (a.cap > 0.f ? (double)a.cap : sc));
+  *cap_mul = a.cap > 0.f ? (float)(sc / a.cap) : 0.f;
 }
 
 }  // namespace
@@ -1224,8 +1277,13 @@ int attention_masked_fwd(const MaskedArgs& a, cudaStream_t s) {
   MaskedFwdParams p;
   memset(&p, 0, sizeof(p));
   if (!head_map(&p.qmap, a.q, a.ldq, a.n_seq, a.S, a.hq, a.hd) || !head_map(&p.kmap, a.k, a.ldk, a.n_seq, a.S, a.hkv, a.hd) ||
-      !head_map(&p.vmap, a.v, a.ldv, a.n_seq, a.S, a.hkv, a.hd) || !head_map(&p.omap, a.o, a.ldo, a.n_seq, a.S, a.hq, a.hd))
+      !head_map(&p.vmap, a.v, a.ldv, a.n_seq, a.S, a.hkv, a.hd))
     return 2;
+  p.o = static_cast<__nv_bfloat16*>(a.o);
+  p.ldo = a.ldo;
+  p.pair_heads = (a.hq / a.hkv) % 2 == 0;
+  const int n_t = (a.S + kTile - 1) / kTile;
+  p.n_units = p.pair_heads ? a.n_seq * n_t * (a.hq / 2) : a.n_seq * ((n_t + 1) / 2) * a.hq;
   carve_plan(const_cast<void*>(a.plan), a.n_seq, a.S, &p.plan);
   p.slopes = a.slopes;
   p.lse = const_cast<float*>(a.lse);
@@ -1236,7 +1294,7 @@ int attention_masked_fwd(const MaskedArgs& a, cudaStream_t s) {
   p.hd = a.hd;
   p.nd = (a.hd + 63) / 64;
   float scale;
-  score_constants(a, &scale, &p.mul, &p.cap_log2);
+  score_constants(a, &scale, &p.mul, &p.cap_mul);
   p.err = a.err;
   if (a.cap > 0.f) return a.slopes ? fwd_launch<true, true>(p, s) : fwd_launch<true, false>(p, s);
   return a.slopes ? fwd_launch<false, true>(p, s) : fwd_launch<false, false>(p, s);
@@ -1266,14 +1324,14 @@ int attention_masked_bwd(const MaskedArgs& a, cudaStream_t s) {
   p.hkv = a.hkv;
   p.hd = a.hd;
   p.nd = (a.hd + 63) / 64;
-  score_constants(a, &p.scale, &p.mul, &p.cap_log2);
+  score_constants(a, &p.scale, &p.mul, &p.cap_mul);
   p.err = a.err;
   MaskedDeltaParams d;
   memset(&d, 0, sizeof(d));
   d.qmap = p.qmap, d.kmap = p.kmap, d.vmap = p.vmap, d.domap = p.domap;
   d.plan = p.plan, d.slopes = p.slopes, d.lse = p.lse, d.delta = delta, d.dq_acc = dq_acc;
   d.n_seq = p.n_seq, d.S = p.S, d.hq = p.hq, d.hkv = p.hkv, d.hd = p.hd, d.nd = p.nd;
-  d.mul = p.mul, d.cap_log2 = p.cap_log2, d.err = p.err;
+  d.mul = p.mul, d.cap_mul = p.cap_mul, d.err = p.err;
   int rc = a.cap > 0.f ? (a.slopes ? delta_launch<true, true>(d, s) : delta_launch<true, false>(d, s))
                        : (a.slopes ? delta_launch<false, true>(d, s) : delta_launch<false, false>(d, s));
   if (rc) return rc;

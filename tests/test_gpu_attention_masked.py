@@ -155,6 +155,18 @@ def test_nothing_seen_at_all_and_defaults():
     hold(got, reference(q, k, v, do, zero, pos + 1, n_seq, hq, hkv, hd))
 
 
+@pytest.mark.parametrize("S,hd,kw", [(1, 8, {}), (77, 64, {}), (300, 128, dict(softcap=5.0)), (130, 96, dict(slopes=True))])
+def test_rows_of_one_key_have_no_score_gradient(S, hd, kw):
+    """P = 1, o = v, dq = dk = 0 exactly (not a rounding's rest), dv = do."""
+    q, k, v, do = inputs(1, S, 2, 2, hd, S)
+    at = torch.arange(S, dtype=torch.int32, device=DEV)
+    if kw.get("slopes"):
+        kw = dict(slopes=torch.tensor([0.5, 0.25], device=DEV))
+    got = call(q, k, v, do, plan_of(at, at + 1, 1, S), 1, 2, 2, hd, **kw)
+    assert (got["dq"] == 0).all() and (got["dk"] == 0).all() and torch.equal(got["o"], v)
+    hold(got, reference(q, k, v, do, at, at + 1, 1, 2, 2, hd, kw.get("softcap", 0.0), kw.get("slopes")))
+
+
 def test_large_scores_and_slopes():
     """Scores of several hundred (one key takes all) and slopes that leave only near keys."""
     n_seq, S, hq, hkv, hd = 1, 400, 4, 2, 64
