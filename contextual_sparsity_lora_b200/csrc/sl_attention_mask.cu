@@ -42,7 +42,8 @@ struct Plan {
   const int4* q_range;
   const int2* k_range;
   const int2* q2_range;  // key tiles of query tiles 2 i and 2 i + 1 together (sequence * ceil(n_t / 2) + i)
-  const int32_t *q_order, *k_order, *q2_order;  // tiles (sequence * n_t + tile) and pairs, the longest ranges first
+  // {tile or pair, range x, range y, 0}, the longest ranges first
+  const int4 *q_order, *k_order, *q2_order;
 };
 
 int64_t plan_tiles(int n_seq, int S) { return (int64_t)n_seq * ((S + kTile - 1) / kTile); }
@@ -63,11 +64,11 @@ int64_t carve_plan(void* buf, int n_seq, int S, Plan* out) {
   p.hi = reinterpret_cast<int32_t*>(take(T * 4));
   p.q_range = reinterpret_cast<int4*>(take(nt * 16));
   p.k_range = reinterpret_cast<int2*>(take(nt * 8));
-  p.q_order = reinterpret_cast<int32_t*>(take(nt * 4));
-  p.k_order = reinterpret_cast<int32_t*>(take(nt * 4));
+  p.q_order = reinterpret_cast<int4*>(take(nt * 16));
+  p.k_order = reinterpret_cast<int4*>(take(nt * 16));
   const int64_t n2 = (int64_t)n_seq * (((S + kTile - 1) / kTile + 1) / 2);
   p.q2_range = reinterpret_cast<int2*>(take(n2 * 8));
-  p.q2_order = reinterpret_cast<int32_t*>(take(n2 * 4));
+  p.q2_order = reinterpret_cast<int4*>(take(n2 * 16));
   if (out) *out = p;
   return off;
 }
@@ -126,7 +127,7 @@ __device__ void plan_rows(const Plan& p, const int32_t* row_lo, const int32_t* r
 // Tiles by the lengths of their ranges, the longest first (equal ones in no set order: the order only
 // says when a unit starts). hist: n_t + 2 counters.
 template <typename R>
-__device__ void plan_order(const R* range, int64_t n, int n_t, int32_t* order, int32_t* hist, int32_t* carry) {
+__device__ void plan_order(const R* range, int64_t n, int n_t, int4* order, int32_t* hist, int32_t* carry) {
   for (int i = threadIdx.x; i < n_t + 2; i += kPlanThreads) hist[i] = 0;
   __syncthreads();
   for (int64_t at = threadIdx.x; at < n; at += kPlanThreads) atomicAdd(&hist[n_t - (range[at].y - range[at].x)], 1);
@@ -152,8 +153,10 @@ __device__ void plan_order(const R* range, int64_t n, int n_t, int32_t* order, i
     if (threadIdx.x == kPlanThreads - 1) *carry = before + inc;
     __syncthreads();
   }
-  for (int64_t at = threadIdx.x; at < n; at += kPlanThreads)
-    order[atomicAdd(&hist[n_t - (range[at].y - range[at].x)], 1)] = (int32_t)at;
+  for (int64_t at = threadIdx.x; at < n; at += kPlanThreads) {
+    const R v = range[at];
+    order[atomicAdd(&hist[n_t - (v.y - v.x)], 1)] = make_int4((int)at, v.x, v.y, 0);
+  }
   __syncthreads();
 }
 
@@ -187,9 +190,9 @@ __device__ void plan_tiles_and_order(const Plan& p, int n_seq, int S, int32_t* h
     const_cast<int2*>(p.q2_range)[at] = v;
   }
   __syncthreads();
-  plan_order(p.q2_range, n2, n_t, const_cast<int32_t*>(p.q2_order), hist, carry);
-  plan_order(p.q_range, n, n_t, const_cast<int32_t*>(p.q_order), hist, carry);
-  plan_order(p.k_range, n, n_t, const_cast<int32_t*>(p.k_order), hist, carry);
+  plan_order(p.q2_range, n2, n_t, const_cast<int4*>(p.q2_order), hist, carry);
+  plan_order(p.q_range, n, n_t, const_cast<int4*>(p.q_order), hist, carry);
+  plan_order(p.k_range, n, n_t, const_cast<int4*>(p.k_order), hist, carry);
   if (threadIdx.x < 3) const_cast<int32_t*>(p.header)[threadIdx.x] = threadIdx.x == 0 ? kPlanMagic : threadIdx.x == 1 ? n_seq : S;
 }
 
@@ -220,31 +223,99 @@ __device__ __forceinline__ float rcp(float x) {
   return y;
 }
 
-// tanh of 32 raw products times mul (= scale / cap), in place. Up to 0.75 an odd polynomial (a least-maximum
+// Two fp32 values in a 64-bit register: multiply-adds, sums and products of both in one instruction, which halves
+// the issue slots of the element-wise work (each element counts: a tile has 128 per thread and only two warps share a
+// scheduler).
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 pk(float a, float b) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ f2 pku(uint32_t a, uint32_t b) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ f2 both(float a) { return pk(a, a); }
+__device__ __forceinline__ void un(f2 v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ void unu(f2 v, uint32_t& a, uint32_t& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=r"(a), "=r"(b) : "l"(v));
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+  f2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float min3(float a, float b, float c) {
+  float r;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// tanh of N raw products times mul (= scale / cap), in place. Up to 0.75 an odd polynomial (a least-maximum
 // fit of tanh(u) / u in u^2, relative error 3e-8, 1.6e-7 with fp32 arithmetic): 7 multiply-adds, and small
 // scores keep their relative exactness. Above, for the whole warp: 1 - 2 / (2^(2 log2(e) u) + 1), error
 // about 1e-7 of 1 (2^x = inf gives 1, 0 gives -1), on the exponential unit, which the softmax needs too.
 // tanh.approx would be off by 5e-4 of the value.
-__device__ __forceinline__ void tanh32(uint32_t (&v)[32], float mul) {
-  float top = 0.f;
+template <int N>
+__device__ __forceinline__ void tanh_n(uint32_t (&v)[N], float mul) {
+  float hi = 0.f, lo = 0.f;
 #pragma unroll
-  for (int e = 0; e < 32; ++e) top = fmaxf(top, fabsf(__uint_as_float(v[e])));
-  if (__any_sync(0xffffffffu, !(top * mul <= 0.75f))) {
-    const float mul2 = mul * (2.f * kLog2e);
+  for (int e = 0; e < N; e += 2) {
+    hi = max3(hi, __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+    lo = min3(lo, __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+  }
+  if (__any_sync(0xffffffffu, !(fmaxf(hi, -lo) * mul <= 0.75f))) {
+    const float mul2x = mul * (2.f * kLog2e);
 #pragma unroll
-    for (int e = 0; e < 32; ++e)
-      v[e] = __float_as_uint(fmaf(-2.f, rcp(ex2(__uint_as_float(v[e]) * mul2) + 1.f), 1.f));
+    for (int e = 0; e < N; ++e)
+      v[e] = __float_as_uint(fmaf(-2.f, rcp(ex2(__uint_as_float(v[e]) * mul2x) + 1.f), 1.f));
   } else {
+    const f2 m = both(mul), c5 = both(-0.0047162557f), c4 = both(0.019582905f), c3 = both(-0.053344428f),
+             c2 = both(0.13325407f), c1 = both(-0.33332959f), c0 = both(1.f);
 #pragma unroll
-    for (int e = 0; e < 32; ++e) {
-      const float u = __uint_as_float(v[e]) * mul, w = u * u;
-      float r = fmaf(w, -0.0047162557f, 0.019582905f);
-      r = fmaf(w, r, -0.053344428f);
-      r = fmaf(w, r, 0.13325407f);
-      r = fmaf(w, r, -0.33332959f);
-      v[e] = __float_as_uint(u * fmaf(w, r, 1.f));
+    for (int e = 0; e < N; e += 2) {
+      const f2 u = mul2(pku(v[e], v[e + 1]), m), w = mul2(u, u);
+      f2 r = fma2(w, c5, c4);
+      r = fma2(w, r, c3);
+      r = fma2(w, r, c2);
+      r = fma2(w, r, c1);
+      unu(mul2(u, fma2(w, r, c0)), v[e], v[e + 1]);
     }
   }
+}
+
+// -inf outside columns [first, end)
+__device__ __forceinline__ void mask32(uint32_t (&v)[32], int first, int end) {
+  const int a = min(max(first, 0), 32), b = min(max(end, 0), 32);
+  const uint32_t see = a >= b ? 0u : (0xffffffffu << a) & (0xffffffffu >> (32 - b));
+#pragma unroll
+  for (int e = 0; e < 32; ++e)
+    if (!(see & (1u << e))) v[e] = 0xff800000u;
+}
+
+__device__ __forceinline__ float max32(const uint32_t (&v)[32]) {
+  float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+  for (int e = 0; e < 32; e += 2)
+    mx[(e >> 1) & 3] = max3(mx[(e >> 1) & 3], __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+  return fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
 }
 
 // The score in powers of two from a raw product (with a cap: its tanh) v: mul = log2(e) scale, or log2(e) cap. away:
@@ -253,6 +324,54 @@ template <bool BIAS>
 __device__ __forceinline__ float score(uint32_t v, float mul, float slope, float away) {
   const float y = __uint_as_float(v) * mul;
   return BIAS ? fmaf(-slope, fabsf(away), y) : y;
+}
+
+// Biased scores of 32 raw products (or their tanh) in place, powers of two: v mul - slope |away - e|. one_side: no
+// key of the warp's tile lies behind its query (away - e >= 0), so the distance needs no absolute value.
+__device__ __forceinline__ void bias32(uint32_t (&v)[32], float mul, float slope, float away, bool one_side) {
+  const f2 m = both(mul), s = both(slope), a = both(-slope * away);
+  if (one_side) {
+#pragma unroll
+    for (int e = 0; e < 32; e += 2)
+      unu(fma2(pku(v[e], v[e + 1]), m, fma2(s, pk((float)e, (float)(e + 1)), a)), v[e], v[e + 1]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(score<true>(v[e], mul, slope, away - (float)e));
+  }
+}
+
+// D[tmem] (+)= A[tmem] * B[smem desc]^T: A is 128 rows (lanes) of 16 bf16, two per 32-bit column.
+__device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                             uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// The 16-element steps of one product, unrolled: the descriptors of a step are the first one's plus a constant (address
+// fields count 16 bytes). One thread issues them all, and with descriptors built anew in a loop over the steps its own
+// instructions, not the tensor cores, set the pace.
+// A and B K-major tiles (N steps over the head dimension, four per 16 KB chunk):
+template <int N>
+__device__ __forceinline__ void mma_kk(uint32_t d, uint64_t a, uint64_t b, uint32_t id) {
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    const uint32_t off = (k >> 2) * (kChunk >> 4) + (k & 3) * 2;
+    umma_bf16(d, a + off, b + off, id, k > 0 ? 1u : 0u);
+  }
+}
+__device__ __forceinline__ void mma_kk_nd(int nd, uint32_t d, uint64_t a, uint64_t b, uint32_t id) {
+  if (nd == 2) mma_kk<8>(d, a, b, id);
+  else mma_kk<4>(d, a, b, id);
+}
+// A in TMEM (8 columns per step), B MN-major (16 token rows, 2 KB, per step); N steps over tokens:
+template <int N>
+__device__ __forceinline__ void mma_tm(uint32_t d, uint32_t a, uint64_t b, uint32_t id, bool add) {
+#pragma unroll
+  for (int k = 0; k < N; ++k) umma_bf16_ts(d, a + 8 * k, b + k * 128, id, (k > 0 || add) ? 1u : 0u);
 }
 
 struct MaskedFwdParams {
@@ -264,7 +383,7 @@ struct MaskedFwdParams {
   float* lse;                    // [n_q_heads][n_seq * seq_len]
   int32_t n_seq, S, hq, hkv, hd, nd;
   int32_t n_units, pair_heads;   // pair_heads: the streams are two heads, else two query tiles
-  float mul, cap_mul;            // see score() and tanh32()
+  float mul, cap_mul;            // see score() and tanh_n()
   int* err;
 };
 
@@ -326,84 +445,87 @@ __device__ __forceinline__ bool bar_and_bwd(bool ok) {
 
 // Persistent CTAs, one per SM, over units of two streams that share their keys and values: two heads of a group at one
 // tile of 128 queries (an even number of heads per group: the streams see the same key tiles), else two
-// neighbouring query tiles of one head. Warp 0 loads each stream's Q and, for both, K and V (two stages each); warp 1
-// issues the products; warps 4-7 and 8-11 are the softmax of stream 0 and 1, a query row per thread (they take over the
-// registers that the first four warps give up). While one
-// stream's softmax runs, the tensor cores work for the other: O_x += P_x V of step t, then S_x = Q_x K^T of step t + 1, for
-// x = 0 and 1 in turn. P replaces S in TMEM (bf16, the first operand of P V), so it never passes through shared
-// memory, and since P V of step t stands before S of step t + 1 in the tensor pipe, a softmax that sees S
-// may rescale O without a further wait. TMEM: S_x / P_x at 128 x, O_x at 256 + 128 x.
+// neighbouring query tiles of one head. Warp 0 loads each stream's Q and, for both, K and V (two stages each); warps 1 and 2
+// issue the products of stream 0 and 1; warps 4-7 and 8-11 are the softmax of stream 0 and 1, a query row per thread. A step is
+// half a key tile (64 keys): each stream has two S buffers in TMEM, so while the softmax works on step h, S of step h + 1
+// is there or on its way, and the order of a stream's products is O_x += P_x V of step h, S_x of step h + 2 (into the same
+// buffer). With whole tiles and one S buffer per stream the softmax waited for a P V and an S in
+// each step, 40% of its time. P replaces S in TMEM (bf16, the first operand of P V) and never passes through
+// shared memory. Each stream has an issuing warp of its own: one thread for both is busy with waits and commits for as long
+// as with products, and the tensor cores, which queue about five, run dry. TMEM: S_x / P_x of step h at 128 x + 64 (h & 1), O_x at 256 + 128 x.
 struct Unit {
   int qt0, qt1, h0, h1, b, j0, j1;
   __device__ __forceinline__ int qt(int x) const { return x ? qt1 : qt0; }
   __device__ __forceinline__ int h(int x) const { return x ? h1 : h0; }
 };
 
+// Unit number of a CTA's i-th unit: the units stand longest first, and a CTA goes through them there and back, so
+// that every CTA gets long and short ones.
+__device__ __forceinline__ int unit_number(int i) {
+  return (i & 1) ? (i + 1) * (int)gridDim.x - 1 - (int)blockIdx.x : i * (int)gridDim.x + (int)blockIdx.x;
+}
+
 __device__ __forceinline__ Unit unit_of(const MaskedFwdParams& p, int u) {
   Unit r;
   if (p.pair_heads) {
     const int n_qt = (p.S + kTile - 1) / kTile, half = p.hq >> 1;
-    const int at = p.plan.q_order[u / half];
-    const int4 range = p.plan.q_range[at];
-    r.b = at / n_qt;
-    r.qt0 = r.qt1 = at % n_qt;
+    const int4 e = p.plan.q_order[u / half];
+    r.b = e.x / n_qt;
+    r.qt0 = r.qt1 = e.x % n_qt;
     r.h0 = 2 * (u % half);
     r.h1 = r.h0 + 1;
-    r.j0 = range.x;
-    r.j1 = range.y;
+    r.j0 = e.y;
+    r.j1 = e.z;
   } else {
     const int n_t2 = ((p.S + kTile - 1) / kTile + 1) >> 1;
-    const int at = p.plan.q2_order[u / p.hq];
-    const int2 range = p.plan.q2_range[at];
-    r.b = at / n_t2;
-    r.qt0 = 2 * (at % n_t2);
+    const int4 e = p.plan.q2_order[u / p.hq];
+    r.b = e.x / n_t2;
+    r.qt0 = 2 * (e.x % n_t2);
     r.qt1 = r.qt0 + 1;
     r.h0 = r.h1 = u % p.hq;
-    r.j0 = range.x;
-    r.j1 = range.y;
+    r.j0 = e.y;
+    r.j1 = e.z;
   }
   return r;
 }
 
-// Steps of a CTA in order: (unit, key tile), the units being blockIdx.x, blockIdx.x + gridDim.x, ...
+// Steps of a CTA in order: (unit, key tile, half). Keys run from the last to the first: with a bias by distance the
+// largest scores mostly come first, and O is rescaled rarely (from the first key on, steep slopes rescaled it in every
+// step: 1076 instead of 758 us at 8192 tokens). The next unit is looked up while this one runs.
 struct Walk {
-  Unit un;
-  int u, i, j, t;  // unit, its number in this CTA, key tile, number of the step in this CTA
-  bool live;
+  Unit un, nx;
+  int i, j, t;  // number of the unit in this CTA, key tile, number of the step in this CTA (t & 1: the tile's half)
+  bool live, more;
+  __device__ __forceinline__ void look(const MaskedFwdParams& p) {
+    const int u = unit_number(i + 1);
+    more = u < p.n_units;
+    if (more) nx = unit_of(p, u);
+  }
   __device__ __forceinline__ void start(const MaskedFwdParams& p, bool ok) {
-    u = blockIdx.x;
     i = t = 0;
-    live = ok && u < p.n_units;
+    live = ok && unit_number(0) < p.n_units;
     if (live) {
-      un = unit_of(p, u);
-      j = un.j0;
+      un = unit_of(p, unit_number(0));
+      j = un.j1 - 1;
+      look(p);
     }
   }
-  __device__ __forceinline__ bool first() const { return j == un.j0; }
-  __device__ __forceinline__ bool last() const { return j == un.j1 - 1; }
+  __device__ __forceinline__ bool first() const { return j == un.j1 - 1 && !(t & 1); }
+  __device__ __forceinline__ bool last() const { return j == un.j0 && (t & 1); }
+  __device__ __forceinline__ int stage() const { return (t >> 1) & 1; }       // of K and V
+  __device__ __forceinline__ uint32_t phase() const { return (t >> 2) & 1; }  // of that stage
   __device__ __forceinline__ void next(const MaskedFwdParams& p) {
-    ++t;
-    if (++j < un.j1) return;
-    u += gridDim.x;
-    ++i;
-    live = u < p.n_units;
+    if (++t & 1) return;
+    if (--j >= un.j0) return;
+    live = more;
     if (live) {
-      un = unit_of(p, u);
-      j = un.j0;
+      ++i;
+      un = nx;
+      j = un.j1 - 1;
+      look(p);
     }
   }
 };
-
-// D[tmem] (+)= A[tmem] * B[smem desc]^T: A is 128 rows (lanes) of 16 bf16, two per 32-bit column.
-__device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                             uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
 
 // Each thread of the warp writes 16 consecutive 32-bit columns of its TMEM lane.
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
@@ -413,6 +535,39 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
+}
+
+// Stores 32 bf16 columns of 32 rows, a row per lane (w: 16 packed pairs), row `lane` at out + lane * ld: four lanes trade
+// 16-byte pieces (a 4 x 4 transposition) so that each store writes 64 consecutive bytes of eight rows instead of 16
+// bytes of 32. Rows from n_rows on and columns from n_cols (a multiple of 8) on are not written.
+__device__ __forceinline__ void store_rows32(__nv_bfloat16* out, int64_t ld, uint32_t (&w)[16], int n_rows, int n_cols) {
+  const int lane = threadIdx.x & 31, sub = lane & 3;
+  // pieces i of this row; stage 1 trades pieces 0 <-> 1, 2 <-> 3 with lane ^ 1, stage 2 pieces 0 <-> 2, 1 <-> 3 with lane ^ 2
+#pragma unroll
+  for (int st = 1; st <= 2; st <<= 1) {
+    const bool upper = (sub & st) != 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i & st) continue;
+      const int k = i | st;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const uint32_t give = upper ? w[4 * i + q] : w[4 * k + q];
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, give, st);
+        if (upper) w[4 * i + q] = got;
+        else w[4 * k + q] = got;
+      }
+    }
+  }
+  // now piece i of this lane is piece `sub` of row (lane & ~3) + i
+  if (8 * sub < n_cols) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = (lane & ~3) + i;
+      if (row < n_rows)
+        *reinterpret_cast<uint4*>(out + row * ld + 8 * sub) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    }
+  }
 }
 
 template <bool CAP, bool BIAS>
@@ -430,11 +585,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1) masked_fwd_kernel(const __grid
   uint64_t* k_empty = bars + 6;    // [2]
   uint64_t* v_full = bars + 8;     // [2]
   uint64_t* v_empty = bars + 10;   // [2]
-  uint64_t* s_full = bars + 12;    // [2] by stream
-  uint64_t* p_full = bars + 14;    // [2]
-  uint64_t* o_full = bars + 16;    // [2]
-  uint64_t* drain = bars + 18;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 19);
+  uint64_t* s_full = bars + 12;    // [2 x + buffer]
+  uint64_t* p_full = bars + 16;    // [2 x + buffer]
+  uint64_t* pv_done = bars + 20;   // [2] by stream
+  uint64_t* drain = bars + 22;     // [2] by stream
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 24);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -444,16 +599,22 @@ __global__ void __launch_bounds__(kFwdThreads, 1) masked_fwd_kernel(const __grid
       mbar_init(&q_full[s], 1);
       mbar_init(&q_empty[s], 1);
       mbar_init(&k_full[s], 1);
-      mbar_init(&k_empty[s], 1);
+      mbar_init(&k_empty[s], 2);  // both streams
       mbar_init(&v_full[s], 1);
-      mbar_init(&v_empty[s], 1);
+      mbar_init(&v_empty[s], 2);
+      mbar_init(&pv_done[s], 1);
+    }
+    for (int s = 0; s < 4; ++s) {
       mbar_init(&s_full[s], 1);
       mbar_init(&p_full[s], 128);
-      mbar_init(&o_full[s], 1);
     }
-    mbar_init(drain, 1);
+    mbar_init(&drain[0], 1);
+    mbar_init(&drain[1], 1);
     *abort_flag = 0;
     fence_barrier_init();
+    tma_prefetch_desc(&p.qmap);
+    tma_prefetch_desc(&p.kmap);
+    tma_prefetch_desc(&p.vmap);
   }
   if (warp == 1) {
     tmem_alloc(tmem_slot, 512);
@@ -466,18 +627,17 @@ __global__ void __launch_bounds__(kFwdThreads, 1) masked_fwd_kernel(const __grid
   pdl_wait();
   const bool plan_ok = plan_fits(p.plan, p.n_seq, p.S, p.err);
 
-  if (warp < 4) {
-    // 384 threads start with 168 registers each: 72 here and 216 in the two softmax groups make the same sum
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if (warp == 0 && lane == 0) {
+  if (warp == 0) {
+    if (lane == 0) {
       Walk w;
       int nq = 0, nk = 0, nv = 0;  // loads issued (Q: of both streams)
       for (w.start(p, plan_ok); w.live; w.next(p)) {
-        const int g = w.un.h0 / hpg, s = w.t & 1;
+        if (w.t & 1) continue;  // a tile's second half came with its first
+        const int g = w.un.h0 / hpg, s = w.stage();
         if (w.first()) {
           bool ok = true;
           for (int x = 0; x < 2 && ok; ++x) {
-            if (w.i > 0) ok = mbar_wait(&q_empty[x], (w.i - 1) & 1, abort_flag, p.err, DEV_TIMEOUT_PRODUCER);
+            if (w.i > 0) ok = mbar_wait_soon(&q_empty[x], (w.i - 1) & 1, abort_flag, p.err, DEV_TIMEOUT_PRODUCER);
             if (!ok) break;
             mbar_arrive_expect_tx(&q_full[x], nd * kChunk);
             for (int c = 0; c < nd; ++c)
@@ -486,12 +646,12 @@ __global__ void __launch_bounds__(kFwdThreads, 1) masked_fwd_kernel(const __grid
           }
           if (!ok) break;
         }
-        if (!mbar_wait(&k_empty[s], ((w.t >> 1) & 1) ^ 1, abort_flag, p.err, DEV_TIMEOUT_PRODUCER)) break;
+        if (!mbar_wait_soon(&k_empty[s], w.phase() ^ 1, abort_flag, p.err, DEV_TIMEOUT_PRODUCER)) break;
         mbar_arrive_expect_tx(&k_full[s], nd * kChunk);
         for (int c = 0; c < nd; ++c)
           tma_load_4d(sk + (2 * s + c) * kChunk, &p.kmap, &k_full[s], 64 * c, g, w.j * kTile, w.un.b);
         ++nk;
-        if (!mbar_wait(&v_empty[s], ((w.t >> 1) & 1) ^ 1, abort_flag, p.err, DEV_TIMEOUT_PRODUCER)) break;
+        if (!mbar_wait_soon(&v_empty[s], w.phase() ^ 1, abort_flag, p.err, DEV_TIMEOUT_PRODUCER)) break;
         mbar_arrive_expect_tx(&v_full[s], nd * kChunk);
         for (int c = 0; c < nd; ++c)
           tma_load_4d(sv + (2 * s + c) * kChunk, &p.vmap, &v_full[s], 64 * c, g, w.j * kTile, w.un.b);
@@ -502,114 +662,140 @@ __global__ void __launch_bounds__(kFwdThreads, 1) masked_fwd_kernel(const __grid
         for (int x = 0; x < 2; ++x) mbar_wait(&q_full[x], (nq - 1) & 1, nullptr, p.err, DEV_TIMEOUT_DRAIN);
       for (int t = max(0, nk - 2); t < nk; ++t) mbar_wait(&k_full[t & 1], (t >> 1) & 1, nullptr, p.err, DEV_TIMEOUT_DRAIN);
       for (int t = max(0, nv - 2); t < nv; ++t) mbar_wait(&v_full[t & 1], (t >> 1) & 1, nullptr, p.err, DEV_TIMEOUT_DRAIN);
-    } else if (warp == 1 && lane == 0) {
-      const uint32_t id_s = idesc_bf16(128, 128, 0, 0);        // S = Q K^T: both K-major over d
+    }
+  } else if (warp == 1 || warp == 2) {
+    if (lane == 0) {
+      const int x = warp - 1;  // stream
+      const uint32_t id_s = idesc_bf16(128, 64, 0, 0);         // S = Q K^T: both K-major over d
       const uint32_t id_pv = idesc_bf16(128, 64 * nd, 0, 1);   // O += P V: P in TMEM, V MN-major
-      auto issue_s = [&](const Walk& w, int x) -> bool {
-        const int s = w.t & 1;
-        if (w.first() && !mbar_wait(&q_full[x], w.i & 1, abort_flag, p.err, DEV_TIMEOUT_MMA)) return false;
-        if (x == 0 && !mbar_wait(&k_full[s], (w.t >> 1) & 1, abort_flag, p.err, DEV_TIMEOUT_MMA)) return false;
+      const uint64_t dq0 = kmajor_desc(smem_u32(sq + 2 * x * kChunk), 0), dk0 = kmajor_desc(smem_u32(sk), 0),
+                     dv0 = mnmajor_desc(smem_u32(sv), 0);
+      auto issue_s = [&](const Walk& w) -> bool {
+        const int s = w.stage(), buf = w.t & 1;
+        if (w.first() && !mbar_wait_soon(&q_full[x], w.i & 1, abort_flag, p.err, DEV_TIMEOUT_MMA)) return false;
+        if (!buf && !mbar_wait_soon(&k_full[s], w.phase(), abort_flag, p.err, DEV_TIMEOUT_MMA)) return false;
         tc_fence_after();
-        const uint32_t aq = smem_u32(sq + 2 * x * kChunk), bk = smem_u32(sk + 2 * s * kChunk);
-        for (int k = 0; k < 4 * nd; ++k)
-          umma_bf16(tmem + 128 * x, kmajor_desc(aq, k), kmajor_desc(bk, k), id_s, k > 0 ? 1u : 0u);
-        umma_commit(&s_full[x]);
+        mma_kk_nd(nd, tmem + 128 * x + 64 * buf, dq0,
+                  dk0 + s * (2 * kChunk >> 4) + (buf ^ 1) * (kChunk / 2 >> 4), id_s);
+        umma_commit(&s_full[2 * x + buf]);
         if (w.last()) umma_commit(&q_empty[x]);
-        if (x == 1) umma_commit(&k_empty[s]);
+        if (buf) umma_commit(&k_empty[s]);
         return true;
       };
-      auto issue_pv = [&](const Walk& w, int x) -> bool {
-        const int s = w.t & 1;
-        if (!mbar_wait(&p_full[x], w.t & 1, abort_flag, p.err, DEV_TIMEOUT_MMA)) return false;
-        if (x == 0 && !mbar_wait(&v_full[s], (w.t >> 1) & 1, abort_flag, p.err, DEV_TIMEOUT_MMA)) return false;
+      auto issue_pv = [&](const Walk& w) -> bool {
+        const int s = w.stage(), buf = w.t & 1;
+        if (!mbar_wait_soon(&p_full[2 * x + buf], (w.t >> 1) & 1, abort_flag, p.err, DEV_TIMEOUT_MMA)) return false;
+        if (!buf && !mbar_wait_soon(&v_full[s], w.phase(), abort_flag, p.err, DEV_TIMEOUT_MMA)) return false;
         tc_fence_after();
-        const uint32_t bv = smem_u32(sv + 2 * s * kChunk);
-        for (int k = 0; k < 8; ++k)
-          umma_bf16_ts(tmem + 256 + 128 * x, tmem + 128 * x + 8 * k, mnmajor_desc(bv, k), id_pv,
-                       (!w.first() || k > 0) ? 1u : 0u);
-        if (w.last()) umma_commit(&o_full[x]);
-        if (x == 1) umma_commit(&v_empty[s]);
+        mma_tm<4>(tmem + 256 + 128 * x, tmem + 128 * x + 64 * buf, dv0 + s * (2 * kChunk >> 4) + (buf ^ 1) * 512, id_pv,
+                  !w.first());
+        umma_commit(&pv_done[x]);
+        if (buf) umma_commit(&v_empty[s]);
         return true;
       };
-      Walk ws, wp;  // S runs a step ahead of P V
+      Walk ws, wp;  // S runs two steps ahead of P V
       ws.start(p, plan_ok);
-      wp.start(p, plan_ok);
-      bool ok = ws.live && issue_s(ws, 0) && issue_s(ws, 1);
-      if (ok) ws.next(p);
+      wp = ws;
+      bool ok = ws.live;
+      for (int k = 0; k < 2 && ok; ++k) {
+        ok = issue_s(ws);
+        ws.next(p);
+      }
       for (; ok && wp.live; wp.next(p)) {
-        ok = issue_pv(wp, 0) && (!ws.live || issue_s(ws, 0)) && issue_pv(wp, 1) && (!ws.live || issue_s(ws, 1));
+        ok = issue_pv(wp) && (!ws.live || issue_s(ws));
         if (ws.live) ws.next(p);
       }
-      umma_commit(drain);
-      mbar_wait(drain, 0, nullptr, p.err, DEV_TIMEOUT_DRAIN);
+      umma_commit(&drain[x]);
+      mbar_wait(&drain[x], 0, nullptr, p.err, DEV_TIMEOUT_DRAIN);
     }
-  } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-    const int x = (warp >> 2) - 1;                   // stream
+  } else if (warp >= 4) {
+    const int x = warp >= 8;                         // stream
     const int quarter = warp & 3;
     const int r = quarter * 32 + lane;               // query row in the tile = TMEM lane
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
     const uint32_t s_tm = tmem + lane_off + 128 * x, o_tm = s_tm + 256;
-    bool ok = plan_ok;
+    bool ok = plan_ok, more = plan_ok && unit_number(0) < p.n_units;
     int t = 0;
-    for (int u = blockIdx.x, i = 0; ok && u < p.n_units; u += gridDim.x, ++i) {
-      const Unit un = unit_of(p, u);
-      const int qt = un.qt(x), h = un.h(x);
+    Unit me, nx;
+    int lo = 0, hi = 0, nlo = 0, nhi = 0;            // the keys [lo, hi) that this row sees (rows past the sequence: none)
+    auto rows_of = [&](const Unit& w, int& l, int& h) {
+      const int q = w.qt(x) * kTile + r;
+      l = h = 0;
+      if (q < p.S) {
+        l = p.plan.lo[(int64_t)w.b * p.S + q];
+        h = p.plan.hi[(int64_t)w.b * p.S + q];
+      }
+    };
+    if (more) {
+      nx = unit_of(p, unit_number(0));
+      rows_of(nx, nlo, nhi);
+    }
+    for (int i = 0; ok && more; ++i) {
+      me = nx;
+      lo = nlo;
+      hi = nhi;
+      more = unit_number(i + 1) < p.n_units;
+      if (more) nx = unit_of(p, unit_number(i + 1));
+      const int qt = me.qt(x), h = me.h(x);
       const int qpos = qt * kTile + r;               // position in the sequence
-      // the keys [lo, hi) that this row sees (rows past the sequence: none)
-      const int64_t row_at = (int64_t)un.b * p.S + qpos;
-      const int lo = qpos < p.S ? p.plan.lo[row_at] : 0, hi = qpos < p.S ? p.plan.hi[row_at] : 0;
       const float slope = BIAS ? p.slopes[h] * kLog2e : 0.f;
       float m = -INFINITY, l = 0.f;
-      for (int j = un.j0; j < un.j1; ++j, ++t) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&s_full[x], t & 1, abort_flag, p.err, DEV_TIMEOUT_EPILOGUE));
+      for (int k0 = me.j1 * kTile - 64; k0 >= me.j0 * kTile; k0 -= 64, ++t) {
+        const int buf = t & 1;
+        ok = __all_sync(0xffffffffu,
+                        mbar_wait_soon(&s_full[2 * x + buf], (t >> 1) & 1, abort_flag, p.err, DEV_TIMEOUT_EPILOGUE));
         if (!ok) break;
         tc_fence_after();
-        uint32_t s[4][32];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(s_tm + 32 * c, s[c]);
+        uint32_t s[2][32];
+        tmem_ld32(s_tm + 64 * buf, s[0]);
+        tmem_ld32(s_tm + 64 * buf + 32, s[1]);
         tmem_ld_wait_regs(s[0]);
         regs_after_wait(s[1]);
-        regs_after_wait(s[2]);
-        regs_after_wait(s[3]);
         if (CAP) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tanh32(s[c], p.cap_mul);
+          tanh_n(s[0], p.cap_mul);
+          tanh_n(s[1], p.cap_mul);
         }
         // With a bias the score itself is formed here (mul = 1 below), else scores stay raw products
-        const int kbase = j * kTile;
         if (BIAS) {
-          const float away = (float)(qpos - kbase);
+          const bool one_side = qt * kTile + 32 * quarter >= k0 + 63;
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              s[c][e] = __float_as_uint(score<true>(s[c][e], p.mul, slope, away - (float)(32 * c + e)));
+          for (int c = 0; c < 2; ++c) bias32(s[c], p.mul, slope, (float)(qpos - k0 - 32 * c), one_side);
         }
         const float mul = BIAS ? 1.f : p.mul;
-        const int kmin = lo - kbase, kmax = hi - 1 - kbase;  // visible columns of this tile
-        if (__any_sync(0xffffffffu, kmin > 0 || kmax < kTile - 1)) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (32 * c + e < kmin || 32 * c + e > kmax) s[c][e] = __float_as_uint(-INFINITY);
+        if (__any_sync(0xffffffffu, lo > k0 || hi < k0 + 64)) {
+          mask32(s[0], lo - k0, hi - k0);
+          mask32(s[1], lo - k0 - 32, hi - k0 - 32);
         }
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-#pragma unroll
-          for (int e = 0; e < 32; e += 2)
-            mx[(e >> 1) & 3] = fmaxf(mx[(e >> 1) & 3], fmaxf(__uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1])));
-        const float mj = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * mul;
+        const float mj = fmaxf(max32(s[0]), max32(s[1])) * mul;
         // The running maximum moves only when a row's maximum grows by more than 2^8: the exponentials then
         // stay below 256 and O and l keep one common reference, so O is rescaled rarely.
         const float m_cand = fmaxf(m, mj);
         const bool grow = m == -INFINITY || m_cand - m > 8.0f;
         const float m_new = grow ? m_cand : m;
         const float mb = m_new == -INFINITY ? 0.f : m_new;  // a row that has seen nothing yet
-        const float corr = (m == -INFINITY) ? 0.f : (grow ? ex2(m - mb) : 1.f);
-        if (j > un.j0 && __any_sync(0xffffffffu, corr != 1.f)) {
+        const float corr = grow && m != -INFINITY ? ex2(m - mb) : 1.f;  // O and l of a row that saw nothing are 0
+        f2 rs[2] = {0, 0};
+        const f2 mul_2 = both(mul), mb_2 = both(-mb);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t pw[16];
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            float x0, x1;
+            un(fma2(pku(s[c][e], s[c][e + 1]), mul_2, mb_2), x0, x1);
+            x0 = ex2(x0);
+            x1 = ex2(x1);
+            rs[(e >> 1) & 1] = add2(rs[(e >> 1) & 1], pk(x0, x1));
+            pw[e / 2] = pack2(x0, x1);
+          }
+          tmem_st16(s_tm + 64 * buf + 16 * c, pw);
+        }
+        if (k0 < me.j1 * kTile - 64 && __any_sync(0xffffffffu, corr != 1.f)) {
+          // O of the steps before is complete once the last P V is
+          ok = __all_sync(0xffffffffu, mbar_wait_soon(&pv_done[x], (t - 1) & 1, abort_flag, p.err, DEV_TIMEOUT_EPILOGUE));
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll 1
           for (int c = 0; c < 2 * nd; ++c) {
             uint32_t ov[32];
             tmem_ld32(o_tm + 32 * c, ov);
@@ -619,48 +805,39 @@ __global__ void __launch_bounds__(kFwdThreads, 1) masked_fwd_kernel(const __grid
             tmem_st32(o_tm + 32 * c, ov);
           }
         }
-        float rs[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t pw[16];
-#pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            const float e0 = ex2(fmaf(__uint_as_float(s[c][e]), mul, -mb));
-            const float e1 = ex2(fmaf(__uint_as_float(s[c][e + 1]), mul, -mb));
-            rs[(e >> 1) & 3] += e0 + e1;
-            pw[e / 2] = pack2(e0, e1);
-          }
-          tmem_st16(s_tm + 16 * c, pw);
-        }
-        l = l * corr + ((rs[0] + rs[1]) + (rs[2] + rs[3]));
+        float r0, r1;
+        un(add2(rs[0], rs[1]), r0, r1);
+        l = l * corr + (r0 + r1);
         m = m_new;
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(&p_full[x]);
+        mbar_arrive(&p_full[2 * x + buf]);
       }
-      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&o_full[x], i & 1, abort_flag, p.err, DEV_TIMEOUT_EPILOGUE));
       if (!ok) break;
-      // O / l as bf16, each thread its own row; the next unit's first P V waits for this softmax's next P
+      if (more) rows_of(nx, nlo, nhi);
+      // S of the last step says that P V of the third last is done: the last two are waited for one by one (a wait for a
+      // barrier's phase is only right once the phase before it is over)
+      ok = __all_sync(0xffffffffu,
+                      mbar_wait_soon(&pv_done[x], t & 1, abort_flag, p.err, DEV_TIMEOUT_EPILOGUE) &&
+                          mbar_wait_soon(&pv_done[x], (t - 1) & 1, abort_flag, p.err, DEV_TIMEOUT_EPILOGUE));
+      if (!ok) break;
+      // O / l as bf16; the next unit's first P V waits for this softmax's next P
       tc_fence_after();
       const float inv = l == 0.f ? 0.f : 1.f / l;  // a row that sees nothing: o = 0
-      __nv_bfloat16* out = p.o + row_at * p.ldo + (int64_t)h * p.hd;
+      const int64_t row0 = (int64_t)me.b * p.S + qt * kTile + 32 * quarter;  // row of lane 0
+      const int n_rows = p.S - (qt * kTile + 32 * quarter);
+#pragma unroll 1
       for (int c = 0; c < 2 * nd; ++c) {
-        uint32_t ov[32];
+        uint32_t ov[32], w[16];
         tmem_ld32(o_tm + 32 * c, ov);
         tmem_ld_wait_regs(ov);
-        if (qpos >= p.S || 32 * c >= p.hd) continue;
-        const int nv = min(32, p.hd - 32 * c) / 8;
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          if (q < nv)
-            *reinterpret_cast<uint4*>(out + 32 * c + 8 * q) = make_uint4(
-                pack2(__uint_as_float(ov[8 * q]) * inv, __uint_as_float(ov[8 * q + 1]) * inv),
-                pack2(__uint_as_float(ov[8 * q + 2]) * inv, __uint_as_float(ov[8 * q + 3]) * inv),
-                pack2(__uint_as_float(ov[8 * q + 4]) * inv, __uint_as_float(ov[8 * q + 5]) * inv),
-                pack2(__uint_as_float(ov[8 * q + 6]) * inv, __uint_as_float(ov[8 * q + 7]) * inv));
+        for (int e = 0; e < 32; e += 2) w[e / 2] = pack2(__uint_as_float(ov[e]) * inv, __uint_as_float(ov[e + 1]) * inv);
+        store_rows32(p.o + row0 * p.ldo + (int64_t)h * p.hd + 32 * c, p.ldo, w, n_rows, p.hd - 32 * c);
       }
       tc_fence_before();
-      if (qpos < p.S) p.lse[(int64_t)h * p.n_seq * p.S + row_at] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
+      if (qpos < p.S)
+        p.lse[(int64_t)h * p.n_seq * p.S + row0 + lane] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
     }
   }
   tc_fence_before();
@@ -705,13 +882,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1) masked_delta_kernel(const __g
   const int n_units = n_qt * p.n_seq * p.hq;
   const int hpg = p.hq / p.hkv;
   auto unit = [&](int u, int& qt, int& h, int& b, int& j0, int& j1) {
-    const int at = p.plan.q_order[u / p.hq];
-    const int4 range = p.plan.q_range[at];
-    qt = at % n_qt;
-    b = at / n_qt;
+    const int4 e = p.plan.q_order[u / p.hq];
+    qt = e.x % n_qt;
+    b = e.x / n_qt;
     h = u % p.hq;
-    j0 = range.x;
-    j1 = range.y;
+    j0 = e.y;
+    j1 = e.z;
   };
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
@@ -743,7 +919,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) masked_delta_kernel(const __g
       for (int u = blockIdx.x, i = 0; ok && u < n_units; u += gridDim.x, ++i) {
         int qt, h, b, j0, j1;
         unit(u, qt, h, b, j0, j1);
-        if (i > 0 && !mbar_wait(q_empty, (i - 1) & 1, abort_flag, p.err, DEV_TIMEOUT_PRODUCER)) break;
+        if (i > 0 && !mbar_wait_soon(q_empty, (i - 1) & 1, abort_flag, p.err, DEV_TIMEOUT_PRODUCER)) break;
         mbar_arrive_expect_tx(q_full, 2 * nd * kChunk);
         for (int c = 0; c < nd; ++c) {
           tma_load_4d(sq + c * kChunk, &p.qmap, q_full, 64 * c, h, qt * kTile, b);
@@ -752,7 +928,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) masked_delta_kernel(const __g
         ++nq;
         for (int j = j0; j < j1; ++j, ++t) {
           const int s = t & 1;
-          if (!mbar_wait(&kv_empty[s], ((t >> 1) & 1) ^ 1, abort_flag, p.err, DEV_TIMEOUT_PRODUCER)) { ok = false; break; }
+          if (!mbar_wait_soon(&kv_empty[s], ((t >> 1) & 1) ^ 1, abort_flag, p.err, DEV_TIMEOUT_PRODUCER)) { ok = false; break; }
           mbar_arrive_expect_tx(&kv_full[s], 2 * nd * kChunk);
           uint8_t* st = skv + s * 2 * nd * kChunk;
           for (int c = 0; c < nd; ++c) {
@@ -762,8 +938,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) masked_delta_kernel(const __g
         }
       }
       // every copy lands before the CTA may exit
-      if (nq > 0) mbar_wait(q_full, (nq - 1) & 1, nullptr, p.err, DEV_TIMEOUT_DRAIN);
-      for (int k = max(0, t - 2); k < t; ++k) mbar_wait(&kv_full[k & 1], (k >> 1) & 1, nullptr, p.err, DEV_TIMEOUT_DRAIN);
+      if (nq > 0) mbar_wait_soon(q_full, (nq - 1) & 1, nullptr, p.err, DEV_TIMEOUT_DRAIN);
+      for (int k = max(0, t - 2); k < t; ++k) mbar_wait_soon(&kv_full[k & 1], (k >> 1) & 1, nullptr, p.err, DEV_TIMEOUT_DRAIN);
     }
   } else if (warp == 1) {
     if (lane == 0) {
@@ -774,27 +950,25 @@ __global__ void __launch_bounds__(kAttnThreads, 1) masked_delta_kernel(const __g
       for (int u = blockIdx.x, i = 0; ok && u < n_units; u += gridDim.x, ++i) {
         int qt, h, b, j0, j1;
         unit(u, qt, h, b, j0, j1);
-        if (!mbar_wait(q_full, i & 1, abort_flag, p.err, DEV_TIMEOUT_MMA)) break;
+        if (!mbar_wait_soon(q_full, i & 1, abort_flag, p.err, DEV_TIMEOUT_MMA)) break;
         for (int j = j0; j < j1; ++j, ++t) {
           const int s = t & 1;
-          if (!mbar_wait(&kv_full[s], (t >> 1) & 1, abort_flag, p.err, DEV_TIMEOUT_MMA) ||
-              (t >= 2 && !mbar_wait(&s_free[s], ((t - 2) >> 1) & 1, abort_flag, p.err, DEV_TIMEOUT_MMA))) {
+          if (!mbar_wait_soon(&kv_full[s], (t >> 1) & 1, abort_flag, p.err, DEV_TIMEOUT_MMA) ||
+              (t >= 2 && !mbar_wait_soon(&s_free[s], ((t - 2) >> 1) & 1, abort_flag, p.err, DEV_TIMEOUT_MMA))) {
             ok = false;
             break;
           }
           tc_fence_after();
           const uint32_t bk = smem_u32(skv + s * 2 * nd * kChunk), bv = bk + nd * kChunk;
-          for (int k = 0; k < 4 * nd; ++k)
-            umma_bf16(tmem + 256 * s, kmajor_desc(aq, k), kmajor_desc(bk, k), id, k > 0 ? 1u : 0u);
-          for (int k = 0; k < 4 * nd; ++k)
-            umma_bf16(tmem + 256 * s + 128, kmajor_desc(ado, k), kmajor_desc(bv, k), id, k > 0 ? 1u : 0u);
+          mma_kk_nd(nd, tmem + 256 * s, kmajor_desc(aq, 0), kmajor_desc(bk, 0), id);
+          mma_kk_nd(nd, tmem + 256 * s + 128, kmajor_desc(ado, 0), kmajor_desc(bv, 0), id);
           umma_commit(&s_full[s]);
           umma_commit(&kv_empty[s]);
           if (j == j1 - 1) umma_commit(q_empty);
         }
       }
       umma_commit(drain);
-      mbar_wait(drain, 0, nullptr, p.err, DEV_TIMEOUT_DRAIN);
+      mbar_wait_soon(drain, 0, nullptr, p.err, DEV_TIMEOUT_DRAIN);
     }
   } else {
     const int quarter = warp & 3, half = (warp - 2) >> 2;
@@ -822,7 +996,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) masked_delta_kernel(const __g
       float sum[2] = {0.f, 0.f};
       for (int j = j0; j < j1 && ok; ++j, ++t) {
         const int s = t & 1;
-        ok = __all_sync(0xffffffffu, mbar_wait(&s_full[s], (t >> 1) & 1, abort_flag, p.err, DEV_TIMEOUT_EPILOGUE));
+        ok = __all_sync(0xffffffffu, mbar_wait_soon(&s_full[s], (t >> 1) & 1, abort_flag, p.err, DEV_TIMEOUT_EPILOGUE));
         if (!ok) break;
         tc_fence_after();
         uint32_t sv[2][32], dv[2][32];
@@ -841,8 +1015,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) masked_delta_kernel(const __g
         const bool whole = lo <= c0 && c0 + 64 <= hi;
         const float away = (float)(qpos - c0);
         if (CAP) {
-          tanh32(sv[0], p.cap_mul);
-          tanh32(sv[1], p.cap_mul);
+          tanh_n(sv[0], p.cap_mul);
+          tanh_n(sv[1], p.cap_mul);
         }
 #pragma unroll
         for (int c = 0; c < 2; ++c)
@@ -947,9 +1121,9 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1) masked_bwd_kernel(const __
   // (key tile, sequence) in the plan's order, and the query tiles q0 .. q1 - 1 that see any of it (at
   // least one, so that a tile that nobody sees takes the same path and gets zeros)
   const bool plan_ok = plan_fits(p.plan, p.n_seq, p.S, p.err);
-  const int at_tile = plan_ok ? p.plan.k_order[blockIdx.x / p.hkv] : 0;
-  const int kt = at_tile % n_t, b = at_tile / n_t;
-  const int q0 = plan_ok ? p.plan.k_range[at_tile].x : 0, q1 = plan_ok ? p.plan.k_range[at_tile].y : 0;
+  const int4 entry = plan_ok ? p.plan.k_order[blockIdx.x / p.hkv] : make_int4(0, 0, 0, 0);
+  const int kt = entry.x % n_t, b = entry.x / n_t;
+  const int q0 = entry.y, q1 = entry.z;
   const int n_it = hpg * (q1 - q0);  // (query head of the group, query tile)
 
   auto it_head = [&](int it) { return g * hpg + it % hpg; };
@@ -969,18 +1143,18 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1) masked_bwd_kernel(const __
       int issued_do = 0, issued_q = 0;
       for (int it = 0; it < n_it; ++it) {
         const int h = it_head(it), qt = it_qtile(it);
-        if (it > 0 && !mbar_wait(do_empty, (it - 1) & 1, abort_flag, p.err, DEV_TIMEOUT_PRODUCER)) break;
+        if (it > 0 && !mbar_wait_soon(do_empty, (it - 1) & 1, abort_flag, p.err, DEV_TIMEOUT_PRODUCER)) break;
         mbar_arrive_expect_tx(do_full, nd * kChunk);
         for (int c = 0; c < nd; ++c) tma_load_4d(sdo + c * kChunk, &p.domap, do_full, 64 * c, h, qt * kTile, b);
         issued_do = it + 1;
-        if (it > 0 && !mbar_wait(q_empty, (it - 1) & 1, abort_flag, p.err, DEV_TIMEOUT_PRODUCER)) break;
+        if (it > 0 && !mbar_wait_soon(q_empty, (it - 1) & 1, abort_flag, p.err, DEV_TIMEOUT_PRODUCER)) break;
         mbar_arrive_expect_tx(q_full, nd * kChunk);
         for (int c = 0; c < nd; ++c) tma_load_4d(sq + c * kChunk, &p.qmap, q_full, 64 * c, h, qt * kTile, b);
         issued_q = it + 1;
       }
-      mbar_wait(kv_full, 0, nullptr, p.err, DEV_TIMEOUT_DRAIN);
-      if (issued_do > 0) mbar_wait(do_full, (issued_do - 1) & 1, nullptr, p.err, DEV_TIMEOUT_DRAIN);
-      if (issued_q > 0) mbar_wait(q_full, (issued_q - 1) & 1, nullptr, p.err, DEV_TIMEOUT_DRAIN);
+      mbar_wait_soon(kv_full, 0, nullptr, p.err, DEV_TIMEOUT_DRAIN);
+      if (issued_do > 0) mbar_wait_soon(do_full, (issued_do - 1) & 1, nullptr, p.err, DEV_TIMEOUT_DRAIN);
+      if (issued_q > 0) mbar_wait_soon(q_full, (issued_q - 1) & 1, nullptr, p.err, DEV_TIMEOUT_DRAIN);
     }
   } else if (warp == 1) {
     if (lane == 0) {
@@ -989,20 +1163,20 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1) masked_bwd_kernel(const __
       const uint32_t id_qd = idesc_bf16(128, 64 * nd, 1, 1);   // dQ = dS K (dS read MN-major from dS^T)
       const uint32_t ak = smem_u32(sk), av = smem_u32(sv), bq = smem_u32(sq), bdo = smem_u32(sdo);
       const uint32_t apt = smem_u32(spt), adst = smem_u32(sdst);
-      bool ok = mbar_wait(kv_full, 0, abort_flag, p.err, DEV_TIMEOUT_MMA);
+      bool ok = mbar_wait_soon(kv_full, 0, abort_flag, p.err, DEV_TIMEOUT_MMA);
       for (int it = 0; ok && it < n_it; ++it) {
         // dP^T (columns 128..255) needs only dO: it may run while the previous dQ is drained
-        if (!mbar_wait(do_full, it & 1, abort_flag, p.err, DEV_TIMEOUT_MMA)) { ok = false; break; }
+        if (!mbar_wait_soon(do_full, it & 1, abort_flag, p.err, DEV_TIMEOUT_MMA)) { ok = false; break; }
         tc_fence_after();
         for (int t = 0; t < 4 * nd; ++t)
           umma_bf16(tmem + 128, kmajor_desc(av, t), kmajor_desc(bdo, t), id_kq, t > 0 ? 1u : 0u);
-        if (!mbar_wait(q_full, it & 1, abort_flag, p.err, DEV_TIMEOUT_MMA)) { ok = false; break; }
-        if (it > 0 && !mbar_wait(dq_free, (it - 1) & 1, abort_flag, p.err, DEV_TIMEOUT_MMA)) { ok = false; break; }
+        if (!mbar_wait_soon(q_full, it & 1, abort_flag, p.err, DEV_TIMEOUT_MMA)) { ok = false; break; }
+        if (it > 0 && !mbar_wait_soon(dq_free, (it - 1) & 1, abort_flag, p.err, DEV_TIMEOUT_MMA)) { ok = false; break; }
         tc_fence_after();
         for (int t = 0; t < 4 * nd; ++t)
           umma_bf16(tmem, kmajor_desc(ak, t), kmajor_desc(bq, t), id_kq, t > 0 ? 1u : 0u);
         umma_commit(s_full);
-        if (!mbar_wait(p_full, it & 1, abort_flag, p.err, DEV_TIMEOUT_MMA)) { ok = false; break; }
+        if (!mbar_wait_soon(p_full, it & 1, abort_flag, p.err, DEV_TIMEOUT_MMA)) { ok = false; break; }
         tc_fence_after();
         for (int t = 0; t < 8; ++t)
           umma_bf16(tmem + t_dv, kmajor_desc(apt, t), mnmajor_desc(bdo, t), id_kd, (it > 0 || t > 0) ? 1u : 0u);
@@ -1015,7 +1189,7 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1) masked_bwd_kernel(const __
         umma_commit(mma2_done);
       }
       umma_commit(drain);
-      mbar_wait(drain, 0, nullptr, p.err, DEV_TIMEOUT_DRAIN);
+      mbar_wait_soon(drain, 0, nullptr, p.err, DEV_TIMEOUT_DRAIN);
     }
   } else {
     // Eight compute warps: warp w reads TMEM lanes 32 (w % 4) .. + 31 and handles one half of the
@@ -1062,7 +1236,7 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1) masked_bwd_kernel(const __
       ok = bar_and_bwd(ok);
       if (!ok) break;
       if (half == 0 && it + 1 < n_it) fetch(it + 1);
-      ok = __all_sync(0xffffffffu, mbar_wait(s_full, it & 1, abort_flag, p.err, DEV_TIMEOUT_EPILOGUE));
+      ok = __all_sync(0xffffffffu, mbar_wait_soon(s_full, it & 1, abort_flag, p.err, DEV_TIMEOUT_EPILOGUE));
       if (ok) {
         tc_fence_after();
         // this warp's previous dQ reductions have read its boxes (rewritten below)
@@ -1080,7 +1254,7 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1) masked_bwd_kernel(const __
           tmem_ld32(tmem + lane_off + 128 + 32 * c, dp);
           tmem_ld_wait_regs(st);
           regs_after_wait(dp);
-          if (CAP) tanh32(st, p.cap_mul);
+          if (CAP) tanh_n(st, p.cap_mul);
           uint32_t pw[16], dw[16];
 #pragma unroll
           for (int i = 0; i < 32; i += 4) {
@@ -1115,7 +1289,7 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1) masked_bwd_kernel(const __
         fence_proxy_async_smem();
         tc_fence_before();
         mbar_arrive(p_full);
-        ok = __all_sync(0xffffffffu, mbar_wait(mma2_done, it & 1, abort_flag, p.err, DEV_TIMEOUT_EPILOGUE));
+        ok = __all_sync(0xffffffffu, mbar_wait_soon(mma2_done, it & 1, abort_flag, p.err, DEV_TIMEOUT_EPILOGUE));
       }
       if (ok) {
         // dQ of this (head, query tile), lane r = query row qt * 128 + r: out of TMEM (which the next
@@ -1242,7 +1416,7 @@ int bwd_launch(const MaskedBwdParams& p, cudaStream_t s) {
   return 0;
 }
 
-// scale, mul of score() and cap_mul of tanh32()
+// scale, mul of score() and cap_mul of tanh_n()
 void score_constants(const MaskedArgs& a, float* scale, float* mul, float* cap_mul) {
   const double sc = a.scale > 0.f ? (double)a.scale : 1.0 / std::sqrt((double)a.hd);
   *scale = (float)sc;

@@ -105,6 +105,15 @@ __device__ __forceinline__ void tma_reduce_add_4d(const CUtensorMap* m, const vo
       : "memory");
 }
 
+// mbar_wait that reads the clock only after a number of tries: a read of the nanosecond timer takes longer than the
+// waits of a running pipeline, and each wait that is not over at once would pay it.
+__device__ __forceinline__ bool mbar_wait_soon(uint64_t* bar, uint32_t parity, volatile int* abort, int* err, int code) {
+#pragma unroll 1
+  for (int i = 0; i < 64; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
+  return mbar_wait(bar, parity, abort, err, code);
+}
+
 // ---- host side
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
