@@ -1336,7 +1336,7 @@ sl_status sl_attention_masked_bwd(const void* q, int64_t ldq, const void* k, int
   if (!rows_ok(q, ldq, nq) || !rows_ok(k, ldk, nk) || !rows_ok(v, ldv, nk) || !rows_ok(d_o, lddo, nq) || !rows_ok(dq, lddq, nq) || !rows_ok(dk, lddk, nk) || !rows_ok(dv, lddv, nk) ||
       !al16(lse))
     return SL_ERR_ALIGNMENT;
-  const size_t scratch = attention_bwd_scratch(n_seq, seq_len, n_q_heads, head_dim);
+  const size_t scratch = attention_masked_scratch(n_seq, seq_len, n_q_heads);
   Carver c(nullptr);
   c.take<uint8_t>(scratch);
   if (sl_status st = ws_check(ws, c.off)) return st;

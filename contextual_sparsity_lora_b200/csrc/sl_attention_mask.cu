@@ -20,11 +20,8 @@ namespace sl {
 
 namespace {
 
-constexpr int kSoftThreads = 256;                   // delta: warps 2..9
-constexpr int kAttnThreads = 64 + kSoftThreads;     // warp 0 TMA, warp 1 MMA + TMEM
-constexpr int kFwdThreads = 384;                    // warp 0 TMA, warp 1 MMA, warps 4..11 softmax
-constexpr int kBwdComputeThreads = 256;                   // backward: warps 2..9
-constexpr int kAttnBwdThreads = 64 + kBwdComputeThreads;  // warp 0 TMA, warp 1 MMA + TMEM
+constexpr int kFwdThreads = 384;  // warp 0 TMA, warps 1 and 2 MMA (warp 1 allocates TMEM), warps 4..11 softmax
+constexpr int kBwdThreads = 384;  // the same; dk, dv: warp 3 reads the query rows
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -301,15 +298,6 @@ __device__ __forceinline__ void tanh_n(uint32_t (&v)[N], float mul) {
   }
 }
 
-// -inf outside columns [first, end)
-__device__ __forceinline__ void mask32(uint32_t (&v)[32], int first, int end) {
-  const int a = min(max(first, 0), 32), b = min(max(end, 0), 32);
-  const uint32_t see = a >= b ? 0u : (0xffffffffu << a) & (0xffffffffu >> (32 - b));
-#pragma unroll
-  for (int e = 0; e < 32; ++e)
-    if (!(see & (1u << e))) v[e] = 0xff800000u;
-}
-
 __device__ __forceinline__ float max32(const uint32_t (&v)[32]) {
   float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -326,11 +314,12 @@ __device__ __forceinline__ float score(uint32_t v, float mul, float slope, float
   return BIAS ? fmaf(-slope, fabsf(away), y) : y;
 }
 
-// Biased scores of 32 raw products (or their tanh) in place, powers of two: v mul - slope |away - e|. one_side: no
-// key of the warp's tile lies behind its query (away - e >= 0), so the distance needs no absolute value.
-__device__ __forceinline__ void bias32(uint32_t (&v)[32], float mul, float slope, float away, bool one_side) {
-  const f2 m = both(mul), s = both(slope), a = both(-slope * away);
-  if (one_side) {
+// Biased scores of 32 raw products (or their tanh) in place, powers of two: v mul - slope |away - e|. side: 1 where
+// away - e >= 0 for the whole warp, -1 where it is <= 0 (the distance then needs no absolute value), else 0.
+__device__ __forceinline__ void bias32(uint32_t (&v)[32], float mul, float slope, float away, int side) {
+  if (side) {
+    const float sl = side > 0 ? slope : -slope;
+    const f2 m = both(mul), s = both(sl), a = both(-sl * away);
 #pragma unroll
     for (int e = 0; e < 32; e += 2)
       unu(fma2(pku(v[e], v[e + 1]), m, fma2(s, pk((float)e, (float)(e + 1)), a)), v[e], v[e + 1]);
@@ -338,6 +327,20 @@ __device__ __forceinline__ void bias32(uint32_t (&v)[32], float mul, float slope
 #pragma unroll
     for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(score<true>(v[e], mul, slope, away - (float)e));
   }
+}
+
+// Bits of the columns [first, end) of 32
+__device__ __forceinline__ uint32_t see_bits(int first, int end) {
+  const int a = min(max(first, 0), 32), b = min(max(end, 0), 32);
+  return a >= b ? 0u : (0xffffffffu << a) & (0xffffffffu >> (32 - b));
+}
+
+// -inf outside columns [first, end)
+__device__ __forceinline__ void mask32(uint32_t (&v)[32], int first, int end) {
+  const uint32_t see = see_bits(first, end);
+#pragma unroll
+  for (int e = 0; e < 32; ++e)
+    if (!(see & (1u << e))) v[e] = 0xff800000u;
 }
 
 // D[tmem] (+)= A[tmem] * B[smem desc]^T: A is 128 rows (lanes) of 16 bf16, two per 32-bit column.
@@ -387,48 +390,22 @@ struct MaskedFwdParams {
   int* err;
 };
 
-struct MaskedDeltaParams {
-  CUtensorMap qmap, kmap, vmap, domap;
-  Plan plan;
-  const float* slopes;
-  const float* lse;              // [hq][T]
-  float* delta;                  // [hq][T]
-  float* dq_acc;                 // [T][hq * hd]
-  int32_t n_seq, S, hq, hkv, hd, nd;
-  float mul, cap_mul;
-  int* err;
-};
-
 struct MaskedBwdParams {
-  CUtensorMap qmap, kmap, vmap, domap;
-  CUtensorMap dqmap;             // dq_acc as [head_dim, hq, seq_len, n_seq] fp32, boxes 32 x 1 x 32 x 1
+  CUtensorMap qmap, kmap, vmap, domap;  // boxes as in the forward
   Plan plan;
   const float* slopes;
   const float* lse;              // [hq][T]
-  const float* delta;            // [hq][T]: D per query row
-  __nv_bfloat16* dk;
-  __nv_bfloat16* dv;
-  int64_t lddk, lddv;
+  float* delta;                  // [hq][T]: D per query row (written by the dq kernel, read by the dk, dv kernel)
+  __nv_bfloat16 *dq, *dk, *dv;
+  int64_t lddq, lddk, lddv;
   int32_t n_seq, S, hq, hkv, hd, nd;
+  int32_t n_units;               // of the dq kernel
   float scale, mul, cap_mul;
   int* err;
 };
 
-// Barrier of the forward's softmax warps that also returns whether `ok` holds in all of them.
-__device__ __forceinline__ bool bar_and_soft(bool ok) {
-  uint32_t all;
-  asm volatile(
-      "{\n\t.reg .pred q, a;\n\t"
-      "setp.ne.u32 q, %1, 0;\n\t"
-      "bar.red.and.pred a, 1, 256, q;\n\t"
-      "selp.u32 %0, 1, 0, a;\n\t}"
-      : "=r"(all)
-      : "r"((uint32_t)ok)
-      : "memory");
-  return all != 0;
-}
-// Barrier of the backward's compute warps that also returns whether `ok` holds in all of them.
-__device__ __forceinline__ bool bar_and_bwd(bool ok) {
+// Barrier of the 256 threads of the compute warps that also returns whether `ok` holds in all of them.
+__device__ __forceinline__ bool bar_and_compute(bool ok) {
   uint32_t all;
   asm volatile(
       "{\n\t.reg .pred q, a;\n\t"
@@ -757,9 +734,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1) masked_fwd_kernel(const __grid
         }
         // With a bias the score itself is formed here (mul = 1 below), else scores stay raw products
         if (BIAS) {
-          const bool one_side = qt * kTile + 32 * quarter >= k0 + 63;
+          const int side = qt * kTile + 32 * quarter >= k0 + 63;
 #pragma unroll
-          for (int c = 0; c < 2; ++c) bias32(s[c], p.mul, slope, (float)(qpos - k0 - 32 * c), one_side);
+          for (int c = 0; c < 2; ++c) bias32(s[c], p.mul, slope, (float)(qpos - k0 - 32 * c), side);
         }
         const float mul = BIAS ? 1.f : p.mul;
         if (__any_sync(0xffffffffu, lo > k0 || hi < k0 + 64)) {
@@ -849,58 +826,130 @@ __global__ void __launch_bounds__(kFwdThreads, 1) masked_fwd_kernel(const __grid
   }
 }
 
-// --------------------------------------------------------------------------- backward pieces
+// ----------------------------------------------------------------------------------------- backward
 
-// D_i = sum_j P_ij dP_ij = dO_i . o_i for every query row and head, and the dQ accumulator's rows set to zero
-// (the backward adds into them). From P and dP in fp32 and not from the stored o: that one is rounded to bf16, and
-// its error, the same for all keys of a row, is as large as all other roundings of dq and dk together where a row's
-// weight lies on few keys (relative error of dq over 4e-3 with 8 keys, against 2.3e-3).
-// Persistent CTAs over the same units as the forward. Warp 0 loads Q, dO and a two-stage ring of (K, V); warp 1 issues
-// S = Q K^T and dP = dO V^T into two alternating pairs of TMEM buffers; warps 2-9 read both, half of the columns
-// each, and sum exp(S - lse) dP per row: nothing waits for the softmax, so the products run ahead.
+// Two kernels. dq: per tile of queries, D and then dQ, over the key tiles that it sees; dk, dv: per tile of keys, over
+// the query tiles that see it. Each forms S and dP for itself (nine products of a tile pair where one kernel for
+// all would have five and a sum for D), but no partial sum leaves the chip: with dQ added up across key tiles in
+// global memory (64 KB of fp32 reductions per tile pair, then a pass to round them) the backward took 1.7 times as
+// long, and dq's last bits depended on the order. Here every sum has a fixed order.
+//
+// D_i = sum_j P_ij dP_ij (= dO_i . o_i) is formed from P and dP in fp32 and not from the stored o: that one is rounded to
+// bf16, and its error, the same for all keys of a row, is as large as all other roundings of dq and dk
+// together where a row's weight lies on few keys (relative error of dq over 4e-3 with 8 keys, against 2.3e-3).
+
+// dS = P (dP - D) (1 - tanh^2) of 32 columns: from raw products s and dp; c1: -lse (powers of two), c2: -D, each
+// one per row (ROW) or read per column from shared memory. P as packed bf16 in pw (when wanted), dS in dw.
+template <bool CAP, bool BIAS, bool ROW, bool WANT_P>
+__device__ __forceinline__ void grad32(uint32_t (&s)[32], uint32_t (&dp)[32], float mul, float cap_mul, float slope,
+                                       float away, int side, bool part, uint32_t see, float c1, float c2,
+                                       const float* col1, const float* col2, uint32_t (&pw)[16], uint32_t (&dw)[16]) {
+  uint32_t th[CAP ? 32 : 2];
+  if (CAP) {
+    tanh_n(s, cap_mul);
+    if (BIAS) {
+#pragma unroll
+      for (int e = 0; e < 32; ++e) th[e] = s[e];
+    }
+  }
+  if (BIAS) bias32(s, mul, slope, away, side);
+  const f2 m = both(BIAS ? 1.f : mul), one = both(1.f);
+  const f2 r1 = both(c1), r2 = both(c2);
+#pragma unroll
+  for (int e = 0; e < 32; e += 4) {
+    f2 a1[2], a2[2];
+    if (ROW) {
+      a1[0] = a1[1] = r1;
+      a2[0] = a2[1] = r2;
+    } else {
+      const ulonglong2 l = *reinterpret_cast<const ulonglong2*>(col1 + e), d = *reinterpret_cast<const ulonglong2*>(col2 + e);
+      a1[0] = l.x, a1[1] = l.y, a2[0] = d.x, a2[1] = d.y;
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int i = e + 2 * k;
+      float x0, x1;
+      un(fma2(pku(s[i], s[i + 1]), m, a1[k]), x0, x1);
+      x0 = ex2(x0);
+      x1 = ex2(x1);
+      if (part) {
+        if (!(see & (1u << i))) x0 = 0.f;
+        if (!(see & (2u << i))) x1 = 0.f;
+      }
+      const f2 pe = pk(x0, x1);
+      f2 ds = mul2(pe, add2(pku(dp[i], dp[i + 1]), a2[k]));
+      if (CAP) {
+        const f2 t = BIAS ? pku(th[i], th[i + 1]) : pku(s[i], s[i + 1]);
+        ds = mul2(ds, fma2(mul2(t, both(-1.f)), t, one));
+      }
+      float d0, d1;
+      un(ds, d0, d1);
+      if (WANT_P) pw[i / 2] = pack2(x0, x1);
+      dw[i / 2] = pack2(d0, d1);
+    }
+  }
+}
+
+// dq: persistent CTAs over units (query tile, head). Q and dO stay, K and V stream through two stages, twice: first for D,
+// then for dQ. Warp 0 loads; warp 1 issues S = Q K^T and dP = dO V^T; warp 2 issues dQ += dS K; warps 4-7 and 8-11 hold
+// a query row per thread and half of the key columns each. They take S and dP into registers at once, so the
+// next tile's products run while they work. TMEM: dQ at 0, S at 128, dP at 256, dS (bf16, two buffers) at 384.
 template <bool CAP, bool BIAS>
-__global__ void __launch_bounds__(kAttnThreads, 1) masked_delta_kernel(const __grid_constant__ MaskedDeltaParams p) {
+__global__ void __launch_bounds__(kBwdThreads, 1) masked_dq_kernel(const __grid_constant__ MaskedBwdParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int nd = p.nd;
-  uint8_t* sq = smem;                       // Q, then dO: nd chunks each
-  uint8_t* skv = sq + 2 * nd * kChunk;      // stage s: K, then V
-  float* s_part = reinterpret_cast<float*>(smem + 12 * kChunk);  // [128]: the second half's sums
-  uint64_t* bars = reinterpret_cast<uint64_t*>(s_part + 128);
+  uint8_t* sq = smem;                       // Q, then dO: 2 chunks each
+  uint8_t* skv = smem + 4 * kChunk;         // stage s: K (2 chunks), then V
+  float* s_part = reinterpret_cast<float*>(smem + 12 * kChunk);  // [2][128]: the halves' sums of D
+  uint64_t* bars = reinterpret_cast<uint64_t*>(s_part + 256);
   uint64_t* q_full = bars;
   uint64_t* q_empty = bars + 1;
   uint64_t* kv_full = bars + 2;    // [2]
   uint64_t* kv_empty = bars + 4;   // [2]
-  uint64_t* s_full = bars + 6;     // [2]
-  uint64_t* s_free = bars + 8;     // [2]
-  uint64_t* drain = bars + 10;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 11);
+  uint64_t* s_full = bars + 6;
+  uint64_t* s_free = bars + 7;
+  uint64_t* ds_full = bars + 8;    // [2]
+  uint64_t* dq_done = bars + 10;   // [2]
+  uint64_t* drain = bars + 12;     // [2]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 14);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n_qt = (p.S + kTile - 1) / kTile;
-  const int n_units = n_qt * p.n_seq * p.hq;
   const int hpg = p.hq / p.hkv;
-  auto unit = [&](int u, int& qt, int& h, int& b, int& j0, int& j1) {
+  struct U {
+    int qt, b, h, j0, j1;
+  };
+  auto unit = [&](int i, U& w) -> bool {
+    const int u = unit_number(i);
+    if (u >= p.n_units) return false;
     const int4 e = p.plan.q_order[u / p.hq];
-    qt = e.x % n_qt;
-    b = e.x / n_qt;
-    h = u % p.hq;
-    j0 = e.y;
-    j1 = e.z;
+    w.qt = e.x % n_qt;
+    w.b = e.x / n_qt;
+    w.h = u % p.hq;
+    w.j0 = e.y;
+    w.j1 = e.z;
+    return true;
   };
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(&kv_full[s], 1);
-      mbar_init(&kv_empty[s], 1);
-      mbar_init(&s_full[s], 1);
-      mbar_init(&s_free[s], kSoftThreads);
+      mbar_init(&kv_empty[s], 2);  // S and dP; dQ
+      mbar_init(&ds_full[s], 256);
+      mbar_init(&dq_done[s], 1);
+      mbar_init(&drain[s], 1);
     }
-    mbar_init(drain, 1);
+    mbar_init(s_full, 1);
+    mbar_init(s_free, 256);
     *abort_flag = 0;
     fence_barrier_init();
+    tma_prefetch_desc(&p.qmap);
+    tma_prefetch_desc(&p.kmap);
+    tma_prefetch_desc(&p.vmap);
+    tma_prefetch_desc(&p.domap);
   }
   if (warp == 1) {
     tmem_alloc(tmem_slot, 512);
@@ -909,130 +958,212 @@ __global__ void __launch_bounds__(kAttnThreads, 1) masked_delta_kernel(const __g
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;  // buffer s: S at 256 s, dP at 256 s + 128
+  const uint32_t tmem = *tmem_slot;
   pdl_wait();
   const bool plan_ok = plan_fits(p.plan, p.n_seq, p.S, p.err);
+
   if (warp == 0) {
     if (lane == 0) {
-      int nq = 0, t = 0;
-      bool ok = plan_ok;
-      for (int u = blockIdx.x, i = 0; ok && u < n_units; u += gridDim.x, ++i) {
-        int qt, h, b, j0, j1;
-        unit(u, qt, h, b, j0, j1);
+      U w, nx;
+      bool ok = plan_ok, live = plan_ok && unit(0, nx);
+      int t = 0, i = 0;
+      for (; ok && live; ++i) {
+        w = nx;
+        live = unit(i + 1, nx);
         if (i > 0 && !mbar_wait_soon(q_empty, (i - 1) & 1, abort_flag, p.err, DEV_TIMEOUT_PRODUCER)) break;
         mbar_arrive_expect_tx(q_full, 2 * nd * kChunk);
         for (int c = 0; c < nd; ++c) {
-          tma_load_4d(sq + c * kChunk, &p.qmap, q_full, 64 * c, h, qt * kTile, b);
-          tma_load_4d(sq + (nd + c) * kChunk, &p.domap, q_full, 64 * c, h, qt * kTile, b);
+          tma_load_4d(sq + c * kChunk, &p.qmap, q_full, 64 * c, w.h, w.qt * kTile, w.b);
+          tma_load_4d(sq + (2 + c) * kChunk, &p.domap, q_full, 64 * c, w.h, w.qt * kTile, w.b);
         }
-        ++nq;
-        for (int j = j0; j < j1; ++j, ++t) {
-          const int s = t & 1;
-          if (!mbar_wait_soon(&kv_empty[s], ((t >> 1) & 1) ^ 1, abort_flag, p.err, DEV_TIMEOUT_PRODUCER)) { ok = false; break; }
-          mbar_arrive_expect_tx(&kv_full[s], 2 * nd * kChunk);
-          uint8_t* st = skv + s * 2 * nd * kChunk;
-          for (int c = 0; c < nd; ++c) {
-            tma_load_4d(st + c * kChunk, &p.kmap, &kv_full[s], 64 * c, h / hpg, j * kTile, b);
-            tma_load_4d(st + (nd + c) * kChunk, &p.vmap, &kv_full[s], 64 * c, h / hpg, j * kTile, b);
+        for (int pass = 0; pass < 2 && ok; ++pass)
+          for (int j = w.j0; j < w.j1; ++j, ++t) {
+            const int s = t & 1;
+            if (!mbar_wait_soon(&kv_empty[s], ((t >> 1) & 1) ^ 1, abort_flag, p.err, DEV_TIMEOUT_PRODUCER)) { ok = false; break; }
+            mbar_arrive_expect_tx(&kv_full[s], 2 * nd * kChunk);
+            uint8_t* st = skv + s * 4 * kChunk;
+            for (int c = 0; c < nd; ++c) {
+              tma_load_4d(st + c * kChunk, &p.kmap, &kv_full[s], 64 * c, w.h / hpg, j * kTile, w.b);
+              tma_load_4d(st + (2 + c) * kChunk, &p.vmap, &kv_full[s], 64 * c, w.h / hpg, j * kTile, w.b);
+            }
           }
-        }
       }
       // every copy lands before the CTA may exit
-      if (nq > 0) mbar_wait_soon(q_full, (nq - 1) & 1, nullptr, p.err, DEV_TIMEOUT_DRAIN);
-      for (int k = max(0, t - 2); k < t; ++k) mbar_wait_soon(&kv_full[k & 1], (k >> 1) & 1, nullptr, p.err, DEV_TIMEOUT_DRAIN);
+      if (i > 0) mbar_wait(q_full, (i - 1) & 1, nullptr, p.err, DEV_TIMEOUT_DRAIN);
+      for (int k = max(0, t - 2); k < t; ++k) mbar_wait(&kv_full[k & 1], (k >> 1) & 1, nullptr, p.err, DEV_TIMEOUT_DRAIN);
     }
   } else if (warp == 1) {
     if (lane == 0) {
       const uint32_t id = idesc_bf16(128, 128, 0, 0);
-      const uint32_t aq = smem_u32(sq), ado = aq + nd * kChunk;
-      bool ok = plan_ok;
+      const uint64_t dq0 = kmajor_desc(smem_u32(sq), 0), ddo0 = dq0 + (2 * kChunk >> 4), dk0 = kmajor_desc(smem_u32(skv), 0);
+      U w, nx;
+      bool ok = plan_ok, live = plan_ok && unit(0, nx);
       int t = 0;
-      for (int u = blockIdx.x, i = 0; ok && u < n_units; u += gridDim.x, ++i) {
-        int qt, h, b, j0, j1;
-        unit(u, qt, h, b, j0, j1);
+      for (int i = 0; ok && live; ++i) {
+        w = nx;
+        live = unit(i + 1, nx);
         if (!mbar_wait_soon(q_full, i & 1, abort_flag, p.err, DEV_TIMEOUT_MMA)) break;
-        for (int j = j0; j < j1; ++j, ++t) {
-          const int s = t & 1;
-          if (!mbar_wait_soon(&kv_full[s], (t >> 1) & 1, abort_flag, p.err, DEV_TIMEOUT_MMA) ||
-              (t >= 2 && !mbar_wait_soon(&s_free[s], ((t - 2) >> 1) & 1, abort_flag, p.err, DEV_TIMEOUT_MMA))) {
-            ok = false;
-            break;
+        for (int pass = 0; pass < 2 && ok; ++pass)
+          for (int j = w.j0; j < w.j1; ++j, ++t) {
+            const int s = t & 1;
+            ok = mbar_wait_soon(&kv_full[s], (t >> 1) & 1, abort_flag, p.err, DEV_TIMEOUT_MMA) &&
+                 (t == 0 || mbar_wait_soon(s_free, (t - 1) & 1, abort_flag, p.err, DEV_TIMEOUT_MMA));
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t bk = dk0 + s * (4 * kChunk >> 4);
+            mma_kk_nd(nd, tmem + 128, dq0, bk, id);
+            mma_kk_nd(nd, tmem + 256, ddo0, bk + (2 * kChunk >> 4), id);
+            umma_commit(s_full);
+            umma_commit(&kv_empty[s]);
+            if (pass == 0) mbar_arrive(&kv_empty[s]);  // no dQ in the first pass
+            if (pass == 1 && j == w.j1 - 1) umma_commit(q_empty);
           }
+      }
+      umma_commit(&drain[0]);
+      mbar_wait(&drain[0], 0, nullptr, p.err, DEV_TIMEOUT_DRAIN);
+    }
+  } else if (warp == 2) {
+    if (lane == 0) {
+      const uint32_t id = idesc_bf16(128, 64 * nd, 0, 1);  // dS in TMEM, K MN-major
+      const uint64_t dk0 = mnmajor_desc(smem_u32(skv), 0);
+      U w, nx;
+      bool ok = plan_ok, live = plan_ok && unit(0, nx);
+      int t = 0, n = 0;  // steps of both passes, steps of the second
+      for (int i = 0; ok && live; ++i) {
+        w = nx;
+        live = unit(i + 1, nx);
+        t += w.j1 - w.j0;
+        for (int j = w.j0; j < w.j1; ++j, ++t, ++n) {
+          const int s = t & 1, d = n & 1;
+          ok = mbar_wait_soon(&ds_full[d], (n >> 1) & 1, abort_flag, p.err, DEV_TIMEOUT_MMA) &&
+               mbar_wait_soon(&kv_full[s], (t >> 1) & 1, abort_flag, p.err, DEV_TIMEOUT_MMA);
+          if (!ok) break;
           tc_fence_after();
-          const uint32_t bk = smem_u32(skv + s * 2 * nd * kChunk), bv = bk + nd * kChunk;
-          mma_kk_nd(nd, tmem + 256 * s, kmajor_desc(aq, 0), kmajor_desc(bk, 0), id);
-          mma_kk_nd(nd, tmem + 256 * s + 128, kmajor_desc(ado, 0), kmajor_desc(bv, 0), id);
-          umma_commit(&s_full[s]);
+          mma_tm<8>(tmem, tmem + 384 + 64 * d, dk0 + s * (4 * kChunk >> 4), id, j > w.j0);
+          umma_commit(&dq_done[d]);
           umma_commit(&kv_empty[s]);
-          if (j == j1 - 1) umma_commit(q_empty);
         }
       }
-      umma_commit(drain);
-      mbar_wait_soon(drain, 0, nullptr, p.err, DEV_TIMEOUT_DRAIN);
+      umma_commit(&drain[1]);
+      mbar_wait(&drain[1], 0, nullptr, p.err, DEV_TIMEOUT_DRAIN);
     }
-  } else {
-    const int quarter = warp & 3, half = (warp - 2) >> 2;
+  } else if (warp >= 4) {
+    const int quarter = warp & 3, half = (warp - 4) >> 2;
     const int r = quarter * 32 + lane;
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
-    bool ok = plan_ok;
-    int t = 0;
-    for (int u = blockIdx.x; plan_ok && u < n_units; u += gridDim.x) {
-      int qt, h, b, j0, j1;
-      unit(u, qt, h, b, j0, j1);
-      const int qpos = qt * kTile + r;
-      const bool in = qpos < p.S;
-      const int64_t row = (int64_t)b * p.S + qpos, T = (int64_t)p.n_seq * p.S;
-      const int lo = in ? p.plan.lo[row] : 0, hi = in ? p.plan.hi[row] : 0;
-      const float lse = lo < hi ? p.lse[(int64_t)h * T + row] * kLog2e : 0.f;
-      // a row that sees one key: P = 1 and D = dP to the bit, so that its dS is 0 and not a rounding's rest
-      const float single = hi - lo == 1 ? 0.f : 1.f;
+    const uint32_t s_tm = tmem + lane_off + 128 + 64 * half, dp_tm = s_tm + 128, ds_tm = tmem + lane_off + 384 + 32 * half;
+    U w, nx;
+    bool ok = plan_ok, live = plan_ok && unit(0, nx);
+    int t = 0, n = 0;
+    int nlo = 0, nhi = 0;
+    float nlse = 0.f;
+    const int64_t T = (int64_t)p.n_seq * p.S;
+    auto rows_of = [&](const U& x) {  // what the row sees, and its lse in powers of two (0 where it sees nothing)
+      const int q = x.qt * kTile + r;
+      const int64_t row = (int64_t)x.b * p.S + q;
+      const bool in = q < p.S;
+      nlo = in ? p.plan.lo[row] : 0;
+      nhi = in ? p.plan.hi[row] : 0;
+      nlse = in ? p.lse[(int64_t)x.h * T + row] * kLog2e : 0.f;
+    };
+    if (live) rows_of(nx);
+    for (int i = 0; ok && live; ++i) {
+      w = nx;
+      const int lo = nlo, hi = nhi, qt0 = w.qt * kTile, h = w.h, b = w.b;
+      const float lse = lo < hi ? nlse : 0.f;
+      live = unit(i + 1, nx);
       const float slope = BIAS ? p.slopes[h] * kLog2e : 0.f;
-      // the accumulator's rows of this unit: 128 x hd fp32, a row per 16 threads
-      for (int k = threadIdx.x - 64; k < 128 * (p.hd / 4); k += kSoftThreads) {
-        const int rr = qt * kTile + k / (p.hd / 4), c = k % (p.hd / 4) * 4;
-        if (rr < p.S)
-          *reinterpret_cast<float4*>(p.dq_acc + (((int64_t)b * p.S + rr) * p.hq + h) * p.hd + c) = make_float4(0.f, 0.f, 0.f, 0.f);
-      }
-      float sum[2] = {0.f, 0.f};
-      for (int j = j0; j < j1 && ok; ++j, ++t) {
-        const int s = t & 1;
-        ok = __all_sync(0xffffffffu, mbar_wait_soon(&s_full[s], (t >> 1) & 1, abort_flag, p.err, DEV_TIMEOUT_EPILOGUE));
-        if (!ok) break;
-        tc_fence_after();
-        uint32_t sv[2][32], dv[2][32];
+      // a row that sees one key: P = 1 and D = dP to the bit, so that its dS is 0 and not a rounding's rest
+      const bool single = hi - lo == 1;
+      float sum = 0.f;
+      for (int pass = 0; pass < 2 && ok; ++pass) {
+        const float nD = pass ? -sum : 0.f;
+        f2 acc[2] = {0, 0};
+        for (int j = w.j0; j < w.j1; ++j, ++t) {
+          ok = __all_sync(0xffffffffu, mbar_wait_soon(s_full, t & 1, abort_flag, p.err, DEV_TIMEOUT_EPILOGUE));
+          if (!ok) break;
+          tc_fence_after();
+          uint32_t s[2][32], dp[2][32];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          tmem_ld32(tmem + lane_off + 256 * s + 64 * half + 32 * c, sv[c]);
-          tmem_ld32(tmem + lane_off + 256 * s + 128 + 64 * half + 32 * c, dv[c]);
-        }
-        tmem_ld_wait_regs(sv[0]);
-        regs_after_wait(sv[1]);
-        regs_after_wait(dv[0]);
-        regs_after_wait(dv[1]);
-        tc_fence_before();
-        mbar_arrive(&s_free[s]);
-        const int c0 = j * kTile + 64 * half;  // key of this thread's first column
-        const bool whole = lo <= c0 && c0 + 64 <= hi;
-        const float away = (float)(qpos - c0);
-        if (CAP) {
-          tanh_n(sv[0], p.cap_mul);
-          tanh_n(sv[1], p.cap_mul);
-        }
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const int col = 32 * c + e;
-            float pe = ex2((score<BIAS>(sv[c][e], p.mul, slope, away - (float)col) - lse));
-            if (!whole) pe = c0 + col < lo || c0 + col >= hi ? 0.f : single == 0.f ? 1.f : pe;
-            sum[e & 1] = fmaf(pe, __uint_as_float(dv[c][e]), sum[e & 1]);
+          for (int c = 0; c < 2; ++c) {
+            tmem_ld32(s_tm + 32 * c, s[c]);
+            tmem_ld32(dp_tm + 32 * c, dp[c]);
           }
+          tmem_ld_wait_regs(s[0]);
+          regs_after_wait(s[1]);
+          regs_after_wait(dp[0]);
+          regs_after_wait(dp[1]);
+          tc_fence_before();
+          mbar_arrive(s_free);
+          const int k0 = j * kTile + 64 * half;  // key of this thread's first column
+          const bool part = __any_sync(0xffffffffu, lo > k0 || hi < k0 + 64);
+          const int side = qt0 + 32 * quarter >= k0 + 63;
+          if (pass == 0) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              if (CAP) tanh_n(s[c], p.cap_mul);
+              if (BIAS) bias32(s[c], p.mul, slope, (float)(qt0 + r - k0 - 32 * c), side);
+              const f2 m = both(BIAS ? 1.f : p.mul), nl = both(-lse);
+              const uint32_t see = see_bits(lo - k0 - 32 * c, hi - k0 - 32 * c);
+#pragma unroll
+              for (int e = 0; e < 32; e += 2) {
+                float x0, x1;
+                un(fma2(pku(s[c][e], s[c][e + 1]), m, nl), x0, x1);
+                x0 = ex2(x0);
+                x1 = ex2(x1);
+                if (part) {
+                  x0 = !(see & (1u << e)) ? 0.f : single ? 1.f : x0;
+                  x1 = !(see & (2u << e)) ? 0.f : single ? 1.f : x1;
+                }
+                acc[(e >> 1) & 1] = fma2(pk(x0, x1), pku(dp[c][e], dp[c][e + 1]), acc[(e >> 1) & 1]);
+              }
+            }
+          } else {
+            const int d = n & 1;
+            // dQ of two steps ago has read this buffer (its predecessors' phases are over: it reads them in order)
+            if (n >= 2) ok = __all_sync(0xffffffffu, mbar_wait_soon(&dq_done[d], ((n >> 1) - 1) & 1, abort_flag, p.err, DEV_TIMEOUT_EPILOGUE));
+            if (!ok) break;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              uint32_t pw[16], dw[16];
+              grad32<CAP, BIAS, true, false>(s[c], dp[c], p.mul, p.cap_mul, slope, (float)(qt0 + r - k0 - 32 * c), side, part,
+                                             see_bits(lo - k0 - 32 * c, hi - k0 - 32 * c), -lse, nD, nullptr, nullptr, pw, dw);
+              tmem_st16(ds_tm + 64 * d + 16 * c, dw);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive(&ds_full[d]);
+            ++n;
+          }
+        }
+        if (pass == 0) {
+          float a0, a1;
+          un(add2(acc[0], acc[1]), a0, a1);
+          s_part[half * 128 + r] = a0 + a1;
+          ok = bar_and_compute(ok);
+          sum = s_part[r] + s_part[128 + r];
+          if (ok && half == 0 && qt0 + r < p.S) p.delta[(int64_t)h * T + (int64_t)b * p.S + qt0 + r] = sum;
+        } else {
+          if (ok && live) rows_of(nx);
+          // both buffers' last products (a unit of one key tile has used one)
+          if (ok) ok = __all_sync(0xffffffffu, mbar_wait_soon(&dq_done[(n - 1) & 1], ((n - 1) >> 1) & 1, abort_flag, p.err, DEV_TIMEOUT_EPILOGUE));
+          ok = bar_and_compute(ok);  // also: s_part is free for the next unit
+        }
       }
-      if (half == 1) s_part[r] = sum[0] + sum[1];
-      ok = bar_and_soft(ok);
-      if (ok && half == 0 && in) p.delta[(int64_t)h * T + row] = sum[0] + sum[1] + s_part[r];
-      ok = bar_and_soft(ok);  // s_part is read before the next unit writes it
       if (!ok) break;
+      tc_fence_after();
+      const int64_t row0 = (int64_t)b * p.S + qt0 + 32 * quarter;
+      const int n_rows = p.S - qt0 - 32 * quarter;
+#pragma unroll 1
+      for (int c = nd * half; c < nd * half + nd; ++c) {
+        uint32_t v[32], pk16[16];
+        tmem_ld32(tmem + lane_off + 32 * c, v);
+        tmem_ld_wait_regs(v);
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) pk16[e / 2] = pack2(__uint_as_float(v[e]) * p.scale, __uint_as_float(v[e + 1]) * p.scale);
+        store_rows32(p.dq + row0 * p.lddq + (int64_t)h * p.hd + 32 * c, p.lddq, pk16, n_rows, p.hd - 32 * c);
+      }
+      tc_fence_before();
     }
   }
   tc_fence_before();
@@ -1044,48 +1175,34 @@ __global__ void __launch_bounds__(kAttnThreads, 1) masked_delta_kernel(const __g
   }
 }
 
-// dq[t * ldq + c] = bf16(acc[t * n + c]) for a [T, n] fp32 accumulator (n % 4 == 0), four
-// columns per thread.
-__global__ void masked_dq_cast_kernel(const float* __restrict__ acc, int64_t T, int64_t n, __nv_bfloat16* __restrict__ dq,
-                                    int64_t ldq) {
-  pdl_wait();
-  const int64_t i = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * 4;
-  if (i >= T * n) return;
-  const int64_t t = i / n, c = i % n;
-  const float4 v = *reinterpret_cast<const float4*>(acc + i);
-  *reinterpret_cast<uint2*>(dq + t * ldq + c) = make_uint2(pack2(v.x, v.y), pack2(v.z, v.w));
-}
-
-// ----------------------------------------------------------------------------------- backward
-
+// dk, dv: one CTA per (key tile, key/value head) in the plan's order, over (query head of the group, query tile). K and V
+// stay, Q and dO stream through two stages. A step is half a query tile (64 queries): S^T = K Q^T and dP^T = V dO^T of
+// step t + 1 run while the compute warps work on step t; P^T and dS^T replace them in TMEM (bf16, first
+// operands of dV += P^T dO and dK += dS^T Q). Warp 0 loads; warp 1 issues S^T and dP^T, warp 2 dV and dK; warp 3 reads the
+// query rows' lse, D and intervals; warps 4-7 and 8-11 take the even and the odd steps, a key row per thread. TMEM: S^T of
+// buffer x at 64 x, dP^T at 128 + 64 x, dV at 256, dK at 384.
 template <bool CAP, bool BIAS>
-__global__ void __launch_bounds__(kAttnBwdThreads, 1) masked_bwd_kernel(const __grid_constant__ MaskedBwdParams p) {
+__global__ void __launch_bounds__(kBwdThreads, 1) masked_dkv_kernel(const __grid_constant__ MaskedBwdParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int nd = p.nd;
-  uint8_t* sk = smem;                  // K_j: nd chunks
-  uint8_t* sv = sk + nd * kChunk;      // V_j
-  uint8_t* sq = sv + nd * kChunk;      // Q_i
-  uint8_t* sdo = sq + nd * kChunk;     // dO_i
-  uint8_t* spt = sdo + nd * kChunk;    // P^T: 2 chunks (128 queries)
-  uint8_t* sdst = spt + 2 * kChunk;    // dS^T: 2 chunks
-  // P^T and dS^T also hold the dQ boxes (32 query rows x 32 fp32 per warp and box, 128-byte
-  // swizzle) once the MMAs of an iteration have read them
-  float* s_lse = reinterpret_cast<float*>(sdst + 2 * kChunk);  // [2][128] by iteration parity
-  float* s_delta = s_lse + 256;                                // [2][128]
-  int2* s_see = reinterpret_cast<int2*>(s_delta + 256);         // [2][128]: keys that each query sees
-  uint64_t* bars = reinterpret_cast<uint64_t*>(s_see + 256);
+  uint8_t* sk = smem;                       // K, then V: 2 chunks each
+  uint8_t* sqd = smem + 4 * kChunk;         // stage s: Q (2 chunks), then dO
+  float* s_lse = reinterpret_cast<float*>(smem + 12 * kChunk);  // [2][128]: -lse in powers of two
+  float* s_del = s_lse + 256;                                   // [2][128]: -D
+  int2* s_see = reinterpret_cast<int2*>(s_del + 256);           // [2][128]: keys that the query sees
+  int* s_whole = reinterpret_cast<int*>(s_see + 256);           // [2]: all of the tile's queries see all of the key tile
+  uint64_t* bars = reinterpret_cast<uint64_t*>(s_whole + 4);
   uint64_t* kv_full = bars;
-  uint64_t* q_full = bars + 1;
-  uint64_t* q_empty = bars + 2;
-  uint64_t* do_full = bars + 3;
-  uint64_t* do_empty = bars + 4;
-  uint64_t* s_full = bars + 5;
-  uint64_t* p_full = bars + 6;
-  uint64_t* mma2_done = bars + 7;
-  uint64_t* dq_free = bars + 8;
-  uint64_t* drain = bars + 9;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 10);
+  uint64_t* qd_full = bars + 1;     // [2] by stage
+  uint64_t* qd_empty = bars + 3;    // [2]
+  uint64_t* rows_full = bars + 5;   // [2]
+  uint64_t* rows_empty = bars + 7;  // [2]
+  uint64_t* sd_full = bars + 9;     // [2] by buffer
+  uint64_t* pd_full = bars + 11;    // [2]
+  uint64_t* pd_done = bars + 13;    // [2]
+  uint64_t* drain = bars + 15;      // [2]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 17);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1095,17 +1212,22 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1) masked_bwd_kernel(const __
   const int64_t T = (int64_t)p.n_seq * p.S;
   if (threadIdx.x == 0) {
     mbar_init(kv_full, 1);
-    mbar_init(q_full, 1);
-    mbar_init(q_empty, 1);
-    mbar_init(do_full, 1);
-    mbar_init(do_empty, 1);
-    mbar_init(s_full, 1);
-    mbar_init(p_full, kBwdComputeThreads);
-    mbar_init(mma2_done, 1);
-    mbar_init(dq_free, kBwdComputeThreads);
-    mbar_init(drain, 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&qd_full[s], 1);
+      mbar_init(&qd_empty[s], 1);
+      mbar_init(&rows_full[s], 1);
+      mbar_init(&rows_empty[s], 8);
+      mbar_init(&sd_full[s], 1);
+      mbar_init(&pd_full[s], 128);
+      mbar_init(&pd_done[s], 1);
+      mbar_init(&drain[s], 1);
+    }
     *abort_flag = 0;
     fence_barrier_init();
+    tma_prefetch_desc(&p.qmap);
+    tma_prefetch_desc(&p.kmap);
+    tma_prefetch_desc(&p.vmap);
+    tma_prefetch_desc(&p.domap);
   }
   if (warp == 1) {
     tmem_alloc(tmem_slot, 512);
@@ -1114,233 +1236,170 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1) masked_bwd_kernel(const __
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  // TMEM: S^T, then dQ, at 0; dP^T at 128; dV at 256; dK at 256 + 64 nd
   const uint32_t tmem = *tmem_slot;
-  const uint32_t t_dv = 256, t_dk = 256 + 64 * nd;
   pdl_wait();
-  // (key tile, sequence) in the plan's order, and the query tiles q0 .. q1 - 1 that see any of it (at
-  // least one, so that a tile that nobody sees takes the same path and gets zeros)
+  // (key tile, sequence) in the plan's order, and the query tiles q0 .. q1 - 1 that see any of it (at least
+  // one, so that a tile that nobody sees takes the same path and gets zeros)
   const bool plan_ok = plan_fits(p.plan, p.n_seq, p.S, p.err);
   const int4 entry = plan_ok ? p.plan.k_order[blockIdx.x / p.hkv] : make_int4(0, 0, 0, 0);
   const int kt = entry.x % n_t, b = entry.x / n_t;
-  const int q0 = entry.y, q1 = entry.z;
-  const int n_it = hpg * (q1 - q0);  // (query head of the group, query tile)
-
+  const int q0 = entry.y, n_it = hpg * (entry.z - q0);
   auto it_head = [&](int it) { return g * hpg + it % hpg; };
   auto it_qtile = [&](int it) { return q0 + it / hpg; };
 
   if (!plan_ok) {
-    // nothing was issued
+    // nothing is issued
   } else if (warp == 0) {
     if (lane == 0) {
       mbar_arrive_expect_tx(kv_full, 2 * nd * kChunk);
       for (int c = 0; c < nd; ++c) {
         tma_load_4d(sk + c * kChunk, &p.kmap, kv_full, 64 * c, g, kt * kTile, b);
-        tma_load_4d(sv + c * kChunk, &p.vmap, kv_full, 64 * c, g, kt * kTile, b);
+        tma_load_4d(sk + (2 + c) * kChunk, &p.vmap, kv_full, 64 * c, g, kt * kTile, b);
       }
-      // dO and Q have one buffer each and separate barriers: dO_(i+1) loads as soon as dV_i has
-      // read dO_i, Q_(i+1) once dK_i has read Q_i
-      int issued_do = 0, issued_q = 0;
-      for (int it = 0; it < n_it; ++it) {
-        const int h = it_head(it), qt = it_qtile(it);
-        if (it > 0 && !mbar_wait_soon(do_empty, (it - 1) & 1, abort_flag, p.err, DEV_TIMEOUT_PRODUCER)) break;
-        mbar_arrive_expect_tx(do_full, nd * kChunk);
-        for (int c = 0; c < nd; ++c) tma_load_4d(sdo + c * kChunk, &p.domap, do_full, 64 * c, h, qt * kTile, b);
-        issued_do = it + 1;
-        if (it > 0 && !mbar_wait_soon(q_empty, (it - 1) & 1, abort_flag, p.err, DEV_TIMEOUT_PRODUCER)) break;
-        mbar_arrive_expect_tx(q_full, nd * kChunk);
-        for (int c = 0; c < nd; ++c) tma_load_4d(sq + c * kChunk, &p.qmap, q_full, 64 * c, h, qt * kTile, b);
-        issued_q = it + 1;
+      int it = 0;
+      for (; it < n_it; ++it) {
+        const int s = it & 1;
+        if (!mbar_wait_soon(&qd_empty[s], ((it >> 1) & 1) ^ 1, abort_flag, p.err, DEV_TIMEOUT_PRODUCER)) break;
+        mbar_arrive_expect_tx(&qd_full[s], 2 * nd * kChunk);
+        uint8_t* st = sqd + s * 4 * kChunk;
+        for (int c = 0; c < nd; ++c) {
+          tma_load_4d(st + c * kChunk, &p.qmap, &qd_full[s], 64 * c, it_head(it), it_qtile(it) * kTile, b);
+          tma_load_4d(st + (2 + c) * kChunk, &p.domap, &qd_full[s], 64 * c, it_head(it), it_qtile(it) * kTile, b);
+        }
       }
-      mbar_wait_soon(kv_full, 0, nullptr, p.err, DEV_TIMEOUT_DRAIN);
-      if (issued_do > 0) mbar_wait_soon(do_full, (issued_do - 1) & 1, nullptr, p.err, DEV_TIMEOUT_DRAIN);
-      if (issued_q > 0) mbar_wait_soon(q_full, (issued_q - 1) & 1, nullptr, p.err, DEV_TIMEOUT_DRAIN);
+      // every copy lands before the CTA may exit
+      mbar_wait(kv_full, 0, nullptr, p.err, DEV_TIMEOUT_DRAIN);
+      for (int k = max(0, it - 2); k < it; ++k) mbar_wait(&qd_full[k & 1], (k >> 1) & 1, nullptr, p.err, DEV_TIMEOUT_DRAIN);
     }
   } else if (warp == 1) {
     if (lane == 0) {
-      const uint32_t id_kq = idesc_bf16(128, 128, 0, 0);       // S^T = K Q^T, dP^T = V dO^T
-      const uint32_t id_kd = idesc_bf16(128, 64 * nd, 0, 1);   // dV += P^T dO, dK += dS^T Q
-      const uint32_t id_qd = idesc_bf16(128, 64 * nd, 1, 1);   // dQ = dS K (dS read MN-major from dS^T)
-      const uint32_t ak = smem_u32(sk), av = smem_u32(sv), bq = smem_u32(sq), bdo = smem_u32(sdo);
-      const uint32_t apt = smem_u32(spt), adst = smem_u32(sdst);
+      const uint32_t id = idesc_bf16(128, 64, 0, 0);
+      const uint64_t dk0 = kmajor_desc(smem_u32(sk), 0), dv0 = dk0 + (2 * kChunk >> 4), dq0 = kmajor_desc(smem_u32(sqd), 0);
       bool ok = mbar_wait_soon(kv_full, 0, abort_flag, p.err, DEV_TIMEOUT_MMA);
-      for (int it = 0; ok && it < n_it; ++it) {
-        // dP^T (columns 128..255) needs only dO: it may run while the previous dQ is drained
-        if (!mbar_wait_soon(do_full, it & 1, abort_flag, p.err, DEV_TIMEOUT_MMA)) { ok = false; break; }
+      for (int t = 0; ok && t < 2 * n_it; ++t) {
+        const int it = t >> 1, s = it & 1, x = t & 1;
+        ok = (x == 1 || mbar_wait_soon(&qd_full[s], (it >> 1) & 1, abort_flag, p.err, DEV_TIMEOUT_MMA)) &&
+             (it == 0 || mbar_wait_soon(&pd_done[x], (it - 1) & 1, abort_flag, p.err, DEV_TIMEOUT_MMA));
+        if (!ok) break;
         tc_fence_after();
-        for (int t = 0; t < 4 * nd; ++t)
-          umma_bf16(tmem + 128, kmajor_desc(av, t), kmajor_desc(bdo, t), id_kq, t > 0 ? 1u : 0u);
-        if (!mbar_wait_soon(q_full, it & 1, abort_flag, p.err, DEV_TIMEOUT_MMA)) { ok = false; break; }
-        if (it > 0 && !mbar_wait_soon(dq_free, (it - 1) & 1, abort_flag, p.err, DEV_TIMEOUT_MMA)) { ok = false; break; }
-        tc_fence_after();
-        for (int t = 0; t < 4 * nd; ++t)
-          umma_bf16(tmem, kmajor_desc(ak, t), kmajor_desc(bq, t), id_kq, t > 0 ? 1u : 0u);
-        umma_commit(s_full);
-        if (!mbar_wait_soon(p_full, it & 1, abort_flag, p.err, DEV_TIMEOUT_MMA)) { ok = false; break; }
-        tc_fence_after();
-        for (int t = 0; t < 8; ++t)
-          umma_bf16(tmem + t_dv, kmajor_desc(apt, t), mnmajor_desc(bdo, t), id_kd, (it > 0 || t > 0) ? 1u : 0u);
-        umma_commit(do_empty);
-        for (int t = 0; t < 8; ++t)
-          umma_bf16(tmem + t_dk, kmajor_desc(adst, t), mnmajor_desc(bq, t), id_kd, (it > 0 || t > 0) ? 1u : 0u);
-        umma_commit(q_empty);
-        for (int t = 0; t < 8; ++t)
-          umma_bf16(tmem, mnmajor_desc(adst, t), mnmajor_desc(ak, t), id_qd, t > 0 ? 1u : 0u);
-        umma_commit(mma2_done);
+        const uint64_t bq = dq0 + s * (4 * kChunk >> 4) + x * (kChunk / 2 >> 4);
+        mma_kk_nd(nd, tmem + 64 * x, dk0, bq, id);
+        mma_kk_nd(nd, tmem + 128 + 64 * x, dv0, bq + (2 * kChunk >> 4), id);
+        umma_commit(&sd_full[x]);
       }
-      umma_commit(drain);
-      mbar_wait_soon(drain, 0, nullptr, p.err, DEV_TIMEOUT_DRAIN);
+      umma_commit(&drain[0]);
+      mbar_wait(&drain[0], 0, nullptr, p.err, DEV_TIMEOUT_DRAIN);
+    }
+  } else if (warp == 2) {
+    if (lane == 0) {
+      const uint32_t id = idesc_bf16(128, 64 * nd, 0, 1);  // P^T, dS^T in TMEM; dO, Q MN-major
+      const uint64_t dq0 = mnmajor_desc(smem_u32(sqd), 0);
+      bool ok = true;
+      for (int t = 0; ok && t < 2 * n_it; ++t) {
+        const int it = t >> 1, s = it & 1, x = t & 1;
+        ok = mbar_wait_soon(&pd_full[x], it & 1, abort_flag, p.err, DEV_TIMEOUT_MMA) &&
+             mbar_wait_soon(&qd_full[s], (it >> 1) & 1, abort_flag, p.err, DEV_TIMEOUT_MMA);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t bq = dq0 + s * (4 * kChunk >> 4) + x * 512;
+        mma_tm<4>(tmem + 256, tmem + 64 * x, bq + (2 * kChunk >> 4), id, t > 0);
+        mma_tm<4>(tmem + 384, tmem + 128 + 64 * x, bq, id, t > 0);
+        umma_commit(&pd_done[x]);
+        if (x == 1) umma_commit(&qd_empty[s]);
+      }
+      umma_commit(&drain[1]);
+      mbar_wait(&drain[1], 0, nullptr, p.err, DEV_TIMEOUT_DRAIN);
+    }
+  } else if (warp == 3) {
+    bool ok = true;
+    for (int it = 0; ok && it < n_it; ++it) {
+      const int s = it & 1, qt = it_qtile(it);
+      float l[4], d[4];
+      int2 see[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int qp = qt * kTile + 32 * k + lane;
+        const int64_t row = (int64_t)b * p.S + qp, at = (int64_t)it_head(it) * T + row;
+        const bool in = qp < p.S;
+        see[k] = in ? make_int2(p.plan.lo[row], p.plan.hi[row]) : make_int2(0, 0);
+        // a row that sees nothing or lies past the sequence: 2^-inf, P = 0 whatever its score
+        l[k] = see[k].x < see[k].y ? -p.lse[at] * kLog2e : -INFINITY;
+        d[k] = in ? -p.delta[at] : 0.f;
+      }
+      const int4 r = p.plan.q_range[b * n_t + qt];
+      ok = __all_sync(0xffffffffu, mbar_wait_soon(&rows_empty[s], ((it >> 1) & 1) ^ 1, abort_flag, p.err, DEV_TIMEOUT_PRODUCER));
+      if (!ok) break;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        s_lse[s * 128 + 32 * k + lane] = l[k];
+        s_del[s * 128 + 32 * k + lane] = d[k];
+        s_see[s * 128 + 32 * k + lane] = see[k];
+      }
+      if (lane == 0) s_whole[s] = r.z <= kt && kt < r.w;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&rows_full[s]);
     }
   } else {
-    // Eight compute warps: warp w reads TMEM lanes 32 (w % 4) .. + 31 and handles one half of the
-    // columns (query columns of S^T / dP^T, head-dimension columns of dQ, dK or dV).
-    const int cw = warp - 2;
-    const int quarter = warp & 3;
-    const int half = cw >> 2;
-    const int r = quarter * 32 + lane;           // key row of the tile (S^T, dP^T, dV, dK) or query row (dQ)
+    const int quarter = warp & 3, x = (warp - 4) >> 2;  // x: buffer, half of each query tile
+    const int r = quarter * 32 + lane;                  // key row of the tile
     const int kpos = kt * kTile + r;
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
-    const float log2e = kLog2e;
-    // This warp's dQ boxes: head-dimension columns 64 half .. + 31 over its rows of P^T chunk `half`,
-    // columns 64 half + 32 .. + 63 over its rows of dS^T chunk `half`: the same shared memory the
-    // warp itself rewrites next (P^T and dS^T rows r, columns 64 half .. + 63), so one wait of its
-    // own bulk reads orders the two.
-    uint8_t* box0 = spt + half * kChunk + quarter * 32 * 128;
-    uint8_t* box1 = sdst + half * kChunk + quarter * 32 * 128;
-    // LSE and delta of a query tile are staged in shared memory (two buffers by iteration parity),
-    // read from global memory one iteration ahead
-    float n_lse = 0.f, n_delta = 0.f;
-    int2 n_see = make_int2(0, 0);
-    auto fetch = [&](int it) {
-      const int qp = it_qtile(it) * kTile + r;
-      const int64_t at = (int64_t)it_head(it) * T + (int64_t)b * p.S + qp;
-      n_lse = qp < p.S ? p.lse[at] * log2e : 0.f;
-      n_delta = qp < p.S ? p.delta[at] : 0.f;
-      const int64_t row = (int64_t)b * p.S + qp;
-      n_see = qp < p.S ? make_int2(p.plan.lo[row], p.plan.hi[row]) : make_int2(0, 0);
-      if (n_see.x >= n_see.y) n_lse = 0.f;  // a row that sees nothing (its lse is -inf): masked below
-    };
-    if (half == 0 && n_it > 0) fetch(0);
+    const uint32_t s_tm = tmem + lane_off + 64 * x, dp_tm = s_tm + 128;
     bool ok = true;
     for (int it = 0; it < n_it; ++it) {
-      const int h = it_head(it), qt = it_qtile(it);
-      float* lse_it = s_lse + (it & 1) * 128;
-      float* delta_it = s_delta + (it & 1) * 128;
-      int2* see_it = s_see + (it & 1) * 128;
-      if (half == 0) {
-        lse_it[r] = n_lse;
-        delta_it[r] = n_delta;
-        see_it[r] = n_see;
-      }
-      // this iteration's LSE and delta are visible; `ok` is the same in every compute thread
-      ok = bar_and_bwd(ok);
+      const int s = it & 1, qt0 = it_qtile(it) * kTile + 64 * x;
+      ok = __all_sync(0xffffffffu, mbar_wait_soon(&rows_full[s], (it >> 1) & 1, abort_flag, p.err, DEV_TIMEOUT_EPILOGUE) &&
+                                       mbar_wait_soon(&sd_full[x], it & 1, abort_flag, p.err, DEV_TIMEOUT_EPILOGUE));
       if (!ok) break;
-      if (half == 0 && it + 1 < n_it) fetch(it + 1);
-      ok = __all_sync(0xffffffffu, mbar_wait_soon(s_full, it & 1, abort_flag, p.err, DEV_TIMEOUT_EPILOGUE));
-      if (ok) {
-        tc_fence_after();
-        // this warp's previous dQ reductions have read its boxes (rewritten below)
-        if (lane == 0) bulk_wait_read<0>();
-        __syncwarp();
-        // a query tile all of whose rows see all of this key tile needs no masks
-        const int4 q_see = p.plan.q_range[b * n_t + qt];
-        const bool whole = q_see.z <= kt && kt < q_see.w;
-        const float slope = BIAS ? p.slopes[h] * log2e : 0.f;
-        const float away = (float)(qt * kTile - kpos);
-        auto soft_chunk = [&](int c, auto masked) {
-          uint32_t st[32], dp[32];
-          __syncwarp();
-          tmem_ld32(tmem + lane_off + 32 * c, st);
-          tmem_ld32(tmem + lane_off + 128 + 32 * c, dp);
-          tmem_ld_wait_regs(st);
-          regs_after_wait(dp);
-          if (CAP) tanh_n(st, p.cap_mul);
-          uint32_t pw[16], dw[16];
+      tc_fence_after();
+      const bool part = !s_whole[s];
+      const float slope = BIAS ? p.slopes[it_head(it)] * kLog2e : 0.f;
+      const int side = qt0 >= kt * kTile + 32 * quarter + 31 ? -1 : 0;
+#pragma unroll 1
+      for (int c = 0; c < 2; ++c) {
+        uint32_t sv[32], dp[32], pw[16], dw[16];
+        tmem_ld32(s_tm + 32 * c, sv);
+        tmem_ld32(dp_tm + 32 * c, dp);
+        tmem_ld_wait_regs(sv);
+        regs_after_wait(dp);
+        const int col = s * 128 + 64 * x + 32 * c;
+        uint32_t see = 0xffffffffu;
+        if (part) {
+          see = 0;
 #pragma unroll
-          for (int i = 0; i < 32; i += 4) {
-            const float4 l4 = *reinterpret_cast<const float4*>(lse_it + 32 * c + i);
-            const float4 d4 = *reinterpret_cast<const float4*>(delta_it + 32 * c + i);
-            const float lv[4] = {l4.x, l4.y, l4.z, l4.w}, dl[4] = {d4.x, d4.y, d4.z, d4.w};
-            float pv[4], dv4[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int col = 32 * c + i + e;
-              float pe = ex2(score<BIAS>(st[i + e], p.mul, slope, away + (float)col) - lv[e]);
-              if (decltype(masked)::value) {
-                const int2 see = see_it[col];
-                pe = (see.x <= kpos && kpos < see.y) ? pe : 0.f;
-              }
-              pv[e] = pe;
-              dv4[e] = pe * (__uint_as_float(dp[i + e]) - dl[e]);
-              if (CAP) dv4[e] *= fmaf(-__uint_as_float(st[i + e]), __uint_as_float(st[i + e]), 1.f);
-            }
-            pw[i / 2] = pack2(pv[0], pv[1]);
-            pw[i / 2 + 1] = pack2(pv[2], pv[3]);
-            dw[i / 2] = pack2(dv4[0], dv4[1]);
-            dw[i / 2 + 1] = pack2(dv4[2], dv4[3]);
+          for (int e = 0; e < 32; ++e) {
+            const int2 w = s_see[col + e];
+            see |= (uint32_t)(w.x <= kpos && kpos < w.y) << e;
           }
-          st_swizzled_row32(spt, r, 32 * c, pw);
-          st_swizzled_row32(sdst, r, 32 * c, dw);
-        };
-        for (int c = 2 * half; c < 2 * half + 2; ++c) {
-          if (whole) soft_chunk(c, std::false_type{});
-          else soft_chunk(c, std::true_type{});
         }
-        fence_proxy_async_smem();
-        tc_fence_before();
-        mbar_arrive(p_full);
-        ok = __all_sync(0xffffffffu, mbar_wait_soon(mma2_done, it & 1, abort_flag, p.err, DEV_TIMEOUT_EPILOGUE));
+        grad32<CAP, BIAS, false, true>(sv, dp, p.mul, p.cap_mul, slope, (float)(kpos - qt0 - 32 * c), side, part, see, 0.f,
+                                       0.f, s_lse + col, s_del + col, pw, dw);
+        tmem_st16(s_tm + 16 * c, pw);
+        tmem_st16(dp_tm + 16 * c, dw);
       }
-      if (ok) {
-        // dQ of this (head, query tile), lane r = query row qt * 128 + r: out of TMEM (which the next
-        // S^T may then overwrite), scaled into this warp's boxes, added to the accumulator by bulk
-        // reductions of 32 rows x 32 columns
-        tc_fence_after();
-        uint32_t v0[32], v1[32];
-        __syncwarp();
-        tmem_ld32(tmem + lane_off + 64 * half, v0);
-        tmem_ld32(tmem + lane_off + 64 * half + 32, v1);
-        tmem_ld_wait_regs(v0);
-        regs_after_wait(v1);
-        tc_fence_before();
-        mbar_arrive(dq_free);
-        st_dq_box_row(box0, lane, v0, p.scale);
-        st_dq_box_row(box1, lane, v1, p.scale);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0 && 64 * half < p.hd) {
-          tma_reduce_add_4d(&p.dqmap, box0, 64 * half, h, qt * kTile + 32 * quarter, b);
-          if (64 * half + 32 < p.hd) tma_reduce_add_4d(&p.dqmap, box1, 64 * half + 32, h, qt * kTile + 32 * quarter, b);
-          bulk_commit();
-        }
-      }
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(&pd_full[x]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&rows_empty[s]);
     }
-    // the reductions have completed before the CTA ends (and before its shared memory is reused)
-    if (lane == 0) bulk_wait_all();
-    // dK (half 1), dV (half 0) of this key tile: the MMAs of the last iteration have completed
-    // (mma2_done); every lane takes part in the (warp-collective) loads, rows past the sequence
-    // store nothing
+    // dV (first group), dK (second) once every product is done
+    if (ok) ok = __all_sync(0xffffffffu, mbar_wait_soon(&drain[1], 0, abort_flag, p.err, DEV_TIMEOUT_EPILOGUE));
     if (ok) {
       tc_fence_after();
-      const bool kok = kpos < p.S;
-      const int64_t row = (int64_t)b * p.S + kpos;
-      const int which = half;
-      __nv_bfloat16* out = (which ? p.dk + row * p.lddk : p.dv + row * p.lddv) + (int64_t)g * p.hd;
-      const float mul = which ? p.scale : 1.f;
+      const int64_t row0 = (int64_t)b * p.S + kt * kTile + 32 * quarter;
+      const int n_rows = p.S - kt * kTile - 32 * quarter;
+      const int64_t ld = x ? p.lddk : p.lddv;
+      __nv_bfloat16* out = (x ? p.dk : p.dv) + row0 * ld + (int64_t)g * p.hd;
+      const float mul = x ? p.scale : 1.f;
+#pragma unroll 1
       for (int c = 0; c < 2 * nd; ++c) {
-        uint32_t v[32];
-        __syncwarp();
-        tmem_ld32(tmem + lane_off + (which ? t_dk : t_dv) + 32 * c, v);
+        uint32_t v[32], w[16];
+        tmem_ld32(tmem + lane_off + 256 + 128 * x + 32 * c, v);
         tmem_ld_wait_regs(v);
-        if (!kok || 32 * c >= p.hd) continue;
-        uint32_t w[16];
 #pragma unroll
-        for (int i = 0; i < 32; i += 2) w[i / 2] = pack2(__uint_as_float(v[i]) * mul, __uint_as_float(v[i + 1]) * mul);
-        uint4* dst = reinterpret_cast<uint4*>(out + 32 * c);
-        const int nv = min(32, p.hd - 32 * c) / 8;
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          if (q < nv) dst[q] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+        for (int e = 0; e < 32; e += 2) w[e / 2] = pack2(__uint_as_float(v[e]) * mul, __uint_as_float(v[e + 1]) * mul);
+        store_rows32(out + 32 * c, ld, w, n_rows, p.hd - 32 * c);
       }
     }
   }
@@ -1358,7 +1417,8 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1) masked_bwd_kernel(const __
 // Shared memory of a launch: sized for head_dim 128 whatever the head dimension, which also keeps
 // one CTA per SM (each CTA allocates all 512 TMEM columns).
 int fwd_smem() { return 1024 + 12 * kChunk + 256; }
-int bwd_smem() { return 1024 + 8 * kChunk + 4 * kChunk + 2 * 256 * 4 + 256 * 8 + 256; }
+int dq_smem() { return 1024 + 12 * kChunk + 1024 + 256; }
+int dkv_smem() { return 1024 + 12 * kChunk + 4096 + 16 + 256; }
 
 // Raises a kernel's shared-memory limit once per device.
 template <typename K>
@@ -1391,26 +1451,18 @@ int fwd_launch(const MaskedFwdParams& p, cudaStream_t s) {
   return 0;
 }
 
-int delta_smem() { return 1024 + 12 * kChunk + 512 + 256; }
-
-template <bool CAP, bool BIAS>
-int delta_launch(const MaskedDeltaParams& p, cudaStream_t s) {
-  static std::atomic<uint64_t> done{0};
-  if (!smem_limit(masked_delta_kernel<CAP, BIAS>, delta_smem(), done)) return 5;
-  const int n_sm = sm_count();
-  if (n_sm <= 0) return 5;
-  const int64_t n_units = plan_tiles(p.n_seq, p.S) * p.hq;
-  launch_kernel(masked_delta_kernel<CAP, BIAS>, (unsigned)std::min<int64_t>(n_units, n_sm), kAttnThreads, delta_smem(), s, p);
-  if (launch_failed("sl_attention_masked")) return 5;
-  note_launch();
-  return 0;
-}
-
 template <bool CAP, bool BIAS>
 int bwd_launch(const MaskedBwdParams& p, cudaStream_t s) {
-  static std::atomic<uint64_t> done{0};
-  if (!smem_limit(masked_bwd_kernel<CAP, BIAS>, bwd_smem(), done)) return 5;
-  launch_kernel(masked_bwd_kernel<CAP, BIAS>, (unsigned)(plan_tiles(p.n_seq, p.S) * p.hkv), kAttnBwdThreads, bwd_smem(), s, p);
+  static std::atomic<uint64_t> done_q{0}, done_kv{0};
+  if (!smem_limit(masked_dq_kernel<CAP, BIAS>, dq_smem(), done_q) ||
+      !smem_limit(masked_dkv_kernel<CAP, BIAS>, dkv_smem(), done_kv))
+    return 5;
+  const int n_sm = sm_count();
+  if (n_sm <= 0) return 5;
+  launch_kernel(masked_dq_kernel<CAP, BIAS>, (unsigned)std::min(p.n_units, n_sm), kBwdThreads, dq_smem(), s, p);
+  if (launch_failed("sl_attention_masked")) return 5;
+  note_launch();
+  launch_kernel(masked_dkv_kernel<CAP, BIAS>, (unsigned)(plan_tiles(p.n_seq, p.S) * p.hkv), kBwdThreads, dkv_smem(), s, p);
   if (launch_failed("sl_attention_masked")) return 5;
   note_launch();
   return 0;
@@ -1474,22 +1526,22 @@ int attention_masked_fwd(const MaskedArgs& a, cudaStream_t s) {
   return a.slopes ? fwd_launch<false, true>(p, s) : fwd_launch<false, false>(p, s);
 }
 
+size_t attention_masked_scratch(int n_seq, int S, int hq) { return (size_t)n_seq * S * hq * 4; }
+
 int attention_masked_bwd(const MaskedArgs& a, cudaStream_t s) {
   MaskedBwdParams p;
   memset(&p, 0, sizeof(p));
   if (!head_map(&p.qmap, a.q, a.ldq, a.n_seq, a.S, a.hq, a.hd) || !head_map(&p.kmap, a.k, a.ldk, a.n_seq, a.S, a.hkv, a.hd) ||
       !head_map(&p.vmap, a.v, a.ldv, a.n_seq, a.S, a.hkv, a.hd) || !head_map(&p.domap, a.d_o, a.lddo, a.n_seq, a.S, a.hq, a.hd))
     return 2;
-  const int64_t T = (int64_t)a.n_seq * a.S;
-  float* dq_acc = static_cast<float*>(a.scratch);
-  float* delta = reinterpret_cast<float*>(static_cast<uint8_t*>(a.scratch) + ((T * a.hq * a.hd * 4 + 255) & ~int64_t(255)));
-  if (!dq_acc_map(&p.dqmap, dq_acc, a.n_seq, a.S, a.hq, a.hd)) return 2;
   carve_plan(const_cast<void*>(a.plan), a.n_seq, a.S, &p.plan);
   p.slopes = a.slopes;
   p.lse = a.lse;
-  p.delta = delta;
+  p.delta = static_cast<float*>(a.scratch);
+  p.dq = static_cast<__nv_bfloat16*>(a.dq);
   p.dk = static_cast<__nv_bfloat16*>(a.dk);
   p.dv = static_cast<__nv_bfloat16*>(a.dv);
+  p.lddq = a.lddq;
   p.lddk = a.lddk;
   p.lddv = a.lddv;
   p.n_seq = a.n_seq;
@@ -1498,27 +1550,11 @@ int attention_masked_bwd(const MaskedArgs& a, cudaStream_t s) {
   p.hkv = a.hkv;
   p.hd = a.hd;
   p.nd = (a.hd + 63) / 64;
+  p.n_units = (int)(plan_tiles(a.n_seq, a.S) * a.hq);
   score_constants(a, &p.scale, &p.mul, &p.cap_mul);
   p.err = a.err;
-  MaskedDeltaParams d;
-  memset(&d, 0, sizeof(d));
-  d.qmap = p.qmap, d.kmap = p.kmap, d.vmap = p.vmap, d.domap = p.domap;
-  d.plan = p.plan, d.slopes = p.slopes, d.lse = p.lse, d.delta = delta, d.dq_acc = dq_acc;
-  d.n_seq = p.n_seq, d.S = p.S, d.hq = p.hq, d.hkv = p.hkv, d.hd = p.hd, d.nd = p.nd;
-  d.mul = p.mul, d.cap_mul = p.cap_mul, d.err = p.err;
-  int rc = a.cap > 0.f ? (a.slopes ? delta_launch<true, true>(d, s) : delta_launch<true, false>(d, s))
-                       : (a.slopes ? delta_launch<false, true>(d, s) : delta_launch<false, false>(d, s));
-  if (rc) return rc;
-  rc = a.cap > 0.f ? (a.slopes ? bwd_launch<true, true>(p, s) : bwd_launch<true, false>(p, s))
-                             : (a.slopes ? bwd_launch<false, true>(p, s) : bwd_launch<false, false>(p, s));
-  if (rc) return rc;
-  // dQ: the dense [T, hq hd] accumulator to bf16 rows
-  const int64_t n = (int64_t)a.hq * a.hd;
-  launch_kernel(masked_dq_cast_kernel, (unsigned)((T * n / 4 + 255) / 256), 256, 0, s, (const float*)dq_acc, T, n,
-                static_cast<__nv_bfloat16*>(a.dq), a.lddq);
-  if (launch_failed("sl_attention_masked")) return 5;
-  note_launch();
-  return 0;
+  if (a.cap > 0.f) return a.slopes ? bwd_launch<true, true>(p, s) : bwd_launch<true, false>(p, s);
+  return a.slopes ? bwd_launch<false, true>(p, s) : bwd_launch<false, false>(p, s);
 }
 
 }  // namespace sl

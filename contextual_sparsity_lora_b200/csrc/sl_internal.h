@@ -286,11 +286,12 @@ struct MaskedArgs {
   int64_t lddo;
   void *dq, *dk, *dv;
   int64_t lddq, lddk, lddv;
-  void* scratch;              // attention_bwd_scratch() bytes
+  void* scratch;              // attention_masked_scratch() bytes: D per query row and head
 };
 // Both return 0, 2 (tensor map), 5 (launch).
 int attention_masked_fwd(const MaskedArgs& a, cudaStream_t s);
 int attention_masked_bwd(const MaskedArgs& a, cudaStream_t s);
+size_t attention_masked_scratch(int n_seq, int S, int hq);
 
 // ---- criterion variants (sl_criteria.cu)
 // Wanda-style channel scores s_i = sum_p sum_j |W_p[i, j]| ||x[:, j]||_2 over n_ctx rows of x

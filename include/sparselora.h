@@ -460,9 +460,9 @@ SL_API sl_status sl_qk_norm_rope_bwd(const void* dyq, int64_t lddyq, const void*
  *     lse (fp32 [n_q_heads][T]) = log sum_j e^(t_ij). A row that sees nothing: o = 0, lse = -inf.
  *     scale = 0 means 1 / sqrt(head_dim); softcap = 0 means no cap. Heads as in sl_attention_fwd.
  *   sl_attention_masked_bwd: dq, dk, dv of the loss whose gradient at o is d_o, from the forward's lse (the
- *     rounded o is not used: the rows' sums of P dP are formed again in fp32; the slopes are constants). Rows that see nothing give and get zeros. dq is summed across key
- *     tiles in fp32 reductions whose order varies between runs (its last bits may differ); dk and dv are
- *     run-to-run identical. Workspace as sl_attention_bwd (the forward needs only the header).
+ *     rounded o is not used: the rows' sums of P dP are formed again in fp32; the slopes are constants). Rows
+ *     that see nothing give and get zeros. All results are run-to-run identical. Workspace: 4 n_q_heads T bytes
+ *     past the header (the forward needs only the header).
  * q, o, d_o, dq: bf16 [T, n_q_heads * head_dim]; k, v, dk, dv: bf16 [T, n_kv_heads * head_dim], each with its
  * own leading dimension (slices of one projection's output need no copy). Values have to be finite in every
  * row, those that nobody sees too (a product of tiles multiplies them by zero). head_dim in [8, 128], a
