@@ -21,7 +21,7 @@ namespace sl {
 namespace {
 
 constexpr int kFwdThreads = 384;  // warp 0 TMA, warps 1 and 2 MMA (warp 1 allocates TMEM), warps 4..11 softmax
-constexpr int kBwdThreads = 384;  // the same; dk, dv: warp 3 reads the query rows
+constexpr int kBwdThreads = 640;  // the same with compute warps 4..19; dk, dv: warp 3 reads the query rows
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -259,12 +259,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-__device__ __forceinline__ float min3(float a, float b, float c) {
-  float r;
-  asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-
 // tanh of N raw products times mul (= scale / cap), in place. Up to 0.75 an odd polynomial (a least-maximum
 // fit of tanh(u) / u in u^2, relative error 3e-8, 1.6e-7 with fp32 arithmetic): 7 multiply-adds, and small
 // scores keep their relative exactness. Above, for the whole warp: 1 - 2 / (2^(2 log2(e) u) + 1), error
@@ -272,13 +266,10 @@ __device__ __forceinline__ float min3(float a, float b, float c) {
 // tanh.approx would be off by 5e-4 of the value.
 template <int N>
 __device__ __forceinline__ void tanh_n(uint32_t (&v)[N], float mul) {
-  float hi = 0.f, lo = 0.f;
+  float top = 0.f;
 #pragma unroll
-  for (int e = 0; e < N; e += 2) {
-    hi = max3(hi, __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
-    lo = min3(lo, __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
-  }
-  if (__any_sync(0xffffffffu, !(fmaxf(hi, -lo) * mul <= 0.75f))) {
+  for (int e = 0; e < N; e += 2) top = fmaxf(fmaxf(top, fabsf(__uint_as_float(v[e]))), fabsf(__uint_as_float(v[e + 1])));
+  if (__any_sync(0xffffffffu, !(top * mul <= 0.75f))) {
     const float mul2x = mul * (2.f * kLog2e);
 #pragma unroll
     for (int e = 0; e < N; ++e)
@@ -335,9 +326,8 @@ __device__ __forceinline__ uint32_t see_bits(int first, int end) {
   return a >= b ? 0u : (0xffffffffu << a) & (0xffffffffu >> (32 - b));
 }
 
-// -inf outside columns [first, end)
-__device__ __forceinline__ void mask32(uint32_t (&v)[32], int first, int end) {
-  const uint32_t see = see_bits(first, end);
+// -inf in the columns whose bit is 0
+__device__ __forceinline__ void mask32(uint32_t (&v)[32], uint32_t see) {
 #pragma unroll
   for (int e = 0; e < 32; ++e)
     if (!(see & (1u << e))) v[e] = 0xff800000u;
@@ -370,11 +360,20 @@ __device__ __forceinline__ void mma_kk_nd(int nd, uint32_t d, uint64_t a, uint64
   if (nd == 2) mma_kk<8>(d, a, b, id);
   else mma_kk<4>(d, a, b, id);
 }
-// A in TMEM (8 columns per step), B MN-major (16 token rows, 2 KB, per step); N steps over tokens:
-template <int N>
+// A in TMEM (8 columns per step, STRIDE columns from one 32-element piece to the next), B MN-major (16 token rows, 2 KB,
+// per step); N steps over tokens:
+template <int N, int STRIDE = 16>
 __device__ __forceinline__ void mma_tm(uint32_t d, uint32_t a, uint64_t b, uint32_t id, bool add) {
 #pragma unroll
-  for (int k = 0; k < N; ++k) umma_bf16_ts(d, a + 8 * k, b + k * 128, id, (k > 0 || add) ? 1u : 0u);
+  for (int k = 0; k < N; ++k)
+    umma_bf16_ts(d, a + 8 * (k & 1) + STRIDE * (k >> 1), b + k * 128, id, (k > 0 || add) ? 1u : 0u);
+}
+
+// One arrival for the whole warp (32 of its threads' own would take turns at the barrier's word, 512 of a block longer than
+// the step that they end): after every lane's tensor-memory accesses are complete and fenced.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
 }
 
 struct MaskedFwdParams {
@@ -404,13 +403,13 @@ struct MaskedBwdParams {
   int* err;
 };
 
-// Barrier of the 256 threads of the compute warps that also returns whether `ok` holds in all of them.
+// Barrier of the 512 threads of the backward's compute warps that also returns whether `ok` holds in all of them.
 __device__ __forceinline__ bool bar_and_compute(bool ok) {
   uint32_t all;
   asm volatile(
       "{\n\t.reg .pred q, a;\n\t"
       "setp.ne.u32 q, %1, 0;\n\t"
-      "bar.red.and.pred a, 1, 256, q;\n\t"
+      "bar.red.and.pred a, 1, 512, q;\n\t"
       "selp.u32 %0, 1, 0, a;\n\t}"
       : "=r"(all)
       : "r"((uint32_t)ok)
@@ -426,7 +425,9 @@ __device__ __forceinline__ bool bar_and_compute(bool ok) {
 // issue the products of stream 0 and 1; warps 4-7 and 8-11 are the softmax of stream 0 and 1, a query row per thread. A step is
 // half a key tile (64 keys): each stream has two S buffers in TMEM, so while the softmax works on step h, S of step h + 1
 // is there or on its way, and the order of a stream's products is O_x += P_x V of step h, S_x of step h + 2 (into the same
-// buffer). With whole tiles and one S buffer per stream the softmax waited for a P V and an S in
+// buffer). Keys run from the last to the first: with a bias by distance the largest scores mostly come first, and O
+// is rescaled rarely (from the first key on, steep slopes rescaled it in every step: 1076 instead of 758 us at 8192
+// tokens). With whole tiles and one S buffer per stream the softmax waited for a P V and an S in
 // each step, 40% of its time. P replaces S in TMEM (bf16, the first operand of P V) and never passes through
 // shared memory. Each stream has an issuing warp of its own: one thread for both is busy with waits and commits for as long
 // as with products, and the tensor cores, which queue about five, run dry. TMEM: S_x / P_x of step h at 128 x + 64 (h & 1), O_x at 256 + 128 x.
@@ -465,44 +466,6 @@ __device__ __forceinline__ Unit unit_of(const MaskedFwdParams& p, int u) {
   }
   return r;
 }
-
-// Steps of a CTA in order: (unit, key tile, half). Keys run from the last to the first: with a bias by distance the
-// largest scores mostly come first, and O is rescaled rarely (from the first key on, steep slopes rescaled it in every
-// step: 1076 instead of 758 us at 8192 tokens). The next unit is looked up while this one runs.
-struct Walk {
-  Unit un, nx;
-  int i, j, t;  // number of the unit in this CTA, key tile, number of the step in this CTA (t & 1: the tile's half)
-  bool live, more;
-  __device__ __forceinline__ void look(const MaskedFwdParams& p) {
-    const int u = unit_number(i + 1);
-    more = u < p.n_units;
-    if (more) nx = unit_of(p, u);
-  }
-  __device__ __forceinline__ void start(const MaskedFwdParams& p, bool ok) {
-    i = t = 0;
-    live = ok && unit_number(0) < p.n_units;
-    if (live) {
-      un = unit_of(p, unit_number(0));
-      j = un.j1 - 1;
-      look(p);
-    }
-  }
-  __device__ __forceinline__ bool first() const { return j == un.j1 - 1 && !(t & 1); }
-  __device__ __forceinline__ bool last() const { return j == un.j0 && (t & 1); }
-  __device__ __forceinline__ int stage() const { return (t >> 1) & 1; }       // of K and V
-  __device__ __forceinline__ uint32_t phase() const { return (t >> 2) & 1; }  // of that stage
-  __device__ __forceinline__ void next(const MaskedFwdParams& p) {
-    if (++t & 1) return;
-    if (--j >= un.j0) return;
-    live = more;
-    if (live) {
-      ++i;
-      un = nx;
-      j = un.j1 - 1;
-      look(p);
-    }
-  }
-};
 
 // Each thread of the warp writes 16 consecutive 32-bit columns of its TMEM lane.
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
@@ -558,13 +521,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1) masked_fwd_kernel(const __grid
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + 12 * kChunk);
   uint64_t* q_full = bars;         // [2] by stream
   uint64_t* q_empty = bars + 2;    // [2]
-  uint64_t* k_full = bars + 4;     // [2] by stage
-  uint64_t* k_empty = bars + 6;    // [2]
-  uint64_t* v_full = bars + 8;     // [2]
-  uint64_t* v_empty = bars + 10;   // [2]
+  uint64_t* kv_full = bars + 4;    // [2] by stage
+  uint64_t* kv_empty = bars + 6;   // [2]
   uint64_t* s_full = bars + 12;    // [2 x + buffer]
   uint64_t* p_full = bars + 16;    // [2 x + buffer]
-  uint64_t* pv_done = bars + 20;   // [2] by stream
+  uint64_t* pv_done = bars + 20;   // [2] by stream: P V of a unit's last two steps
   uint64_t* drain = bars + 22;     // [2] by stream
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 24);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -575,15 +536,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1) masked_fwd_kernel(const __grid
     for (int s = 0; s < 2; ++s) {
       mbar_init(&q_full[s], 1);
       mbar_init(&q_empty[s], 1);
-      mbar_init(&k_full[s], 1);
-      mbar_init(&k_empty[s], 2);  // both streams
-      mbar_init(&v_full[s], 1);
-      mbar_init(&v_empty[s], 2);
+      mbar_init(&kv_full[s], 1);
+      mbar_init(&kv_empty[s], 2);  // both streams
       mbar_init(&pv_done[s], 1);
     }
     for (int s = 0; s < 4; ++s) {
       mbar_init(&s_full[s], 1);
-      mbar_init(&p_full[s], 128);
+      mbar_init(&p_full[s], 4);
     }
     mbar_init(&drain[0], 1);
     mbar_init(&drain[1], 1);
@@ -606,39 +565,37 @@ __global__ void __launch_bounds__(kFwdThreads, 1) masked_fwd_kernel(const __grid
 
   if (warp == 0) {
     if (lane == 0) {
-      Walk w;
-      int nq = 0, nk = 0, nv = 0;  // loads issued (Q: of both streams)
-      for (w.start(p, plan_ok); w.live; w.next(p)) {
-        if (w.t & 1) continue;  // a tile's second half came with its first
-        const int g = w.un.h0 / hpg, s = w.stage();
-        if (w.first()) {
-          bool ok = true;
-          for (int x = 0; x < 2 && ok; ++x) {
-            if (w.i > 0) ok = mbar_wait_soon(&q_empty[x], (w.i - 1) & 1, abort_flag, p.err, DEV_TIMEOUT_PRODUCER);
-            if (!ok) break;
-            mbar_arrive_expect_tx(&q_full[x], nd * kChunk);
-            for (int c = 0; c < nd; ++c)
-              tma_load_4d(sq + (2 * x + c) * kChunk, &p.qmap, &q_full[x], 64 * c, w.un.h(x), w.un.qt(x) * kTile, w.un.b);
-            if (x == 1) ++nq;
-          }
+      Unit un, nx;
+      bool ok = plan_ok, live = plan_ok && unit_number(0) < p.n_units;
+      int i = 0, t = 0;  // units and key tiles loaded
+      if (live) nx = unit_of(p, unit_number(0));
+      for (; ok && live; ++i) {
+        un = nx;
+        live = unit_number(i + 1) < p.n_units;
+        if (live) nx = unit_of(p, unit_number(i + 1));
+        const int g = un.h0 / hpg;
+        for (int x = 0; x < 2 && ok; ++x) {
+          if (i > 0) ok = mbar_wait_soon(&q_empty[x], (i - 1) & 1, abort_flag, p.err, DEV_TIMEOUT_PRODUCER);
           if (!ok) break;
+          mbar_arrive_expect_tx(&q_full[x], nd * kChunk);
+          for (int c = 0; c < nd; ++c)
+            tma_load_4d(sq + (2 * x + c) * kChunk, &p.qmap, &q_full[x], 64 * c, un.h(x), un.qt(x) * kTile, un.b);
         }
-        if (!mbar_wait_soon(&k_empty[s], w.phase() ^ 1, abort_flag, p.err, DEV_TIMEOUT_PRODUCER)) break;
-        mbar_arrive_expect_tx(&k_full[s], nd * kChunk);
-        for (int c = 0; c < nd; ++c)
-          tma_load_4d(sk + (2 * s + c) * kChunk, &p.kmap, &k_full[s], 64 * c, g, w.j * kTile, w.un.b);
-        ++nk;
-        if (!mbar_wait_soon(&v_empty[s], w.phase() ^ 1, abort_flag, p.err, DEV_TIMEOUT_PRODUCER)) break;
-        mbar_arrive_expect_tx(&v_full[s], nd * kChunk);
-        for (int c = 0; c < nd; ++c)
-          tma_load_4d(sv + (2 * s + c) * kChunk, &p.vmap, &v_full[s], 64 * c, g, w.j * kTile, w.un.b);
-        ++nv;
+        for (int j = un.j1 - 1; ok && j >= un.j0; --j, ++t) {
+          const int s = t & 1;
+          ok = mbar_wait_soon(&kv_empty[s], ((t >> 1) & 1) ^ 1, abort_flag, p.err, DEV_TIMEOUT_PRODUCER);
+          if (!ok) break;
+          mbar_arrive_expect_tx(&kv_full[s], 2 * nd * kChunk);
+          for (int c = 0; c < nd; ++c)
+            tma_load_4d(sk + (2 * s + c) * kChunk, &p.kmap, &kv_full[s], 64 * c, g, j * kTile, un.b);
+          for (int c = 0; c < nd; ++c)
+            tma_load_4d(sv + (2 * s + c) * kChunk, &p.vmap, &kv_full[s], 64 * c, g, j * kTile, un.b);
+        }
       }
-      // every copy lands before the CTA may exit
-      if (nq > 0)
-        for (int x = 0; x < 2; ++x) mbar_wait(&q_full[x], (nq - 1) & 1, nullptr, p.err, DEV_TIMEOUT_DRAIN);
-      for (int t = max(0, nk - 2); t < nk; ++t) mbar_wait(&k_full[t & 1], (t >> 1) & 1, nullptr, p.err, DEV_TIMEOUT_DRAIN);
-      for (int t = max(0, nv - 2); t < nv; ++t) mbar_wait(&v_full[t & 1], (t >> 1) & 1, nullptr, p.err, DEV_TIMEOUT_DRAIN);
+      // every copy lands before the CTA may exit (a Q whose turn did not come was not loaded: its barrier's phase is over)
+      if (ok && i > 0)
+        for (int x = 0; x < 2; ++x) mbar_wait(&q_full[x], (i - 1) & 1, nullptr, p.err, DEV_TIMEOUT_DRAIN);
+      for (int k = max(0, t - 2); k < t; ++k) mbar_wait(&kv_full[k & 1], (k >> 1) & 1, nullptr, p.err, DEV_TIMEOUT_DRAIN);
     }
   } else if (warp == 1 || warp == 2) {
     if (lane == 0) {
@@ -647,40 +604,62 @@ __global__ void __launch_bounds__(kFwdThreads, 1) masked_fwd_kernel(const __grid
       const uint32_t id_pv = idesc_bf16(128, 64 * nd, 0, 1);   // O += P V: P in TMEM, V MN-major
       const uint64_t dq0 = kmajor_desc(smem_u32(sq + 2 * x * kChunk), 0), dk0 = kmajor_desc(smem_u32(sk), 0),
                      dv0 = mnmajor_desc(smem_u32(sv), 0);
-      auto issue_s = [&](const Walk& w) -> bool {
-        const int s = w.stage(), buf = w.t & 1;
-        if (w.first() && !mbar_wait_soon(&q_full[x], w.i & 1, abort_flag, p.err, DEV_TIMEOUT_MMA)) return false;
-        if (!buf && !mbar_wait_soon(&k_full[s], w.phase(), abort_flag, p.err, DEV_TIMEOUT_MMA)) return false;
-        tc_fence_after();
-        mma_kk_nd(nd, tmem + 128 * x + 64 * buf, dq0,
-                  dk0 + s * (2 * kChunk >> 4) + (buf ^ 1) * (kChunk / 2 >> 4), id_s);
+      // Key tiles of this CTA's unit i (0: there is none)
+      auto tiles_of = [&](int i) -> int {
+        const int u = unit_number(i);
+        if (!plan_ok || u >= p.n_units) return 0;
+        const int4 e = p.pair_heads ? p.plan.q_order[u / (p.hq >> 1)] : p.plan.q2_order[u / p.hq];
+        return e.z - e.y;
+      };
+      // S of key tile t, half buf (the second half of the keys first); first: of its unit, last: the unit's last tile
+      auto issue_s = [&](int t, int buf, bool last) {
+        const int s = t & 1;
+        mma_kk_nd(nd, tmem + 128 * x + 64 * buf, dq0, dk0 + s * (2 * kChunk >> 4) + (buf ^ 1) * (kChunk / 2 >> 4), id_s);
         umma_commit(&s_full[2 * x + buf]);
-        if (w.last()) umma_commit(&q_empty[x]);
-        if (buf) umma_commit(&k_empty[s]);
-        return true;
+        if (last && buf) umma_commit(&q_empty[x]);
       };
-      auto issue_pv = [&](const Walk& w) -> bool {
-        const int s = w.stage(), buf = w.t & 1;
-        if (!mbar_wait_soon(&p_full[2 * x + buf], (w.t >> 1) & 1, abort_flag, p.err, DEV_TIMEOUT_MMA)) return false;
-        if (!buf && !mbar_wait_soon(&v_full[s], w.phase(), abort_flag, p.err, DEV_TIMEOUT_MMA)) return false;
+      auto arrived = [&](int t, int i, bool first) -> bool {  // K and V of tile t, and its unit's Q
+        return (!first || mbar_wait_soon(&q_full[x], i & 1, abort_flag, p.err, DEV_TIMEOUT_MMA)) &&
+               mbar_wait_soon(&kv_full[t & 1], (t >> 1) & 1, abort_flag, p.err, DEV_TIMEOUT_MMA);
+      };
+      int n = tiles_of(0), n_next = tiles_of(1), i = 0, j = 0;  // tiles of this unit and the next, unit, tile in it
+      bool ok = n > 0 && arrived(0, 0, true);
+      if (ok) {
         tc_fence_after();
-        mma_tm<4>(tmem + 256 + 128 * x, tmem + 128 * x + 64 * buf, dv0 + s * (2 * kChunk >> 4) + (buf ^ 1) * 512, id_pv,
-                  !w.first());
-        umma_commit(&pv_done[x]);
-        if (buf) umma_commit(&v_empty[s]);
-        return true;
-      };
-      Walk ws, wp;  // S runs two steps ahead of P V
-      ws.start(p, plan_ok);
-      wp = ws;
-      bool ok = ws.live;
-      for (int k = 0; k < 2 && ok; ++k) {
-        ok = issue_s(ws);
-        ws.next(p);
+        issue_s(0, 0, n == 1);
+        issue_s(0, 1, n == 1);
       }
-      for (; ok && wp.live; wp.next(p)) {
-        ok = issue_pv(wp) && (!ws.live || issue_s(ws));
-        if (ws.live) ws.next(p);
+      for (int t = 0; ok; ++t) {
+        // P V of tile t, and S of tile t + 1 (the next unit's first after this one's last) a tile ahead
+        const bool last = j == n - 1, more = !last || n_next > 0;
+        const int s = t & 1;
+#pragma unroll
+        for (int buf = 0; buf < 2; ++buf) {
+          ok = mbar_wait_soon(&p_full[2 * x + buf], t & 1, abort_flag, p.err, DEV_TIMEOUT_MMA);
+          if (!ok) break;
+          tc_fence_after();
+          mma_tm<4>(tmem + 256 + 128 * x, tmem + 128 * x + 64 * buf, dv0 + s * (2 * kChunk >> 4) + (buf ^ 1) * 512, id_pv,
+                    j > 0 || buf > 0);
+          if (last) umma_commit(&pv_done[x]);
+          if (buf) umma_commit(&kv_empty[s]);
+          if (more) {
+            if (buf == 0) {
+              ok = arrived(t + 1, i + 1, last);
+              if (!ok) break;
+              tc_fence_after();
+            }
+            issue_s(t + 1, buf, last ? n_next == 1 : j + 1 == n - 1);
+          }
+        }
+        if (!more) break;
+        if (last) {
+          ++i;
+          j = 0;
+          n = n_next;
+          n_next = tiles_of(i + 1);
+        } else {
+          ++j;
+        }
       }
       umma_commit(&drain[x]);
       mbar_wait(&drain[x], 0, nullptr, p.err, DEV_TIMEOUT_DRAIN);
@@ -740,8 +719,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1) masked_fwd_kernel(const __grid
         }
         const float mul = BIAS ? 1.f : p.mul;
         if (__any_sync(0xffffffffu, lo > k0 || hi < k0 + 64)) {
-          mask32(s[0], lo - k0, hi - k0);
-          mask32(s[1], lo - k0 - 32, hi - k0 - 32);
+          mask32(s[0], see_bits(lo - k0, hi - k0));
+          mask32(s[1], see_bits(lo - k0 - 32, hi - k0 - 32));
         }
         const float mj = fmaxf(max32(s[0]), max32(s[1])) * mul;
         // The running maximum moves only when a row's maximum grows by more than 2^8: the exponentials then
@@ -768,8 +747,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1) masked_fwd_kernel(const __grid
           tmem_st16(s_tm + 64 * buf + 16 * c, pw);
         }
         if (k0 < me.j1 * kTile - 64 && __any_sync(0xffffffffu, corr != 1.f)) {
-          // O of the steps before is complete once the last P V is
-          ok = __all_sync(0xffffffffu, mbar_wait_soon(&pv_done[x], (t - 1) & 1, abort_flag, p.err, DEV_TIMEOUT_EPILOGUE));
+          // O of the steps before is complete once their last P V is: S of the next step stands behind it in the tensor
+          // pipe; after a unit's last S its own barrier tells
+          uint64_t* bar = k0 > me.j0 * kTile ? &s_full[2 * x + (buf ^ 1)] : &pv_done[x];
+          const uint32_t phase = k0 > me.j0 * kTile ? ((t + 1) >> 1) & 1 : 0;
+          ok = __all_sync(0xffffffffu, mbar_wait_soon(bar, phase, abort_flag, p.err, DEV_TIMEOUT_EPILOGUE));
           if (!ok) break;
           tc_fence_after();
 #pragma unroll 1
@@ -788,15 +770,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1) masked_fwd_kernel(const __grid
         m = m_new;
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(&p_full[2 * x + buf]);
+        warp_arrive(&p_full[2 * x + buf], lane);
       }
       if (!ok) break;
       if (more) rows_of(nx, nlo, nhi);
-      // S of the last step says that P V of the third last is done: the last two are waited for one by one (a wait for a
-      // barrier's phase is only right once the phase before it is over)
-      ok = __all_sync(0xffffffffu,
-                      mbar_wait_soon(&pv_done[x], t & 1, abort_flag, p.err, DEV_TIMEOUT_EPILOGUE) &&
-                          mbar_wait_soon(&pv_done[x], (t - 1) & 1, abort_flag, p.err, DEV_TIMEOUT_EPILOGUE));
+      // P V of the unit's last two steps, one by one (a wait for a barrier's phase is right once the phase before it is over)
+      ok = __all_sync(0xffffffffu, mbar_wait_soon(&pv_done[x], 0, abort_flag, p.err, DEV_TIMEOUT_EPILOGUE) &&
+                                       mbar_wait_soon(&pv_done[x], 1, abort_flag, p.err, DEV_TIMEOUT_EPILOGUE));
       if (!ok) break;
       // O / l as bf16; the next unit's first P V waits for this softmax's next P
       tc_fence_after();
@@ -847,12 +827,11 @@ __device__ __forceinline__ void grad32(uint32_t (&s)[32], uint32_t (&dp)[32], fl
   uint32_t th[CAP ? 32 : 2];
   if (CAP) {
     tanh_n(s, cap_mul);
-    if (BIAS) {
 #pragma unroll
-      for (int e = 0; e < 32; ++e) th[e] = s[e];
-    }
+    for (int e = 0; e < 32; ++e) th[e] = s[e];
   }
   if (BIAS) bias32(s, mul, slope, away, side);
+  if (part) mask32(s, see);  // -inf: P = 0
   const f2 m = both(BIAS ? 1.f : mul), one = both(1.f);
   const f2 r1 = both(c1), r2 = both(c2);
 #pragma unroll
@@ -872,14 +851,10 @@ __device__ __forceinline__ void grad32(uint32_t (&s)[32], uint32_t (&dp)[32], fl
       un(fma2(pku(s[i], s[i + 1]), m, a1[k]), x0, x1);
       x0 = ex2(x0);
       x1 = ex2(x1);
-      if (part) {
-        if (!(see & (1u << i))) x0 = 0.f;
-        if (!(see & (2u << i))) x1 = 0.f;
-      }
       const f2 pe = pk(x0, x1);
       f2 ds = mul2(pe, add2(pku(dp[i], dp[i + 1]), a2[k]));
       if (CAP) {
-        const f2 t = BIAS ? pku(th[i], th[i + 1]) : pku(s[i], s[i + 1]);
+        const f2 t = pku(th[i], th[i + 1]);
         ds = mul2(ds, fma2(mul2(t, both(-1.f)), t, one));
       }
       float d0, d1;
@@ -891,8 +866,9 @@ __device__ __forceinline__ void grad32(uint32_t (&s)[32], uint32_t (&dp)[32], fl
 }
 
 // dq: persistent CTAs over units (query tile, head). Q and dO stay, K and V stream through two stages, twice: first for D,
-// then for dQ. Warp 0 loads; warp 1 issues S = Q K^T and dP = dO V^T; warp 2 issues dQ += dS K; warps 4-7 and 8-11 hold
-// a query row per thread and half of the key columns each. They take S and dP into registers at once, so the
+// then for dQ. Warp 0 loads; warp 1 issues S = Q K^T and dP = dO V^T; warp 2 issues dQ += dS K; warps 4-19 hold a query row
+// and 32 of the key columns per thread (with 64 columns and half as many warps a scheduler has two to choose from,
+// and most of the time neither can issue). They take S and dP into registers at once, so the
 // next tile's products run while they work. TMEM: dQ at 0, S at 128, dP at 256, dS (bf16, two buffers) at 384.
 template <bool CAP, bool BIAS>
 __global__ void __launch_bounds__(kBwdThreads, 1) masked_dq_kernel(const __grid_constant__ MaskedBwdParams p) {
@@ -901,8 +877,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) masked_dq_kernel(const __grid_
   const int nd = p.nd;
   uint8_t* sq = smem;                       // Q, then dO: 2 chunks each
   uint8_t* skv = smem + 4 * kChunk;         // stage s: K (2 chunks), then V
-  float* s_part = reinterpret_cast<float*>(smem + 12 * kChunk);  // [2][128]: the halves' sums of D
-  uint64_t* bars = reinterpret_cast<uint64_t*>(s_part + 256);
+  float* s_part = reinterpret_cast<float*>(smem + 12 * kChunk);  // [4][128]: the quarters' sums of D
+  uint64_t* bars = reinterpret_cast<uint64_t*>(s_part + 512);
   uint64_t* q_full = bars;
   uint64_t* q_empty = bars + 1;
   uint64_t* kv_full = bars + 2;    // [2]
@@ -938,12 +914,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1) masked_dq_kernel(const __grid_
     for (int s = 0; s < 2; ++s) {
       mbar_init(&kv_full[s], 1);
       mbar_init(&kv_empty[s], 2);  // S and dP; dQ
-      mbar_init(&ds_full[s], 256);
+      mbar_init(&ds_full[s], 16);
       mbar_init(&dq_done[s], 1);
       mbar_init(&drain[s], 1);
     }
     mbar_init(s_full, 1);
-    mbar_init(s_free, 256);
+    mbar_init(s_free, 16);
     *abort_flag = 0;
     fence_barrier_init();
     tma_prefetch_desc(&p.qmap);
@@ -962,8 +938,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1) masked_dq_kernel(const __grid_
   pdl_wait();
   const bool plan_ok = plan_fits(p.plan, p.n_seq, p.S, p.err);
 
-  if (warp == 0) {
-    if (lane == 0) {
+  // 640 threads start with 96 registers each; 56 in the first four warps and 104 in the others stay within their sum
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (warp == 0 && lane == 0) {
       U w, nx;
       bool ok = plan_ok, live = plan_ok && unit(0, nx);
       int t = 0, i = 0;
@@ -991,9 +969,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) masked_dq_kernel(const __grid_
       // every copy lands before the CTA may exit
       if (i > 0) mbar_wait(q_full, (i - 1) & 1, nullptr, p.err, DEV_TIMEOUT_DRAIN);
       for (int k = max(0, t - 2); k < t; ++k) mbar_wait(&kv_full[k & 1], (k >> 1) & 1, nullptr, p.err, DEV_TIMEOUT_DRAIN);
-    }
-  } else if (warp == 1) {
-    if (lane == 0) {
+    } else if (warp == 1 && lane == 0) {
       const uint32_t id = idesc_bf16(128, 128, 0, 0);
       const uint64_t dq0 = kmajor_desc(smem_u32(sq), 0), ddo0 = dq0 + (2 * kChunk >> 4), dk0 = kmajor_desc(smem_u32(skv), 0);
       U w, nx;
@@ -1021,9 +997,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) masked_dq_kernel(const __grid_
       }
       umma_commit(&drain[0]);
       mbar_wait(&drain[0], 0, nullptr, p.err, DEV_TIMEOUT_DRAIN);
-    }
-  } else if (warp == 2) {
-    if (lane == 0) {
+    } else if (warp == 2 && lane == 0) {
       const uint32_t id = idesc_bf16(128, 64 * nd, 0, 1);  // dS in TMEM, K MN-major
       const uint64_t dk0 = mnmajor_desc(smem_u32(skv), 0);
       U w, nx;
@@ -1047,18 +1021,19 @@ __global__ void __launch_bounds__(kBwdThreads, 1) masked_dq_kernel(const __grid_
       umma_commit(&drain[1]);
       mbar_wait(&drain[1], 0, nullptr, p.err, DEV_TIMEOUT_DRAIN);
     }
-  } else if (warp >= 4) {
-    const int quarter = warp & 3, half = (warp - 4) >> 2;
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+    const int quarter = warp & 3, cq = (warp - 4) >> 2;  // rows (TMEM lanes); 32 of the 128 key columns
     const int r = quarter * 32 + lane;
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
-    const uint32_t s_tm = tmem + lane_off + 128 + 64 * half, dp_tm = s_tm + 128, ds_tm = tmem + lane_off + 384 + 32 * half;
+    const uint32_t s_tm = tmem + lane_off + 128 + 32 * cq, dp_tm = s_tm + 128, ds_tm = tmem + lane_off + 384 + 16 * cq;
     U w, nx;
     bool ok = plan_ok, live = plan_ok && unit(0, nx);
     int t = 0, n = 0;
     int nlo = 0, nhi = 0;
     float nlse = 0.f;
     const int64_t T = (int64_t)p.n_seq * p.S;
-    auto rows_of = [&](const U& x) {  // what the row sees, and its lse in powers of two (0 where it sees nothing)
+    auto rows_of = [&](const U& x) {  // what the row sees, and its lse in powers of two
       const int q = x.qt * kTile + r;
       const int64_t row = (int64_t)x.b * p.S + q;
       const bool in = q < p.S;
@@ -1070,82 +1045,75 @@ __global__ void __launch_bounds__(kBwdThreads, 1) masked_dq_kernel(const __grid_
     for (int i = 0; ok && live; ++i) {
       w = nx;
       const int lo = nlo, hi = nhi, qt0 = w.qt * kTile, h = w.h, b = w.b;
-      const float lse = lo < hi ? nlse : 0.f;
+      const float nl = lo < hi ? -nlse : -INFINITY;  // a row that sees nothing: P = 0 whatever its score
       live = unit(i + 1, nx);
       const float slope = BIAS ? p.slopes[h] * kLog2e : 0.f;
       // a row that sees one key: P = 1 and D = dP to the bit, so that its dS is 0 and not a rounding's rest
       const bool single = hi - lo == 1;
+      const bool singles = __any_sync(0xffffffffu, single);
       float sum = 0.f;
       for (int pass = 0; pass < 2 && ok; ++pass) {
         const float nD = pass ? -sum : 0.f;
         f2 acc[2] = {0, 0};
+        float only = 0.f;
         for (int j = w.j0; j < w.j1; ++j, ++t) {
           ok = __all_sync(0xffffffffu, mbar_wait_soon(s_full, t & 1, abort_flag, p.err, DEV_TIMEOUT_EPILOGUE));
           if (!ok) break;
           tc_fence_after();
-          uint32_t s[2][32], dp[2][32];
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            tmem_ld32(s_tm + 32 * c, s[c]);
-            tmem_ld32(dp_tm + 32 * c, dp[c]);
-          }
-          tmem_ld_wait_regs(s[0]);
-          regs_after_wait(s[1]);
-          regs_after_wait(dp[0]);
-          regs_after_wait(dp[1]);
+          uint32_t s[32], dp[32];
+          tmem_ld32(s_tm, s);
+          tmem_ld32(dp_tm, dp);
+          tmem_ld_wait_regs(s);
+          regs_after_wait(dp);
           tc_fence_before();
-          mbar_arrive(s_free);
-          const int k0 = j * kTile + 64 * half;  // key of this thread's first column
-          const bool part = __any_sync(0xffffffffu, lo > k0 || hi < k0 + 64);
-          const int side = qt0 + 32 * quarter >= k0 + 63;
+          warp_arrive(s_free, lane);
+          const int k0 = j * kTile + 32 * cq;  // key of this thread's first column
+          const bool part = __any_sync(0xffffffffu, lo > k0 || hi < k0 + 32);
+          const uint32_t see = see_bits(lo - k0, hi - k0);
+          const int side = qt0 + 32 * quarter >= k0 + 31;
           if (pass == 0) {
+            if (CAP) tanh_n(s, p.cap_mul);
+            if (BIAS) bias32(s, p.mul, slope, (float)(qt0 + r - k0), side);
+            if (part) {
+              mask32(s, see);
+              if (singles) {
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              if (CAP) tanh_n(s[c], p.cap_mul);
-              if (BIAS) bias32(s[c], p.mul, slope, (float)(qt0 + r - k0 - 32 * c), side);
-              const f2 m = both(BIAS ? 1.f : p.mul), nl = both(-lse);
-              const uint32_t see = see_bits(lo - k0 - 32 * c, hi - k0 - 32 * c);
-#pragma unroll
-              for (int e = 0; e < 32; e += 2) {
-                float x0, x1;
-                un(fma2(pku(s[c][e], s[c][e + 1]), m, nl), x0, x1);
-                x0 = ex2(x0);
-                x1 = ex2(x1);
-                if (part) {
-                  x0 = !(see & (1u << e)) ? 0.f : single ? 1.f : x0;
-                  x1 = !(see & (2u << e)) ? 0.f : single ? 1.f : x1;
-                }
-                acc[(e >> 1) & 1] = fma2(pk(x0, x1), pku(dp[c][e], dp[c][e + 1]), acc[(e >> 1) & 1]);
+                for (int e = 0; e < 32; ++e)
+                  if (see & (1u << e)) only = __uint_as_float(dp[e]);
               }
+            }
+            const f2 m = both(BIAS ? 1.f : p.mul), l2 = both(nl);
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              float x0, x1;
+              un(fma2(pku(s[e], s[e + 1]), m, l2), x0, x1);
+              acc[(e >> 1) & 1] = fma2(pk(ex2(x0), ex2(x1)), pku(dp[e], dp[e + 1]), acc[(e >> 1) & 1]);
             }
           } else {
             const int d = n & 1;
+            uint32_t pw[16], dw[16];
+            grad32<CAP, BIAS, true, false>(s, dp, p.mul, p.cap_mul, slope, (float)(qt0 + r - k0), side, part, see, nl, nD,
+                                           nullptr, nullptr, pw, dw);
             // dQ of two steps ago has read this buffer (its predecessors' phases are over: it reads them in order)
-            if (n >= 2) ok = __all_sync(0xffffffffu, mbar_wait_soon(&dq_done[d], ((n >> 1) - 1) & 1, abort_flag, p.err, DEV_TIMEOUT_EPILOGUE));
+            if (n >= 2)
+              ok = __all_sync(0xffffffffu, mbar_wait_soon(&dq_done[d], ((n >> 1) - 1) & 1, abort_flag, p.err, DEV_TIMEOUT_EPILOGUE));
             if (!ok) break;
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              uint32_t pw[16], dw[16];
-              grad32<CAP, BIAS, true, false>(s[c], dp[c], p.mul, p.cap_mul, slope, (float)(qt0 + r - k0 - 32 * c), side, part,
-                                             see_bits(lo - k0 - 32 * c, hi - k0 - 32 * c), -lse, nD, nullptr, nullptr, pw, dw);
-              tmem_st16(ds_tm + 64 * d + 16 * c, dw);
-            }
+            tmem_st16(ds_tm + 64 * d, dw);
             tmem_st_wait();
             tc_fence_before();
-            mbar_arrive(&ds_full[d]);
+            warp_arrive(&ds_full[d], lane);
             ++n;
           }
         }
         if (pass == 0) {
           float a0, a1;
           un(add2(acc[0], acc[1]), a0, a1);
-          s_part[half * 128 + r] = a0 + a1;
+          s_part[cq * 128 + r] = single ? only : a0 + a1;
           ok = bar_and_compute(ok);
-          sum = s_part[r] + s_part[128 + r];
-          if (ok && half == 0 && qt0 + r < p.S) p.delta[(int64_t)h * T + (int64_t)b * p.S + qt0 + r] = sum;
+          sum = (s_part[r] + s_part[128 + r]) + (s_part[256 + r] + s_part[384 + r]);
+          if (ok && cq == 0 && qt0 + r < p.S) p.delta[(int64_t)h * T + (int64_t)b * p.S + qt0 + r] = sum;
         } else {
           if (ok && live) rows_of(nx);
-          // both buffers' last products (a unit of one key tile has used one)
           if (ok) ok = __all_sync(0xffffffffu, mbar_wait_soon(&dq_done[(n - 1) & 1], ((n - 1) >> 1) & 1, abort_flag, p.err, DEV_TIMEOUT_EPILOGUE));
           ok = bar_and_compute(ok);  // also: s_part is free for the next unit
         }
@@ -1154,14 +1122,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1) masked_dq_kernel(const __grid_
       tc_fence_after();
       const int64_t row0 = (int64_t)b * p.S + qt0 + 32 * quarter;
       const int n_rows = p.S - qt0 - 32 * quarter;
-#pragma unroll 1
-      for (int c = nd * half; c < nd * half + nd; ++c) {
+      if (cq < 2 * nd) {
         uint32_t v[32], pk16[16];
-        tmem_ld32(tmem + lane_off + 32 * c, v);
+        tmem_ld32(tmem + lane_off + 32 * cq, v);
         tmem_ld_wait_regs(v);
 #pragma unroll
         for (int e = 0; e < 32; e += 2) pk16[e / 2] = pack2(__uint_as_float(v[e]) * p.scale, __uint_as_float(v[e + 1]) * p.scale);
-        store_rows32(p.dq + row0 * p.lddq + (int64_t)h * p.hd + 32 * c, p.lddq, pk16, n_rows, p.hd - 32 * c);
+        store_rows32(p.dq + row0 * p.lddq + (int64_t)h * p.hd + 32 * cq, p.lddq, pk16, n_rows, p.hd - 32 * cq);
       }
       tc_fence_before();
     }
@@ -1179,7 +1146,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) masked_dq_kernel(const __grid_
 // stay, Q and dO stream through two stages. A step is half a query tile (64 queries): S^T = K Q^T and dP^T = V dO^T of
 // step t + 1 run while the compute warps work on step t; P^T and dS^T replace them in TMEM (bf16, first
 // operands of dV += P^T dO and dK += dS^T Q). Warp 0 loads; warp 1 issues S^T and dP^T, warp 2 dV and dK; warp 3 reads the
-// query rows' lse, D and intervals; warps 4-7 and 8-11 take the even and the odd steps, a key row per thread. TMEM: S^T of
+// query rows' lse, D and intervals; warps 4-11 and 12-19 take the even and the odd steps, a key row and 32 of the 64 query
+// columns per thread. TMEM: S^T of
 // buffer x at 64 x, dP^T at 128 + 64 x, dV at 256, dK at 384.
 template <bool CAP, bool BIAS>
 __global__ void __launch_bounds__(kBwdThreads, 1) masked_dkv_kernel(const __grid_constant__ MaskedBwdParams p) {
@@ -1216,9 +1184,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1) masked_dkv_kernel(const __grid
       mbar_init(&qd_full[s], 1);
       mbar_init(&qd_empty[s], 1);
       mbar_init(&rows_full[s], 1);
-      mbar_init(&rows_empty[s], 8);
+      mbar_init(&rows_empty[s], 16);
       mbar_init(&sd_full[s], 1);
-      mbar_init(&pd_full[s], 128);
+      mbar_init(&pd_full[s], 8);
       mbar_init(&pd_done[s], 1);
       mbar_init(&drain[s], 1);
     }
@@ -1247,10 +1215,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1) masked_dkv_kernel(const __grid
   auto it_head = [&](int it) { return g * hpg + it % hpg; };
   auto it_qtile = [&](int it) { return q0 + it / hpg; };
 
-  if (!plan_ok) {
-    // nothing is issued
-  } else if (warp == 0) {
-    if (lane == 0) {
+  // 640 threads start with 96 registers each; 56 in the first four warps and 104 in the others stay within their sum
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (!plan_ok) {
+      // nothing is issued
+    } else if (warp == 0 && lane == 0) {
       mbar_arrive_expect_tx(kv_full, 2 * nd * kChunk);
       for (int c = 0; c < nd; ++c) {
         tma_load_4d(sk + c * kChunk, &p.kmap, kv_full, 64 * c, g, kt * kTile, b);
@@ -1270,9 +1240,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) masked_dkv_kernel(const __grid
       // every copy lands before the CTA may exit
       mbar_wait(kv_full, 0, nullptr, p.err, DEV_TIMEOUT_DRAIN);
       for (int k = max(0, it - 2); k < it; ++k) mbar_wait(&qd_full[k & 1], (k >> 1) & 1, nullptr, p.err, DEV_TIMEOUT_DRAIN);
-    }
-  } else if (warp == 1) {
-    if (lane == 0) {
+    } else if (warp == 1 && lane == 0) {
       const uint32_t id = idesc_bf16(128, 64, 0, 0);
       const uint64_t dk0 = kmajor_desc(smem_u32(sk), 0), dv0 = dk0 + (2 * kChunk >> 4), dq0 = kmajor_desc(smem_u32(sqd), 0);
       bool ok = mbar_wait_soon(kv_full, 0, abort_flag, p.err, DEV_TIMEOUT_MMA);
@@ -1289,9 +1257,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) masked_dkv_kernel(const __grid
       }
       umma_commit(&drain[0]);
       mbar_wait(&drain[0], 0, nullptr, p.err, DEV_TIMEOUT_DRAIN);
-    }
-  } else if (warp == 2) {
-    if (lane == 0) {
+    } else if (warp == 2 && lane == 0) {
       const uint32_t id = idesc_bf16(128, 64 * nd, 0, 1);  // P^T, dS^T in TMEM; dO, Q MN-major
       const uint64_t dq0 = mnmajor_desc(smem_u32(sqd), 0);
       bool ok = true;
@@ -1302,15 +1268,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1) masked_dkv_kernel(const __grid
         if (!ok) break;
         tc_fence_after();
         const uint64_t bq = dq0 + s * (4 * kChunk >> 4) + x * 512;
-        mma_tm<4>(tmem + 256, tmem + 64 * x, bq + (2 * kChunk >> 4), id, t > 0);
-        mma_tm<4>(tmem + 384, tmem + 128 + 64 * x, bq, id, t > 0);
+        mma_tm<4, 32>(tmem + 256, tmem + 64 * x, bq + (2 * kChunk >> 4), id, t > 0);
+        mma_tm<4, 32>(tmem + 384, tmem + 128 + 64 * x, bq, id, t > 0);
         umma_commit(&pd_done[x]);
         if (x == 1) umma_commit(&qd_empty[s]);
       }
       umma_commit(&drain[1]);
       mbar_wait(&drain[1], 0, nullptr, p.err, DEV_TIMEOUT_DRAIN);
-    }
-  } else if (warp == 3) {
+    } else if (warp == 3) {
     bool ok = true;
     for (int it = 0; ok && it < n_it; ++it) {
       const int s = it & 1, qt = it_qtile(it);
@@ -1339,15 +1304,17 @@ __global__ void __launch_bounds__(kBwdThreads, 1) masked_dkv_kernel(const __grid
       __syncwarp();
       if (lane == 0) mbar_arrive(&rows_full[s]);
     }
+    }
   } else {
-    const int quarter = warp & 3, x = (warp - 4) >> 2;  // x: buffer, half of each query tile
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+    const int quarter = warp & 3, x = (warp - 4) >> 3, c = ((warp - 4) >> 2) & 1;  // x: buffer, half of each query tile; c: 32 columns
     const int r = quarter * 32 + lane;                  // key row of the tile
     const int kpos = kt * kTile + r;
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
-    const uint32_t s_tm = tmem + lane_off + 64 * x, dp_tm = s_tm + 128;
-    bool ok = true;
-    for (int it = 0; it < n_it; ++it) {
-      const int s = it & 1, qt0 = it_qtile(it) * kTile + 64 * x;
+    const uint32_t s_tm = tmem + lane_off + 64 * x + 32 * c, dp_tm = s_tm + 128;
+    bool ok = plan_ok;
+    for (int it = 0; ok && it < n_it; ++it) {
+      const int s = it & 1, qt0 = it_qtile(it) * kTile + 64 * x + 32 * c;
       ok = __all_sync(0xffffffffu, mbar_wait_soon(&rows_full[s], (it >> 1) & 1, abort_flag, p.err, DEV_TIMEOUT_EPILOGUE) &&
                                        mbar_wait_soon(&sd_full[x], it & 1, abort_flag, p.err, DEV_TIMEOUT_EPILOGUE));
       if (!ok) break;
@@ -1355,32 +1322,29 @@ __global__ void __launch_bounds__(kBwdThreads, 1) masked_dkv_kernel(const __grid
       const bool part = !s_whole[s];
       const float slope = BIAS ? p.slopes[it_head(it)] * kLog2e : 0.f;
       const int side = qt0 >= kt * kTile + 32 * quarter + 31 ? -1 : 0;
-#pragma unroll 1
-      for (int c = 0; c < 2; ++c) {
-        uint32_t sv[32], dp[32], pw[16], dw[16];
-        tmem_ld32(s_tm + 32 * c, sv);
-        tmem_ld32(dp_tm + 32 * c, dp);
-        tmem_ld_wait_regs(sv);
-        regs_after_wait(dp);
-        const int col = s * 128 + 64 * x + 32 * c;
-        uint32_t see = 0xffffffffu;
-        if (part) {
-          see = 0;
+      uint32_t sv[32], dp[32], pw[16], dw[16];
+      tmem_ld32(s_tm, sv);
+      tmem_ld32(dp_tm, dp);
+      tmem_ld_wait_regs(sv);
+      regs_after_wait(dp);
+      const int col = s * 128 + 64 * x + 32 * c;
+      uint32_t see = 0xffffffffu;
+      if (part) {
+        see = 0;
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const int2 w = s_see[col + e];
-            see |= (uint32_t)(w.x <= kpos && kpos < w.y) << e;
-          }
+        for (int e = 0; e < 32; ++e) {
+          const int2 w = s_see[col + e];
+          see |= (uint32_t)(w.x <= kpos && kpos < w.y) << e;
         }
-        grad32<CAP, BIAS, false, true>(sv, dp, p.mul, p.cap_mul, slope, (float)(kpos - qt0 - 32 * c), side, part, see, 0.f,
-                                       0.f, s_lse + col, s_del + col, pw, dw);
-        tmem_st16(s_tm + 16 * c, pw);
-        tmem_st16(dp_tm + 16 * c, dw);
       }
+      grad32<CAP, BIAS, false, true>(sv, dp, p.mul, p.cap_mul, slope, (float)(kpos - qt0), side, part, see, 0.f, 0.f,
+                                     s_lse + col, s_del + col, pw, dw);
+      // over the scores and products that this warp itself has read: words 0-15 and 32-47 of the buffers
+      tmem_st16(s_tm, pw);
+      tmem_st16(dp_tm, dw);
       tmem_st_wait();
       tc_fence_before();
-      mbar_arrive(&pd_full[x]);
-      __syncwarp();
+      warp_arrive(&pd_full[x], lane);
       if (lane == 0) mbar_arrive(&rows_empty[s]);
     }
     // dV (first group), dK (second) once every product is done
@@ -1393,13 +1357,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1) masked_dkv_kernel(const __grid
       __nv_bfloat16* out = (x ? p.dk : p.dv) + row0 * ld + (int64_t)g * p.hd;
       const float mul = x ? p.scale : 1.f;
 #pragma unroll 1
-      for (int c = 0; c < 2 * nd; ++c) {
+      for (int k = c; k < 2 * nd; k += 2) {
         uint32_t v[32], w[16];
-        tmem_ld32(tmem + lane_off + 256 + 128 * x + 32 * c, v);
+        tmem_ld32(tmem + lane_off + 256 + 128 * x + 32 * k, v);
         tmem_ld_wait_regs(v);
 #pragma unroll
         for (int e = 0; e < 32; e += 2) w[e / 2] = pack2(__uint_as_float(v[e]) * mul, __uint_as_float(v[e + 1]) * mul);
-        store_rows32(out + 32 * c, ld, w, n_rows, p.hd - 32 * c);
+        store_rows32(out + 32 * k, ld, w, n_rows, p.hd - 32 * k);
       }
     }
   }
@@ -1417,7 +1381,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) masked_dkv_kernel(const __grid
 // Shared memory of a launch: sized for head_dim 128 whatever the head dimension, which also keeps
 // one CTA per SM (each CTA allocates all 512 TMEM columns).
 int fwd_smem() { return 1024 + 12 * kChunk + 256; }
-int dq_smem() { return 1024 + 12 * kChunk + 1024 + 256; }
+int dq_smem() { return 1024 + 12 * kChunk + 2048 + 256; }
 int dkv_smem() { return 1024 + 12 * kChunk + 4096 + 16 + 256; }
 
 // Raises a kernel's shared-memory limit once per device.
