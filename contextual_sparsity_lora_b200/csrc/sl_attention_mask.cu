@@ -81,7 +81,7 @@ constexpr int kPlanThreads = 1024;
 
 // Rows of the tiles (sequence * n_t + tile) first, first + step, ...: a warp per tile.
 __device__ void plan_rows(const Plan& p, const int32_t* row_lo, const int32_t* row_hi, int n_seq, int S, int64_t first,
-                          int64_t step) {
+                          int64_t step, int4* q_range) {
   const int n_t = (S + kTile - 1) / kTile, lane = threadIdx.x & 31;
   int32_t *lo = const_cast<int32_t*>(p.lo), *hi = const_cast<int32_t*>(p.hi);
   for (int64_t at = first; at < (int64_t)n_seq * n_t; at += step) {
@@ -115,8 +115,7 @@ __device__ void plan_rows(const Plan& p, const int32_t* row_lo, const int32_t* r
       int4 v = h_max == 0 ? make_int4(0, 1, 0, 0)
                           : make_int4(l_min / kTile, (h_max + kTile - 1) / kTile, (l_max + kTile - 1) / kTile, h_min / kTile);
       if (any_empty) v.z = v.w = 0;
-      const_cast<int4*>(p.q_range)[at] = v;
-      const_cast<int2*>(p.k_range)[at] = make_int2(n_t, 0);
+      q_range[at] = v;
     }
   }
 }
@@ -162,6 +161,8 @@ __device__ void plan_tiles_and_order(const Plan& p, int n_seq, int S, int32_t* h
   const int n_t = (S + kTile - 1) / kTile;
   const int64_t n = (int64_t)n_seq * n_t;
   int2* kr = const_cast<int2*>(p.k_range);
+  for (int64_t at = threadIdx.x; at < n; at += kPlanThreads) kr[at] = make_int2(n_t, 0);
+  __syncthreads();
   for (int64_t at = threadIdx.x; at < n; at += kPlanThreads) {
     const int4 v = p.q_range[at];
     const int t = (int)(at % n_t);
@@ -196,20 +197,62 @@ __device__ void plan_tiles_and_order(const Plan& p, int n_seq, int S, int32_t* h
 __global__ void __launch_bounds__(kPlanThreads) plan_rows_kernel(Plan p, const int32_t* lo, const int32_t* hi, int n_seq, int S) {
   pdl_wait();
   const int64_t warp = ((int64_t)blockIdx.x * kPlanThreads + threadIdx.x) >> 5;
-  plan_rows(p, lo, hi, n_seq, S, warp, (int64_t)gridDim.x * (kPlanThreads / 32));
+  plan_rows(p, lo, hi, n_seq, S, warp, (int64_t)gridDim.x * (kPlanThreads / 32), const_cast<int4*>(p.q_range));
 }
 
-// rows: also the rows (a plan of few tiles is one launch)
-__global__ void __launch_bounds__(kPlanThreads) plan_tiles_kernel(Plan p, const int32_t* lo, const int32_t* hi, int n_seq, int S,
-                                                                  bool rows) {
+__global__ void __launch_bounds__(kPlanThreads) plan_tiles_kernel(Plan p, int n_seq, int S) {
   extern __shared__ int32_t hist[];
   __shared__ int32_t carry;
   pdl_wait();
-  if (rows) {
-    plan_rows(p, lo, hi, n_seq, S, threadIdx.x >> 5, kPlanThreads / 32);
-    __syncthreads();
-  }
   plan_tiles_and_order(p, n_seq, S, hist, &carry);
+}
+
+// A plan of at most kPlanSmall tiles in one block and one launch: ranges in shared memory, and each tile's place by
+// counting the longer ones (equal ones stand by their number).
+constexpr int kPlanSmall = 128;
+__global__ void __launch_bounds__(kPlanThreads) plan_small_kernel(Plan p, const int32_t* lo, const int32_t* hi, int n_seq, int S) {
+  __shared__ int4 q[kPlanSmall];
+  __shared__ int2 k[kPlanSmall], q2[kPlanSmall];
+  pdl_wait();
+  const int n_t = (S + kTile - 1) / kTile, n = n_seq * n_t, n_t2 = (n_t + 1) / 2, n2 = n_seq * n_t2, at = threadIdx.x;
+  if (at < n) k[at] = make_int2(n_t, 0);
+  plan_rows(p, lo, hi, n_seq, S, threadIdx.x >> 5, kPlanThreads / 32, q);
+  __syncthreads();
+  if (at < n) {
+    const int t = at % n_t, seq0 = at - t;
+    for (int j = q[at].x; j < q[at].y; ++j) {
+      atomicMin(&k[seq0 + j].x, t);
+      atomicMax(&k[seq0 + j].y, t + 1);
+    }
+  } else if (at >= kPlanSmall && at - kPlanSmall < n2) {
+    const int i = at - kPlanSmall, a = i / n_t2 * n_t + i % n_t2 * 2;
+    int2 v = make_int2(q[a].x, q[a].y);
+    if (i % n_t2 * 2 + 1 < n_t) v = make_int2(min(v.x, q[a + 1].x), max(v.y, q[a + 1].y));
+    q2[i] = v;
+  }
+  __syncthreads();
+  if (at < n && k[at].y == 0) k[at] = make_int2(0, 1);
+  __syncthreads();
+  auto place = [&](int me, int count, auto range_of, int4* order) {
+    const int2 r = range_of(me);
+    const int len = r.y - r.x;
+    int rank = 0;
+    for (int j = 0; j < count; ++j) {
+      const int2 o = range_of(j);
+      rank += o.y - o.x > len || (o.y - o.x == len && j < me);
+    }
+    order[rank] = make_int4(me, r.x, r.y, 0);
+  };
+  const int which = at / kPlanSmall, me = at % kPlanSmall;
+  if (which == 0 && me < n) place(me, n, [&](int j) { return make_int2(q[j].x, q[j].y); }, const_cast<int4*>(p.q_order));
+  if (which == 1 && me < n) place(me, n, [&](int j) { return k[j]; }, const_cast<int4*>(p.k_order));
+  if (which == 2 && me < n2) place(me, n2, [&](int j) { return q2[j]; }, const_cast<int4*>(p.q2_order));
+  if (which == 3 && me < n) {
+    const_cast<int4*>(p.q_range)[me] = q[me];
+    const_cast<int2*>(p.k_range)[me] = k[me];
+    if (me < n2) const_cast<int2*>(p.q2_range)[me] = q2[me];
+  }
+  if (at < 3) const_cast<int32_t*>(p.header)[at] = at == 0 ? kPlanMagic : at == 1 ? n_seq : S;
 }
 
 // ----------------------------------------------------------------------------------------- scores
@@ -1448,16 +1491,17 @@ int attention_plan(const int32_t* row_lo, const int32_t* row_hi, int n_seq, int 
   Plan p;
   carve_plan(plan, n_seq, S, &p);
   const int64_t tiles = plan_tiles(n_seq, S);
-  // up to 64 tiles one block does it all; more: the rows over many blocks first
-  const bool one = tiles <= 64;
-  if (!one) {
-    launch_kernel(plan_rows_kernel, (unsigned)std::min<int64_t>((tiles + 31) / 32, 148), kPlanThreads, 0, s, p, row_lo,
-                  row_hi, n_seq, S);
+  if (tiles <= kPlanSmall) {
+    launch_kernel(plan_small_kernel, 1u, kPlanThreads, 0, s, p, row_lo, row_hi, n_seq, S);
     if (launch_failed("sl_attention_plan")) return 5;
     note_launch();
+    return 0;
   }
-  const size_t smem = ((size_t)(S + kTile - 1) / kTile + 2) * 4;
-  launch_kernel(plan_tiles_kernel, 1u, kPlanThreads, smem, s, p, row_lo, row_hi, n_seq, S, one);
+  launch_kernel(plan_rows_kernel, (unsigned)std::min<int64_t>((tiles + 31) / 32, 148), kPlanThreads, 0, s, p, row_lo, row_hi,
+                n_seq, S);
+  if (launch_failed("sl_attention_plan")) return 5;
+  note_launch();
+  launch_kernel(plan_tiles_kernel, 1u, kPlanThreads, ((size_t)(S + kTile - 1) / kTile + 2) * 4, s, p, n_seq, S);
   if (launch_failed("sl_attention_plan")) return 5;
   note_launch();
   return 0;

@@ -11,7 +11,8 @@
 // The top k (k <= 32): while the sums are taken, the maximum of every 16 consecutive logits goes to
 // shared memory. The k largest logits lie in k of these chunks: those whose maximum exceeds the k-th
 // largest maximum, and the first of those that equal it. Their 16 k logits are read again and
-// ranked by (value, lowest index first).
+// ranked by (value, lowest index first). The k-th largest maximum itself is looked for only where many are equal
+// (local_top); mostly a bound close below it does (local_top_few), from one value per thread.
 //
 // Both passes are bound by memory: the forward reads each logit once, the backward reads and
 // writes it once. Few rows: a cluster of up to 8 CTAs shares a row, each with a contiguous part of the
@@ -34,9 +35,10 @@ constexpr int kLpThreads = 512;
 constexpr int kLpWarps = kLpThreads / 32;
 constexpr int kLpChunk = 16;    // logits per chunk
 constexpr int kLpMaxTop = 32;
+constexpr int kLpFewChunks = 128;
 constexpr float kLog2e = 1.44269504f;
 constexpr float kLn2 = 0.693147181f;
-constexpr float kHuge = 1e37f;  // logits below -kHuge count as -infinity; one above kHuge makes its row NaN
+constexpr float kHuge = 10633823966279326983230456482242756608.f;  // 2^123: logits below -kHuge count as -infinity; one above kHuge makes its row NaN
 
 struct LpParams {
   const void* z;
@@ -59,9 +61,6 @@ __device__ __forceinline__ float lp_ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-
-// x 2^x with 0 where 2^x is 0 (x = -inf); NaN stays NaN.
-__device__ __forceinline__ float times_x(float e, float x) { return e * fmaxf(x, -1000.f); }
 
 __device__ __forceinline__ void move_ref(Sums& a, float r) {
   const float d = a.r - r, c = lp_ex2(d);
@@ -88,32 +87,79 @@ __device__ __forceinline__ float from_order_key(uint32_t k) {
   return k == 0 ? __int_as_float(0x7fffffff) : __uint_as_float((k & 0x80000000u) ? k & 0x7fffffffu : ~k);
 }
 
-// 16 consecutive logits of a row from column c (of n; columns at n and behind read as -inf).
+// 16 consecutive logits as they lie in memory, and the reads of two chunks of them in flight at once.
 template <typename T>
-__device__ __forceinline__ void load16(const T* row, int64_t c, int64_t n, float (&z)[kLpChunk]) {
+struct Chunk {
+  uint4 w[sizeof(T)];
+};
+// Columns at n and behind read as -inf.
+template <typename T>
+__device__ __forceinline__ void load16(const T* row, int64_t c, int64_t n, Chunk<T>& q) {
   if (c + kLpChunk <= n) {
-    if constexpr (sizeof(T) == 2) {
 #pragma unroll
-      for (int v = 0; v < 2; ++v) {
-        const uint4 t = *reinterpret_cast<const uint4*>(row + c + 8 * v);
-        const uint32_t w[4] = {t.x, t.y, t.z, t.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          z[8 * v + 2 * i] = __uint_as_float(w[i] << 16);
-          z[8 * v + 2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-        }
-      }
-    } else {
-#pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        const float4 t = *reinterpret_cast<const float4*>(row + c + 4 * v);
-        z[4 * v] = t.x; z[4 * v + 1] = t.y; z[4 * v + 2] = t.z; z[4 * v + 3] = t.w;
-      }
-    }
+    for (int v = 0; v < (int)sizeof(T); ++v) q.w[v] = *(reinterpret_cast<const uint4*>(row + c) + v);
   } else {
+    T* e = reinterpret_cast<T*>(q.w);
 #pragma unroll
-    for (int i = 0; i < kLpChunk; ++i) z[i] = c + i < n ? (float)row[c + i] : -INFINITY;
+    for (int i = 0; i < kLpChunk; ++i) e[i] = c + i < n ? row[c + i] : (T)(-INFINITY);
   }
+}
+
+typedef unsigned long long f2;  // two fp32 values: one instruction for both
+__device__ __forceinline__ f2 pk(float a, float b) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void un(f2 v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+  f2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// Raises a chunk's logits to -kHuge at least (so that 2^x x is 0, not NaN, where the logit is -infinity); NaN stays. Returns
+// their maximum, NaN when one is NaN; top: the largest logit that is a number, as it was.
+__device__ __forceinline__ float clamp_max(Chunk<__nv_bfloat16>& q, float& top) {
+  __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(q.w);
+  const __nv_bfloat162 low = __float2bfloat162_rn(-kHuge);
+  __nv_bfloat162 t = h[0], m;
+#pragma unroll
+  for (int i = 1; i < 8; ++i) t = __hmax2(t, h[i]);
+  top = fmaxf(__low2float(t), __high2float(t));
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    h[i] = __hmax2_nan(h[i], low);
+    m = i ? __hmax2_nan(m, h[i]) : h[0];
+  }
+  const float a = __low2float(m), b = __high2float(m);
+  return a != a ? a : b != b ? b : fmaxf(a, b);
+}
+__device__ __forceinline__ float clamp_max(Chunk<float>& q, float& top) {
+  float* z = reinterpret_cast<float*>(q.w);
+  top = z[0];
+  float bad = 0.f;
+#pragma unroll
+  for (int i = 0; i < kLpChunk; ++i) {
+    top = fmaxf(top, z[i]);
+    if (z[i] != z[i]) bad = z[i];
+    else z[i] = fmaxf(z[i], -kHuge);
+  }
+  return bad != bad ? bad : fmaxf(top, -kHuge);
+}
+__device__ __forceinline__ void pair_of(const Chunk<__nv_bfloat16>& q, int i, float& a, float& b) {
+  const uint32_t w = reinterpret_cast<const uint32_t*>(q.w)[i];
+  a = __uint_as_float(w << 16);
+  b = __uint_as_float(w & 0xffff0000u);
+}
+__device__ __forceinline__ void pair_of(const Chunk<float>& q, int i, float& a, float& b) {
+  a = reinterpret_cast<const float*>(q.w)[2 * i];
+  b = reinterpret_cast<const float*>(q.w)[2 * i + 1];
 }
 
 template <typename T>
@@ -130,6 +176,7 @@ struct LpShared {
   Sums mine;                                    // this CTA's sums
   int count[2][kLpWarps];
   int pick[kLpMaxTop];                          // chosen chunks
+  int few[kLpFewChunks];                        // chunks that reach the bound
   int n_pick, n_cand;
   unsigned long long cand[kLpMaxTop * kLpChunk];  // (key, ~index) of candidates
   unsigned long long best[kLpMaxTop];           // this CTA's top k, best first (0: none)
@@ -156,10 +203,52 @@ __device__ __forceinline__ void rank_into(const unsigned long long* cand, int n,
   }
 }
 
+// The same from few chunks: the k-th largest of the threads' own largest keys (to 16 bits) is a bound that k chunks reach, and
+// hardly more do. Only the threads that reach it look for theirs, and only those chunks are read again. False when
+// more chunks or logits reach the bound than there is room for (many equal ones): nothing is done then.
+template <typename T>
+__device__ bool local_top_few(LpShared& sh, const KeyOf<T>* keys, KeyOf<T> top_key, const T* row, int64_t c0, int64_t n, int k) {
+  constexpr int kShift = 8 * (int)sizeof(KeyOf<T>) - 16;
+  const int n_chunk = (int)((n + kLpChunk - 1) / kLpChunk);
+  if (min(n_chunk, kLpThreads) <= k) return false;
+  const uint32_t mine = (uint32_t)top_key >> kShift;
+  if (threadIdx.x == 0) sh.n_pick = sh.n_cand = 0;
+  if (threadIdx.x < kLpMaxTop) sh.best[threadIdx.x] = 0;
+  uint32_t bound = 0;
+#pragma unroll 1
+  for (int b = 15; b >= 0; --b)
+    if (__syncthreads_count(mine >= (bound | (1u << b))) >= k) bound |= 1u << b;
+  if (mine >= bound)
+    for (int c = threadIdx.x; c < n_chunk; c += kLpThreads)
+      if ((uint32_t)keys[c] >> kShift >= bound) {
+        const int at = atomicAdd(&sh.n_pick, 1);
+        if (at < kLpFewChunks) sh.few[at] = c;
+      }
+  __syncthreads();
+  const int n_pick = sh.n_pick;
+  if (n_pick > kLpFewChunks) return false;
+  for (int i = threadIdx.x; i < n_pick * kLpChunk; i += kLpThreads) {
+    const int64_t c = c0 + (int64_t)sh.few[i / kLpChunk] * kLpChunk + i % kLpChunk;
+    if (c >= c0 + n) continue;
+    const uint32_t key = order_key((float)row[c]);
+    if (key >> 16 >= bound) {
+      const int at = atomicAdd(&sh.n_cand, 1);
+      if (at < kLpMaxTop * kLpChunk) sh.cand[at] = ((unsigned long long)key << 32) | (uint32_t)~(uint32_t)c;
+    }
+  }
+  __syncthreads();
+  const int n_cand = sh.n_cand;
+  if (n_cand > kLpMaxTop * kLpChunk) return false;
+  rank_into(sh.cand, n_cand, k, sh.best);
+  __syncthreads();
+  return true;
+}
+
 // This CTA's k largest logits of columns [c0, c0 + n) into sh.best, from the chunks' keys.
 template <typename T>
 __device__ void local_top(LpShared& sh, const KeyOf<T>* keys, const T* row, int64_t c0, int64_t n, int k) {
   const int n_chunk = (int)((n + kLpChunk - 1) / kLpChunk);
+  __syncthreads();
   const int per = (n_chunk + kLpThreads - 1) / kLpThreads;
   const int a = min(n_chunk, (int)threadIdx.x * per), e = min(n_chunk, a + per);
   if (threadIdx.x == 0) sh.n_pick = sh.n_cand = 0;
@@ -227,35 +316,45 @@ __global__ void __launch_bounds__(kLpThreads) logprob_fwd_kernel(const __grid_co
   const int64_t c0 = min(p.vocab, (int64_t)rank * p.seg), c1 = min(p.vocab, c0 + p.seg), n = c1 - c0;
   const int k = p.k;
 
-  // the sums of this thread's chunks; two chunks are in flight
+  // the sums of this thread's chunks, the next chunk's logits on their way
   Sums a = {-3e38f, 0.f, 0.f};
   const int n_chunk = (int)((n + kLpChunk - 1) / kLpChunk);
+  KeyOf<T> top_key = 0;  // of this thread's chunks
+  Chunk<T> q, q_next;
+  if ((int)threadIdx.x < n_chunk) load16(row, c0 + (int64_t)threadIdx.x * kLpChunk, c1, q_next);
   for (int c = threadIdx.x; c < n_chunk; c += kLpThreads) {
-    float z[kLpChunk];
-    load16(row, c0 + (int64_t)c * kLpChunk, c1, z);
-    float m = z[0];
-#pragma unroll
-    for (int i = 1; i < kLpChunk; ++i) m = fmaxf(m, z[i]);
-    if (k > 0) keys[c] = chunk_key<T>(m);
-    if (m < -kHuge) {  // nothing here, unless NaN stands among it
-#pragma unroll
-      for (int i = 0; i < kLpChunk; ++i)
-        if (z[i] != z[i]) a.s = z[i];
-      continue;
+    q = q_next;
+    if (c + kLpThreads < n_chunk) load16(row, c0 + (int64_t)(c + kLpThreads) * kLpChunk, c1, q_next);
+    float top;
+    const float m = clamp_max(q, top);
+    if (k > 0) {
+      const KeyOf<T> key = chunk_key<T>(top);
+      keys[c] = key;
+      top_key = max(top_key, key);
     }
-    if (m > kHuge) a.s = __int_as_float(0x7fffffff);
+    if (m == -kHuge) continue;  // nothing here
+    if (!(m <= kHuge)) a.s = __int_as_float(0x7fffffff);
     const float mr = ceilf(m * kLog2e);
     if (mr > a.r) move_ref(a, mr);
-    float s[2] = {0.f, 0.f}, w[2] = {0.f, 0.f};
+    f2 s[2] = {0, 0}, w[2] = {0, 0};
+    const f2 l2e = pk(kLog2e, kLog2e), ref = pk(-a.r, -a.r);
 #pragma unroll
-    for (int i = 0; i < kLpChunk; ++i) {
-      const float x = fmaf(z[i], kLog2e, -a.r);
-      const float e = lp_ex2(x);
-      s[i & 1] += e;
-      if (ENT) w[i & 1] += times_x(e, x);
+    for (int i = 0; i < kLpChunk / 2; ++i) {
+      float z0, z1;
+      pair_of(q, i, z0, z1);
+      const f2 x = fma2(pk(z0, z1), l2e, ref);
+      un(x, z0, z1);
+      const f2 e = pk(lp_ex2(z0), lp_ex2(z1));
+      s[i & 1] = add2(s[i & 1], e);
+      if (ENT) w[i & 1] = fma2(e, x, w[i & 1]);
     }
-    a.s += s[0] + s[1];
-    a.w += w[0] + w[1];
+    float s0, s1;
+    un(add2(s[0], s[1]), s0, s1);
+    a.s += s0 + s1;
+    if (ENT) {
+      un(add2(w[0], w[1]), s0, s1);
+      a.w += s0 + s1;
+    }
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -271,8 +370,8 @@ __global__ void __launch_bounds__(kLpThreads) logprob_fwd_kernel(const __grid_co
     for (int w = 1; w < kLpWarps; ++w) a = join(a, sh.part[w]);
     sh.mine = a;
   }
-  if (k > 0) local_top<T>(sh, keys, row, c0, n, k);
-  else __syncthreads();
+  __syncthreads();
+  if (k > 0 && !local_top_few<T>(sh, keys, top_key, row, c0, n, k)) local_top<T>(sh, keys, row, c0, n, k);
 
   if (n_cta > 1) {
     cluster.sync();

@@ -5,10 +5,12 @@
 // Backward: dn = (rotation by -p f_i) dy;  dg = sum over rows of dn x rstd;
 //   dx = rstd (g dn) - x rstd^3 mean_j(x_j g_j dn_j).
 //
-// Both passes move each element once and are bound by memory. A warp takes one token and a share of
-// its heads; a group of lanes holds one head, each lane two vectors of it that contain both
-// members of its pairs, so the rotation needs no exchange and the norm one short shuffle sum. The
-// token's cosines and sines are computed once per warp and serve all its heads.
+// Both passes move each element once and are bound by memory. A warp takes tokens in turn, and of each the heads of q
+// or of k; a group of lanes holds one head, each lane two vectors of it that contain both members of its
+// pairs, so the rotation needs no exchange and the norm one short shuffle sum. The token's cosines and sines are
+// computed a pair per lane and serve all its heads through shared memory; the next heads' vectors are on their way
+// meanwhile. (One block per token, each lane one head: 400 of 616 instructions a warp went into set-up, and the
+// forward was bound by issue at 1.8 TB/s.) Blocks of q stand before blocks of k.
 // Angles: p f_i in turns as a 64-bit fraction (f_i / 2 pi scaled by 2^64, times p, wrapping), so
 // far positions lose nothing to the range reduction; one rounding to fp32 before sincospi.
 #include <cuda_bf16.h>
@@ -23,19 +25,27 @@ namespace {
 
 constexpr int kRotThreads = 128;
 constexpr int kRotWarps = kRotThreads / 32;
+constexpr int kRotMaxPairs = 128;  // of a head: head_dim <= 256
+
+struct RotSide {
+  const __nv_bfloat16* x;   // inputs (backward: the forward's inputs; not read without the norm)
+  const __nv_bfloat16* dy;  // backward: gradients of the outputs
+  __nv_bfloat16* o;         // outputs (backward: gradients of the inputs)
+  const __nv_bfloat16* g;   // gains
+  int64_t ldx, lddy, ldo;
+  int32_t heads;
+  int32_t trips, split;     // trips of a warp over a token's heads, and the warps that share them
+  int32_t blocks;
+};
 
 struct RotParams {
-  const __nv_bfloat16 *xq, *xk;    // inputs (backward: the forward's inputs; null without the norm)
-  const __nv_bfloat16 *dyq, *dyk;  // backward: gradients of the outputs
-  __nv_bfloat16 *oq, *ok;          // outputs (backward: gradients of the inputs)
-  int64_t ldxq, ldxk, lddq, lddk, ldoq, ldok;
+  RotSide side[2];  // q, k
   const int32_t* pos;
   const float* inv_freq;
-  const __nv_bfloat16 *gq, *gk;  // gains (null without the norm)
-  float* partial;                // [gridDim.x][2][hd] sums of dg (backward with gain gradients)
-  float eps, inv_hd, sign;       // sign: +1 forward, -1 backward
+  float* partial;   // [q's blocks, then k's][hd] sums of dg (backward with gain gradients)
+  float eps, inv_hd, sign;  // sign: +1 forward, -1 backward
   int64_t n_tok;
-  int32_t hq, hkv, hd, rot, group, split;
+  int32_t hd, rot, group;
 };
 
 template <int V>
@@ -86,19 +96,23 @@ __device__ __forceinline__ uint64_t turn_step(float f, bool& ok) {
 // is (2 i, 2 i + 1), else (i, i + rot / 2). BWD: the norm's backward (without the norm the backward
 // is the forward kernel with the sign of the sines turned).
 template <int V, bool NORM, bool PAIRS, bool BWD>
-__global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_constant__ RotParams p) {
+__global__ void __launch_bounds__(kRotThreads, BWD ? 4 : 6) rotary_kernel(const __grid_constant__ RotParams p) {
+  __shared__ uint64_t s_step[kRotMaxPairs];              // a pair's angle per position; bit 0: not finite
+  __shared__ float2 s_turn[kRotWarps][kRotMaxPairs];     // the warp's token: (cos, sin) per pair
+  extern __shared__ float s_dg[];                        // at the end the groups' sums of dg
   pdl_wait();
+  const bool is_k = blockIdx.x >= (unsigned)p.side[0].blocks;
+  const RotSide& sd = p.side[is_k];
+  const int block = blockIdx.x - (is_k ? p.side[0].blocks : 0);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = lane & (p.group - 1), gi = lane / p.group, n_groups = 32 / p.group;
-  // this lane's two vectors of a head
   const int half = p.rot >> 1;
+  // this lane's two vectors of a head
   int off0, off1;
-  bool on0, on1, turn0, turn1;
+  bool turn0, turn1;
   if (PAIRS) {
     off0 = 2 * V * sub;
     off1 = off0 + V;
-    on0 = off0 < p.hd;
-    on1 = off1 < p.hd;
     turn0 = off0 < p.rot;
     turn1 = off1 < p.rot;
   } else {
@@ -106,80 +120,98 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_consta
     turn0 = turn1 = sub < n_pair;
     off0 = turn0 ? V * sub : p.rot + 2 * V * (sub - n_pair);
     off1 = turn0 ? off0 + half : off0 + V;
-    on0 = off0 < p.hd;
-    on1 = off1 < p.hd;
   }
-  // the lane's V pairs: pair index, step in turns
-  uint64_t step[V];
-  bool fine[V];
-#pragma unroll
-  for (int e = 0; e < V; ++e) {
-    const int i = PAIRS ? (e < V / 2 ? off0 : off1) / 2 + e % (V / 2) : off0 + e;
-    const bool t = PAIRS ? (e < V / 2 ? turn0 : turn1) : turn0;
-    step[e] = turn_step(t ? p.inv_freq[i] : 0.f, fine[e]);
+  const bool on0 = off0 < p.hd, on1 = off1 < p.hd;
+  Raw<V> gr0 = {}, gr1 = {};
+  if constexpr (NORM) {
+    if (on0) ld_raw(gr0, sd.g + off0);
+    if (on1) ld_raw(gr1, sd.g + off1);
   }
-  const int nh = p.hq + p.hkv;
-  const int per = (nh + p.split - 1) / p.split;
-  float dgq[NORM && BWD ? 2 * V : 1], dgk[NORM && BWD ? 2 * V : 1];
+  float dg[NORM && BWD ? 2 * V : 1];
   if constexpr (NORM && BWD) {
 #pragma unroll
-    for (int e = 0; e < 2 * V; ++e) dgq[e] = dgk[e] = 0.f;
+    for (int e = 0; e < 2 * V; ++e) dg[e] = 0.f;
   }
-  const int64_t n_items = p.n_tok * p.split;
-  for (int64_t item = (int64_t)blockIdx.x * kRotWarps + warp; item < n_items; item += (int64_t)gridDim.x * kRotWarps) {
-    const int64_t tok = item / p.split;
-    const int h0 = (int)(item % p.split) * per, h1 = min(nh, h0 + per);
-    float cs[V], sn[V];
-    if (p.rot > 0) {
-      const int64_t pos = p.pos[tok];
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float turns = (float)(int64_t)(step[e] * (uint64_t)pos) * 5.421010862427522e-20f;  // 2^-64
-        sincospif(2.f * turns, &sn[e], &cs[e]);
-        sn[e] *= p.sign;
-        if (!fine[e]) cs[e] = sn[e] = __int_as_float(0x7fffffff);
-      }
+  // raw vectors of this trip, then of the next (two trips ahead gained nothing)
+  struct Head {
+    Raw<V> x0, x1, d0, d1;
+  };
+  Head raw = {};
+  auto fetch = [&](int64_t tok, int trip, Head& r) {
+    const int h = trip * n_groups + gi;
+    if (h >= sd.heads) return;
+    if (!BWD || NORM) {
+      const __nv_bfloat16* x = sd.x + tok * sd.ldx + (int64_t)h * p.hd;
+      if (on0) ld_raw(r.x0, x + off0);
+      if (on1) ld_raw(r.x1, x + off1);
     }
-    for (int h = h0 + gi; h < h1 + gi; h += n_groups) {  // the same trips for every group of the warp
-      const bool live = h < h1;
-      const bool is_q = h < p.hq;
-      const int hh = is_q ? h : h - p.hq;
-      const int64_t at = (int64_t)hh * p.hd;
-      const bool l0 = live && on0, l1 = live && on1;
-      Raw<V> r0, r1;
+    if constexpr (BWD) {
+      const __nv_bfloat16* dy = sd.dy + tok * sd.lddy + (int64_t)h * p.hd;
+      if (on0) ld_raw(r.d0, dy + off0);
+      if (on1) ld_raw(r.d1, dy + off1);
+    }
+  };
+  // items: (token, share of its trips)
+  const int64_t n_items = p.n_tok * sd.split, stride = (int64_t)sd.blocks * kRotWarps;
+  const int per = (sd.trips + sd.split - 1) / sd.split;
+  int64_t item = (int64_t)block * kRotWarps + warp;
+  int64_t tok = item / sd.split;
+  int trip = (int)(item % sd.split) * per;
+  int pos = 0;
+  if (item < n_items) {
+    fetch(tok, trip, raw);
+    if (half) pos = p.pos[tok];
+  }
+  for (int i = threadIdx.x; i < half; i += kRotThreads) {
+    bool fine;
+    const uint64_t f = turn_step(p.inv_freq[i], fine) & ~1ull;
+    s_step[i] = fine ? f : 1ull;
+  }
+  __syncthreads();
+  for (; item < n_items; item += stride) {
+    const int64_t next = item + stride, tok_next = next / sd.split;
+    const int trip_next = (int)(next % sd.split) * per;
+    const int end = min(sd.trips, trip + per);
+    if (half) {
+      __syncwarp();  // the last token's table has been read
+      for (int i = lane; i < half; i += 32) {
+        const uint64_t f = s_step[i];
+        float2 v;
+        sincospif(2.f * ((float)(int64_t)(f * (uint64_t)(int64_t)pos) * 5.421010862427522e-20f), &v.y, &v.x);  // 2^-64
+        v.y *= p.sign;
+        if (f & 1) v.x = v.y = __int_as_float(0x7fffffff);
+        s_turn[warp][i] = v;
+      }
+      __syncwarp();
+      if (next < n_items) pos = p.pos[tok_next];
+    }
+    const float2* mine = s_turn[warp];
+    for (; trip < end; ++trip) {
+      const int h = trip * n_groups + gi;
+      const bool live = h < sd.heads;
       float x0[V], x1[V], y0[V], y1[V];
-#pragma unroll
-      for (int e = 0; e < V; ++e) x0[e] = x1[e] = y0[e] = y1[e] = 0.f;
-      float rs = 1.f;
-      if (!BWD || NORM) {
-        const __nv_bfloat16* x = (is_q ? p.xq + tok * p.ldxq : p.xk + tok * p.ldxk) + at;
-        if (l0) { ld_raw(r0, x + off0); widen(r0, x0); }
-        if (l1) { ld_raw(r1, x + off1); widen(r1, x1); }
-      }
-      float g0[V], g1[V];
-      if constexpr (NORM) {
-        const __nv_bfloat16* g = is_q ? p.gq : p.gk;
-#pragma unroll
-        for (int e = 0; e < V; ++e) g0[e] = g1[e] = 0.f;
-        if (on0) { ld_raw(r0, g + off0); widen(r0, g0); }
-        if (on1) { ld_raw(r1, g + off1); widen(r1, g1); }
-      }
+      widen(raw.x0, x0);
+      widen(raw.x1, x1);
       if constexpr (BWD) {
-        const __nv_bfloat16* dy = (is_q ? p.dyq + tok * p.lddq : p.dyk + tok * p.lddk) + at;
-        if (l0) { ld_raw(r0, dy + off0); widen(r0, y0); }
-        if (l1) { ld_raw(r1, dy + off1); widen(r1, y1); }
+        widen(raw.d0, y0);
+        widen(raw.d1, y1);
       }
+      if (trip + 1 < end) fetch(tok, trip + 1, raw);
+      else if (next < n_items) fetch(tok_next, trip_next, raw);
+      float rs = 1.f;
       if constexpr (NORM && !BWD) {
         float ss = 0.f;
 #pragma unroll
         for (int e = 0; e < V; ++e) ss = fmaf(x0[e], x0[e], fmaf(x1[e], x1[e], ss));
         for (int o = p.group >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
         rs = rsqrtf(ss * p.inv_hd + p.eps);
+        float g[V];
+        widen(gr0, g);
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          y0[e] = x0[e] * rs * g0[e];
-          y1[e] = x1[e] * rs * g1[e];
-        }
+        for (int e = 0; e < V; ++e) y0[e] = x0[e] * rs * g[e];
+        widen(gr1, g);
+#pragma unroll
+        for (int e = 0; e < V; ++e) y1[e] = x1[e] * rs * g[e];
       }
       if constexpr (!NORM && !BWD) {
 #pragma unroll
@@ -193,26 +225,33 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_consta
 #pragma unroll
         for (int e = 0; e < V / 2; ++e) {
           if (turn0) {
+            const float2 t = mine[off0 / 2 + e];
             const float a = y0[2 * e], b = y0[2 * e + 1];
-            y0[2 * e] = a * cs[e] - b * sn[e];
-            y0[2 * e + 1] = b * cs[e] + a * sn[e];
+            y0[2 * e] = a * t.x - b * t.y;
+            y0[2 * e + 1] = b * t.x + a * t.y;
           }
           if (turn1) {
+            const float2 t = mine[off1 / 2 + e];
             const float a = y1[2 * e], b = y1[2 * e + 1];
-            y1[2 * e] = a * cs[V / 2 + e] - b * sn[V / 2 + e];
-            y1[2 * e + 1] = b * cs[V / 2 + e] + a * sn[V / 2 + e];
+            y1[2 * e] = a * t.x - b * t.y;
+            y1[2 * e + 1] = b * t.x + a * t.y;
           }
         }
       } else if (turn0) {
 #pragma unroll
         for (int e = 0; e < V; ++e) {
+          const float2 t = mine[off0 + e];
           const float a = y0[e], b = y1[e];
-          y0[e] = a * cs[e] - b * sn[e];
-          y1[e] = b * cs[e] + a * sn[e];
+          y0[e] = a * t.x - b * t.y;
+          y1[e] = b * t.x + a * t.y;
         }
       }
       if constexpr (NORM && BWD) {
+        // y is dn here
         float ss = 0.f, dot = 0.f;
+        float g0[V], g1[V];
+        widen(gr0, g0);
+        widen(gr1, g1);
 #pragma unroll
         for (int e = 0; e < V; ++e) {
           ss = fmaf(x0[e], x0[e], fmaf(x1[e], x1[e], ss));
@@ -223,12 +262,11 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_consta
           dot += __shfl_xor_sync(0xffffffffu, dot, o);
         }
         rs = rsqrtf(ss * p.inv_hd + p.eps);
-        if (live) {
+        if (live && p.partial) {
 #pragma unroll
           for (int e = 0; e < V; ++e) {
-            const float a = y0[e] * x0[e] * rs, b = y1[e] * x1[e] * rs;
-            if (is_q) { dgq[e] += a; dgq[V + e] += b; }
-            else { dgk[e] += a; dgk[V + e] += b; }
+            dg[e] += y0[e] * x0[e] * rs;
+            dg[V + e] += y1[e] * x1[e] * rs;
           }
         }
         const float c = rs * rs * dot * p.inv_hd;
@@ -238,50 +276,55 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_consta
           y1[e] = rs * (g1[e] * y1[e] - x1[e] * c);
         }
       }
-      __nv_bfloat16* o = (is_q ? p.oq + tok * p.ldoq : p.ok + tok * p.ldok) + at;
-      if (l0) { narrow(r0, y0); st_raw(o + off0, r0); }
-      if (l1) { narrow(r1, y1); st_raw(o + off1, r1); }
+      if (live) {
+        __nv_bfloat16* o = sd.o + tok * sd.ldo + (int64_t)h * p.hd;
+        Raw<V> w;
+        if (on0) { narrow(w, y0); st_raw(o + off0, w); }
+        if (on1) { narrow(w, y1); st_raw(o + off1, w); }
+      }
     }
+    tok = tok_next;
+    trip = trip_next;
   }
   if constexpr (NORM && BWD) {
     if (p.partial) {
-      // every group of the block adds its share in a fixed order: [warp and group][2][hd]
-      extern __shared__ float s_dg[];
-      float* mine = s_dg + (size_t)(warp * n_groups + gi) * 2 * p.hd;
+      // every group of the block adds its share in a fixed order: [group][hd]
+      float* out = s_dg + (size_t)(threadIdx.x / p.group) * p.hd;
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        if (on0) { mine[off0 + e] = dgq[e]; mine[p.hd + off0 + e] = dgk[e]; }
-        if (on1) { mine[off1 + e] = dgq[V + e]; mine[p.hd + off1 + e] = dgk[V + e]; }
+        if (on0) out[off0 + e] = dg[e];
+        if (on1) out[off1 + e] = dg[V + e];
       }
       __syncthreads();
-      for (int c = threadIdx.x; c < 2 * p.hd; c += kRotThreads) {
-        float s = 0.f;
-        for (int w = 0; w < kRotWarps * n_groups; ++w) s += s_dg[(size_t)w * 2 * p.hd + c];
-        p.partial[(int64_t)blockIdx.x * 2 * p.hd + c] = s;
+      for (int c = threadIdx.x; c < p.hd; c += kRotThreads) {
+        float v = 0.f;
+        for (int w = 0; w < kRotThreads / p.group; ++w) v += s_dg[(size_t)w * p.hd + c];
+        p.partial[(int64_t)blockIdx.x * p.hd + c] = v;
       }
     }
   }
 }
 
-// dg[c] = sum over the blocks' partials, 32 columns per block; 32 interleaved sums per column, then
-// one tree: a fixed order.
-__global__ void __launch_bounds__(1024) rotary_gain_kernel(const float* __restrict__ partial, int n_part, int hd,
+// dg[c] = sum over the blocks' partials: rows [0, n_q) for q, [n_q, n_q + n_k) for k (blockIdx.y), 32 columns per
+// block; 32 interleaved sums per column, then one tree: a fixed order.
+__global__ void __launch_bounds__(1024) rotary_gain_kernel(const float* __restrict__ partial, int n_q, int n_k, int hd,
                                                           float* __restrict__ dgq, float* __restrict__ dgk) {
   pdl_wait();
   __shared__ float s[32][33];
   const int c = blockIdx.x * 32 + (threadIdx.x & 31), r = threadIdx.x >> 5;
+  const int row0 = blockIdx.y ? n_q : 0, n = blockIdx.y ? n_k : n_q;
   float v = 0.f;
-  if (c < 2 * hd)
-    for (int i = r; i < n_part; i += 32) v += partial[(int64_t)i * 2 * hd + c];
+  if (c < hd) {
+#pragma unroll 8
+    for (int i = r; i < n; i += 32) v += partial[(int64_t)(row0 + i) * hd + c];
+  }
   s[r][threadIdx.x & 31] = v;
   __syncthreads();
   v = s[threadIdx.x & 31][r];  // lane = partial sum, warp = column
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   const int col = blockIdx.x * 32 + r;
-  if ((threadIdx.x & 31) == 0 && col < 2 * hd) {
-    float* out = col < hd ? dgq : dgk;
-    if (out) out[col < hd ? col : col - hd] = v;
-  }
+  float* out = blockIdx.y ? dgk : dgq;
+  if ((threadIdx.x & 31) == 0 && col < hd && out) out[col] = v;
 }
 
 template <int V, bool NORM, bool BWD>
@@ -289,67 +332,64 @@ auto pick_style(bool pairs) {
   return pairs ? rotary_kernel<V, NORM, true, BWD> : rotary_kernel<V, NORM, false, BWD>;
 }
 
-// Blocks of a launch: enough to fill the SMs, tokens strided over them.
-int64_t rot_blocks(int64_t n_items) { return std::min<int64_t>((n_items + kRotWarps - 1) / kRotWarps, 148 * 8); }
+// Blocks of a launch: several times what the SMs hold at once, so that those that end early make room (20011 tokens:
+// forward 60 against 66 us, backward 97 against 104 with one load); with gain gradients each leaves one row of partial
+// sums.
+constexpr int kRotBlocks = 148 * 24, kRotBwdBlocks = 148 * 8;
 
 }  // namespace
 
-int64_t rotary_partial_floats(int64_t n_tok, int hd) {
-  return std::min<int64_t>(rot_blocks(n_tok * 64), 148 * 8) * 2 * hd;
-}
+int64_t rotary_partial_floats(int64_t n_tok, int hd) { return (int64_t)(kRotBwdBlocks + 2) * hd; }
 
 int rotary(const RotaryArgs& a, cudaStream_t s) {
   RotParams p = {};
   const bool norm = a.gq != nullptr, bwd = a.dyq != nullptr && norm;
-  p.xq = static_cast<const __nv_bfloat16*>(a.dyq && !norm ? a.dyq : a.xq);
-  p.xk = static_cast<const __nv_bfloat16*>(a.dyq && !norm ? a.dyk : a.xk);
-  p.ldxq = a.dyq && !norm ? a.lddq : a.ldxq;
-  p.ldxk = a.dyq && !norm ? a.lddk : a.ldxk;
-  p.dyq = static_cast<const __nv_bfloat16*>(a.dyq);
-  p.dyk = static_cast<const __nv_bfloat16*>(a.dyk);
-  p.lddq = a.lddq;
-  p.lddk = a.lddk;
-  p.oq = static_cast<__nv_bfloat16*>(a.oq);
-  p.ok = static_cast<__nv_bfloat16*>(a.ok);
-  p.ldoq = a.ldoq;
-  p.ldok = a.ldok;
-  p.pos = a.pos;
-  p.inv_freq = a.inv_freq;
-  p.gq = static_cast<const __nv_bfloat16*>(a.gq);
-  p.gk = static_cast<const __nv_bfloat16*>(a.gk);
-  p.eps = a.eps;
-  p.inv_hd = 1.f / (float)a.hd;
-  p.sign = a.dyq ? -1.f : 1.f;
-  p.n_tok = a.n_tok;
-  p.hq = a.hq;
-  p.hkv = a.hkv;
-  p.hd = a.hd;
-  p.rot = a.rot;
+  const bool turn_back = a.dyq && !norm;  // without the norm the gradient is rotated like an input
   const int V = a.pairs || a.rot % 16 == 0 ? 8 : 4;
   // lanes per head: one slot of two vectors each
   const int slots = a.pairs ? (a.hd + 2 * V - 1) / (2 * V) : a.rot / 2 / V + (a.hd - a.rot + 2 * V - 1) / (2 * V);
   int group = 1;
   while (group < slots) group *= 2;
-  p.group = group;
-  // few tokens: the heads of a token are spread over several warps
-  const int nh = a.hq + a.hkv, n_groups = 32 / group;
-  int split = 1;
-  while (split * n_groups < nh && a.n_tok * split < 148 * 16) split *= 2;
-  p.split = std::min(split, 64);
-  const int64_t grid = rot_blocks(a.n_tok * p.split);
   const bool gains = bwd && (a.dgq || a.dgk);
+  for (int k = 0; k < 2; ++k) {
+    RotSide& d = p.side[k];
+    d.x = static_cast<const __nv_bfloat16*>(turn_back ? (k ? a.dyk : a.dyq) : (k ? a.xk : a.xq));
+    d.ldx = turn_back ? (k ? a.lddk : a.lddq) : (k ? a.ldxk : a.ldxq);
+    d.dy = static_cast<const __nv_bfloat16*>(k ? a.dyk : a.dyq);
+    d.lddy = k ? a.lddk : a.lddq;
+    d.o = static_cast<__nv_bfloat16*>(k ? a.ok : a.oq);
+    d.ldo = k ? a.ldok : a.ldoq;
+    d.g = static_cast<const __nv_bfloat16*>(k ? a.gk : a.gq);
+    d.heads = k ? a.hkv : a.hq;
+    d.trips = (d.heads * group + 31) / 32;
+    // the blocks in proportion to the heads; few tokens: a token's trips over several warps
+    const int64_t share = std::max<int64_t>(1, (int64_t)(bwd ? kRotBwdBlocks : kRotBlocks) * d.heads / (a.hq + a.hkv));
+    int split = 1;
+    while (split < d.trips && a.n_tok * split * 2 <= share * kRotWarps) split *= 2;
+    d.split = std::min(split, d.trips);
+    d.blocks = (int)std::min((a.n_tok * d.split + kRotWarps - 1) / kRotWarps, share);
+  }
+  p.pos = a.pos;
+  p.inv_freq = a.inv_freq;
+  p.eps = a.eps;
+  p.inv_hd = 1.f / (float)a.hd;
+  p.sign = a.dyq ? -1.f : 1.f;
+  p.n_tok = a.n_tok;
+  p.hd = a.hd;
+  p.rot = a.rot;
+  p.group = group;
   p.partial = gains ? a.partial : nullptr;
-  const size_t smem = gains ? (size_t)kRotWarps * n_groups * 2 * a.hd * 4 : 0;
+  const size_t smem = gains ? (size_t)(kRotThreads / group) * a.hd * 4 : 0;
   auto kernel = V == 8 ? (norm ? (bwd ? pick_style<8, true, true>(a.pairs) : pick_style<8, true, false>(a.pairs))
                                : pick_style<8, false, false>(a.pairs))
                        : (norm ? (bwd ? rotary_kernel<4, true, false, true> : rotary_kernel<4, true, false, false>)
                                : rotary_kernel<4, false, false, false>);
-  launch_kernel(kernel, (unsigned)grid, kRotThreads, smem, s, p);
+  launch_kernel(kernel, (unsigned)(p.side[0].blocks + p.side[1].blocks), kRotThreads, smem, s, p);
   if (launch_failed("sl_qk_norm_rope")) return 5;
   note_launch();
   if (gains) {
-    launch_kernel(rotary_gain_kernel, (unsigned)((2 * a.hd + 31) / 32), 1024, 0, s, (const float*)a.partial, (int)grid,
-                  a.hd, a.dgq, a.dgk);
+    launch_kernel(rotary_gain_kernel, dim3((unsigned)((a.hd + 31) / 32), 2), 1024, 0, s, (const float*)a.partial,
+                  p.side[0].blocks, p.side[1].blocks, a.hd, a.dgq, a.dgk);
     if (launch_failed("sl_qk_norm_rope")) return 5;
     note_launch();
   }
