@@ -20,8 +20,12 @@ namespace sl {
 
 namespace {
 
+// Every wait is for one phase of a barrier by its parity, so no barrier may complete a phase before everyone who waits for
+// the last one has passed: each producer below is held back by an answer of its consumers, or has a second barrier
+// to alternate with.
 constexpr int kFwdThreads = 384;  // warp 0 TMA, warps 1 and 2 MMA (warp 1 allocates TMEM), warps 4..11 softmax
-constexpr int kBwdThreads = 640;  // the same with compute warps 4..19; dk, dv: warp 3 reads the query rows
+constexpr int kBwdThreads = 640;  // dq: warp 0 TMA, warp 1 MMA, warps 4..19 compute
+constexpr int kDkvThreads = 384;  // dk, dv: warp 0 TMA, warp 1 MMA, warp 3 reads the query rows, warps 4..11 compute
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -391,17 +395,16 @@ __device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, u
 // fields count 16 bytes). One thread issues them all, and with descriptors built anew in a loop over the steps its own
 // instructions, not the tensor cores, set the pace.
 // A and B K-major tiles (N steps over the head dimension, four per 16 KB chunk):
-template <int N>
+template <int N, int B_CHUNK>
 __device__ __forceinline__ void mma_kk(uint32_t d, uint64_t a, uint64_t b, uint32_t id) {
 #pragma unroll
-  for (int k = 0; k < N; ++k) {
-    const uint32_t off = (k >> 2) * (kChunk >> 4) + (k & 3) * 2;
-    umma_bf16(d, a + off, b + off, id, k > 0 ? 1u : 0u);
-  }
+  for (int k = 0; k < N; ++k)
+    umma_bf16(d, a + (k >> 2) * (kChunk >> 4) + (k & 3) * 2, b + (k >> 2) * (B_CHUNK >> 4) + (k & 3) * 2, id, k > 0 ? 1u : 0u);
 }
+template <int B_CHUNK = kChunk>  // bytes from one 64-column chunk of B to the next
 __device__ __forceinline__ void mma_kk_nd(int nd, uint32_t d, uint64_t a, uint64_t b, uint32_t id) {
-  if (nd == 2) mma_kk<8>(d, a, b, id);
-  else mma_kk<4>(d, a, b, id);
+  if (nd == 2) mma_kk<8, B_CHUNK>(d, a, b, id);
+  else mma_kk<4, B_CHUNK>(d, a, b, id);
 }
 // A in TMEM (8 columns per step, STRIDE columns from one 32-element piece to the next), B MN-major (16 token rows, 2 KB,
 // per step); N steps over tokens:
@@ -434,6 +437,7 @@ struct MaskedFwdParams {
 
 struct MaskedBwdParams {
   CUtensorMap qmap, kmap, vmap, domap;  // boxes as in the forward
+  CUtensorMap qmap64, domap64;          // boxes of 64 rows
   Plan plan;
   const float* slopes;
   const float* lse;              // [hq][T]
@@ -568,9 +572,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1) masked_fwd_kernel(const __grid
   uint64_t* kv_empty = bars + 6;   // [2]
   uint64_t* s_full = bars + 12;    // [2 x + buffer]
   uint64_t* p_full = bars + 16;    // [2 x + buffer]
-  uint64_t* pv_done = bars + 20;   // [2] by stream: P V of a unit's last two steps
-  uint64_t* drain = bars + 22;     // [2] by stream
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 24);
+  uint64_t* pv_done = bars + 20;   // [2 x + buffer]: P V of a unit's last two steps
+  uint64_t* drain = bars + 24;     // [2] by stream
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 26);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -581,9 +585,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1) masked_fwd_kernel(const __grid
       mbar_init(&q_empty[s], 1);
       mbar_init(&kv_full[s], 1);
       mbar_init(&kv_empty[s], 2);  // both streams
-      mbar_init(&pv_done[s], 1);
     }
     for (int s = 0; s < 4; ++s) {
+      mbar_init(&pv_done[s], 1);
       mbar_init(&s_full[s], 1);
       mbar_init(&p_full[s], 4);
     }
@@ -683,7 +687,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) masked_fwd_kernel(const __grid
           tc_fence_after();
           mma_tm<4>(tmem + 256 + 128 * x, tmem + 128 * x + 64 * buf, dv0 + s * (2 * kChunk >> 4) + (buf ^ 1) * 512, id_pv,
                     j > 0 || buf > 0);
-          if (last) umma_commit(&pv_done[x]);
+          if (last) umma_commit(&pv_done[2 * x + buf]);
           if (buf) umma_commit(&kv_empty[s]);
           if (more) {
             if (buf == 0) {
@@ -792,8 +796,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1) masked_fwd_kernel(const __grid
         if (k0 < me.j1 * kTile - 64 && __any_sync(0xffffffffu, corr != 1.f)) {
           // O of the steps before is complete once their last P V is: S of the next step stands behind it in the tensor
           // pipe; after a unit's last S its own barrier tells
-          uint64_t* bar = k0 > me.j0 * kTile ? &s_full[2 * x + (buf ^ 1)] : &pv_done[x];
-          const uint32_t phase = k0 > me.j0 * kTile ? ((t + 1) >> 1) & 1 : 0;
+          uint64_t* bar = k0 > me.j0 * kTile ? &s_full[2 * x + (buf ^ 1)] : &pv_done[2 * x];
+          const uint32_t phase = k0 > me.j0 * kTile ? ((t + 1) >> 1) & 1 : i & 1;
           ok = __all_sync(0xffffffffu, mbar_wait_soon(bar, phase, abort_flag, p.err, DEV_TIMEOUT_EPILOGUE));
           if (!ok) break;
           tc_fence_after();
@@ -817,9 +821,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) masked_fwd_kernel(const __grid
       }
       if (!ok) break;
       if (more) rows_of(nx, nlo, nhi);
-      // P V of the unit's last two steps, one by one (a wait for a barrier's phase is right once the phase before it is over)
-      ok = __all_sync(0xffffffffu, mbar_wait_soon(&pv_done[x], 0, abort_flag, p.err, DEV_TIMEOUT_EPILOGUE) &&
-                                       mbar_wait_soon(&pv_done[x], 1, abort_flag, p.err, DEV_TIMEOUT_EPILOGUE));
+      ok = __all_sync(0xffffffffu, mbar_wait_soon(&pv_done[2 * x + 1], i & 1, abort_flag, p.err, DEV_TIMEOUT_EPILOGUE));
       if (!ok) break;
       // O / l as bf16; the next unit's first P V waits for this softmax's next P
       tc_fence_after();
@@ -909,10 +911,12 @@ __device__ __forceinline__ void grad32(uint32_t (&s)[32], uint32_t (&dp)[32], fl
 }
 
 // dq: persistent CTAs over units (query tile, head). Q and dO stay, K and V stream through two stages, twice: first for D,
-// then for dQ. Warp 0 loads; warp 1 issues S = Q K^T and dP = dO V^T; warp 2 issues dQ += dS K; warps 4-19 hold a query row
-// and 32 of the key columns per thread (with 64 columns and half as many warps a scheduler has two to choose from,
-// and most of the time neither can issue). They take S and dP into registers at once, so the
-// next tile's products run while they work. TMEM: dQ at 0, S at 128, dP at 256, dS (bf16, two buffers) at 384.
+// then for dQ. Warp 0 loads; warp 1 issues the products in the order S = Q K^T of step t + 1, dP = dO V^T of step t + 1,
+// dQ += dS K of step t: while the compute warps work on step t the tensor cores are a step ahead, and one thread's order
+// is all that the buffers need (S has two, dS takes the place of its S; dP has one, which the compute warps
+// take into registers at once). The second pass begins with the last two key tiles, whose K and V are still there (documents of up
+// to 256 keys are read once), and goes back from the one before them. Warps 4-19 hold a query row and 32 of the key columns per thread. TMEM: dQ at 0, S / dS of
+// step t at 128 + 128 (t & 1), dP at 384.
 template <bool CAP, bool BIAS>
 __global__ void __launch_bounds__(kBwdThreads, 1) masked_dq_kernel(const __grid_constant__ MaskedBwdParams p) {
   extern __shared__ uint8_t smem_raw[];
@@ -926,12 +930,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1) masked_dq_kernel(const __grid_
   uint64_t* q_empty = bars + 1;
   uint64_t* kv_full = bars + 2;    // [2]
   uint64_t* kv_empty = bars + 4;   // [2]
-  uint64_t* s_full = bars + 6;
-  uint64_t* s_free = bars + 7;
-  uint64_t* ds_full = bars + 8;    // [2]
-  uint64_t* dq_done = bars + 10;   // [2]
-  uint64_t* drain = bars + 12;     // [2]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 14);
+  uint64_t* s_full = bars + 6;     // S and dP of a step
+  uint64_t* dp_free = bars + 7;    // S and dP of a step are in registers
+  uint64_t* ds_full = bars + 8;    // [2], in turn: the compute warps may end a step before the last one's dS is asked for
+  uint64_t* dq_done = bars + 10;   // a unit's dQ
+  uint64_t* drain = bars + 11;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 12);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -956,13 +960,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1) masked_dq_kernel(const __grid_
     mbar_init(q_empty, 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(&kv_full[s], 1);
-      mbar_init(&kv_empty[s], 2);  // S and dP; dQ
-      mbar_init(&ds_full[s], 16);
-      mbar_init(&dq_done[s], 1);
-      mbar_init(&drain[s], 1);
+      mbar_init(&kv_empty[s], 1);
     }
     mbar_init(s_full, 1);
-    mbar_init(s_free, 16);
+    mbar_init(dp_free, 16);
+    mbar_init(&ds_full[0], 16);
+    mbar_init(&ds_full[1], 16);
+    mbar_init(dq_done, 1);
+    mbar_init(drain, 1);
     *abort_flag = 0;
     fence_barrier_init();
     tma_prefetch_desc(&p.qmap);
@@ -997,82 +1002,99 @@ __global__ void __launch_bounds__(kBwdThreads, 1) masked_dq_kernel(const __grid_
           tma_load_4d(sq + c * kChunk, &p.qmap, q_full, 64 * c, w.h, w.qt * kTile, w.b);
           tma_load_4d(sq + (2 + c) * kChunk, &p.domap, q_full, 64 * c, w.h, w.qt * kTile, w.b);
         }
-        for (int pass = 0; pass < 2 && ok; ++pass)
-          for (int j = w.j0; j < w.j1; ++j, ++t) {
-            const int s = t & 1;
-            if (!mbar_wait_soon(&kv_empty[s], ((t >> 1) & 1) ^ 1, abort_flag, p.err, DEV_TIMEOUT_PRODUCER)) { ok = false; break; }
-            mbar_arrive_expect_tx(&kv_full[s], 2 * nd * kChunk);
-            uint8_t* st = skv + s * 4 * kChunk;
-            for (int c = 0; c < nd; ++c) {
-              tma_load_4d(st + c * kChunk, &p.kmap, &kv_full[s], 64 * c, w.h / hpg, j * kTile, w.b);
-              tma_load_4d(st + (2 + c) * kChunk, &p.vmap, &kv_full[s], 64 * c, w.h / hpg, j * kTile, w.b);
-            }
+        // the second pass loads all but the last two tiles again
+        for (int k = 0; k < 2 * (w.j1 - w.j0) - min(2, w.j1 - w.j0); ++k, ++t) {
+          const int s = t & 1, j = k < w.j1 - w.j0 ? w.j0 + k : w.j1 - 3 - (k - (w.j1 - w.j0));
+          if (!mbar_wait_soon(&kv_empty[s], ((t >> 1) & 1) ^ 1, abort_flag, p.err, DEV_TIMEOUT_PRODUCER)) { ok = false; break; }
+          mbar_arrive_expect_tx(&kv_full[s], 2 * nd * kChunk);
+          uint8_t* st = skv + s * 4 * kChunk;
+          for (int c = 0; c < nd; ++c) {
+            tma_load_4d(st + c * kChunk, &p.kmap, &kv_full[s], 64 * c, w.h / hpg, j * kTile, w.b);
+            tma_load_4d(st + (2 + c) * kChunk, &p.vmap, &kv_full[s], 64 * c, w.h / hpg, j * kTile, w.b);
           }
+        }
       }
       // every copy lands before the CTA may exit
       if (i > 0) mbar_wait(q_full, (i - 1) & 1, nullptr, p.err, DEV_TIMEOUT_DRAIN);
       for (int k = max(0, t - 2); k < t; ++k) mbar_wait(&kv_full[k & 1], (k >> 1) & 1, nullptr, p.err, DEV_TIMEOUT_DRAIN);
     } else if (warp == 1 && lane == 0) {
-      const uint32_t id = idesc_bf16(128, 128, 0, 0);
-      const uint64_t dq0 = kmajor_desc(smem_u32(sq), 0), ddo0 = dq0 + (2 * kChunk >> 4), dk0 = kmajor_desc(smem_u32(skv), 0);
-      U w, nx;
-      bool ok = plan_ok, live = plan_ok && unit(0, nx);
-      int t = 0;
-      for (int i = 0; ok && live; ++i) {
-        w = nx;
-        live = unit(i + 1, nx);
-        if (!mbar_wait_soon(q_full, i & 1, abort_flag, p.err, DEV_TIMEOUT_MMA)) break;
-        for (int pass = 0; pass < 2 && ok; ++pass)
-          for (int j = w.j0; j < w.j1; ++j, ++t) {
-            const int s = t & 1;
-            ok = mbar_wait_soon(&kv_full[s], (t >> 1) & 1, abort_flag, p.err, DEV_TIMEOUT_MMA) &&
-                 (t == 0 || mbar_wait_soon(s_free, (t - 1) & 1, abort_flag, p.err, DEV_TIMEOUT_MMA));
-            if (!ok) break;
-            tc_fence_after();
-            const uint64_t bk = dk0 + s * (4 * kChunk >> 4);
-            mma_kk_nd(nd, tmem + 128, dq0, bk, id);
-            mma_kk_nd(nd, tmem + 256, ddo0, bk + (2 * kChunk >> 4), id);
-            umma_commit(s_full);
-            umma_commit(&kv_empty[s]);
-            if (pass == 0) mbar_arrive(&kv_empty[s]);  // no dQ in the first pass
-            if (pass == 1 && j == w.j1 - 1) umma_commit(q_empty);
-          }
-      }
-      umma_commit(&drain[0]);
-      mbar_wait(&drain[0], 0, nullptr, p.err, DEV_TIMEOUT_DRAIN);
-    } else if (warp == 2 && lane == 0) {
-      const uint32_t id = idesc_bf16(128, 64 * nd, 0, 1);  // dS in TMEM, K MN-major
-      const uint64_t dk0 = mnmajor_desc(smem_u32(skv), 0);
-      U w, nx;
-      bool ok = plan_ok, live = plan_ok && unit(0, nx);
-      int t = 0, n = 0;  // steps of both passes, steps of the second
-      for (int i = 0; ok && live; ++i) {
-        w = nx;
-        live = unit(i + 1, nx);
-        t += w.j1 - w.j0;
-        for (int j = w.j0; j < w.j1; ++j, ++t, ++n) {
-          const int s = t & 1, d = n & 1;
-          ok = mbar_wait_soon(&ds_full[d], (n >> 1) & 1, abort_flag, p.err, DEV_TIMEOUT_MMA) &&
-               mbar_wait_soon(&kv_full[s], (t >> 1) & 1, abort_flag, p.err, DEV_TIMEOUT_MMA);
+      const uint32_t id_s = idesc_bf16(128, 128, 0, 0), id_dq = idesc_bf16(128, 64 * nd, 0, 1);
+      const uint64_t dq0 = kmajor_desc(smem_u32(sq), 0), ddo0 = dq0 + (2 * kChunk >> 4), dk0 = kmajor_desc(smem_u32(skv), 0),
+                     dkm0 = mnmajor_desc(smem_u32(skv), 0);
+      // key tiles of this CTA's unit i (0: there is none); a unit has twice as many steps
+      auto tiles_of = [&](int i) -> int {
+        const int u = unit_number(i);
+        if (!plan_ok || u >= p.n_units) return 0;
+        const int4 e = p.plan.q_order[u / p.hq];
+        return e.z - e.y;
+      };
+      int n = tiles_of(0), n_next = tiles_of(1), i = 0, j = 0;  // tiles of this unit and the next, unit, step in it
+      // The load (of this CTA's) whose K and V step j of a unit of n tiles works on, the unit's first being load l0
+      auto load_of = [](int l0, int n, int j) {
+        const int r = min(2, n);
+        return l0 + (j < n ? j : j - r);
+      };
+      // S and dP of step t, which is step j of unit iu (n tiles, first load l0)
+      auto issue_s = [&](int t, int iu, int j, int n, int l0) -> bool {
+        const int l = load_of(l0, n, j), s = l & 1;
+        if ((j == 0 && !mbar_wait_soon(q_full, iu & 1, abort_flag, p.err, DEV_TIMEOUT_MMA)) ||
+            !mbar_wait_soon(&kv_full[s], (l >> 1) & 1, abort_flag, p.err, DEV_TIMEOUT_MMA))
+          return false;
+        tc_fence_after();
+        const uint64_t bk = dk0 + s * (4 * kChunk >> 4);
+        mma_kk_nd(nd, tmem + 128 + 128 * (t & 1), dq0, bk, id_s);
+        if (t > 0) {
+          if (!mbar_wait_soon(dp_free, (t - 1) & 1, abort_flag, p.err, DEV_TIMEOUT_MMA)) return false;
+          tc_fence_after();
+        }
+        mma_kk_nd(nd, tmem + 384, ddo0, bk + (2 * kChunk >> 4), id_s);
+        umma_commit(s_full);
+        if (j < n - 2) umma_commit(&kv_empty[s]);  // the last two tiles stay for the second pass
+        if (j == 2 * n - 1) umma_commit(q_empty);
+        return true;
+      };
+      int l0 = 0;  // this unit's first load
+      bool ok = n > 0 && issue_s(0, 0, 0, n, 0);
+      int c = 0;  // dQ products so far
+      for (int t = 0; ok; ++t) {
+        const bool unit_end = j == 2 * n - 1;
+        const int l0_next = l0 + 2 * n - min(2, n);
+        if (!unit_end) ok = issue_s(t + 1, i, j + 1, n, l0);
+        else if (n_next > 0) ok = issue_s(t + 1, i + 1, 0, n_next, l0_next);
+        if (!ok) break;
+        if (j >= n) {
+          ok = mbar_wait_soon(&ds_full[c & 1], (c >> 1) & 1, abort_flag, p.err, DEV_TIMEOUT_MMA);
           if (!ok) break;
           tc_fence_after();
-          mma_tm<8>(tmem, tmem + 384 + 64 * d, dk0 + s * (4 * kChunk >> 4), id, j > w.j0);
-          umma_commit(&dq_done[d]);
-          umma_commit(&kv_empty[s]);
+          const int st = load_of(l0, n, j) & 1;
+          mma_tm<8, 32>(tmem, tmem + 128 + 128 * (t & 1), dkm0 + st * (4 * kChunk >> 4), id_dq, j > n);
+          umma_commit(&kv_empty[st]);
+          ++c;
+        }
+        if (unit_end) {
+          umma_commit(dq_done);
+          if (n_next == 0) break;
+          ++i;
+          j = 0;
+          n = n_next;
+          n_next = tiles_of(i + 1);
+          l0 = l0_next;
+        } else {
+          ++j;
         }
       }
-      umma_commit(&drain[1]);
-      mbar_wait(&drain[1], 0, nullptr, p.err, DEV_TIMEOUT_DRAIN);
+      umma_commit(drain);
+      mbar_wait(drain, 0, nullptr, p.err, DEV_TIMEOUT_DRAIN);
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
     const int quarter = warp & 3, cq = (warp - 4) >> 2;  // rows (TMEM lanes); 32 of the 128 key columns
     const int r = quarter * 32 + lane;
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
-    const uint32_t s_tm = tmem + lane_off + 128 + 32 * cq, dp_tm = s_tm + 128, ds_tm = tmem + lane_off + 384 + 16 * cq;
+    const uint32_t s_tm = tmem + lane_off + 128 + 32 * cq, dp_tm = tmem + lane_off + 384 + 32 * cq;
     U w, nx;
     bool ok = plan_ok, live = plan_ok && unit(0, nx);
-    int t = 0, n = 0;
+    int t = 0, c = 0;  // steps, those of the second pass
     int nlo = 0, nhi = 0;
     float nlse = 0.f;
     const int64_t T = (int64_t)p.n_seq * p.S;
@@ -1099,17 +1121,20 @@ __global__ void __launch_bounds__(kBwdThreads, 1) masked_dq_kernel(const __grid_
         const float nD = pass ? -sum : 0.f;
         f2 acc[2] = {0, 0};
         float only = 0.f;
-        for (int j = w.j0; j < w.j1; ++j, ++t) {
+        const int n = w.j1 - w.j0, kept = min(2, n);
+        for (int k = 0; k < n; ++k, ++t) {
+          // the second pass: the last two tiles, then back from the one before them
+          const int j = w.j0 + (pass == 0 ? k : k < kept ? n - kept + k : n - 1 - k);
           ok = __all_sync(0xffffffffu, mbar_wait_soon(s_full, t & 1, abort_flag, p.err, DEV_TIMEOUT_EPILOGUE));
           if (!ok) break;
           tc_fence_after();
           uint32_t s[32], dp[32];
-          tmem_ld32(s_tm, s);
+          tmem_ld32(s_tm + 128 * (t & 1), s);
           tmem_ld32(dp_tm, dp);
           tmem_ld_wait_regs(s);
           regs_after_wait(dp);
           tc_fence_before();
-          warp_arrive(s_free, lane);
+          warp_arrive(dp_free, lane);
           const int k0 = j * kTile + 32 * cq;  // key of this thread's first column
           const bool part = __any_sync(0xffffffffu, lo > k0 || hi < k0 + 32);
           const uint32_t see = see_bits(lo - k0, hi - k0);
@@ -1133,19 +1158,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1) masked_dq_kernel(const __grid_
               acc[(e >> 1) & 1] = fma2(pk(ex2(x0), ex2(x1)), pku(dp[e], dp[e + 1]), acc[(e >> 1) & 1]);
             }
           } else {
-            const int d = n & 1;
             uint32_t pw[16], dw[16];
             grad32<CAP, BIAS, true, false>(s, dp, p.mul, p.cap_mul, slope, (float)(qt0 + r - k0), side, part, see, nl, nD,
                                            nullptr, nullptr, pw, dw);
-            // dQ of two steps ago has read this buffer (its predecessors' phases are over: it reads them in order)
-            if (n >= 2)
-              ok = __all_sync(0xffffffffu, mbar_wait_soon(&dq_done[d], ((n >> 1) - 1) & 1, abort_flag, p.err, DEV_TIMEOUT_EPILOGUE));
-            if (!ok) break;
-            tmem_st16(ds_tm + 64 * d, dw);
+            tmem_st16(s_tm + 128 * (t & 1), dw);  // over the scores that this warp itself has read
             tmem_st_wait();
             tc_fence_before();
-            warp_arrive(&ds_full[d], lane);
-            ++n;
+            warp_arrive(&ds_full[c & 1], lane);
+            ++c;
           }
         }
         if (pass == 0) {
@@ -1157,7 +1177,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) masked_dq_kernel(const __grid_
           if (ok && cq == 0 && qt0 + r < p.S) p.delta[(int64_t)h * T + (int64_t)b * p.S + qt0 + r] = sum;
         } else {
           if (ok && live) rows_of(nx);
-          if (ok) ok = __all_sync(0xffffffffu, mbar_wait_soon(&dq_done[(n - 1) & 1], ((n - 1) >> 1) & 1, abort_flag, p.err, DEV_TIMEOUT_EPILOGUE));
+          if (ok) ok = __all_sync(0xffffffffu, mbar_wait_soon(dq_done, i & 1, abort_flag, p.err, DEV_TIMEOUT_EPILOGUE));
           ok = bar_and_compute(ok);  // also: s_part is free for the next unit
         }
       }
@@ -1186,34 +1206,34 @@ __global__ void __launch_bounds__(kBwdThreads, 1) masked_dq_kernel(const __grid_
 }
 
 // dk, dv: one CTA per (key tile, key/value head) in the plan's order, over (query head of the group, query tile). K and V
-// stay, Q and dO stream through two stages. A step is half a query tile (64 queries): S^T = K Q^T and dP^T = V dO^T of
+// stay, Q and dO stream through four stages of 64 queries. A step is half a query tile (64 queries): S^T = K Q^T and dP^T = V dO^T of
 // step t + 1 run while the compute warps work on step t; P^T and dS^T replace them in TMEM (bf16, first
-// operands of dV += P^T dO and dK += dS^T Q). Warp 0 loads; warp 1 issues S^T and dP^T, warp 2 dV and dK; warp 3 reads the
-// query rows' lse, D and intervals; warps 4-11 and 12-19 take the even and the odd steps, a key row and 32 of the 64 query
-// columns per thread. TMEM: S^T of
+// operands of dV += P^T dO and dK += dS^T Q). Warp 0 loads; warp 1 issues dV and dK of step t, then S^T and dP^T of step
+// t + 2 into the same buffers (two threads for the two pairs had to wait for each other: 290 us at 4096 causal tokens,
+// half of the tensor cores' time); warp 3 reads the
+// query rows' lse, D and intervals; warps 4-7 and 8-11 take the even and the odd steps, a key row per thread. TMEM: S^T of
 // buffer x at 64 x, dP^T at 128 + 64 x, dV at 256, dK at 384.
 template <bool CAP, bool BIAS>
-__global__ void __launch_bounds__(kBwdThreads, 1) masked_dkv_kernel(const __grid_constant__ MaskedBwdParams p) {
+__global__ void __launch_bounds__(kDkvThreads, 1) masked_dkv_kernel(const __grid_constant__ MaskedBwdParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int nd = p.nd;
   uint8_t* sk = smem;                       // K, then V: 2 chunks each
-  uint8_t* sqd = smem + 4 * kChunk;         // stage s: Q (2 chunks), then dO
+  uint8_t* sqd = smem + 4 * kChunk;         // stage s: Q (2 half chunks), then dO
   float* s_lse = reinterpret_cast<float*>(smem + 12 * kChunk);  // [2][128]: -lse in powers of two
   float* s_del = s_lse + 256;                                   // [2][128]: -D
   int2* s_see = reinterpret_cast<int2*>(s_del + 256);           // [2][128]: keys that the query sees
   int* s_whole = reinterpret_cast<int*>(s_see + 256);           // [2]: all of the tile's queries see all of the key tile
   uint64_t* bars = reinterpret_cast<uint64_t*>(s_whole + 4);
   uint64_t* kv_full = bars;
-  uint64_t* qd_full = bars + 1;     // [2] by stage
-  uint64_t* qd_empty = bars + 3;    // [2]
-  uint64_t* rows_full = bars + 5;   // [2]
-  uint64_t* rows_empty = bars + 7;  // [2]
-  uint64_t* sd_full = bars + 9;     // [2] by buffer
-  uint64_t* pd_full = bars + 11;    // [2]
-  uint64_t* pd_done = bars + 13;    // [2]
-  uint64_t* drain = bars + 15;      // [2]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 17);
+  uint64_t* qd_full = bars + 1;     // [4] by stage
+  uint64_t* qd_empty = bars + 5;    // [4]
+  uint64_t* rows_full = bars + 9;   // [2]
+  uint64_t* rows_empty = bars + 11; // [2]
+  uint64_t* sd_full = bars + 13;    // [2] by buffer
+  uint64_t* pd_full = bars + 15;    // [2]
+  uint64_t* drain = bars + 17;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 18);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1223,16 +1243,17 @@ __global__ void __launch_bounds__(kBwdThreads, 1) masked_dkv_kernel(const __grid
   const int64_t T = (int64_t)p.n_seq * p.S;
   if (threadIdx.x == 0) {
     mbar_init(kv_full, 1);
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < 4; ++s) {
       mbar_init(&qd_full[s], 1);
       mbar_init(&qd_empty[s], 1);
-      mbar_init(&rows_full[s], 1);
-      mbar_init(&rows_empty[s], 16);
-      mbar_init(&sd_full[s], 1);
-      mbar_init(&pd_full[s], 8);
-      mbar_init(&pd_done[s], 1);
-      mbar_init(&drain[s], 1);
     }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&rows_full[s], 1);
+      mbar_init(&rows_empty[s], 8);
+      mbar_init(&sd_full[s], 1);
+      mbar_init(&pd_full[s], 4);
+    }
+    mbar_init(drain, 1);
     *abort_flag = 0;
     fence_barrier_init();
     tma_prefetch_desc(&p.qmap);
@@ -1258,9 +1279,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) masked_dkv_kernel(const __grid
   auto it_head = [&](int it) { return g * hpg + it % hpg; };
   auto it_qtile = [&](int it) { return q0 + it / hpg; };
 
-  // 640 threads start with 96 registers each; 56 in the first four warps and 104 in the others stay within their sum
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (!plan_ok) {
       // nothing is issued
     } else if (warp == 0 && lane == 0) {
@@ -1269,55 +1288,50 @@ __global__ void __launch_bounds__(kBwdThreads, 1) masked_dkv_kernel(const __grid
         tma_load_4d(sk + c * kChunk, &p.kmap, kv_full, 64 * c, g, kt * kTile, b);
         tma_load_4d(sk + (2 + c) * kChunk, &p.vmap, kv_full, 64 * c, g, kt * kTile, b);
       }
-      int it = 0;
-      for (; it < n_it; ++it) {
-        const int s = it & 1;
-        if (!mbar_wait_soon(&qd_empty[s], ((it >> 1) & 1) ^ 1, abort_flag, p.err, DEV_TIMEOUT_PRODUCER)) break;
-        mbar_arrive_expect_tx(&qd_full[s], 2 * nd * kChunk);
-        uint8_t* st = sqd + s * 4 * kChunk;
+      int t = 0;
+      for (; t < 2 * n_it; ++t) {
+        const int s = t & 3, row = it_qtile(t >> 1) * kTile + 64 * (t & 1);
+        if (!mbar_wait_soon(&qd_empty[s], ((t >> 2) & 1) ^ 1, abort_flag, p.err, DEV_TIMEOUT_PRODUCER)) break;
+        mbar_arrive_expect_tx(&qd_full[s], nd * kChunk);
+        uint8_t* st = sqd + s * 2 * kChunk;
         for (int c = 0; c < nd; ++c) {
-          tma_load_4d(st + c * kChunk, &p.qmap, &qd_full[s], 64 * c, it_head(it), it_qtile(it) * kTile, b);
-          tma_load_4d(st + (2 + c) * kChunk, &p.domap, &qd_full[s], 64 * c, it_head(it), it_qtile(it) * kTile, b);
+          tma_load_4d(st + c * (kChunk / 2), &p.qmap64, &qd_full[s], 64 * c, it_head(t >> 1), row, b);
+          tma_load_4d(st + kChunk + c * (kChunk / 2), &p.domap64, &qd_full[s], 64 * c, it_head(t >> 1), row, b);
         }
       }
       // every copy lands before the CTA may exit
       mbar_wait(kv_full, 0, nullptr, p.err, DEV_TIMEOUT_DRAIN);
-      for (int k = max(0, it - 2); k < it; ++k) mbar_wait(&qd_full[k & 1], (k >> 1) & 1, nullptr, p.err, DEV_TIMEOUT_DRAIN);
+      for (int k = max(0, t - 4); k < t; ++k) mbar_wait(&qd_full[k & 3], (k >> 2) & 1, nullptr, p.err, DEV_TIMEOUT_DRAIN);
     } else if (warp == 1 && lane == 0) {
-      const uint32_t id = idesc_bf16(128, 64, 0, 0);
-      const uint64_t dk0 = kmajor_desc(smem_u32(sk), 0), dv0 = dk0 + (2 * kChunk >> 4), dq0 = kmajor_desc(smem_u32(sqd), 0);
-      bool ok = mbar_wait_soon(kv_full, 0, abort_flag, p.err, DEV_TIMEOUT_MMA);
-      for (int t = 0; ok && t < 2 * n_it; ++t) {
-        const int it = t >> 1, s = it & 1, x = t & 1;
-        ok = (x == 1 || mbar_wait_soon(&qd_full[s], (it >> 1) & 1, abort_flag, p.err, DEV_TIMEOUT_MMA)) &&
-             (it == 0 || mbar_wait_soon(&pd_done[x], (it - 1) & 1, abort_flag, p.err, DEV_TIMEOUT_MMA));
-        if (!ok) break;
+      const uint32_t id_s = idesc_bf16(128, 64, 0, 0), id_d = idesc_bf16(128, 64 * nd, 0, 1);  // P^T, dS^T in TMEM; dO, Q MN-major
+      const uint64_t dk0 = kmajor_desc(smem_u32(sk), 0), dv0 = dk0 + (2 * kChunk >> 4), dq0 = kmajor_desc(smem_u32(sqd), 0),
+                     dqm0 = smem_desc_sw128(smem_u32(sqd), kChunk / 2, 1024);  // MN-major, 64-column chunks 8 KB apart
+      // S^T and dP^T of step t once its queries have come
+      auto issue_s = [&](int t) -> bool {
+        const int s = t & 3, x = t & 1;
+        if (!mbar_wait_soon(&qd_full[s], (t >> 2) & 1, abort_flag, p.err, DEV_TIMEOUT_MMA)) return false;
         tc_fence_after();
-        const uint64_t bq = dq0 + s * (4 * kChunk >> 4) + x * (kChunk / 2 >> 4);
-        mma_kk_nd(nd, tmem + 64 * x, dk0, bq, id);
-        mma_kk_nd(nd, tmem + 128 + 64 * x, dv0, bq + (2 * kChunk >> 4), id);
+        const uint64_t bq = dq0 + s * (2 * kChunk >> 4);
+        mma_kk_nd<kChunk / 2>(nd, tmem + 64 * x, dk0, bq, id_s);
+        mma_kk_nd<kChunk / 2>(nd, tmem + 128 + 64 * x, dv0, bq + (kChunk >> 4), id_s);
         umma_commit(&sd_full[x]);
-      }
-      umma_commit(&drain[0]);
-      mbar_wait(&drain[0], 0, nullptr, p.err, DEV_TIMEOUT_DRAIN);
-    } else if (warp == 2 && lane == 0) {
-      const uint32_t id = idesc_bf16(128, 64 * nd, 0, 1);  // P^T, dS^T in TMEM; dO, Q MN-major
-      const uint64_t dq0 = mnmajor_desc(smem_u32(sqd), 0);
-      bool ok = true;
-      for (int t = 0; ok && t < 2 * n_it; ++t) {
-        const int it = t >> 1, s = it & 1, x = t & 1;
-        ok = mbar_wait_soon(&pd_full[x], it & 1, abort_flag, p.err, DEV_TIMEOUT_MMA) &&
-             mbar_wait_soon(&qd_full[s], (it >> 1) & 1, abort_flag, p.err, DEV_TIMEOUT_MMA);
+        return true;
+      };
+      const int n_step = 2 * n_it;
+      bool ok = mbar_wait_soon(kv_full, 0, abort_flag, p.err, DEV_TIMEOUT_MMA) && issue_s(0) && issue_s(1);
+      for (int t = 0; ok && t < n_step; ++t) {
+        const int x = t & 1;
+        ok = mbar_wait_soon(&pd_full[x], (t >> 1) & 1, abort_flag, p.err, DEV_TIMEOUT_MMA);
         if (!ok) break;
         tc_fence_after();
-        const uint64_t bq = dq0 + s * (4 * kChunk >> 4) + x * 512;
-        mma_tm<4, 32>(tmem + 256, tmem + 64 * x, bq + (2 * kChunk >> 4), id, t > 0);
-        mma_tm<4, 32>(tmem + 384, tmem + 128 + 64 * x, bq, id, t > 0);
-        umma_commit(&pd_done[x]);
-        if (x == 1) umma_commit(&qd_empty[s]);
+        const uint64_t bq = dqm0 + (t & 3) * (2 * kChunk >> 4);
+        mma_tm<4>(tmem + 256, tmem + 64 * x, bq + (kChunk >> 4), id_d, t > 0);
+        mma_tm<4>(tmem + 384, tmem + 128 + 64 * x, bq, id_d, t > 0);
+        umma_commit(&qd_empty[t & 3]);
+        if (t + 2 < n_step) ok = issue_s(t + 2);
       }
-      umma_commit(&drain[1]);
-      mbar_wait(&drain[1], 0, nullptr, p.err, DEV_TIMEOUT_DRAIN);
+      umma_commit(drain);
+      mbar_wait(drain, 0, nullptr, p.err, DEV_TIMEOUT_DRAIN);
     } else if (warp == 3) {
     bool ok = true;
     for (int it = 0; ok && it < n_it; ++it) {
@@ -1349,15 +1363,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1) masked_dkv_kernel(const __grid
     }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
-    const int quarter = warp & 3, x = (warp - 4) >> 3, c = ((warp - 4) >> 2) & 1;  // x: buffer, half of each query tile; c: 32 columns
+    const int quarter = warp & 3, x = (warp - 4) >> 2;  // x: buffer, half of each query tile
     const int r = quarter * 32 + lane;                  // key row of the tile
     const int kpos = kt * kTile + r;
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
-    const uint32_t s_tm = tmem + lane_off + 64 * x + 32 * c, dp_tm = s_tm + 128;
+    const uint32_t s_tm = tmem + lane_off + 64 * x, dp_tm = s_tm + 128;
     bool ok = plan_ok;
     for (int it = 0; ok && it < n_it; ++it) {
-      const int s = it & 1, qt0 = it_qtile(it) * kTile + 64 * x + 32 * c;
+      const int s = it & 1, qt0 = it_qtile(it) * kTile + 64 * x;
       ok = __all_sync(0xffffffffu, mbar_wait_soon(&rows_full[s], (it >> 1) & 1, abort_flag, p.err, DEV_TIMEOUT_EPILOGUE) &&
                                        mbar_wait_soon(&sd_full[x], it & 1, abort_flag, p.err, DEV_TIMEOUT_EPILOGUE));
       if (!ok) break;
@@ -1365,33 +1378,35 @@ __global__ void __launch_bounds__(kBwdThreads, 1) masked_dkv_kernel(const __grid
       const bool part = !s_whole[s];
       const float slope = BIAS ? p.slopes[it_head(it)] * kLog2e : 0.f;
       const int side = qt0 >= kt * kTile + 32 * quarter + 31 ? -1 : 0;
-      uint32_t sv[32], dp[32], pw[16], dw[16];
-      tmem_ld32(s_tm, sv);
-      tmem_ld32(dp_tm, dp);
-      tmem_ld_wait_regs(sv);
-      regs_after_wait(dp);
-      const int col = s * 128 + 64 * x + 32 * c;
-      uint32_t see = 0xffffffffu;
-      if (part) {
-        see = 0;
+#pragma unroll 1
+      for (int c = 0; c < 2; ++c) {
+        uint32_t sv[32], dp[32], pw[16], dw[16];
+        tmem_ld32(s_tm + 32 * c, sv);
+        tmem_ld32(dp_tm + 32 * c, dp);
+        tmem_ld_wait_regs(sv);
+        regs_after_wait(dp);
+        const int col = s * 128 + 64 * x + 32 * c;
+        uint32_t see = 0xffffffffu;
+        if (part) {
+          see = 0;
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          const int2 w = s_see[col + e];
-          see |= (uint32_t)(w.x <= kpos && kpos < w.y) << e;
+          for (int e = 0; e < 32; ++e) {
+            const int2 w = s_see[col + e];
+            see |= (uint32_t)(w.x <= kpos && kpos < w.y) << e;
+          }
         }
+        grad32<CAP, BIAS, false, true>(sv, dp, p.mul, p.cap_mul, slope, (float)(kpos - qt0 - 32 * c), side, part, see, 0.f,
+                                       0.f, s_lse + col, s_del + col, pw, dw);
+        tmem_st16(s_tm + 16 * c, pw);  // behind the scores still to read
+        tmem_st16(dp_tm + 16 * c, dw);
       }
-      grad32<CAP, BIAS, false, true>(sv, dp, p.mul, p.cap_mul, slope, (float)(kpos - qt0), side, part, see, 0.f, 0.f,
-                                     s_lse + col, s_del + col, pw, dw);
-      // over the scores and products that this warp itself has read: words 0-15 and 32-47 of the buffers
-      tmem_st16(s_tm, pw);
-      tmem_st16(dp_tm, dw);
       tmem_st_wait();
       tc_fence_before();
       warp_arrive(&pd_full[x], lane);
       if (lane == 0) mbar_arrive(&rows_empty[s]);
     }
     // dV (first group), dK (second) once every product is done
-    if (ok) ok = __all_sync(0xffffffffu, mbar_wait_soon(&drain[1], 0, abort_flag, p.err, DEV_TIMEOUT_EPILOGUE));
+    if (ok) ok = __all_sync(0xffffffffu, mbar_wait_soon(drain, 0, abort_flag, p.err, DEV_TIMEOUT_EPILOGUE));
     if (ok) {
       tc_fence_after();
       const int64_t row0 = (int64_t)b * p.S + kt * kTile + 32 * quarter;
@@ -1400,7 +1415,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) masked_dkv_kernel(const __grid
       __nv_bfloat16* out = (x ? p.dk : p.dv) + row0 * ld + (int64_t)g * p.hd;
       const float mul = x ? p.scale : 1.f;
 #pragma unroll 1
-      for (int k = c; k < 2 * nd; k += 2) {
+      for (int k = 0; k < 2 * nd; ++k) {
         uint32_t v[32], w[16];
         tmem_ld32(tmem + lane_off + 256 + 128 * x + 32 * k, v);
         tmem_ld_wait_regs(v);
@@ -1469,7 +1484,7 @@ int bwd_launch(const MaskedBwdParams& p, cudaStream_t s) {
   launch_kernel(masked_dq_kernel<CAP, BIAS>, (unsigned)std::min(p.n_units, n_sm), kBwdThreads, dq_smem(), s, p);
   if (launch_failed("sl_attention_masked")) return 5;
   note_launch();
-  launch_kernel(masked_dkv_kernel<CAP, BIAS>, (unsigned)(plan_tiles(p.n_seq, p.S) * p.hkv), kBwdThreads, dkv_smem(), s, p);
+  launch_kernel(masked_dkv_kernel<CAP, BIAS>, (unsigned)(plan_tiles(p.n_seq, p.S) * p.hkv), kDkvThreads, dkv_smem(), s, p);
   if (launch_failed("sl_attention_masked")) return 5;
   note_launch();
   return 0;
@@ -1540,7 +1555,8 @@ int attention_masked_bwd(const MaskedArgs& a, cudaStream_t s) {
   MaskedBwdParams p;
   memset(&p, 0, sizeof(p));
   if (!head_map(&p.qmap, a.q, a.ldq, a.n_seq, a.S, a.hq, a.hd) || !head_map(&p.kmap, a.k, a.ldk, a.n_seq, a.S, a.hkv, a.hd) ||
-      !head_map(&p.vmap, a.v, a.ldv, a.n_seq, a.S, a.hkv, a.hd) || !head_map(&p.domap, a.d_o, a.lddo, a.n_seq, a.S, a.hq, a.hd))
+      !head_map(&p.vmap, a.v, a.ldv, a.n_seq, a.S, a.hkv, a.hd) || !head_map(&p.domap, a.d_o, a.lddo, a.n_seq, a.S, a.hq, a.hd) ||
+      !head_map(&p.qmap64, a.q, a.ldq, a.n_seq, a.S, a.hq, a.hd, 64) || !head_map(&p.domap64, a.d_o, a.lddo, a.n_seq, a.S, a.hq, a.hd, 64))
     return 2;
   carve_plan(const_cast<void*>(a.plan), a.n_seq, a.S, &p.plan);
   p.slopes = a.slopes;

@@ -133,13 +133,13 @@ EncodeTiledFn encode_fn() {
 }
 
 // [hd, heads, S, n_seq] view of a [n_seq * S, ld] bf16 matrix whose head h occupies columns
-// [h hd, (h + 1) hd); boxes of 64 x 1 x 128 x 1, 128-byte swizzle, zero fill outside.
-bool head_map(CUtensorMap* m, const void* ptr, int64_t ld, int n_seq, int S, int heads, int hd) {
+// [h hd, (h + 1) hd); boxes of 64 x 1 x box_rows x 1, 128-byte swizzle, zero fill outside.
+bool head_map(CUtensorMap* m, const void* ptr, int64_t ld, int n_seq, int S, int heads, int hd, int box_rows = 128) {
   auto enc = encode_fn();
   if (!enc) return false;
   cuuint64_t dims[4] = {(cuuint64_t)hd, (cuuint64_t)heads, (cuuint64_t)S, (cuuint64_t)n_seq};
   cuuint64_t strides[3] = {(cuuint64_t)hd * 2, (cuuint64_t)ld * 2, (cuuint64_t)S * ld * 2};
-  cuuint32_t box[4] = {64, 1, 128, 1};
+  cuuint32_t box[4] = {64, 1, (cuuint32_t)box_rows, 1};
   cuuint32_t es[4] = {1, 1, 1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), dims, strides, box, es,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
