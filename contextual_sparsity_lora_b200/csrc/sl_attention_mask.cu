@@ -24,8 +24,10 @@ namespace {
 // the last one has passed: each producer below is held back by an answer of its consumers, or has a second barrier
 // to alternate with.
 constexpr int kFwdThreads = 384;  // warp 0 TMA, warps 1 and 2 MMA (warp 1 allocates TMEM), warps 4..11 softmax
-constexpr int kBwdThreads = 640;  // dq: warp 0 TMA, warp 1 MMA, warps 4..19 compute
-constexpr int kDkvThreads = 384;  // dk, dv: warp 0 TMA, warp 1 MMA, warp 3 reads the query rows, warps 4..11 compute
+constexpr int kBwdThreads = 640;  // dq: warp 0 loads, warps 1, 2 and 3 MMA, warps 4..19 compute
+// dk, dv: warp 0 loads, warps 1, 2 and 3 MMA, the others compute
+template <bool CAP>
+constexpr int kDkvThreads = CAP ? 384 : 640;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -437,7 +439,6 @@ struct MaskedFwdParams {
 
 struct MaskedBwdParams {
   CUtensorMap qmap, kmap, vmap, domap;  // boxes as in the forward
-  CUtensorMap qmap64, domap64;          // boxes of 64 rows
   Plan plan;
   const float* slopes;
   const float* lse;              // [hq][T]
@@ -911,10 +912,10 @@ __device__ __forceinline__ void grad32(uint32_t (&s)[32], uint32_t (&dp)[32], fl
 }
 
 // dq: persistent CTAs over units (query tile, head). Q and dO stay, K and V stream through two stages, twice: first for D,
-// then for dQ. Warp 0 loads; warp 1 issues the products in the order S = Q K^T of step t + 1, dP = dO V^T of step t + 1,
-// dQ += dS K of step t: while the compute warps work on step t the tensor cores are a step ahead, and one thread's order
-// is all that the buffers need (S has two, dS takes the place of its S; dP has one, which the compute warps
-// take into registers at once). The second pass begins with the last two key tiles, whose K and V are still there (documents of up
+// then for dQ. Warp 0 loads; warps 1, 2 and 3 issue S = Q K^T, dP = dO V^T and dQ += dS K, S and dP a step ahead of the compute
+// warps (S has two buffers, and dS takes the place of its S; dP has one, which the compute warps take into registers at
+// once). Warps 4-19 hold a query row and 32 of the key columns per thread. TMEM: dQ at 0, S / dS of step t at
+// 128 + 128 (t & 1), dP at 384. The second pass begins with the last two key tiles, whose K and V are still there (documents of up
 // to 256 keys are read once), and goes back from the one before them. Warps 4-19 hold a query row and 32 of the key columns per thread. TMEM: dQ at 0, S / dS of
 // step t at 128 + 128 (t & 1), dP at 384.
 template <bool CAP, bool BIAS>
@@ -930,12 +931,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1) masked_dq_kernel(const __grid_
   uint64_t* q_empty = bars + 1;
   uint64_t* kv_full = bars + 2;    // [2]
   uint64_t* kv_empty = bars + 4;   // [2]
-  uint64_t* s_full = bars + 6;     // S and dP of a step
-  uint64_t* dp_free = bars + 7;    // S and dP of a step are in registers
-  uint64_t* ds_full = bars + 8;    // [2], in turn: the compute warps may end a step before the last one's dS is asked for
-  uint64_t* dq_done = bars + 10;   // a unit's dQ
-  uint64_t* drain = bars + 11;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 12);
+  uint64_t* s_full = bars + 6;     // [2] by buffer
+  uint64_t* s_read = bars + 8;     // [2]: S is in registers
+  uint64_t* ds_full = bars + 10;   // [2]: dS in the buffer
+  uint64_t* ds_done = bars + 12;   // [2]: dQ has read it
+  uint64_t* dp_full = bars + 14;
+  uint64_t* dp_read = bars + 15;
+  uint64_t* dq_done = bars + 16;   // a unit's dQ
+  uint64_t* drain = bars + 17;     // [3]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 20);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -957,17 +961,19 @@ __global__ void __launch_bounds__(kBwdThreads, 1) masked_dq_kernel(const __grid_
   };
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
-    mbar_init(q_empty, 1);
+    mbar_init(q_empty, 2);  // S, dP
     for (int s = 0; s < 2; ++s) {
       mbar_init(&kv_full[s], 1);
-      mbar_init(&kv_empty[s], 1);
+      mbar_init(&kv_empty[s], 2);  // S and dP of the first pass, or dQ (which arrives twice)
+      mbar_init(&s_full[s], 1);
+      mbar_init(&s_read[s], 16);
+      mbar_init(&ds_full[s], 16);
+      mbar_init(&ds_done[s], 1);
     }
-    mbar_init(s_full, 1);
-    mbar_init(dp_free, 16);
-    mbar_init(&ds_full[0], 16);
-    mbar_init(&ds_full[1], 16);
+    mbar_init(dp_full, 1);
+    mbar_init(dp_read, 16);
     mbar_init(dq_done, 1);
-    mbar_init(drain, 1);
+    for (int s = 0; s < 3; ++s) mbar_init(&drain[s], 1);
     *abort_flag = 0;
     fence_barrier_init();
     tma_prefetch_desc(&p.qmap);
@@ -1017,10 +1023,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) masked_dq_kernel(const __grid_
       // every copy lands before the CTA may exit
       if (i > 0) mbar_wait(q_full, (i - 1) & 1, nullptr, p.err, DEV_TIMEOUT_DRAIN);
       for (int k = max(0, t - 2); k < t; ++k) mbar_wait(&kv_full[k & 1], (k >> 1) & 1, nullptr, p.err, DEV_TIMEOUT_DRAIN);
-    } else if (warp == 1 && lane == 0) {
-      const uint32_t id_s = idesc_bf16(128, 128, 0, 0), id_dq = idesc_bf16(128, 64 * nd, 0, 1);
-      const uint64_t dq0 = kmajor_desc(smem_u32(sq), 0), ddo0 = dq0 + (2 * kChunk >> 4), dk0 = kmajor_desc(smem_u32(skv), 0),
-                     dkm0 = mnmajor_desc(smem_u32(skv), 0);
+    } else if (warp > 0 && lane == 0) {
       // key tiles of this CTA's unit i (0: there is none); a unit has twice as many steps
       auto tiles_of = [&](int i) -> int {
         const int u = unit_number(i);
@@ -1028,63 +1031,66 @@ __global__ void __launch_bounds__(kBwdThreads, 1) masked_dq_kernel(const __grid_
         const int4 e = p.plan.q_order[u / p.hq];
         return e.z - e.y;
       };
-      int n = tiles_of(0), n_next = tiles_of(1), i = 0, j = 0;  // tiles of this unit and the next, unit, step in it
-      // The load (of this CTA's) whose K and V step j of a unit of n tiles works on, the unit's first being load l0
-      auto load_of = [](int l0, int n, int j) {
-        const int r = min(2, n);
-        return l0 + (j < n ? j : j - r);
-      };
-      // S and dP of step t, which is step j of unit iu (n tiles, first load l0)
-      auto issue_s = [&](int t, int iu, int j, int n, int l0) -> bool {
-        const int l = load_of(l0, n, j), s = l & 1;
-        if ((j == 0 && !mbar_wait_soon(q_full, iu & 1, abort_flag, p.err, DEV_TIMEOUT_MMA)) ||
-            !mbar_wait_soon(&kv_full[s], (l >> 1) & 1, abort_flag, p.err, DEV_TIMEOUT_MMA))
-          return false;
-        tc_fence_after();
-        const uint64_t bk = dk0 + s * (4 * kChunk >> 4);
-        mma_kk_nd(nd, tmem + 128 + 128 * (t & 1), dq0, bk, id_s);
-        if (t > 0) {
-          if (!mbar_wait_soon(dp_free, (t - 1) & 1, abort_flag, p.err, DEV_TIMEOUT_MMA)) return false;
-          tc_fence_after();
-        }
-        mma_kk_nd(nd, tmem + 384, ddo0, bk + (2 * kChunk >> 4), id_s);
-        umma_commit(s_full);
-        if (j < n - 2) umma_commit(&kv_empty[s]);  // the last two tiles stay for the second pass
-        if (j == 2 * n - 1) umma_commit(q_empty);
-        return true;
-      };
-      int l0 = 0;  // this unit's first load
-      bool ok = n > 0 && issue_s(0, 0, 0, n, 0);
-      int c = 0;  // dQ products so far
-      for (int t = 0; ok; ++t) {
-        const bool unit_end = j == 2 * n - 1;
-        const int l0_next = l0 + 2 * n - min(2, n);
-        if (!unit_end) ok = issue_s(t + 1, i, j + 1, n, l0);
-        else if (n_next > 0) ok = issue_s(t + 1, i + 1, 0, n_next, l0_next);
-        if (!ok) break;
-        if (j >= n) {
-          ok = mbar_wait_soon(&ds_full[c & 1], (c >> 1) & 1, abort_flag, p.err, DEV_TIMEOUT_MMA);
-          if (!ok) break;
-          tc_fence_after();
-          const int st = load_of(l0, n, j) & 1;
-          mma_tm<8, 32>(tmem, tmem + 128 + 128 * (t & 1), dkm0 + st * (4 * kChunk >> 4), id_dq, j > n);
-          umma_commit(&kv_empty[st]);
-          ++c;
-        }
-        if (unit_end) {
-          umma_commit(dq_done);
-          if (n_next == 0) break;
-          ++i;
-          j = 0;
-          n = n_next;
+      bool ok = true;
+      int t = 0, l0 = 0;  // step, the unit's first load; step j of a unit of n tiles works on load l0 + (j < n ? j : j - min(2, n))
+      int n = tiles_of(0), n_next;
+      if (warp == 3) {
+        const uint32_t id = idesc_bf16(128, 64 * nd, 0, 1);
+        const uint64_t dk0 = mnmajor_desc(smem_u32(skv), 0);
+        int used[2] = {0, 0};  // dS in each buffer so far
+        for (int i = 0; ok && n > 0; ++i, n = n_next) {
           n_next = tiles_of(i + 1);
-          l0 = l0_next;
-        } else {
-          ++j;
+          const int kept = min(2, n);
+          t += n;
+          for (int j = n; j < 2 * n; ++j, ++t) {
+            const int b = t & 1, s = (l0 + j - kept) & 1;
+            // the step's K has come: its S has read it
+            ok = mbar_wait_soon(&ds_full[b], (b ? used[1]++ : used[0]++) & 1, abort_flag, p.err, DEV_TIMEOUT_MMA);
+            if (!ok) break;
+            tc_fence_after();
+            mma_tm<8, 32>(tmem, tmem + 128 + 128 * b, dk0 + s * (4 * kChunk >> 4), id, j > n);
+            umma_commit(&ds_done[b]);
+            umma_commit(&kv_empty[s]);
+            mbar_arrive(&kv_empty[s]);
+          }
+          if (ok) umma_commit(dq_done);
+          l0 += 2 * n - kept;
+        }
+      } else {
+        // warp 1: S of step t into buffer t & 1; warp 2: dP of step t
+        const bool is_s = warp == 1;
+        const uint32_t id = idesc_bf16(128, 128, 0, 0);
+        const uint64_t a0 = kmajor_desc(smem_u32(sq), 0) + (is_s ? 0 : 2 * kChunk >> 4),
+                       b0 = kmajor_desc(smem_u32(skv), 0) + (is_s ? 0 : 2 * kChunk >> 4);
+        int used[2] = {0, 0};
+        bool held[2] = {false, false};  // the buffer's last S has become a dS
+        for (int i = 0; ok && n > 0; ++i, n = n_next) {
+          n_next = tiles_of(i + 1);
+          const int kept = min(2, n);
+          ok = mbar_wait_soon(q_full, i & 1, abort_flag, p.err, DEV_TIMEOUT_MMA);
+          for (int j = 0; ok && j < 2 * n; ++j, ++t) {
+            const int l = l0 + (j < n ? j : j - kept), s = l & 1, b = t & 1;
+            ok = mbar_wait_soon(&kv_full[s], (l >> 1) & 1, abort_flag, p.err, DEV_TIMEOUT_MMA);
+            if (ok && is_s) {
+              if (t >= 2) ok = mbar_wait_soon(&s_read[b], ((t >> 1) - 1) & 1, abort_flag, p.err, DEV_TIMEOUT_MMA);
+              if (ok && (b ? held[1] : held[0]))
+                ok = mbar_wait_soon(&ds_done[b], (b ? used[1]++ : used[0]++) & 1, abort_flag, p.err, DEV_TIMEOUT_MMA);
+              (b ? held[1] : held[0]) = j >= n;
+            } else if (ok && t > 0) {
+              ok = mbar_wait_soon(dp_read, (t - 1) & 1, abort_flag, p.err, DEV_TIMEOUT_MMA);
+            }
+            if (!ok) break;
+            tc_fence_after();
+            mma_kk_nd(nd, is_s ? tmem + 128 + 128 * b : tmem + 384, a0, b0 + s * (4 * kChunk >> 4), id);
+            umma_commit(is_s ? &s_full[b] : dp_full);
+            if (j < n - kept) umma_commit(&kv_empty[s]);  // the last two tiles stay for the second pass
+            if (j == 2 * n - 1) umma_commit(q_empty);
+          }
+          l0 += 2 * n - kept;
         }
       }
-      umma_commit(drain);
-      mbar_wait(drain, 0, nullptr, p.err, DEV_TIMEOUT_DRAIN);
+      umma_commit(&drain[warp - 1]);
+      mbar_wait(&drain[warp - 1], 0, nullptr, p.err, DEV_TIMEOUT_DRAIN);
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
@@ -1094,7 +1100,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) masked_dq_kernel(const __grid_
     const uint32_t s_tm = tmem + lane_off + 128 + 32 * cq, dp_tm = tmem + lane_off + 384 + 32 * cq;
     U w, nx;
     bool ok = plan_ok, live = plan_ok && unit(0, nx);
-    int t = 0, c = 0;  // steps, those of the second pass
+    int t = 0;
     int nlo = 0, nhi = 0;
     float nlse = 0.f;
     const int64_t T = (int64_t)p.n_seq * p.S;
@@ -1125,7 +1131,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) masked_dq_kernel(const __grid_
         for (int k = 0; k < n; ++k, ++t) {
           // the second pass: the last two tiles, then back from the one before them
           const int j = w.j0 + (pass == 0 ? k : k < kept ? n - kept + k : n - 1 - k);
-          ok = __all_sync(0xffffffffu, mbar_wait_soon(s_full, t & 1, abort_flag, p.err, DEV_TIMEOUT_EPILOGUE));
+          ok = __all_sync(0xffffffffu, mbar_wait_soon(&s_full[t & 1], (t >> 1) & 1, abort_flag, p.err, DEV_TIMEOUT_EPILOGUE) &&
+                                           mbar_wait_soon(dp_full, t & 1, abort_flag, p.err, DEV_TIMEOUT_EPILOGUE));
           if (!ok) break;
           tc_fence_after();
           uint32_t s[32], dp[32];
@@ -1134,7 +1141,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) masked_dq_kernel(const __grid_
           tmem_ld_wait_regs(s);
           regs_after_wait(dp);
           tc_fence_before();
-          warp_arrive(dp_free, lane);
+          warp_arrive(dp_read, lane);
+          if (lane == 0) mbar_arrive(&s_read[t & 1]);
           const int k0 = j * kTile + 32 * cq;  // key of this thread's first column
           const bool part = __any_sync(0xffffffffu, lo > k0 || hi < k0 + 32);
           const uint32_t see = see_bits(lo - k0, hi - k0);
@@ -1164,8 +1172,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) masked_dq_kernel(const __grid_
             tmem_st16(s_tm + 128 * (t & 1), dw);  // over the scores that this warp itself has read
             tmem_st_wait();
             tc_fence_before();
-            warp_arrive(&ds_full[c & 1], lane);
-            ++c;
+            warp_arrive(&ds_full[t & 1], lane);
           }
         }
         if (pass == 0) {
@@ -1206,33 +1213,35 @@ __global__ void __launch_bounds__(kBwdThreads, 1) masked_dq_kernel(const __grid_
 }
 
 // dk, dv: one CTA per (key tile, key/value head) in the plan's order, over (query head of the group, query tile). K and V
-// stay, Q and dO stream through four stages of 64 queries. A step is half a query tile (64 queries): S^T = K Q^T and dP^T = V dO^T of
+// stay, Q and dO stream through two stages. A step is half a query tile (64 queries): S^T = K Q^T and dP^T = V dO^T of
 // step t + 1 run while the compute warps work on step t; P^T and dS^T replace them in TMEM (bf16, first
-// operands of dV += P^T dO and dK += dS^T Q). Warp 0 loads; warp 1 issues dV and dK of step t, then S^T and dP^T of step
-// t + 2 into the same buffers (two threads for the two pairs had to wait for each other: 290 us at 4096 causal tokens,
-// half of the tensor cores' time); warp 3 reads the
-// query rows' lse, D and intervals; warps 4-7 and 8-11 take the even and the odd steps, a key row per thread. TMEM: S^T of
-// buffer x at 64 x, dP^T at 128 + 64 x, dV at 256, dK at 384.
+// operands of dV += P^T dO and dK += dS^T Q). Warp 0 loads, the query rows' lse, D and intervals too; warps 1, 2 and 3 issue
+// S^T, dP^T, and dV and dK (a thread that issues also waits and commits, and meanwhile the tensor cores, which queue about
+// five products, run dry: @@DKV@@); the others compute, one half for the even and one for the odd steps, a key row and 32 query columns per thread at a
+// time: 16 warps, or 8 where a cap's tanh needs the registers (with 16 it spills: 335 against 316 us at 4096 capped tokens,
+// without a cap 16 gain 10%). TMEM: S^T of buffer x at 64 x, dP^T at 128 + 64 x, dV at 256, dK at 384.
 template <bool CAP, bool BIAS>
-__global__ void __launch_bounds__(kDkvThreads, 1) masked_dkv_kernel(const __grid_constant__ MaskedBwdParams p) {
+__global__ void __launch_bounds__(kDkvThreads<CAP>, 1) masked_dkv_kernel(const __grid_constant__ MaskedBwdParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int nd = p.nd;
+  constexpr int kWarps = (kDkvThreads<CAP> - 128) / 32, kCols = kWarps == 16 ? 1 : 2;  // 32-column pieces per thread and step
   uint8_t* sk = smem;                       // K, then V: 2 chunks each
-  uint8_t* sqd = smem + 4 * kChunk;         // stage s: Q (2 half chunks), then dO
+  uint8_t* sqd = smem + 4 * kChunk;         // stage s: Q (2 chunks), then dO
   float* s_lse = reinterpret_cast<float*>(smem + 12 * kChunk);  // [2][128]: -lse in powers of two
   float* s_del = s_lse + 256;                                   // [2][128]: -D
   int2* s_see = reinterpret_cast<int2*>(s_del + 256);           // [2][128]: keys that the query sees
   int* s_whole = reinterpret_cast<int*>(s_see + 256);           // [2]: all of the tile's queries see all of the key tile
   uint64_t* bars = reinterpret_cast<uint64_t*>(s_whole + 4);
   uint64_t* kv_full = bars;
-  uint64_t* qd_full = bars + 1;     // [4] by stage
-  uint64_t* qd_empty = bars + 5;    // [4]
-  uint64_t* rows_full = bars + 9;   // [2]
-  uint64_t* rows_empty = bars + 11; // [2]
-  uint64_t* sd_full = bars + 13;    // [2] by buffer
-  uint64_t* pd_full = bars + 15;    // [2]
-  uint64_t* drain = bars + 17;
+  uint64_t* qd_full = bars + 1;     // [2] by stage
+  uint64_t* qd_empty = bars + 3;    // [2]
+  uint64_t* rows_full = bars + 5;   // [2]
+  uint64_t* rows_empty = bars + 7;  // [2]
+  uint64_t* sd_full = bars + 9;     // [2] by buffer
+  uint64_t* pd_full = bars + 11;    // [2]
+  uint64_t* pd_done = bars + 13;    // [2]
+  uint64_t* drain = bars + 15;      // [3]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 18);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -1243,17 +1252,16 @@ __global__ void __launch_bounds__(kDkvThreads, 1) masked_dkv_kernel(const __grid
   const int64_t T = (int64_t)p.n_seq * p.S;
   if (threadIdx.x == 0) {
     mbar_init(kv_full, 1);
-    for (int s = 0; s < 4; ++s) {
+    for (int s = 0; s < 2; ++s) {
       mbar_init(&qd_full[s], 1);
       mbar_init(&qd_empty[s], 1);
-    }
-    for (int s = 0; s < 2; ++s) {
       mbar_init(&rows_full[s], 1);
-      mbar_init(&rows_empty[s], 8);
-      mbar_init(&sd_full[s], 1);
-      mbar_init(&pd_full[s], 4);
+      mbar_init(&rows_empty[s], kWarps);
+      mbar_init(&sd_full[s], 2);  // S^T, dP^T
+      mbar_init(&pd_full[s], kWarps / 2);
+      mbar_init(&pd_done[s], 1);
     }
-    mbar_init(drain, 1);
+    for (int s = 0; s < 3; ++s) mbar_init(&drain[s], 1);
     *abort_flag = 0;
     fence_barrier_init();
     tma_prefetch_desc(&p.qmap);
@@ -1279,91 +1287,110 @@ __global__ void __launch_bounds__(kDkvThreads, 1) masked_dkv_kernel(const __grid
   auto it_head = [&](int it) { return g * hpg + it % hpg; };
   auto it_qtile = [&](int it) { return q0 + it / hpg; };
 
+  // 640 threads start with 96 registers each; 56 in the first four warps and 104 in the others stay within their sum
   if (warp < 4) {
+    if (kWarps == 16) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (!plan_ok) {
       // nothing is issued
-    } else if (warp == 0 && lane == 0) {
-      mbar_arrive_expect_tx(kv_full, 2 * nd * kChunk);
-      for (int c = 0; c < nd; ++c) {
-        tma_load_4d(sk + c * kChunk, &p.kmap, kv_full, 64 * c, g, kt * kTile, b);
-        tma_load_4d(sk + (2 + c) * kChunk, &p.vmap, kv_full, 64 * c, g, kt * kTile, b);
-      }
-      int t = 0;
-      for (; t < 2 * n_it; ++t) {
-        const int s = t & 3, row = it_qtile(t >> 1) * kTile + 64 * (t & 1);
-        if (!mbar_wait_soon(&qd_empty[s], ((t >> 2) & 1) ^ 1, abort_flag, p.err, DEV_TIMEOUT_PRODUCER)) break;
-        mbar_arrive_expect_tx(&qd_full[s], nd * kChunk);
-        uint8_t* st = sqd + s * 2 * kChunk;
+    } else if (warp == 0) {
+      if (lane == 0) {
+        mbar_arrive_expect_tx(kv_full, 2 * nd * kChunk);
         for (int c = 0; c < nd; ++c) {
-          tma_load_4d(st + c * (kChunk / 2), &p.qmap64, &qd_full[s], 64 * c, it_head(t >> 1), row, b);
-          tma_load_4d(st + kChunk + c * (kChunk / 2), &p.domap64, &qd_full[s], 64 * c, it_head(t >> 1), row, b);
+          tma_load_4d(sk + c * kChunk, &p.kmap, kv_full, 64 * c, g, kt * kTile, b);
+          tma_load_4d(sk + (2 + c) * kChunk, &p.vmap, kv_full, 64 * c, g, kt * kTile, b);
         }
       }
+      int it = 0;
+      for (; it < n_it; ++it) {
+        const int s = it & 1, qt = it_qtile(it);
+        // the rows' values first (they come while the stage is waited for)
+        float l[4], d[4];
+        int2 see[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int qp = qt * kTile + 32 * k + lane;
+          const int64_t row = (int64_t)b * p.S + qp, at = (int64_t)it_head(it) * T + row;
+          const bool in = qp < p.S;
+          see[k] = in ? make_int2(p.plan.lo[row], p.plan.hi[row]) : make_int2(0, 0);
+          // a row that sees nothing or lies past the sequence: 2^-inf, P = 0 whatever its score
+          l[k] = see[k].x < see[k].y ? -p.lse[at] * kLog2e : -INFINITY;
+          d[k] = in ? -p.delta[at] : 0.f;
+        }
+        const int4 r = p.plan.q_range[b * n_t + qt];
+        if (!__all_sync(0xffffffffu, mbar_wait_soon(&qd_empty[s], ((it >> 1) & 1) ^ 1, abort_flag, p.err, DEV_TIMEOUT_PRODUCER))) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&qd_full[s], 2 * nd * kChunk);
+          uint8_t* st = sqd + s * 4 * kChunk;
+          for (int c = 0; c < nd; ++c) {
+            tma_load_4d(st + c * kChunk, &p.qmap, &qd_full[s], 64 * c, it_head(it), qt * kTile, b);
+            tma_load_4d(st + (2 + c) * kChunk, &p.domap, &qd_full[s], 64 * c, it_head(it), qt * kTile, b);
+          }
+        }
+        __syncwarp();
+        if (!__all_sync(0xffffffffu, mbar_wait_soon(&rows_empty[s], ((it >> 1) & 1) ^ 1, abort_flag, p.err, DEV_TIMEOUT_PRODUCER))) {
+          ++it;
+          break;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          s_lse[s * 128 + 32 * k + lane] = l[k];
+          s_del[s * 128 + 32 * k + lane] = d[k];
+          s_see[s * 128 + 32 * k + lane] = see[k];
+        }
+        if (lane == 0) s_whole[s] = r.z <= kt && kt < r.w;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&rows_full[s]);
+      }
       // every copy lands before the CTA may exit
-      mbar_wait(kv_full, 0, nullptr, p.err, DEV_TIMEOUT_DRAIN);
-      for (int k = max(0, t - 4); k < t; ++k) mbar_wait(&qd_full[k & 3], (k >> 2) & 1, nullptr, p.err, DEV_TIMEOUT_DRAIN);
-    } else if (warp == 1 && lane == 0) {
-      const uint32_t id_s = idesc_bf16(128, 64, 0, 0), id_d = idesc_bf16(128, 64 * nd, 0, 1);  // P^T, dS^T in TMEM; dO, Q MN-major
-      const uint64_t dk0 = kmajor_desc(smem_u32(sk), 0), dv0 = dk0 + (2 * kChunk >> 4), dq0 = kmajor_desc(smem_u32(sqd), 0),
-                     dqm0 = smem_desc_sw128(smem_u32(sqd), kChunk / 2, 1024);  // MN-major, 64-column chunks 8 KB apart
-      // S^T and dP^T of step t once its queries have come
-      auto issue_s = [&](int t) -> bool {
-        const int s = t & 3, x = t & 1;
-        if (!mbar_wait_soon(&qd_full[s], (t >> 2) & 1, abort_flag, p.err, DEV_TIMEOUT_MMA)) return false;
-        tc_fence_after();
-        const uint64_t bq = dq0 + s * (2 * kChunk >> 4);
-        mma_kk_nd<kChunk / 2>(nd, tmem + 64 * x, dk0, bq, id_s);
-        mma_kk_nd<kChunk / 2>(nd, tmem + 128 + 64 * x, dv0, bq + (kChunk >> 4), id_s);
-        umma_commit(&sd_full[x]);
-        return true;
-      };
-      const int n_step = 2 * n_it;
-      bool ok = mbar_wait_soon(kv_full, 0, abort_flag, p.err, DEV_TIMEOUT_MMA) && issue_s(0) && issue_s(1);
-      for (int t = 0; ok && t < n_step; ++t) {
-        const int x = t & 1;
-        ok = mbar_wait_soon(&pd_full[x], (t >> 1) & 1, abort_flag, p.err, DEV_TIMEOUT_MMA);
-        if (!ok) break;
-        tc_fence_after();
-        const uint64_t bq = dqm0 + (t & 3) * (2 * kChunk >> 4);
-        mma_tm<4>(tmem + 256, tmem + 64 * x, bq + (kChunk >> 4), id_d, t > 0);
-        mma_tm<4>(tmem + 384, tmem + 128 + 64 * x, bq, id_d, t > 0);
-        umma_commit(&qd_empty[t & 3]);
-        if (t + 2 < n_step) ok = issue_s(t + 2);
+      if (lane == 0) {
+        mbar_wait(kv_full, 0, nullptr, p.err, DEV_TIMEOUT_DRAIN);
+        for (int k = max(0, it - 2); k < it; ++k) mbar_wait(&qd_full[k & 1], (k >> 1) & 1, nullptr, p.err, DEV_TIMEOUT_DRAIN);
       }
-      umma_commit(drain);
-      mbar_wait(drain, 0, nullptr, p.err, DEV_TIMEOUT_DRAIN);
-    } else if (warp == 3) {
-    bool ok = true;
-    for (int it = 0; ok && it < n_it; ++it) {
-      const int s = it & 1, qt = it_qtile(it);
-      float l[4], d[4];
-      int2 see[4];
+    } else if (warp < 3 && lane == 0) {
+      // warp 1: S^T = K Q^T; warp 2: dP^T = V dO^T
+      const int w = warp - 1;
+      const uint32_t id = idesc_bf16(128, 64, 0, 0), d0 = tmem + 128 * w;
+      const uint64_t a0 = kmajor_desc(smem_u32(sk), 0) + w * (2 * kChunk >> 4), b0 = kmajor_desc(smem_u32(sqd), 0) + w * (2 * kChunk >> 4);
+      bool ok = mbar_wait_soon(kv_full, 0, abort_flag, p.err, DEV_TIMEOUT_MMA);
+      for (int it = 0; ok && it < n_it; ++it) {
+        ok = mbar_wait_soon(&qd_full[it & 1], (it >> 1) & 1, abort_flag, p.err, DEV_TIMEOUT_MMA);
+        const uint64_t bq = b0 + (it & 1) * (4 * kChunk >> 4);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int qp = qt * kTile + 32 * k + lane;
-        const int64_t row = (int64_t)b * p.S + qp, at = (int64_t)it_head(it) * T + row;
-        const bool in = qp < p.S;
-        see[k] = in ? make_int2(p.plan.lo[row], p.plan.hi[row]) : make_int2(0, 0);
-        // a row that sees nothing or lies past the sequence: 2^-inf, P = 0 whatever its score
-        l[k] = see[k].x < see[k].y ? -p.lse[at] * kLog2e : -INFINITY;
-        d[k] = in ? -p.delta[at] : 0.f;
+        for (int x = 0; x < 2; ++x) {
+          if (ok && it > 0) ok = mbar_wait_soon(&pd_done[x], (it - 1) & 1, abort_flag, p.err, DEV_TIMEOUT_MMA);
+          if (!ok) break;
+          tc_fence_after();
+          mma_kk_nd(nd, d0 + 64 * x, a0, bq + x * (kChunk / 2 >> 4), id);
+          umma_commit(&sd_full[x]);
+        }
       }
-      const int4 r = p.plan.q_range[b * n_t + qt];
-      ok = __all_sync(0xffffffffu, mbar_wait_soon(&rows_empty[s], ((it >> 1) & 1) ^ 1, abort_flag, p.err, DEV_TIMEOUT_PRODUCER));
-      if (!ok) break;
+      umma_commit(&drain[w]);
+      mbar_wait(&drain[w], 0, nullptr, p.err, DEV_TIMEOUT_DRAIN);
+    } else if (warp == 3 && lane == 0) {
+      const uint32_t id = idesc_bf16(128, 64 * nd, 0, 1);  // P^T, dS^T in TMEM; dO, Q MN-major
+      const uint64_t dqm0 = mnmajor_desc(smem_u32(sqd), 0);
+      bool ok = true;
+      for (int it = 0; ok && it < n_it; ++it) {
+        const uint64_t bq = dqm0 + (it & 1) * (4 * kChunk >> 4);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        s_lse[s * 128 + 32 * k + lane] = l[k];
-        s_del[s * 128 + 32 * k + lane] = d[k];
-        s_see[s * 128 + 32 * k + lane] = see[k];
+        for (int x = 0; x < 2; ++x) {
+          // the step's queries have come: its S^T and dP^T have read them
+          ok = mbar_wait_soon(&pd_full[x], it & 1, abort_flag, p.err, DEV_TIMEOUT_MMA);
+          if (!ok) break;
+          tc_fence_after();
+          mma_tm<4, 32>(tmem + 256, tmem + 64 * x, bq + (2 * kChunk >> 4) + x * 512, id, it > 0 || x > 0);
+          mma_tm<4, 32>(tmem + 384, tmem + 128 + 64 * x, bq + x * 512, id, it > 0 || x > 0);
+          umma_commit(&pd_done[x]);
+          if (x == 1) umma_commit(&qd_empty[it & 1]);
+        }
       }
-      if (lane == 0) s_whole[s] = r.z <= kt && kt < r.w;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&rows_full[s]);
-    }
+      umma_commit(&drain[2]);
+      mbar_wait(&drain[2], 0, nullptr, p.err, DEV_TIMEOUT_DRAIN);
     }
   } else {
-    const int quarter = warp & 3, x = (warp - 4) >> 2;  // x: buffer, half of each query tile
+    if (kWarps == 16) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+    // x: buffer, half of each query tile; c0: first 32 columns of it
+    const int quarter = warp & 3, x = (warp - 4) / (kWarps / 2), c0 = kCols == 1 ? ((warp - 4) >> 2) & 1 : 0;
     const int r = quarter * 32 + lane;                  // key row of the tile
     const int kpos = kt * kTile + r;
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
@@ -1379,7 +1406,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1) masked_dkv_kernel(const __grid
       const float slope = BIAS ? p.slopes[it_head(it)] * kLog2e : 0.f;
       const int side = qt0 >= kt * kTile + 32 * quarter + 31 ? -1 : 0;
 #pragma unroll 1
-      for (int c = 0; c < 2; ++c) {
+      for (int c = c0; c < c0 + kCols; ++c) {
         uint32_t sv[32], dp[32], pw[16], dw[16];
         tmem_ld32(s_tm + 32 * c, sv);
         tmem_ld32(dp_tm + 32 * c, dp);
@@ -1397,8 +1424,8 @@ __global__ void __launch_bounds__(kDkvThreads, 1) masked_dkv_kernel(const __grid
         }
         grad32<CAP, BIAS, false, true>(sv, dp, p.mul, p.cap_mul, slope, (float)(kpos - qt0 - 32 * c), side, part, see, 0.f,
                                        0.f, s_lse + col, s_del + col, pw, dw);
-        tmem_st16(s_tm + 16 * c, pw);  // behind the scores still to read
-        tmem_st16(dp_tm + 16 * c, dw);
+        tmem_st16(s_tm + 32 * c, pw);  // over the scores and products that this warp itself has read
+        tmem_st16(dp_tm + 32 * c, dw);
       }
       tmem_st_wait();
       tc_fence_before();
@@ -1406,7 +1433,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1) masked_dkv_kernel(const __grid
       if (lane == 0) mbar_arrive(&rows_empty[s]);
     }
     // dV (first group), dK (second) once every product is done
-    if (ok) ok = __all_sync(0xffffffffu, mbar_wait_soon(drain, 0, abort_flag, p.err, DEV_TIMEOUT_EPILOGUE));
+    if (ok) ok = __all_sync(0xffffffffu, mbar_wait_soon(&drain[2], 0, abort_flag, p.err, DEV_TIMEOUT_EPILOGUE));
     if (ok) {
       tc_fence_after();
       const int64_t row0 = (int64_t)b * p.S + kt * kTile + 32 * quarter;
@@ -1415,7 +1442,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1) masked_dkv_kernel(const __grid
       __nv_bfloat16* out = (x ? p.dk : p.dv) + row0 * ld + (int64_t)g * p.hd;
       const float mul = x ? p.scale : 1.f;
 #pragma unroll 1
-      for (int k = 0; k < 2 * nd; ++k) {
+      for (int k = c0; k < 2 * nd; k += kCols == 1 ? 2 : 1) {
         uint32_t v[32], w[16];
         tmem_ld32(tmem + lane_off + 256 + 128 * x + 32 * k, v);
         tmem_ld_wait_regs(v);
@@ -1484,7 +1511,7 @@ int bwd_launch(const MaskedBwdParams& p, cudaStream_t s) {
   launch_kernel(masked_dq_kernel<CAP, BIAS>, (unsigned)std::min(p.n_units, n_sm), kBwdThreads, dq_smem(), s, p);
   if (launch_failed("sl_attention_masked")) return 5;
   note_launch();
-  launch_kernel(masked_dkv_kernel<CAP, BIAS>, (unsigned)(plan_tiles(p.n_seq, p.S) * p.hkv), kDkvThreads, dkv_smem(), s, p);
+  launch_kernel(masked_dkv_kernel<CAP, BIAS>, (unsigned)(plan_tiles(p.n_seq, p.S) * p.hkv), kDkvThreads<CAP>, dkv_smem(), s, p);
   if (launch_failed("sl_attention_masked")) return 5;
   note_launch();
   return 0;
@@ -1555,8 +1582,7 @@ int attention_masked_bwd(const MaskedArgs& a, cudaStream_t s) {
   MaskedBwdParams p;
   memset(&p, 0, sizeof(p));
   if (!head_map(&p.qmap, a.q, a.ldq, a.n_seq, a.S, a.hq, a.hd) || !head_map(&p.kmap, a.k, a.ldk, a.n_seq, a.S, a.hkv, a.hd) ||
-      !head_map(&p.vmap, a.v, a.ldv, a.n_seq, a.S, a.hkv, a.hd) || !head_map(&p.domap, a.d_o, a.lddo, a.n_seq, a.S, a.hq, a.hd) ||
-      !head_map(&p.qmap64, a.q, a.ldq, a.n_seq, a.S, a.hq, a.hd, 64) || !head_map(&p.domap64, a.d_o, a.lddo, a.n_seq, a.S, a.hq, a.hd, 64))
+      !head_map(&p.vmap, a.v, a.ldv, a.n_seq, a.S, a.hkv, a.hd) || !head_map(&p.domap, a.d_o, a.lddo, a.n_seq, a.S, a.hq, a.hd))
     return 2;
   carve_plan(const_cast<void*>(a.plan), a.n_seq, a.S, &p.plan);
   p.slopes = a.slopes;
