@@ -182,12 +182,18 @@ def _check(fn, code):
         raise SparseLoRAError(fn, code)
 
 
+# the current device and the raw handle of its current stream (what torch.cuda.current_device() and
+# torch.cuda.current_stream().cuda_stream give, without the Python objects in between: 3 us of a call)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _ptr(t):
     return None if t is None else c_void_p(t.data_ptr())
 
 
 def _stream():
-    return c_void_p(torch.cuda.current_stream().cuda_stream)
+    return c_void_p(_raw_stream(_current_device()))
 
 
 def _ptrs(ts):
@@ -209,15 +215,16 @@ class Workspace:
     def _alloc(self, nbytes):
         self.buf = torch.empty(int(nbytes), dtype=torch.uint8, device=self.device)
         self.c = SlWorkspaceC(self.buf.data_ptr(), self.buf.numel(), 0)
+        self.ref = ctypes.byref(self.c)
         _check("sl_workspace_init", lib().sl_workspace_init(ctypes.byref(self.c), _stream()))
 
     def call(self, fn_name, *args):
         """Run one library call with this workspace, growing it once if the call asks for more."""
         fn = getattr(lib(), fn_name)
-        code = fn(*args, ctypes.byref(self.c), _stream())
+        code = fn(*args, self.ref, _raw_stream(_current_device()))
         if code == SL_ERR_WORKSPACE and self.c.needed > self.c.bytes:
             self._alloc(self.c.needed + (1 << 20))
-            code = fn(*args, ctypes.byref(self.c), _stream())
+            code = fn(*args, self.ref, _raw_stream(_current_device()))
         _check(fn_name, code)
 
     def read_device_flag(self) -> int:
@@ -445,46 +452,47 @@ def sl_attention_bwd(ws: Workspace, q, k, v, o, d_o, lse, n_seq, n_q_heads, n_kv
             _ptr(dv))
 
 
-def _need(fn, ok):
-    """An argument that the library could not check itself (a tensor's type, shape, device or strides)."""
-    if not ok:
-        raise SparseLoRAError(fn, SL_ERR_INVALID_ARG)
+def _refuse(fn):
+    raise SparseLoRAError(fn, SL_ERR_INVALID_ARG)
 
 
 def _rows(fn, t, shape, dtype, dev):
     """`t` as rows for the library: its address and leading dimension. 2-D, of this type and shape, on the
     current device, its rows contiguous (a row may be a slice of a longer one)."""
-    _need(fn, t.dtype == dtype and t.shape == shape and t.stride(1) == 1 and t.get_device() == dev)
+    stride = t.stride()
+    if t.dtype is not dtype or t.shape != shape or stride[1] != 1 or t.get_device() != dev:
+        _refuse(fn)
     # the stride of a single row says nothing
-    return t.data_ptr(), (t.stride(0) if shape[0] > 1 else -(-shape[1] // 8) * 8)
+    return t.data_ptr(), stride[0] if shape[0] > 1 else -(-shape[1] // 8) * 8
 
 
 def _flat(fn, t, n, dtype, dev):
     """The address of a dense tensor of n elements (None stays None)."""
     if t is None:
         return None
-    _need(fn, t.dtype == dtype and t.numel() == n and t.is_contiguous() and t.get_device() == dev)
+    if t.dtype is not dtype or t.numel() != n or not t.is_contiguous() or t.get_device() != dev:
+        _refuse(fn)
     return t.data_ptr()
 
 
 def _device(fn, t):
     """The index of t's device, which has to be the current one (the calls go to its current stream)."""
     dev = t.get_device()
-    _need(fn, dev >= 0 and dev == torch.cuda.current_device())
+    if dev < 0 or dev != _current_device():
+        _refuse(fn)
     return dev
 
 
-def _raw_stream(dev):
-    return torch._C._cuda_getCurrentRawStream(dev)
-
-
 def _rope_args(fn, q, k, positions, inv_freq, head_dim, gq, gk, eps, style, dev):
-    _need(fn, head_dim > 0 and q.dim() == 2 and k.dim() == 2 and q.shape[0] == k.shape[0]
-          and q.shape[1] % head_dim == 0 and k.shape[1] % head_dim == 0)
-    T, rot = q.shape[0], 0 if inv_freq is None else 2 * inv_freq.numel()
-    return ((_flat(fn, positions, T, torch.int32, dev), _flat(fn, inv_freq, rot // 2, torch.float32, dev), rot, style,
-             _flat(fn, gq, head_dim, torch.bfloat16, dev), _flat(fn, gk, head_dim, torch.bfloat16, dev), eps, T,
-             q.shape[1] // head_dim, k.shape[1] // head_dim, head_dim))
+    if q.dim() != 2 or k.dim() != 2 or head_dim < 1:
+        _refuse(fn)
+    (T, nq), (Tk, nk) = q.shape, k.shape
+    if T != Tk or nq % head_dim or nk % head_dim:
+        _refuse(fn)
+    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
+    return (_flat(fn, positions, T, torch.int32, dev), _flat(fn, inv_freq, rot // 2, torch.float32, dev), rot, style,
+            _flat(fn, gq, head_dim, torch.bfloat16, dev), _flat(fn, gk, head_dim, torch.bfloat16, dev), eps, T,
+            nq // head_dim, nk // head_dim, head_dim)
 
 
 def sl_qk_norm_rope_fwd(q, k, positions, inv_freq, head_dim, yq, yk, gq=None, gk=None, eps=1e-6,
@@ -508,7 +516,8 @@ def sl_qk_norm_rope_bwd(ws: Workspace, dyq, dyk, q, k, positions, inv_freq, head
     rest = _rope_args(fn, dyq, dyk, positions, inv_freq, head_dim, gq, gk, eps, style, dev)
     xs = (None, 0, None, 0)
     if gq is not None:
-        _need(fn, q is not None and k is not None)
+        if q is None or k is None:
+            _refuse(fn)
         xs = (*_rows(fn, q, dyq.shape, bf, dev), *_rows(fn, k, dyk.shape, bf, dev))
     ws.call(fn, *_rows(fn, dyq, dyq.shape, bf, dev), *_rows(fn, dyk, dyk.shape, bf, dev), *xs, *rest,
             *_rows(fn, dq, dyq.shape, bf, dev), *_rows(fn, dk, dyk.shape, bf, dev),
@@ -533,9 +542,11 @@ def sl_attention_plan(row_lo, row_hi, n_seq, plan, seq_len=None):
     fn = "sl_attention_plan"
     dev = _device(fn, plan)
     rows = row_lo if row_lo is not None else row_hi
-    _need(fn, n_seq > 0 and (seq_len is not None if rows is None else rows.numel() % n_seq == 0))
+    if n_seq < 1 or (seq_len is None if rows is None else rows.numel() % n_seq):
+        _refuse(fn)
     T = n_seq * seq_len if rows is None else rows.numel()
-    _need(fn, seq_len is None or T == n_seq * seq_len)
+    if seq_len is not None and T != n_seq * seq_len:
+        _refuse(fn)
     _check(fn, lib().sl_attention_plan(_flat(fn, row_lo, T, torch.int32, dev), _flat(fn, row_hi, T, torch.int32, dev),
                                        n_seq, T // n_seq, _flat(fn, plan, plan.numel(), torch.uint8, dev),
                                        plan.numel(), _raw_stream(dev)))
@@ -543,7 +554,8 @@ def sl_attention_plan(row_lo, row_hi, n_seq, plan, seq_len=None):
 
 def _masked_args(fn, q, k, n_seq, n_q_heads, n_kv_heads, head_dim):
     T = q.shape[0]
-    _need(fn, n_seq > 0 and T % n_seq == 0)
+    if n_seq < 1 or T % n_seq:
+        _refuse(fn)
     return (T, n_q_heads * head_dim), (T, n_kv_heads * head_dim)
 
 
@@ -575,7 +587,8 @@ def sl_attention_masked_bwd(ws: Workspace, q, k, v, o, d_o, lse, n_seq, n_q_head
 
 
 def _logits(fn, t, shape, dtype, dev):
-    _need(fn, t.dim() == 2 and dtype in (torch.bfloat16, torch.float32))
+    if t.dim() != 2 or dtype not in (torch.bfloat16, torch.float32):
+        _refuse(fn)
     return _rows(fn, t, shape, dtype, dev)
 
 

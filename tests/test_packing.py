@@ -101,7 +101,7 @@ def test_attention_plan_and_call_refuse(lib):
     assert bwd(S=301) == bwd(hd=12) == bwd(cap=bad) == bwd(pb=0) == B.SL_ERR_SHAPE
     assert fwd(q=ODD) == fwd(ldq=252) == fwd(ldq=248) == fwd(pl=ODD) == fwd(lse=A + 4) == bwd(lddv=120) == \
         B.SL_ERR_ALIGNMENT
-    assert fwd(ws=None) == fwd(ws=_ws(16)) == bwd(ws=_ws(1 << 17)) == B.SL_ERR_WORKSPACE
+    assert fwd(ws=None) == fwd(ws=_ws(16)) == bwd(ws=_ws(1 << 16)) == B.SL_ERR_WORKSPACE
 
 
 def test_token_logprobs_refuse(lib):
