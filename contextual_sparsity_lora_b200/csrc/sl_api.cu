@@ -11,6 +11,7 @@
 
 #include "../../include/sparselora.h"
 #include "sl_internal.h"
+#include "sl_packed.h"
 
 using namespace sl;
 
@@ -1284,7 +1285,7 @@ sl_status masked_args(int32_t n_seq, int32_t seq_len, int32_t hq, int32_t hkv, i
                       const void* plan, int64_t plan_bytes) {
   if (!plan_sizes_ok(n_seq, seq_len) || hq < 1 || hkv < 1 || hq % hkv || hd < 8 || hd > 128 || hd % 8 || hq > 65535)
     return SL_ERR_SHAPE;
-  if (((int64_t)seq_len + 127) / 128 * n_seq * hq > 0x7fffffff) return SL_ERR_SHAPE;
+  if (((int64_t)seq_len + 127) / 128 * n_seq * hq > 1 << 30) return SL_ERR_SHAPE;  // the kernels' unit numbers are int32
   if (!(scale >= 0.f && scale < INFINITY) || !(cap >= 0.f && cap < INFINITY)) return SL_ERR_SHAPE;
   if (plan_bytes < attention_plan_bytes(n_seq, seq_len)) return SL_ERR_SHAPE;
   return al16(plan) ? SL_OK : SL_ERR_ALIGNMENT;

@@ -15,6 +15,7 @@
 #include <cmath>
 
 #include "sl_attn.cuh"
+#include "sl_packed.h"
 
 namespace sl {
 
@@ -474,11 +475,18 @@ __device__ __forceinline__ bool bar_and_compute(bool ok) {
 // half a key tile (64 keys): each stream has two S buffers in TMEM, so while the softmax works on step h, S of step h + 1
 // is there or on its way, and the order of a stream's products is O_x += P_x V of step h, S_x of step h + 2 (into the same
 // buffer). Keys run from the last to the first: with a bias by distance the largest scores mostly come first, and O
-// is rescaled rarely (from the first key on, steep slopes rescaled it in every step: 1076 instead of 758 us at 8192
+// is rescaled rarely (from the first key on, steep slopes rescaled it in every step: 1076 against 908 us at 8192
 // tokens). With whole tiles and one S buffer per stream the softmax waited for a P V and an S in
 // each step, 40% of its time. P replaces S in TMEM (bf16, the first operand of P V) and never passes through
 // shared memory. Each stream has an issuing warp of its own: one thread for both is busy with waits and commits for as long
-// as with products, and the tensor cores, which queue about five, run dry. TMEM: S_x / P_x of step h at 128 x + 64 (h & 1), O_x at 256 + 128 x.
+// as with products, and the tensor cores, which queue about five, run dry (8192 tokens: 908 us with one, 613 with two);
+// a third one for S alone loses what a stream's order gives (604 against 589). TMEM: S_x / P_x of step h at
+// 128 x + 64 (h & 1), O_x at 256 + 128 x.
+//
+// Measured (32 query, 8 key/value heads of 128, one sequence): 8192 tokens with a prefix and a bias 589 us (947 TFLOP/s
+// over the visible pairs, 0.58 of a library bf16 product's rate), 4096 tokens causal 140 us, with a cap 130 us
+// (its documents see fewer tiles), 8 x 512 tokens 39 us. The tensor pipe is busy 48% of the time; the rest are waits between
+// the products and a softmax whose exponentials, 64 per row and step, take as long as the step's products.
 struct Unit {
   int qt0, qt1, h0, h1, b, j0, j1;
   __device__ __forceinline__ int qt(int x) const { return x ? qt1 : qt0; }
@@ -615,7 +623,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) masked_fwd_kernel(const __grid
     if (lane == 0) {
       Unit un, nx;
       bool ok = plan_ok, live = plan_ok && unit_number(0) < p.n_units;
-      int i = 0, t = 0;  // units and key tiles loaded
+      int i = 0, t = 0, n_q[2] = {0, 0};  // units, key tiles loaded, each stream's query tiles
       if (live) nx = unit_of(p, unit_number(0));
       for (; ok && live; ++i) {
         un = nx;
@@ -628,6 +636,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) masked_fwd_kernel(const __grid
           mbar_arrive_expect_tx(&q_full[x], nd * kChunk);
           for (int c = 0; c < nd; ++c)
             tma_load_4d(sq + (2 * x + c) * kChunk, &p.qmap, &q_full[x], 64 * c, un.h(x), un.qt(x) * kTile, un.b);
+          ++(x ? n_q[1] : n_q[0]);
         }
         for (int j = un.j1 - 1; ok && j >= un.j0; --j, ++t) {
           const int s = t & 1;
@@ -640,9 +649,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1) masked_fwd_kernel(const __grid
             tma_load_4d(sv + (2 * s + c) * kChunk, &p.vmap, &kv_full[s], 64 * c, g, j * kTile, un.b);
         }
       }
-      // every copy lands before the CTA may exit (a Q whose turn did not come was not loaded: its barrier's phase is over)
-      if (ok && i > 0)
-        for (int x = 0; x < 2; ++x) mbar_wait(&q_full[x], (i - 1) & 1, nullptr, p.err, DEV_TIMEOUT_DRAIN);
+      // every copy lands before the CTA may exit
+      if (n_q[0]) mbar_wait(&q_full[0], (n_q[0] - 1) & 1, nullptr, p.err, DEV_TIMEOUT_DRAIN);
+      if (n_q[1]) mbar_wait(&q_full[1], (n_q[1] - 1) & 1, nullptr, p.err, DEV_TIMEOUT_DRAIN);
       for (int k = max(0, t - 2); k < t; ++k) mbar_wait(&kv_full[k & 1], (k >> 1) & 1, nullptr, p.err, DEV_TIMEOUT_DRAIN);
     }
   } else if (warp == 1 || warp == 2) {
@@ -856,9 +865,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1) masked_fwd_kernel(const __grid
 
 // Two kernels. dq: per tile of queries, D and then dQ, over the key tiles that it sees; dk, dv: per tile of keys, over
 // the query tiles that see it. Each forms S and dP for itself (nine products of a tile pair where one kernel for
-// all would have five and a sum for D), but no partial sum leaves the chip: with dQ added up across key tiles in
-// global memory (64 KB of fp32 reductions per tile pair, then a pass to round them) the backward took 1.7 times as
-// long, and dq's last bits depended on the order. Here every sum has a fixed order.
+// all would have five and a sum for D), but no partial sum leaves the chip and every sum has a fixed order. With dQ
+// added up across key tiles in global memory (64 KB of fp32 reductions per tile pair, a kernel for D before it and a pass
+// that rounds after it) the backward took 161 us at 8 x 512 tokens and 631 at 4096 capped ones, against 131 and 618, and
+// dq's last bits depended on the order.
 //
 // D_i = sum_j P_ij dP_ij (= dO_i . o_i) is formed from P and dP in fp32 and not from the stored o: that one is rounded to
 // bf16, and its error, the same for all keys of a row, is as large as all other roundings of dq and dk
@@ -911,13 +921,16 @@ __device__ __forceinline__ void grad32(uint32_t (&s)[32], uint32_t (&dp)[32], fl
   }
 }
 
-// dq: persistent CTAs over units (query tile, head). Q and dO stay, K and V stream through two stages, twice: first for D,
-// then for dQ. Warp 0 loads; warps 1, 2 and 3 issue S = Q K^T, dP = dO V^T and dQ += dS K, S and dP a step ahead of the compute
-// warps (S has two buffers, and dS takes the place of its S; dP has one, which the compute warps take into registers at
-// once). Warps 4-19 hold a query row and 32 of the key columns per thread. TMEM: dQ at 0, S / dS of step t at
-// 128 + 128 (t & 1), dP at 384. The second pass begins with the last two key tiles, whose K and V are still there (documents of up
-// to 256 keys are read once), and goes back from the one before them. Warps 4-19 hold a query row and 32 of the key columns per thread. TMEM: dQ at 0, S / dS of
-// step t at 128 + 128 (t & 1), dP at 384.
+// dq: persistent CTAs over units (query tile, head). Q and dO stay, K and V stream through two stages, twice: first for
+// D, then for dQ. Warp 0 loads; warps 1, 2 and 3 issue S = Q K^T, dP = dO V^T and dQ += dS K, S and dP a step ahead of
+// the compute warps (S has two buffers, and dS takes the place of its S; dP has one, which the compute warps take into
+// registers at once). Warps 4-19 hold a query row and 32 of the 128 key columns per thread. The second pass begins with
+// the last two key tiles, whose K and V are still there (documents of up to 256 keys are read once), and goes back from
+// the one before them. TMEM: dQ at 0, S / dS of step t at 128 + 128 (t & 1), dP at 384.
+//
+// Measured (32 query, 8 key/value heads of 128): 4096 causal tokens 349 us (five products of a tile pair, 1015 TFLOP/s),
+// capped documents 318 us, 8 x 512 tokens 69 us. The products read both operands of S and dP from shared memory, at
+// its full rate, so the tensor pipe cannot be busy more than 3/4 of the time; it is for half of it.
 template <bool CAP, bool BIAS>
 __global__ void __launch_bounds__(kBwdThreads, 1) masked_dq_kernel(const __grid_constant__ MaskedBwdParams p) {
   extern __shared__ uint8_t smem_raw[];
@@ -998,8 +1011,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) masked_dq_kernel(const __grid_
     if (warp == 0 && lane == 0) {
       U w, nx;
       bool ok = plan_ok, live = plan_ok && unit(0, nx);
-      int t = 0, i = 0;
-      for (; ok && live; ++i) {
+      int t = 0, n_q = 0;
+      for (int i = 0; ok && live; ++i) {
         w = nx;
         live = unit(i + 1, nx);
         if (i > 0 && !mbar_wait_soon(q_empty, (i - 1) & 1, abort_flag, p.err, DEV_TIMEOUT_PRODUCER)) break;
@@ -1008,6 +1021,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) masked_dq_kernel(const __grid_
           tma_load_4d(sq + c * kChunk, &p.qmap, q_full, 64 * c, w.h, w.qt * kTile, w.b);
           tma_load_4d(sq + (2 + c) * kChunk, &p.domap, q_full, 64 * c, w.h, w.qt * kTile, w.b);
         }
+        ++n_q;
         // the second pass loads all but the last two tiles again
         for (int k = 0; k < 2 * (w.j1 - w.j0) - min(2, w.j1 - w.j0); ++k, ++t) {
           const int s = t & 1, j = k < w.j1 - w.j0 ? w.j0 + k : w.j1 - 3 - (k - (w.j1 - w.j0));
@@ -1021,7 +1035,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) masked_dq_kernel(const __grid_
         }
       }
       // every copy lands before the CTA may exit
-      if (i > 0) mbar_wait(q_full, (i - 1) & 1, nullptr, p.err, DEV_TIMEOUT_DRAIN);
+      if (n_q) mbar_wait(q_full, (n_q - 1) & 1, nullptr, p.err, DEV_TIMEOUT_DRAIN);
       for (int k = max(0, t - 2); k < t; ++k) mbar_wait(&kv_full[k & 1], (k >> 1) & 1, nullptr, p.err, DEV_TIMEOUT_DRAIN);
     } else if (warp > 0 && lane == 0) {
       // key tiles of this CTA's unit i (0: there is none); a unit has twice as many steps
@@ -1216,10 +1230,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1) masked_dq_kernel(const __grid_
 // stay, Q and dO stream through two stages. A step is half a query tile (64 queries): S^T = K Q^T and dP^T = V dO^T of
 // step t + 1 run while the compute warps work on step t; P^T and dS^T replace them in TMEM (bf16, first
 // operands of dV += P^T dO and dK += dS^T Q). Warp 0 loads, the query rows' lse, D and intervals too; warps 1, 2 and 3 issue
-// S^T, dP^T, and dV and dK (a thread that issues also waits and commits, and meanwhile the tensor cores, which queue about
-// five products, run dry: @@DKV@@); the others compute, one half for the even and one for the odd steps, a key row and 32 query columns per thread at a
-// time: 16 warps, or 8 where a cap's tanh needs the registers (with 16 it spills: 335 against 316 us at 4096 capped tokens,
-// without a cap 16 gain 10%). TMEM: S^T of buffer x at 64 x, dP^T at 128 + 64 x, dV at 256, dK at 384.
+// S^T, dP^T, and dV and dK (a thread that issues also waits and commits, and meanwhile the tensor cores, which queue
+// about five products, run dry: 340 us at 4096 causal tokens with one such thread, 320 with two, 277 with three); the
+// others compute, one half for the even and one for the odd steps, a key row and 32 query columns per thread at a time:
+// 16 warps, or 8 where a cap's tanh needs the registers (with 16 it spills: 335 against 318 us at 4096 capped
+// tokens, 300 since; without a cap 16 gain 10%). TMEM: S^T of buffer x at 64 x, dP^T at 128 + 64 x, dV at 256, dK at
+// 384. Measured besides: 8 x 512 tokens 62 us; 4096 causal tokens are 1023 TFLOP/s of four products per tile pair.
 template <bool CAP, bool BIAS>
 __global__ void __launch_bounds__(kDkvThreads<CAP>, 1) masked_dkv_kernel(const __grid_constant__ MaskedBwdParams p) {
   extern __shared__ uint8_t smem_raw[];

@@ -23,7 +23,7 @@
 #include <algorithm>
 #include <atomic>
 
-#include "sl_internal.h"
+#include "sl_packed.h"
 
 namespace sl {
 

@@ -17,7 +17,6 @@ enum : int {
   DEV_TIMEOUT_DRAIN = 4,
   DEV_BAD_TILE = 5,
   DEV_TIMEOUT_ESTIMATOR = 6,
-  DEV_BAD_PLAN = 7,  // an attention plan of other sizes than the call's
 };
 
 // Upper bound of any single wait inside a kernel. Correct kernels wait microseconds.

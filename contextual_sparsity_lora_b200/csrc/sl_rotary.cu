@@ -17,7 +17,7 @@
 
 #include <algorithm>
 
-#include "sl_internal.h"
+#include "sl_packed.h"
 
 namespace sl {
 

@@ -102,6 +102,10 @@ def test_attention_plan_and_call_refuse(lib):
     assert fwd(q=ODD) == fwd(ldq=252) == fwd(ldq=248) == fwd(pl=ODD) == fwd(lse=A + 4) == bwd(lddv=120) == \
         B.SL_ERR_ALIGNMENT
     assert fwd(ws=None) == fwd(ws=_ws(16)) == bwd(ws=_ws(1 << 16)) == B.SL_ERR_WORKSPACE
+    # more (head, query tile) pairs than the kernels count in 32 bits: 2^30 - 200 one-token sequences, two heads
+    many = (1 << 30) - 200
+    assert f(A, 16, A, 8, A, 8, many, 1, 2, 1, 8, 0.0, 0.0, None, A, lib.sl_attention_plan_bytes(many, 1), A, 16, A, _ws(),
+             None) == B.SL_ERR_SHAPE
 
 
 def test_token_logprobs_refuse(lib):
