@@ -79,7 +79,8 @@ int64_t carve_plan(void* buf, int n_seq, int S, Plan* out) {
 
 // Whether the buffer holds a plan of these sizes (else the error word is set and nothing is computed).
 __device__ __forceinline__ bool plan_fits(const Plan& p, int n_seq, int S, int* err) {
-  const bool ok = p.header[0] == kPlanMagic && p.header[1] == n_seq && p.header[2] == S;
+  const int4 h = *reinterpret_cast<const int4*>(p.header);
+  const bool ok = h.x == kPlanMagic && h.y == n_seq && h.z == S;
   if (!ok && threadIdx.x == 0 && blockIdx.x == 0) record_error(err, DEV_BAD_PLAN);
   return ok;
 }
@@ -499,11 +500,16 @@ __device__ __forceinline__ int unit_number(int i) {
   return (i & 1) ? (i + 1) * (int)gridDim.x - 1 - (int)blockIdx.x : i * (int)gridDim.x + (int)blockIdx.x;
 }
 
-__device__ __forceinline__ Unit unit_of(const MaskedFwdParams& p, int u) {
+// A unit's entry of the plan, read a unit ahead, and what it says (apart, so that nothing waits for the read).
+__device__ __forceinline__ int4 unit_entry(const MaskedFwdParams& p, int u) {
+  if (u >= p.n_units) return make_int4(0, 0, 0, 0);
+  return p.pair_heads ? p.plan.q_order[u / (p.hq >> 1)] : p.plan.q2_order[u / p.hq];
+}
+
+__device__ __forceinline__ Unit unit_of(const MaskedFwdParams& p, int u, const int4& e) {
   Unit r;
   if (p.pair_heads) {
     const int n_qt = (p.S + kTile - 1) / kTile, half = p.hq >> 1;
-    const int4 e = p.plan.q_order[u / half];
     r.b = e.x / n_qt;
     r.qt0 = r.qt1 = e.x % n_qt;
     r.h0 = 2 * (u % half);
@@ -512,7 +518,6 @@ __device__ __forceinline__ Unit unit_of(const MaskedFwdParams& p, int u) {
     r.j1 = e.z;
   } else {
     const int n_t2 = ((p.S + kTile - 1) / kTile + 1) >> 1;
-    const int4 e = p.plan.q2_order[u / p.hq];
     r.b = e.x / n_t2;
     r.qt0 = 2 * (e.x % n_t2);
     r.qt1 = r.qt0 + 1;
@@ -617,18 +622,17 @@ __global__ void __launch_bounds__(kFwdThreads, 1) masked_fwd_kernel(const __grid
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   pdl_wait();
+  int4 e0 = unit_entry(p, unit_number(0)), e1 = unit_entry(p, unit_number(1));  // this unit and the next
   const bool plan_ok = plan_fits(p.plan, p.n_seq, p.S, p.err);
 
   if (warp == 0) {
     if (lane == 0) {
-      Unit un, nx;
-      bool ok = plan_ok, live = plan_ok && unit_number(0) < p.n_units;
+      bool ok = plan_ok;
       int i = 0, t = 0, n_q[2] = {0, 0};  // units, key tiles loaded, each stream's query tiles
-      if (live) nx = unit_of(p, unit_number(0));
-      for (; ok && live; ++i) {
-        un = nx;
-        live = unit_number(i + 1) < p.n_units;
-        if (live) nx = unit_of(p, unit_number(i + 1));
+      for (; ok && unit_number(i) < p.n_units; ++i) {
+        const Unit un = unit_of(p, unit_number(i), e0);
+        e0 = e1;
+        e1 = unit_entry(p, unit_number(i + 2));
         const int g = un.h0 / hpg;
         for (int x = 0; x < 2 && ok; ++x) {
           if (i > 0) ok = mbar_wait_soon(&q_empty[x], (i - 1) & 1, abort_flag, p.err, DEV_TIMEOUT_PRODUCER);
@@ -661,13 +665,6 @@ __global__ void __launch_bounds__(kFwdThreads, 1) masked_fwd_kernel(const __grid
       const uint32_t id_pv = idesc_bf16(128, 64 * nd, 0, 1);   // O += P V: P in TMEM, V MN-major
       const uint64_t dq0 = kmajor_desc(smem_u32(sq + 2 * x * kChunk), 0), dk0 = kmajor_desc(smem_u32(sk), 0),
                      dv0 = mnmajor_desc(smem_u32(sv), 0);
-      // Key tiles of this CTA's unit i (0: there is none)
-      auto tiles_of = [&](int i) -> int {
-        const int u = unit_number(i);
-        if (!plan_ok || u >= p.n_units) return 0;
-        const int4 e = p.pair_heads ? p.plan.q_order[u / (p.hq >> 1)] : p.plan.q2_order[u / p.hq];
-        return e.z - e.y;
-      };
       // S of key tile t, half buf (the second half of the keys first); first: of its unit, last: the unit's last tile
       auto issue_s = [&](int t, int buf, bool last) {
         const int s = t & 1;
@@ -679,15 +676,16 @@ __global__ void __launch_bounds__(kFwdThreads, 1) masked_fwd_kernel(const __grid
         return (!first || mbar_wait_soon(&q_full[x], i & 1, abort_flag, p.err, DEV_TIMEOUT_MMA)) &&
                mbar_wait_soon(&kv_full[t & 1], (t >> 1) & 1, abort_flag, p.err, DEV_TIMEOUT_MMA);
       };
-      int n = tiles_of(0), n_next = tiles_of(1), i = 0, j = 0;  // tiles of this unit and the next, unit, tile in it
-      bool ok = n > 0 && arrived(0, 0, true);
+      int n = e0.z - e0.y, n_next = e1.z - e1.y, i = 0, j = 0;  // tiles of this unit and the next (0: none), unit, tile in it
+      int4 e2 = unit_entry(p, unit_number(2));
+      bool ok = plan_ok && n > 0 && arrived(0, 0, true);
       if (ok) {
         tc_fence_after();
         issue_s(0, 0, n == 1);
         issue_s(0, 1, n == 1);
       }
       for (int t = 0; ok; ++t) {
-        // P V of tile t, and S of tile t + 1 (the next unit's first after this one's last) a tile ahead
+        // P V of tile t, and S of tile t + 1 a tile ahead; S of the next unit, whose Q is on its way, behind both P V
         const bool last = j == n - 1, more = !last || n_next > 0;
         const int s = t & 1;
 #pragma unroll
@@ -699,21 +697,27 @@ __global__ void __launch_bounds__(kFwdThreads, 1) masked_fwd_kernel(const __grid
                     j > 0 || buf > 0);
           if (last) umma_commit(&pv_done[2 * x + buf]);
           if (buf) umma_commit(&kv_empty[s]);
-          if (more) {
+          if (!last) {
             if (buf == 0) {
-              ok = arrived(t + 1, i + 1, last);
+              ok = arrived(t + 1, i, false);
               if (!ok) break;
               tc_fence_after();
             }
-            issue_s(t + 1, buf, last ? n_next == 1 : j + 1 == n - 1);
+            issue_s(t + 1, buf, j + 1 == n - 1);
           }
         }
-        if (!more) break;
+        if (!more || !ok) break;
         if (last) {
           ++i;
           j = 0;
           n = n_next;
-          n_next = tiles_of(i + 1);
+          n_next = e2.z - e2.y;
+          e2 = unit_entry(p, unit_number(i + 2));
+          ok = arrived(t + 1, i, true);
+          if (!ok) break;
+          tc_fence_after();
+          issue_s(t + 1, 0, n == 1);
+          issue_s(t + 1, 1, n == 1);
         } else {
           ++j;
         }
@@ -740,7 +744,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) masked_fwd_kernel(const __grid
       }
     };
     if (more) {
-      nx = unit_of(p, unit_number(0));
+      nx = unit_of(p, unit_number(0), e0);
       rows_of(nx, nlo, nhi);
     }
     for (int i = 0; ok && more; ++i) {
@@ -748,7 +752,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1) masked_fwd_kernel(const __grid
       lo = nlo;
       hi = nhi;
       more = unit_number(i + 1) < p.n_units;
-      if (more) nx = unit_of(p, unit_number(i + 1));
+      if (more) {
+        nx = unit_of(p, unit_number(i + 1), e1);
+        e1 = unit_entry(p, unit_number(i + 2));
+      }
       const int qt = me.qt(x), h = me.h(x);
       const int qpos = qt * kTile + r;               // position in the sequence
       const float slope = BIAS ? p.slopes[h] * kLog2e : 0.f;
@@ -839,13 +846,19 @@ __global__ void __launch_bounds__(kFwdThreads, 1) masked_fwd_kernel(const __grid
       const int64_t row0 = (int64_t)me.b * p.S + qt * kTile + 32 * quarter;  // row of lane 0
       const int n_rows = p.S - (qt * kTile + 32 * quarter);
 #pragma unroll 1
-      for (int c = 0; c < 2 * nd; ++c) {
-        uint32_t ov[32], w[16];
-        tmem_ld32(o_tm + 32 * c, ov);
-        tmem_ld_wait_regs(ov);
+      for (int c = 0; c < 2 * nd; c += 2) {
+        uint32_t ov[2][32], w[2][16];
+        tmem_ld32(o_tm + 32 * c, ov[0]);
+        tmem_ld32(o_tm + 32 * c + 32, ov[1]);
+        tmem_ld_wait_regs(ov[0]);
+        regs_after_wait(ov[1]);
 #pragma unroll
-        for (int e = 0; e < 32; e += 2) w[e / 2] = pack2(__uint_as_float(ov[e]) * inv, __uint_as_float(ov[e + 1]) * inv);
-        store_rows32(p.o + row0 * p.ldo + (int64_t)h * p.hd + 32 * c, p.ldo, w, n_rows, p.hd - 32 * c);
+        for (int k = 0; k < 2; ++k) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 2)
+            w[k][e / 2] = pack2(__uint_as_float(ov[k][e]) * inv, __uint_as_float(ov[k][e + 1]) * inv);
+          store_rows32(p.o + row0 * p.ldo + (int64_t)h * p.hd + 32 * (c + k), p.ldo, w[k], n_rows, p.hd - 32 * (c + k));
+        }
       }
       tc_fence_before();
       if (qpos < p.S)
@@ -921,12 +934,14 @@ __device__ __forceinline__ void grad32(uint32_t (&s)[32], uint32_t (&dp)[32], fl
   }
 }
 
-// dq: persistent CTAs over units (query tile, head). Q and dO stay, K and V stream through two stages, twice: first for
-// D, then for dQ. Warp 0 loads; warps 1, 2 and 3 issue S = Q K^T, dP = dO V^T and dQ += dS K, S and dP a step ahead of
-// the compute warps (S has two buffers, and dS takes the place of its S; dP has one, which the compute warps take into
-// registers at once). Warps 4-19 hold a query row and 32 of the 128 key columns per thread. The second pass begins with
-// the last two key tiles, whose K and V are still there (documents of up to 256 keys are read once), and goes back from
-// the one before them. TMEM: dQ at 0, S / dS of step t at 128 + 128 (t & 1), dP at 384.
+// dq: persistent CTAs over units (query tile, head). Q and dO stay, K and V stream through two stages, for D and then, from
+// the last key tile to the first, for dQ. S, dP and K of the last two tiles are kept, so the second pass forms
+// them again only from the third on (documents of up to 256 keys: once). Warp 0 loads; warps 1, 2 and 3 issue
+// S = Q K^T, dP = dO V^T and dQ += dS K, S and dP ahead of the compute warps. Warps 4-19 hold a query row and 32 of
+// the 128 key columns per thread. A step has a stage of K and V and a buffer of S (dS takes the place of its S), both of the
+// same number: with n key tiles in unit i, step m < n of the first pass has number (i + m) & 1, the k-th of the second
+// pass (kept or formed again) (i + n - 1 + k) & 1. TMEM: S / dS at 128 and 256, dP at 384; that of the last tile (of two
+// or more) at 0, where dQ is added up once it has been read.
 //
 // Measured (32 query, 8 key/value heads of 128): 4096 causal tokens 349 us (five products of a tile pair, 1015 TFLOP/s),
 // capped documents 318 us, 8 x 512 tokens 69 us. The products read both operands of S and dP from shared memory, at
@@ -945,32 +960,23 @@ __global__ void __launch_bounds__(kBwdThreads, 1) masked_dq_kernel(const __grid_
   uint64_t* kv_full = bars + 2;    // [2]
   uint64_t* kv_empty = bars + 4;   // [2]
   uint64_t* s_full = bars + 6;     // [2] by buffer
-  uint64_t* s_read = bars + 8;     // [2]: S is in registers
+  uint64_t* s_read = bars + 8;     // [2]: S is in registers and not kept
   uint64_t* ds_full = bars + 10;   // [2]: dS in the buffer
   uint64_t* ds_done = bars + 12;   // [2]: dQ has read it
-  uint64_t* dp_full = bars + 14;
-  uint64_t* dp_read = bars + 15;
-  uint64_t* dq_done = bars + 16;   // a unit's dQ
-  uint64_t* drain = bars + 17;     // [3]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 20);
+  uint64_t* dp_full = bars + 14;   // [2]: dP in its place, in dQ's place
+  uint64_t* dp_read = bars + 16;   // dP's place is free
+  uint64_t* dq_done = bars + 17;   // a unit's dQ
+  uint64_t* dq_read = bars + 18;   // dQ's place is free
+  uint64_t* drain = bars + 19;     // [3]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 22);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n_qt = (p.S + kTile - 1) / kTile;
   const int hpg = p.hq / p.hkv;
-  struct U {
-    int qt, b, h, j0, j1;
-  };
-  auto unit = [&](int i, U& w) -> bool {
+  auto entry = [&](int i) -> int4 {  // of this CTA's unit i, read ahead (no key tiles: there is no such unit)
     const int u = unit_number(i);
-    if (u >= p.n_units) return false;
-    const int4 e = p.plan.q_order[u / p.hq];
-    w.qt = e.x % n_qt;
-    w.b = e.x / n_qt;
-    w.h = u % p.hq;
-    w.j0 = e.y;
-    w.j1 = e.z;
-    return true;
+    return u < p.n_units ? p.plan.q_order[u / p.hq] : make_int4(0, 0, 0, 0);
   };
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
@@ -982,10 +988,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1) masked_dq_kernel(const __grid_
       mbar_init(&s_read[s], 16);
       mbar_init(&ds_full[s], 16);
       mbar_init(&ds_done[s], 1);
+      mbar_init(&dp_full[s], 1);
     }
-    mbar_init(dp_full, 1);
     mbar_init(dp_read, 16);
     mbar_init(dq_done, 1);
+    mbar_init(dq_read, 16);
     for (int s = 0; s < 3; ++s) mbar_init(&drain[s], 1);
     *abort_flag = 0;
     fence_barrier_init();
@@ -1003,104 +1010,106 @@ __global__ void __launch_bounds__(kBwdThreads, 1) masked_dq_kernel(const __grid_
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   pdl_wait();
+  int4 e = entry(0);
   const bool plan_ok = plan_fits(p.plan, p.n_seq, p.S, p.err);
 
   // 640 threads start with 96 registers each; 56 in the first four warps and 104 in the others stay within their sum
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == 0 && lane == 0) {
-      U w, nx;
-      bool ok = plan_ok, live = plan_ok && unit(0, nx);
-      int t = 0, n_q = 0;
-      for (int i = 0; ok && live; ++i) {
-        w = nx;
-        live = unit(i + 1, nx);
+      bool ok = plan_ok;
+      int n_q = 0, used[2] = {0, 0};  // query tiles loaded, loads of each stage
+      for (int i = 0; ok && e.z > e.y; ++i) {
+        const int qt0 = e.x % n_qt * kTile, b = e.x / n_qt, h = unit_number(i) % p.hq, j0 = e.y, j1 = e.z;
+        e = entry(i + 1);
         if (i > 0 && !mbar_wait_soon(q_empty, (i - 1) & 1, abort_flag, p.err, DEV_TIMEOUT_PRODUCER)) break;
         mbar_arrive_expect_tx(q_full, 2 * nd * kChunk);
         for (int c = 0; c < nd; ++c) {
-          tma_load_4d(sq + c * kChunk, &p.qmap, q_full, 64 * c, w.h, w.qt * kTile, w.b);
-          tma_load_4d(sq + (2 + c) * kChunk, &p.domap, q_full, 64 * c, w.h, w.qt * kTile, w.b);
+          tma_load_4d(sq + c * kChunk, &p.qmap, q_full, 64 * c, h, qt0, b);
+          tma_load_4d(sq + (2 + c) * kChunk, &p.domap, q_full, 64 * c, h, qt0, b);
         }
         ++n_q;
-        // the second pass loads all but the last two tiles again
-        for (int k = 0; k < 2 * (w.j1 - w.j0) - min(2, w.j1 - w.j0); ++k, ++t) {
-          const int s = t & 1, j = k < w.j1 - w.j0 ? w.j0 + k : w.j1 - 3 - (k - (w.j1 - w.j0));
-          if (!mbar_wait_soon(&kv_empty[s], ((t >> 1) & 1) ^ 1, abort_flag, p.err, DEV_TIMEOUT_PRODUCER)) { ok = false; break; }
+        const int n = j1 - j0, steps = 2 * n - min(2, n), g = h / hpg;
+        for (int m = 0; m < steps; ++m) {
+          const int s = (i + m + (m >= n)) & 1, j = m < n ? j0 + m : j1 - 3 - (m - n);
+          ok = mbar_wait_soon(&kv_empty[s], ((s ? used[1]++ : used[0]++) & 1) ^ 1, abort_flag, p.err, DEV_TIMEOUT_PRODUCER);
+          if (!ok) {
+            --(s ? used[1] : used[0]);
+            break;
+          }
           mbar_arrive_expect_tx(&kv_full[s], 2 * nd * kChunk);
           uint8_t* st = skv + s * 4 * kChunk;
           for (int c = 0; c < nd; ++c) {
-            tma_load_4d(st + c * kChunk, &p.kmap, &kv_full[s], 64 * c, w.h / hpg, j * kTile, w.b);
-            tma_load_4d(st + (2 + c) * kChunk, &p.vmap, &kv_full[s], 64 * c, w.h / hpg, j * kTile, w.b);
+            tma_load_4d(st + c * kChunk, &p.kmap, &kv_full[s], 64 * c, g, j * kTile, b);
+            tma_load_4d(st + (2 + c) * kChunk, &p.vmap, &kv_full[s], 64 * c, g, j * kTile, b);
           }
         }
       }
       // every copy lands before the CTA may exit
       if (n_q) mbar_wait(q_full, (n_q - 1) & 1, nullptr, p.err, DEV_TIMEOUT_DRAIN);
-      for (int k = max(0, t - 2); k < t; ++k) mbar_wait(&kv_full[k & 1], (k >> 1) & 1, nullptr, p.err, DEV_TIMEOUT_DRAIN);
+      if (used[0]) mbar_wait(&kv_full[0], (used[0] - 1) & 1, nullptr, p.err, DEV_TIMEOUT_DRAIN);
+      if (used[1]) mbar_wait(&kv_full[1], (used[1] - 1) & 1, nullptr, p.err, DEV_TIMEOUT_DRAIN);
     } else if (warp > 0 && lane == 0) {
-      // key tiles of this CTA's unit i (0: there is none); a unit has twice as many steps
-      auto tiles_of = [&](int i) -> int {
-        const int u = unit_number(i);
-        if (!plan_ok || u >= p.n_units) return 0;
-        const int4 e = p.plan.q_order[u / p.hq];
-        return e.z - e.y;
-      };
-      bool ok = true;
-      int t = 0, l0 = 0;  // step, the unit's first load; step j of a unit of n tiles works on load l0 + (j < n ? j : j - min(2, n))
-      int n = tiles_of(0), n_next;
+      bool ok = plan_ok;
       if (warp == 3) {
         const uint32_t id = idesc_bf16(128, 64 * nd, 0, 1);
         const uint64_t dk0 = mnmajor_desc(smem_u32(skv), 0);
         int used[2] = {0, 0};  // dS in each buffer so far
-        for (int i = 0; ok && n > 0; ++i, n = n_next) {
-          n_next = tiles_of(i + 1);
-          const int kept = min(2, n);
-          t += n;
-          for (int j = n; j < 2 * n; ++j, ++t) {
-            const int b = t & 1, s = (l0 + j - kept) & 1;
-            // the step's K has come: its S has read it
+        for (int i = 0; ok && e.z > e.y; ++i) {
+          const int n = e.z - e.y;
+          e = entry(i + 1);
+          for (int k = 0; k < n; ++k) {
+            const int b = (i + n - 1 + k) & 1;
+            // the step's K has come (its S has read it), and the first dS is written when dP has been read in dQ's place
             ok = mbar_wait_soon(&ds_full[b], (b ? used[1]++ : used[0]++) & 1, abort_flag, p.err, DEV_TIMEOUT_MMA);
             if (!ok) break;
             tc_fence_after();
-            mma_tm<8, 32>(tmem, tmem + 128 + 128 * b, dk0 + s * (4 * kChunk >> 4), id, j > n);
+            mma_tm<8, 32>(tmem, tmem + 128 + 128 * b, dk0 + b * (4 * kChunk >> 4), id, k > 0);
             umma_commit(&ds_done[b]);
-            umma_commit(&kv_empty[s]);
-            mbar_arrive(&kv_empty[s]);
+            umma_commit(&kv_empty[b]);
+            mbar_arrive(&kv_empty[b]);
           }
           if (ok) umma_commit(dq_done);
-          l0 += 2 * n - kept;
         }
       } else {
-        // warp 1: S of step t into buffer t & 1; warp 2: dP of step t
+        // warp 1: S, warp 2: dP of every step
         const bool is_s = warp == 1;
         const uint32_t id = idesc_bf16(128, 128, 0, 0);
         const uint64_t a0 = kmajor_desc(smem_u32(sq), 0) + (is_s ? 0 : 2 * kChunk >> 4),
                        b0 = kmajor_desc(smem_u32(skv), 0) + (is_s ? 0 : 2 * kChunk >> 4);
-        int used[2] = {0, 0};
-        bool held[2] = {false, false};  // the buffer's last S has become a dS
-        for (int i = 0; ok && n > 0; ++i, n = n_next) {
-          n_next = tiles_of(i + 1);
-          const int kept = min(2, n);
+        int used[2] = {0, 0};            // steps of each number
+        int read[2] = {0, 0}, done[2] = {0, 0};  // S of each buffer that were read once, that became a dS
+        bool held[2] = {false, false};   // the buffer's last S becomes a dS
+        int n_dp = 0;                    // dP in its place
+        for (int i = 0; ok && e.z > e.y; ++i) {
+          const int n = e.z - e.y, kept = min(2, n), steps = 2 * n - kept;
+          e = entry(i + 1);
           ok = mbar_wait_soon(q_full, i & 1, abort_flag, p.err, DEV_TIMEOUT_MMA);
-          for (int j = 0; ok && j < 2 * n; ++j, ++t) {
-            const int l = l0 + (j < n ? j : j - kept), s = l & 1, b = t & 1;
-            ok = mbar_wait_soon(&kv_full[s], (l >> 1) & 1, abort_flag, p.err, DEV_TIMEOUT_MMA);
+          for (int m = 0; ok && m < steps; ++m) {
+            const int b = (i + m + (m >= n)) & 1;
+            const bool once = m < n - kept, in_dq = n > 1 && m == n - 1;
+            const int u = b ? used[1]++ : used[0]++;
+            ok = mbar_wait_soon(&kv_full[b], u & 1, abort_flag, p.err, DEV_TIMEOUT_MMA);
             if (ok && is_s) {
-              if (t >= 2) ok = mbar_wait_soon(&s_read[b], ((t >> 1) - 1) & 1, abort_flag, p.err, DEV_TIMEOUT_MMA);
-              if (ok && (b ? held[1] : held[0]))
-                ok = mbar_wait_soon(&ds_done[b], (b ? used[1]++ : used[0]++) & 1, abort_flag, p.err, DEV_TIMEOUT_MMA);
-              (b ? held[1] : held[0]) = j >= n;
-            } else if (ok && t > 0) {
-              ok = mbar_wait_soon(dp_read, (t - 1) & 1, abort_flag, p.err, DEV_TIMEOUT_MMA);
+              if (u > 0) {
+                const bool ds = b ? held[1] : held[0];
+                int& c = ds ? (b ? done[1] : done[0]) : (b ? read[1] : read[0]);
+                ok = mbar_wait_soon(ds ? &ds_done[b] : &s_read[b], c++ & 1, abort_flag, p.err, DEV_TIMEOUT_MMA);
+              }
+              (b ? held[1] : held[0]) = !once;
+            } else if (ok && in_dq) {
+              if (i > 0) ok = mbar_wait_soon(dq_read, (i - 1) & 1, abort_flag, p.err, DEV_TIMEOUT_MMA);
+            } else if (ok) {
+              if (n_dp > 0) ok = mbar_wait_soon(dp_read, (n_dp - 1) & 1, abort_flag, p.err, DEV_TIMEOUT_MMA);
+              ++n_dp;
             }
             if (!ok) break;
             tc_fence_after();
-            mma_kk_nd(nd, is_s ? tmem + 128 + 128 * b : tmem + 384, a0, b0 + s * (4 * kChunk >> 4), id);
-            umma_commit(is_s ? &s_full[b] : dp_full);
-            if (j < n - kept) umma_commit(&kv_empty[s]);  // the last two tiles stay for the second pass
-            if (j == 2 * n - 1) umma_commit(q_empty);
+            mma_kk_nd(nd, is_s ? tmem + 128 + 128 * b : (in_dq ? tmem : tmem + 384), a0, b0 + b * (4 * kChunk >> 4), id);
+            umma_commit(is_s ? &s_full[b] : &dp_full[in_dq]);
+            if (once) umma_commit(&kv_empty[b]);
+            if (m == steps - 1) umma_commit(q_empty);
           }
-          l0 += 2 * n - kept;
         }
       }
       umma_commit(&drain[warp - 1]);
@@ -1111,110 +1120,122 @@ __global__ void __launch_bounds__(kBwdThreads, 1) masked_dq_kernel(const __grid_
     const int quarter = warp & 3, cq = (warp - 4) >> 2;  // rows (TMEM lanes); 32 of the 128 key columns
     const int r = quarter * 32 + lane;
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
-    const uint32_t s_tm = tmem + lane_off + 128 + 32 * cq, dp_tm = tmem + lane_off + 384 + 32 * cq;
-    U w, nx;
-    bool ok = plan_ok, live = plan_ok && unit(0, nx);
-    int t = 0;
+    const uint32_t dq_tm = tmem + lane_off + 32 * cq, s_tm = dq_tm + 128, dp_tm = dq_tm + 384;
+    bool ok = plan_ok, live = plan_ok && e.z > e.y;
+    uint32_t phases = 0;  // of s_full (bits 0, 1) and dp_full (2, 3), turned with each wait
     int nlo = 0, nhi = 0;
     float nlse = 0.f;
     const int64_t T = (int64_t)p.n_seq * p.S;
-    auto rows_of = [&](const U& x) {  // what the row sees, and its lse in powers of two
-      const int q = x.qt * kTile + r;
-      const int64_t row = (int64_t)x.b * p.S + q;
+    auto rows_of = [&](int i) {  // what the row of unit i (entry e) sees, and its lse in powers of two
+      const int q = e.x % n_qt * kTile + r, row = e.x / n_qt * p.S + q;
       const bool in = q < p.S;
       nlo = in ? p.plan.lo[row] : 0;
       nhi = in ? p.plan.hi[row] : 0;
-      nlse = in ? p.lse[(int64_t)x.h * T + row] * kLog2e : 0.f;
+      nlse = in ? p.lse[(int64_t)(unit_number(i) % p.hq) * T + row] * kLog2e : 0.f;
     };
-    if (live) rows_of(nx);
+    if (live) rows_of(0);
     for (int i = 0; ok && live; ++i) {
-      w = nx;
-      const int lo = nlo, hi = nhi, qt0 = w.qt * kTile, h = w.h, b = w.b;
+      const int lo = nlo, hi = nhi, qt0 = e.x % n_qt * kTile, first = e.x / n_qt * p.S + qt0, h = unit_number(i) % p.hq;
+      const int j0 = e.y, j1 = e.z;
       const float nl = lo < hi ? -nlse : -INFINITY;  // a row that sees nothing: P = 0 whatever its score
-      live = unit(i + 1, nx);
+      e = entry(i + 1);
       const float slope = BIAS ? p.slopes[h] * kLog2e : 0.f;
       // a row that sees one key: P = 1 and D = dP to the bit, so that its dS is 0 and not a rounding's rest
       const bool single = hi - lo == 1;
       const bool singles = __any_sync(0xffffffffu, single);
-      float sum = 0.f;
-      for (int pass = 0; pass < 2 && ok; ++pass) {
-        const float nD = pass ? -sum : 0.f;
-        f2 acc[2] = {0, 0};
-        float only = 0.f;
-        const int n = w.j1 - w.j0, kept = min(2, n);
-        for (int k = 0; k < n; ++k, ++t) {
-          // the second pass: the last two tiles, then back from the one before them
-          const int j = w.j0 + (pass == 0 ? k : k < kept ? n - kept + k : n - 1 - k);
-          ok = __all_sync(0xffffffffu, mbar_wait_soon(&s_full[t & 1], (t >> 1) & 1, abort_flag, p.err, DEV_TIMEOUT_EPILOGUE) &&
-                                           mbar_wait_soon(dp_full, t & 1, abort_flag, p.err, DEV_TIMEOUT_EPILOGUE));
-          if (!ok) break;
+      const int n = j1 - j0, kept = min(2, n);
+      // S and dP of a step in registers; fresh: they have to be waited for
+      uint32_t s[32], dp[32];
+      auto take = [&](int bf, bool in_dq, bool fresh) {
+        if (fresh) {
+          ok = __all_sync(0xffffffffu, mbar_wait_soon(&s_full[bf], (phases >> bf) & 1, abort_flag, p.err, DEV_TIMEOUT_EPILOGUE) &&
+                                           mbar_wait_soon(&dp_full[in_dq], (phases >> (2 + in_dq)) & 1, abort_flag, p.err,
+                                                          DEV_TIMEOUT_EPILOGUE));
+          if (!ok) return;
+          phases ^= 1u << bf | 4u << in_dq;
           tc_fence_after();
-          uint32_t s[32], dp[32];
-          tmem_ld32(s_tm + 128 * (t & 1), s);
-          tmem_ld32(dp_tm, dp);
-          tmem_ld_wait_regs(s);
-          regs_after_wait(dp);
-          tc_fence_before();
-          warp_arrive(dp_read, lane);
-          if (lane == 0) mbar_arrive(&s_read[t & 1]);
-          const int k0 = j * kTile + 32 * cq;  // key of this thread's first column
-          const bool part = __any_sync(0xffffffffu, lo > k0 || hi < k0 + 32);
+        }
+        tmem_ld32(s_tm + 128 * bf, s);
+        tmem_ld32(in_dq ? dq_tm : dp_tm, dp);
+        tmem_ld_wait_regs(s);
+        regs_after_wait(dp);
+        tc_fence_before();
+        __syncwarp();
+      };
+      f2 acc[2] = {0, 0};
+      float only = 0.f;
+#pragma unroll 1
+      for (int k = 0; k < n; ++k) {
+        const int bf = (i + k) & 1;
+        take(bf, n > 1 && k == n - 1, true);
+        if (!ok) break;
+        if (lane == 0 && k < n - kept) {
+          mbar_arrive(dp_read);
+          mbar_arrive(&s_read[bf]);
+        }
+        const int k0 = (j0 + k) * kTile + 32 * cq;  // key of this thread's first column
+        if (CAP) tanh_n(s, p.cap_mul);
+        if (BIAS) bias32(s, p.mul, slope, (float)(qt0 + r - k0), qt0 + 32 * quarter >= k0 + 31);
+        if (__any_sync(0xffffffffu, lo > k0 || hi < k0 + 32)) {
           const uint32_t see = see_bits(lo - k0, hi - k0);
-          const int side = qt0 + 32 * quarter >= k0 + 31;
-          if (pass == 0) {
-            if (CAP) tanh_n(s, p.cap_mul);
-            if (BIAS) bias32(s, p.mul, slope, (float)(qt0 + r - k0), side);
-            if (part) {
-              mask32(s, see);
-              if (singles) {
+          mask32(s, see);
+          if (singles) {
 #pragma unroll
-                for (int e = 0; e < 32; ++e)
-                  if (see & (1u << e)) only = __uint_as_float(dp[e]);
-              }
-            }
-            const f2 m = both(BIAS ? 1.f : p.mul), l2 = both(nl);
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              float x0, x1;
-              un(fma2(pku(s[e], s[e + 1]), m, l2), x0, x1);
-              acc[(e >> 1) & 1] = fma2(pk(ex2(x0), ex2(x1)), pku(dp[e], dp[e + 1]), acc[(e >> 1) & 1]);
-            }
-          } else {
-            uint32_t pw[16], dw[16];
-            grad32<CAP, BIAS, true, false>(s, dp, p.mul, p.cap_mul, slope, (float)(qt0 + r - k0), side, part, see, nl, nD,
-                                           nullptr, nullptr, pw, dw);
-            tmem_st16(s_tm + 128 * (t & 1), dw);  // over the scores that this warp itself has read
-            tmem_st_wait();
-            tc_fence_before();
-            warp_arrive(&ds_full[t & 1], lane);
+            for (int e = 0; e < 32; ++e)
+              if (see & (1u << e)) only = __uint_as_float(dp[e]);
           }
         }
-        if (pass == 0) {
-          float a0, a1;
-          un(add2(acc[0], acc[1]), a0, a1);
-          s_part[cq * 128 + r] = single ? only : a0 + a1;
-          ok = bar_and_compute(ok);
-          sum = (s_part[r] + s_part[128 + r]) + (s_part[256 + r] + s_part[384 + r]);
-          if (ok && cq == 0 && qt0 + r < p.S) p.delta[(int64_t)h * T + (int64_t)b * p.S + qt0 + r] = sum;
-        } else {
-          if (ok && live) rows_of(nx);
-          if (ok) ok = __all_sync(0xffffffffu, mbar_wait_soon(dq_done, i & 1, abort_flag, p.err, DEV_TIMEOUT_EPILOGUE));
-          ok = bar_and_compute(ok);  // also: s_part is free for the next unit
+        const f2 m = both(BIAS ? 1.f : p.mul), l2 = both(nl);
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+          float x0, x1;
+          un(fma2(pku(s[e], s[e + 1]), m, l2), x0, x1);
+          acc[(e >> 1) & 1] = fma2(pk(ex2(x0), ex2(x1)), pku(dp[e], dp[e + 1]), acc[(e >> 1) & 1]);
         }
       }
+      float a0, a1;
+      un(add2(acc[0], acc[1]), a0, a1);
+      s_part[cq * 128 + r] = single ? only : a0 + a1;
+      ok = bar_and_compute(ok);
+      const float sum = (s_part[r] + s_part[128 + r]) + (s_part[256 + r] + s_part[384 + r]);
+      if (ok && cq == 0 && qt0 + r < p.S) p.delta[(int64_t)h * T + first + r] = sum;
+#pragma unroll 1
+      for (int k = 0; ok && k < n; ++k) {
+        const int bf = (i + n - 1 + k) & 1;
+        const bool in_dq = n > 1 && k == 0;
+        take(bf, in_dq, k >= kept);
+        if (!ok) break;
+        if (lane == 0 && !in_dq) mbar_arrive(dp_read);
+        const int k0 = (j1 - 1 - k) * kTile + 32 * cq;
+        const bool part = __any_sync(0xffffffffu, lo > k0 || hi < k0 + 32);
+        uint32_t pw[16], dw[16];
+        grad32<CAP, BIAS, true, false>(s, dp, p.mul, p.cap_mul, slope, (float)(qt0 + r - k0), qt0 + 32 * quarter >= k0 + 31,
+                                       part, see_bits(lo - k0, hi - k0), nl, -sum, nullptr, nullptr, pw, dw);
+        tmem_st16(s_tm + 128 * bf, dw);  // over the scores that this warp itself has read
+        tmem_st_wait();
+        tc_fence_before();
+        warp_arrive(&ds_full[bf], lane);
+      }
+      live = e.z > e.y;
+      if (ok && live) rows_of(i + 1);
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait_soon(dq_done, i & 1, abort_flag, p.err, DEV_TIMEOUT_EPILOGUE));
+      ok = bar_and_compute(ok);  // also: s_part is free for the next unit
       if (!ok) break;
       tc_fence_after();
-      const int64_t row0 = (int64_t)b * p.S + qt0 + 32 * quarter;
+      const int64_t row0 = first + 32 * quarter;
       const int n_rows = p.S - qt0 - 32 * quarter;
       if (cq < 2 * nd) {
         uint32_t v[32], pk16[16];
-        tmem_ld32(tmem + lane_off + 32 * cq, v);
+        tmem_ld32(dq_tm, v);
         tmem_ld_wait_regs(v);
+        tc_fence_before();
+        warp_arrive(dq_read, lane);
 #pragma unroll
         for (int e = 0; e < 32; e += 2) pk16[e / 2] = pack2(__uint_as_float(v[e]) * p.scale, __uint_as_float(v[e + 1]) * p.scale);
         store_rows32(p.dq + row0 * p.lddq + (int64_t)h * p.hd + 32 * cq, p.lddq, pk16, n_rows, p.hd - 32 * cq);
+      } else {
+        warp_arrive(dq_read, lane);
       }
-      tc_fence_before();
     }
   }
   tc_fence_before();
