@@ -938,27 +938,27 @@ __device__ __forceinline__ void grad32(uint32_t (&s)[32], uint32_t (&dp)[32], fl
 // the last key tile to the first, for dQ. S, dP and K of the last two tiles are kept, so the second pass forms
 // them again only from the third on (documents of up to 256 keys: once). Warp 0 loads; warps 1, 2 and 3 issue
 // S = Q K^T, dP = dO V^T and dQ += dS K, S and dP ahead of the compute warps. Warps 4-19 hold a query row and 32 of
-// the 128 key columns per thread. A step has a stage of K and V and a buffer of S (dS takes the place of its S), both of the
-// same number: with n key tiles in unit i, step m < n of the first pass has number (i + m) & 1, the k-th of the second
-// pass (kept or formed again) (i + n - 1 + k) & 1. TMEM: S / dS at 128 and 256, dP at 384; that of the last tile (of two
-// or more) at 0, where dQ is added up once it has been read.
+// the 128 key columns per thread. With n key tiles in unit i, step m < n of the first pass has S in buffer (i + m) & 1, the
+// k-th of the second pass (kept or formed again) in buffer (i + n - 1 + k) & 1, where dS takes its place. TMEM: S / dS at
+// 128 and 256, dP at 384; that of the last tile (of two or more) at 0, where dQ is added up once it has been read. K has
+// three stages, since it stays until dS K is done, V two.
 //
 // Measured (32 query, 8 key/value heads of 128): 4096 causal tokens 349 us (five products of a tile pair, 1015 TFLOP/s),
 // capped documents 318 us, 8 x 512 tokens 69 us. The products read both operands of S and dP from shared memory, at
 // its full rate, so the tensor pipe cannot be busy more than 3/4 of the time; it is for half of it.
 template <bool CAP, bool BIAS>
 __global__ void __launch_bounds__(kBwdThreads, 1) masked_dq_kernel(const __grid_constant__ MaskedBwdParams p) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem_dq[];
   const int nd = p.nd;
-  uint8_t* sq = smem;                       // Q, then dO: 2 chunks each
-  uint8_t* skv = smem + 4 * kChunk;         // stage s: K (2 chunks), then V
-  float* s_part = reinterpret_cast<float*>(smem + 12 * kChunk);  // [4][128]: the quarters' sums of D
+  uint8_t* sq = smem_dq;                    // Q, then dO: 2 chunks each
+  uint8_t* sk = smem_dq + 4 * kChunk;       // [3] stages of K
+  uint8_t* sv = smem_dq + 10 * kChunk;      // [2] stages of V
+  float* s_part = reinterpret_cast<float*>(smem_dq + 14 * kChunk);  // [4][128]: the quarters' sums of D
   uint64_t* bars = reinterpret_cast<uint64_t*>(s_part + 512);
   uint64_t* q_full = bars;
   uint64_t* q_empty = bars + 1;
-  uint64_t* kv_full = bars + 2;    // [2]
-  uint64_t* kv_empty = bars + 4;   // [2]
+  uint64_t* v_full = bars + 2;     // [2]
+  uint64_t* v_empty = bars + 4;    // [2]
   uint64_t* s_full = bars + 6;     // [2] by buffer
   uint64_t* s_read = bars + 8;     // [2]: S is in registers and not kept
   uint64_t* ds_full = bars + 10;   // [2]: dS in the buffer
@@ -968,7 +968,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1) masked_dq_kernel(const __grid_
   uint64_t* dq_done = bars + 17;   // a unit's dQ
   uint64_t* dq_read = bars + 18;   // dQ's place is free
   uint64_t* drain = bars + 19;     // [3]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 22);
+  uint64_t* k_full = bars + 22;    // [3]
+  uint64_t* k_empty = bars + 25;   // [3]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 28);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -982,8 +984,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) masked_dq_kernel(const __grid_
     mbar_init(q_full, 1);
     mbar_init(q_empty, 2);  // S, dP
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&kv_full[s], 1);
-      mbar_init(&kv_empty[s], 2);  // S and dP of the first pass, or dQ (which arrives twice)
+      mbar_init(&v_full[s], 1);
+      mbar_init(&v_empty[s], 1);
       mbar_init(&s_full[s], 1);
       mbar_init(&s_read[s], 16);
       mbar_init(&ds_full[s], 16);
@@ -993,7 +995,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1) masked_dq_kernel(const __grid_
     mbar_init(dp_read, 16);
     mbar_init(dq_done, 1);
     mbar_init(dq_read, 16);
-    for (int s = 0; s < 3; ++s) mbar_init(&drain[s], 1);
+    for (int s = 0; s < 3; ++s) {
+      mbar_init(&drain[s], 1);
+      mbar_init(&k_full[s], 1);
+      mbar_init(&k_empty[s], 1);  // S of the first pass, or dQ
+    }
     *abort_flag = 0;
     fence_barrier_init();
     tma_prefetch_desc(&p.qmap);
@@ -1018,7 +1024,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) masked_dq_kernel(const __grid_
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == 0 && lane == 0) {
       bool ok = plan_ok;
-      int n_q = 0, used[2] = {0, 0};  // query tiles loaded, loads of each stage
+      int n_q = 0, n_k = 0, n_v = 0;  // query tiles, K, V loaded
       for (int i = 0; ok && e.z > e.y; ++i) {
         const int qt0 = e.x % n_qt * kTile, b = e.x / n_qt, h = unit_number(i) % p.hq, j0 = e.y, j1 = e.z;
         e = entry(i + 1);
@@ -1031,29 +1037,31 @@ __global__ void __launch_bounds__(kBwdThreads, 1) masked_dq_kernel(const __grid_
         ++n_q;
         const int n = j1 - j0, steps = 2 * n - min(2, n), g = h / hpg;
         for (int m = 0; m < steps; ++m) {
-          const int s = (i + m + (m >= n)) & 1, j = m < n ? j0 + m : j1 - 3 - (m - n);
-          ok = mbar_wait_soon(&kv_empty[s], ((s ? used[1]++ : used[0]++) & 1) ^ 1, abort_flag, p.err, DEV_TIMEOUT_PRODUCER);
-          if (!ok) {
-            --(s ? used[1] : used[0]);
-            break;
-          }
-          mbar_arrive_expect_tx(&kv_full[s], 2 * nd * kChunk);
-          uint8_t* st = skv + s * 4 * kChunk;
-          for (int c = 0; c < nd; ++c) {
-            tma_load_4d(st + c * kChunk, &p.kmap, &kv_full[s], 64 * c, g, j * kTile, b);
-            tma_load_4d(st + (2 + c) * kChunk, &p.vmap, &kv_full[s], 64 * c, g, j * kTile, b);
-          }
+          const int j = m < n ? j0 + m : j1 - 3 - (m - n), sk_ = n_k % 3, sv_ = n_v & 1;
+          ok = mbar_wait_soon(&k_empty[sk_], ((n_k / 3) & 1) ^ 1, abort_flag, p.err, DEV_TIMEOUT_PRODUCER);
+          if (!ok) break;
+          mbar_arrive_expect_tx(&k_full[sk_], nd * kChunk);
+          for (int c = 0; c < nd; ++c)
+            tma_load_4d(sk + (2 * sk_ + c) * kChunk, &p.kmap, &k_full[sk_], 64 * c, g, j * kTile, b);
+          ++n_k;
+          ok = mbar_wait_soon(&v_empty[sv_], ((n_v >> 1) & 1) ^ 1, abort_flag, p.err, DEV_TIMEOUT_PRODUCER);
+          if (!ok) break;
+          mbar_arrive_expect_tx(&v_full[sv_], nd * kChunk);
+          for (int c = 0; c < nd; ++c)
+            tma_load_4d(sv + (2 * sv_ + c) * kChunk, &p.vmap, &v_full[sv_], 64 * c, g, j * kTile, b);
+          ++n_v;
         }
       }
       // every copy lands before the CTA may exit
       if (n_q) mbar_wait(q_full, (n_q - 1) & 1, nullptr, p.err, DEV_TIMEOUT_DRAIN);
-      if (used[0]) mbar_wait(&kv_full[0], (used[0] - 1) & 1, nullptr, p.err, DEV_TIMEOUT_DRAIN);
-      if (used[1]) mbar_wait(&kv_full[1], (used[1] - 1) & 1, nullptr, p.err, DEV_TIMEOUT_DRAIN);
+      for (int l = max(0, n_k - 3); l < n_k; ++l) mbar_wait(&k_full[l % 3], (l / 3) & 1, nullptr, p.err, DEV_TIMEOUT_DRAIN);
+      for (int l = max(0, n_v - 2); l < n_v; ++l) mbar_wait(&v_full[l & 1], (l >> 1) & 1, nullptr, p.err, DEV_TIMEOUT_DRAIN);
     } else if (warp > 0 && lane == 0) {
       bool ok = plan_ok;
       if (warp == 3) {
         const uint32_t id = idesc_bf16(128, 64 * nd, 0, 1);
-        const uint64_t dk0 = mnmajor_desc(smem_u32(skv), 0);
+        const uint64_t dk0 = mnmajor_desc(smem_u32(sk), 0);
+        int l0 = 0;            // the unit's first load
         int used[2] = {0, 0};  // dS in each buffer so far
         for (int i = 0; ok && e.z > e.y; ++i) {
           const int n = e.z - e.y;
@@ -1064,20 +1072,22 @@ __global__ void __launch_bounds__(kBwdThreads, 1) masked_dq_kernel(const __grid_
             ok = mbar_wait_soon(&ds_full[b], (b ? used[1]++ : used[0]++) & 1, abort_flag, p.err, DEV_TIMEOUT_MMA);
             if (!ok) break;
             tc_fence_after();
-            mma_tm<8, 32>(tmem, tmem + 128 + 128 * b, dk0 + b * (4 * kChunk >> 4), id, k > 0);
+            const int s = (l0 + (k < min(2, n) ? n - 1 - k : n - 2 + k)) % 3;
+            mma_tm<8, 32>(tmem, tmem + 128 + 128 * b, dk0 + s * (2 * kChunk >> 4), id, k > 0);
             umma_commit(&ds_done[b]);
-            umma_commit(&kv_empty[b]);
-            mbar_arrive(&kv_empty[b]);
+            umma_commit(&k_empty[s]);
           }
           if (ok) umma_commit(dq_done);
+          l0 += 2 * n - min(2, n);
         }
       } else {
         // warp 1: S, warp 2: dP of every step
         const bool is_s = warp == 1;
         const uint32_t id = idesc_bf16(128, 128, 0, 0);
         const uint64_t a0 = kmajor_desc(smem_u32(sq), 0) + (is_s ? 0 : 2 * kChunk >> 4),
-                       b0 = kmajor_desc(smem_u32(skv), 0) + (is_s ? 0 : 2 * kChunk >> 4);
-        int used[2] = {0, 0};            // steps of each number
+                       b0 = kmajor_desc(smem_u32(is_s ? sk : sv), 0);
+        int l = 0;                       // steps so far
+        int used[2] = {0, 0};            // of each number
         int read[2] = {0, 0}, done[2] = {0, 0};  // S of each buffer that were read once, that became a dS
         bool held[2] = {false, false};   // the buffer's last S becomes a dS
         int n_dp = 0;                    // dP in its place
@@ -1085,11 +1095,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1) masked_dq_kernel(const __grid_
           const int n = e.z - e.y, kept = min(2, n), steps = 2 * n - kept;
           e = entry(i + 1);
           ok = mbar_wait_soon(q_full, i & 1, abort_flag, p.err, DEV_TIMEOUT_MMA);
-          for (int m = 0; ok && m < steps; ++m) {
+          for (int m = 0; ok && m < steps; ++m, ++l) {
             const int b = (i + m + (m >= n)) & 1;
             const bool once = m < n - kept, in_dq = n > 1 && m == n - 1;
-            const int u = b ? used[1]++ : used[0]++;
-            ok = mbar_wait_soon(&kv_full[b], u & 1, abort_flag, p.err, DEV_TIMEOUT_MMA);
+            const int u = b ? used[1]++ : used[0]++, s = is_s ? l % 3 : l & 1;
+            ok = mbar_wait_soon(is_s ? &k_full[s] : &v_full[s], (is_s ? l / 3 : l >> 1) & 1, abort_flag, p.err, DEV_TIMEOUT_MMA);
             if (ok && is_s) {
               if (u > 0) {
                 const bool ds = b ? held[1] : held[0];
@@ -1105,9 +1115,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1) masked_dq_kernel(const __grid_
             }
             if (!ok) break;
             tc_fence_after();
-            mma_kk_nd(nd, is_s ? tmem + 128 + 128 * b : (in_dq ? tmem : tmem + 384), a0, b0 + b * (4 * kChunk >> 4), id);
+            mma_kk_nd(nd, is_s ? tmem + 128 + 128 * b : (in_dq ? tmem : tmem + 384), a0, b0 + s * (2 * kChunk >> 4), id);
             umma_commit(is_s ? &s_full[b] : &dp_full[in_dq]);
-            if (once) umma_commit(&kv_empty[b]);
+            if (!is_s) umma_commit(&v_empty[s]);
+            else if (once) umma_commit(&k_empty[s]);
             if (m == steps - 1) umma_commit(q_empty);
           }
         }
@@ -1503,7 +1514,7 @@ __global__ void __launch_bounds__(kDkvThreads<CAP>, 1) masked_dkv_kernel(const _
 // Shared memory of a launch: sized for head_dim 128 whatever the head dimension, which also keeps
 // one CTA per SM (each CTA allocates all 512 TMEM columns).
 int fwd_smem() { return 1024 + 12 * kChunk + 256; }
-int dq_smem() { return 1024 + 12 * kChunk + 2048 + 256; }
+int dq_smem() { return 14 * kChunk + 2048 + 256; }
 int dkv_smem() { return 1024 + 12 * kChunk + 4096 + 16 + 256; }
 
 // Raises a kernel's shared-memory limit once per device.
