@@ -940,8 +940,8 @@ __device__ __forceinline__ void grad32(uint32_t (&s)[32], uint32_t (&dp)[32], fl
 // S = Q K^T, dP = dO V^T and dQ += dS K, S and dP ahead of the compute warps. Warps 4-19 hold a query row and 32 of
 // the 128 key columns per thread. With n key tiles in unit i, step m < n of the first pass has S in buffer (i + m) & 1, the
 // k-th of the second pass (kept or formed again) in buffer (i + n - 1 + k) & 1, where dS takes its place. TMEM: S / dS at
-// 128 and 256, dP at 384; that of the last tile (of two or more) at 0, where dQ is added up once it has been read. K has
-// three stages, since it stays until dS K is done, V two.
+// 128 and 256, dP at 384 and, in the first pass, every other one at 0, the last tile's among them (of two or more):
+// dQ is added up there once that one has been read. K has three stages, since it stays until dS K is done, V two.
 //
 // Measured (32 query, 8 key/value heads of 128): 4096 causal tokens 349 us (five products of a tile pair, 1015 TFLOP/s),
 // capped documents 318 us, 8 x 512 tokens 69 us. The products read both operands of S and dP from shared memory, at
@@ -964,13 +964,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1) masked_dq_kernel(const __grid_
   uint64_t* ds_full = bars + 10;   // [2]: dS in the buffer
   uint64_t* ds_done = bars + 12;   // [2]: dQ has read it
   uint64_t* dp_full = bars + 14;   // [2]: dP in its place, in dQ's place
-  uint64_t* dp_read = bars + 16;   // dP's place is free
-  uint64_t* dq_done = bars + 17;   // a unit's dQ
-  uint64_t* dq_read = bars + 18;   // dQ's place is free
-  uint64_t* drain = bars + 19;     // [3]
-  uint64_t* k_full = bars + 22;    // [3]
-  uint64_t* k_empty = bars + 25;   // [3]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 28);
+  uint64_t* dp_read = bars + 16;   // [2]: dP is in registers and not kept
+  uint64_t* dq_done = bars + 18;   // a unit's dQ
+  uint64_t* dq_read = bars + 19;   // it is in registers
+  uint64_t* drain = bars + 20;     // [3]
+  uint64_t* k_full = bars + 23;    // [3]
+  uint64_t* k_empty = bars + 26;   // [3]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 29);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -991,8 +991,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) masked_dq_kernel(const __grid_
       mbar_init(&ds_full[s], 16);
       mbar_init(&ds_done[s], 1);
       mbar_init(&dp_full[s], 1);
+      mbar_init(&dp_read[s], 16);
     }
-    mbar_init(dp_read, 16);
     mbar_init(dq_done, 1);
     mbar_init(dq_read, 16);
     for (int s = 0; s < 3; ++s) {
@@ -1090,14 +1090,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1) masked_dq_kernel(const __grid_
         int used[2] = {0, 0};            // of each number
         int read[2] = {0, 0}, done[2] = {0, 0};  // S of each buffer that were read once, that became a dS
         bool held[2] = {false, false};   // the buffer's last S becomes a dS
-        int n_dp = 0;                    // dP in its place
+        int n_dp[2] = {0, 0};            // dP in each place that were read and not kept
         for (int i = 0; ok && e.z > e.y; ++i) {
           const int n = e.z - e.y, kept = min(2, n), steps = 2 * n - kept;
           e = entry(i + 1);
           ok = mbar_wait_soon(q_full, i & 1, abort_flag, p.err, DEV_TIMEOUT_MMA);
           for (int m = 0; ok && m < steps; ++m, ++l) {
             const int b = (i + m + (m >= n)) & 1;
-            const bool once = m < n - kept, in_dq = n > 1 && m == n - 1;
+            const bool once = m < n - kept, in_dq = n > 1 && m < n && !((n - 1 - m) & 1);
             const int u = b ? used[1]++ : used[0]++, s = is_s ? l % 3 : l & 1;
             ok = mbar_wait_soon(is_s ? &k_full[s] : &v_full[s], (is_s ? l / 3 : l >> 1) & 1, abort_flag, p.err, DEV_TIMEOUT_MMA);
             if (ok && is_s) {
@@ -1108,10 +1108,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1) masked_dq_kernel(const __grid_
               }
               (b ? held[1] : held[0]) = !once;
             } else if (ok && in_dq) {
-              if (i > 0) ok = mbar_wait_soon(dq_read, (i - 1) & 1, abort_flag, p.err, DEV_TIMEOUT_MMA);
-            } else if (ok) {
-              if (n_dp > 0) ok = mbar_wait_soon(dp_read, (n_dp - 1) & 1, abort_flag, p.err, DEV_TIMEOUT_MMA);
-              ++n_dp;
+              // behind the unit's dP two steps ago, or the last unit's dQ
+              if (m >= 2) ok = mbar_wait_soon(&dp_read[1], n_dp[1]++ & 1, abort_flag, p.err, DEV_TIMEOUT_MMA);
+              else if (i > 0) ok = mbar_wait_soon(dq_read, (i - 1) & 1, abort_flag, p.err, DEV_TIMEOUT_MMA);
+            } else if (ok && (i > 0 || m >= 2)) {
+              ok = mbar_wait_soon(&dp_read[0], n_dp[0]++ & 1, abort_flag, p.err, DEV_TIMEOUT_MMA);
             }
             if (!ok) break;
             tc_fence_after();
@@ -1121,6 +1122,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) masked_dq_kernel(const __grid_
             else if (once) umma_commit(&k_empty[s]);
             if (m == steps - 1) umma_commit(q_empty);
           }
+          // each phase of dq_read is waited for once, also where dQ's place held no dP
+          if (ok && !is_s && n == 1 && i > 0) ok = mbar_wait_soon(dq_read, (i - 1) & 1, abort_flag, p.err, DEV_TIMEOUT_MMA);
         }
       }
       umma_commit(&drain[warp - 1]);
@@ -1178,10 +1181,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1) masked_dq_kernel(const __grid_
 #pragma unroll 1
       for (int k = 0; k < n; ++k) {
         const int bf = (i + k) & 1;
-        take(bf, n > 1 && k == n - 1, true);
+        const bool in_dq = n > 1 && !((n - 1 - k) & 1);
+        take(bf, in_dq, true);
         if (!ok) break;
         if (lane == 0 && k < n - kept) {
-          mbar_arrive(dp_read);
+          mbar_arrive(&dp_read[in_dq]);
           mbar_arrive(&s_read[bf]);
         }
         const int k0 = (j0 + k) * kTile + 32 * cq;  // key of this thread's first column
@@ -1216,7 +1220,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) masked_dq_kernel(const __grid_
         const bool in_dq = n > 1 && k == 0;
         take(bf, in_dq, k >= kept);
         if (!ok) break;
-        if (lane == 0 && !in_dq) mbar_arrive(dp_read);
+        if (lane == 0 && !in_dq) mbar_arrive(&dp_read[0]);
         const int k0 = (j1 - 1 - k) * kTile + 32 * cq;
         const bool part = __any_sync(0xffffffffu, lo > k0 || hi < k0 + 32);
         uint32_t pw[16], dw[16];
