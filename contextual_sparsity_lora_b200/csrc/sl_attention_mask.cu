@@ -460,6 +460,7 @@ struct MaskedFwdParams {
 
 struct MaskedBwdParams {
   CUtensorMap qmap, kmap, vmap, domap;  // boxes as in the forward
+  CUtensorMap qmap64, domap64;          // of half the rows
   Plan plan;
   const float* slopes;
   const float* lse;              // [hq][T]
@@ -1282,7 +1283,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) masked_dq_kernel(const __grid_
 }
 
 // dk, dv: one CTA per (key tile, key/value head) in the plan's order, over (query head of the group, query tile). K and V
-// stay, Q and dO stream through two stages. A step is half a query tile (64 queries): S^T = K Q^T and dP^T = V dO^T of
+// stay, Q and dO stream through five stages of half a query tile. A step is half a query tile (64 queries): S^T = K Q^T and dP^T = V dO^T of
 // step t + 1 run while the compute warps work on step t; P^T and dS^T replace them in TMEM (bf16, first
 // operands of dV += P^T dO and dK += dS^T Q). Warp 0 loads, the query rows' lse, D and intervals too; warps 1, 2 and 3 issue
 // S^T, dP^T, and dV and dK (a thread that issues also waits and commits, and meanwhile the tensor cores, which queue
@@ -1291,29 +1292,30 @@ __global__ void __launch_bounds__(kBwdThreads, 1) masked_dq_kernel(const __grid_
 // 16 warps, or 8 where a cap's tanh needs the registers (with 16 it spills: 335 against 318 us at 4096 capped
 // tokens, 300 since; without a cap 16 gain 10%). TMEM: S^T of buffer x at 64 x, dP^T at 128 + 64 x, dV at 256, dK at
 // 384. Measured besides: 8 x 512 tokens 62 us; 4096 causal tokens are 1023 TFLOP/s of four products per tile pair.
+constexpr int kQdStages = 5;
+
 template <bool CAP, bool BIAS>
 __global__ void __launch_bounds__(kDkvThreads<CAP>, 1) masked_dkv_kernel(const __grid_constant__ MaskedBwdParams p) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem_dkv[];
   const int nd = p.nd;
   constexpr int kWarps = (kDkvThreads<CAP> - 128) / 32, kCols = kWarps == 16 ? 1 : 2;  // 32-column pieces per thread and step
-  uint8_t* sk = smem;                       // K, then V: 2 chunks each
-  uint8_t* sqd = smem + 4 * kChunk;         // stage s: Q (2 chunks), then dO
-  float* s_lse = reinterpret_cast<float*>(smem + 12 * kChunk);  // [2][128]: -lse in powers of two
-  float* s_del = s_lse + 256;                                   // [2][128]: -D
-  int2* s_see = reinterpret_cast<int2*>(s_del + 256);           // [2][128]: keys that the query sees
-  int* s_whole = reinterpret_cast<int*>(s_see + 256);           // [2]: all of the tile's queries see all of the key tile
+  uint8_t* sk = smem_dkv;                   // K, then V: 2 chunks each
+  uint8_t* sqd = smem_dkv + 4 * kChunk;     // stage s of half a query tile: Q (2 half chunks), then dO
+  float* s_lse = reinterpret_cast<float*>(smem_dkv + 14 * kChunk);  // [2][64]: -lse in powers of two
+  float* s_del = s_lse + 128;                                       // [2][64]: -D
+  int2* s_see = reinterpret_cast<int2*>(s_del + 128);               // [2][64]: keys that the query sees
+  int* s_whole = reinterpret_cast<int*>(s_see + 128);               // [2]: all of the tile's queries see all of the key tile
   uint64_t* bars = reinterpret_cast<uint64_t*>(s_whole + 4);
   uint64_t* kv_full = bars;
-  uint64_t* qd_full = bars + 1;     // [2] by stage
-  uint64_t* qd_empty = bars + 3;    // [2]
-  uint64_t* rows_full = bars + 5;   // [2]
-  uint64_t* rows_empty = bars + 7;  // [2]
-  uint64_t* sd_full = bars + 9;     // [2] by buffer
-  uint64_t* pd_full = bars + 11;    // [2]
-  uint64_t* pd_done = bars + 13;    // [2]
-  uint64_t* drain = bars + 15;      // [3]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 18);
+  uint64_t* qd_full = bars + 1;     // [5] by stage
+  uint64_t* qd_empty = bars + 6;    // [5]
+  uint64_t* rows_full = bars + 11;  // [2] by half
+  uint64_t* rows_empty = bars + 13; // [2]
+  uint64_t* sd_full = bars + 15;    // [2] by buffer = half
+  uint64_t* pd_full = bars + 17;    // [2]
+  uint64_t* pd_done = bars + 19;    // [2]
+  uint64_t* drain = bars + 21;      // [3]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 24);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1323,11 +1325,13 @@ __global__ void __launch_bounds__(kDkvThreads<CAP>, 1) masked_dkv_kernel(const _
   const int64_t T = (int64_t)p.n_seq * p.S;
   if (threadIdx.x == 0) {
     mbar_init(kv_full, 1);
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < kQdStages; ++s) {
       mbar_init(&qd_full[s], 1);
       mbar_init(&qd_empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
       mbar_init(&rows_full[s], 1);
-      mbar_init(&rows_empty[s], kWarps);
+      mbar_init(&rows_empty[s], kWarps / 2);
       mbar_init(&sd_full[s], 2);  // S^T, dP^T
       mbar_init(&pd_full[s], kWarps / 2);
       mbar_init(&pd_done[s], 1);
@@ -1335,10 +1339,10 @@ __global__ void __launch_bounds__(kDkvThreads<CAP>, 1) masked_dkv_kernel(const _
     for (int s = 0; s < 3; ++s) mbar_init(&drain[s], 1);
     *abort_flag = 0;
     fence_barrier_init();
-    tma_prefetch_desc(&p.qmap);
+    tma_prefetch_desc(&p.qmap64);
     tma_prefetch_desc(&p.kmap);
     tma_prefetch_desc(&p.vmap);
-    tma_prefetch_desc(&p.domap);
+    tma_prefetch_desc(&p.domap64);
   }
   if (warp == 1) {
     tmem_alloc(tmem_slot, 512);
@@ -1371,67 +1375,74 @@ __global__ void __launch_bounds__(kDkvThreads<CAP>, 1) masked_dkv_kernel(const _
           tma_load_4d(sk + (2 + c) * kChunk, &p.vmap, kv_full, 64 * c, g, kt * kTile, b);
         }
       }
-      int it = 0;
-      for (; it < n_it; ++it) {
-        const int s = it & 1, qt = it_qtile(it);
-        // the rows' values first (they come while the stage is waited for)
-        float l[4], d[4];
-        int2 see[4];
+      // the rows' values of a half tile, read one ahead: nothing waits for them then
+      float l[2], d[2];
+      int2 see[2];
+      int4 range;
+      auto read_rows = [&](int t) {
+        const int it = t >> 1, qt = it_qtile(it), h = it_head(it);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int qp = qt * kTile + 32 * k + lane;
-          const int64_t row = (int64_t)b * p.S + qp, at = (int64_t)it_head(it) * T + row;
-          const bool in = qp < p.S;
-          see[k] = in ? make_int2(p.plan.lo[row], p.plan.hi[row]) : make_int2(0, 0);
-          // a row that sees nothing or lies past the sequence: 2^-inf, P = 0 whatever its score
-          l[k] = see[k].x < see[k].y ? -p.lse[at] * kLog2e : -INFINITY;
-          d[k] = in ? -p.delta[at] : 0.f;
+        for (int k = 0; k < 2; ++k) {
+          const int qp = min(qt * kTile + 64 * (t & 1) + 32 * k + lane, p.S - 1);
+          const int64_t row = (int64_t)b * p.S + qp, at = (int64_t)h * T + row;
+          see[k] = make_int2(p.plan.lo[row], p.plan.hi[row]);
+          l[k] = p.lse[at];
+          d[k] = p.delta[at];
         }
-        const int4 r = p.plan.q_range[b * n_t + qt];
-        if (!__all_sync(0xffffffffu, mbar_wait_soon(&qd_empty[s], ((it >> 1) & 1) ^ 1, abort_flag, p.err, DEV_TIMEOUT_PRODUCER))) break;
+        range = p.plan.q_range[b * n_t + qt];
+      };
+      if (n_it > 0) read_rows(0);
+      int t = 0;  // half tiles loaded
+      for (; t < 2 * n_it; ++t) {
+        const int it = t >> 1, x = t & 1, s = t % kQdStages, first = it_qtile(it) * kTile + 64 * x;
+        if (!__all_sync(0xffffffffu, mbar_wait_soon(&qd_empty[s], ((t / kQdStages) & 1) ^ 1, abort_flag, p.err, DEV_TIMEOUT_PRODUCER))) break;
         if (lane == 0) {
-          mbar_arrive_expect_tx(&qd_full[s], 2 * nd * kChunk);
-          uint8_t* st = sqd + s * 4 * kChunk;
+          mbar_arrive_expect_tx(&qd_full[s], nd * kChunk);
+          uint8_t* st = sqd + s * 2 * kChunk;
           for (int c = 0; c < nd; ++c) {
-            tma_load_4d(st + c * kChunk, &p.qmap, &qd_full[s], 64 * c, it_head(it), qt * kTile, b);
-            tma_load_4d(st + (2 + c) * kChunk, &p.domap, &qd_full[s], 64 * c, it_head(it), qt * kTile, b);
+            tma_load_4d(st + c * (kChunk / 2), &p.qmap64, &qd_full[s], 64 * c, it_head(it), first, b);
+            tma_load_4d(st + (2 + c) * (kChunk / 2), &p.domap64, &qd_full[s], 64 * c, it_head(it), first, b);
           }
         }
         __syncwarp();
-        if (!__all_sync(0xffffffffu, mbar_wait_soon(&rows_empty[s], ((it >> 1) & 1) ^ 1, abort_flag, p.err, DEV_TIMEOUT_PRODUCER))) {
-          ++it;
+        if (!__all_sync(0xffffffffu, mbar_wait_soon(&rows_empty[x], (it & 1) ^ 1, abort_flag, p.err, DEV_TIMEOUT_PRODUCER))) {
+          ++t;
           break;
         }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          s_lse[s * 128 + 32 * k + lane] = l[k];
-          s_del[s * 128 + 32 * k + lane] = d[k];
-          s_see[s * 128 + 32 * k + lane] = see[k];
+        for (int k = 0; k < 2; ++k) {
+          // a row that sees nothing or lies past the sequence: 2^-inf, P = 0 whatever its score
+          const bool in = first + 32 * k + lane < p.S, sees = in && see[k].x < see[k].y;
+          s_lse[x * 64 + 32 * k + lane] = sees ? -l[k] * kLog2e : -INFINITY;
+          s_del[x * 64 + 32 * k + lane] = sees ? -d[k] : 0.f;
+          s_see[x * 64 + 32 * k + lane] = sees ? see[k] : make_int2(0, 0);
         }
-        if (lane == 0) s_whole[s] = r.z <= kt && kt < r.w;
+        if (lane == 0) s_whole[x] = range.z <= kt && kt < range.w;
         __syncwarp();
-        if (lane == 0) mbar_arrive(&rows_full[s]);
+        if (lane == 0) mbar_arrive(&rows_full[x]);
+        if (t + 1 < 2 * n_it) read_rows(t + 1);
       }
       // every copy lands before the CTA may exit
       if (lane == 0) {
         mbar_wait(kv_full, 0, nullptr, p.err, DEV_TIMEOUT_DRAIN);
-        for (int k = max(0, it - 2); k < it; ++k) mbar_wait(&qd_full[k & 1], (k >> 1) & 1, nullptr, p.err, DEV_TIMEOUT_DRAIN);
+        for (int k = max(0, t - kQdStages); k < t; ++k)
+          mbar_wait(&qd_full[k % kQdStages], (k / kQdStages) & 1, nullptr, p.err, DEV_TIMEOUT_DRAIN);
       }
     } else if (warp < 3 && lane == 0) {
       // warp 1: S^T = K Q^T; warp 2: dP^T = V dO^T
       const int w = warp - 1;
       const uint32_t id = idesc_bf16(128, 64, 0, 0), d0 = tmem + 128 * w;
-      const uint64_t a0 = kmajor_desc(smem_u32(sk), 0) + w * (2 * kChunk >> 4), b0 = kmajor_desc(smem_u32(sqd), 0) + w * (2 * kChunk >> 4);
+      const uint64_t a0 = kmajor_desc(smem_u32(sk), 0) + w * (2 * kChunk >> 4), b0 = kmajor_desc(smem_u32(sqd), 0) + w * (kChunk >> 4);
       bool ok = mbar_wait_soon(kv_full, 0, abort_flag, p.err, DEV_TIMEOUT_MMA);
       for (int it = 0; ok && it < n_it; ++it) {
-        ok = mbar_wait_soon(&qd_full[it & 1], (it >> 1) & 1, abort_flag, p.err, DEV_TIMEOUT_MMA);
-        const uint64_t bq = b0 + (it & 1) * (4 * kChunk >> 4);
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
+          const int t = 2 * it + x, s = t % kQdStages;
+          if (ok) ok = mbar_wait_soon(&qd_full[s], (t / kQdStages) & 1, abort_flag, p.err, DEV_TIMEOUT_MMA);
           if (ok && it > 0) ok = mbar_wait_soon(&pd_done[x], (it - 1) & 1, abort_flag, p.err, DEV_TIMEOUT_MMA);
           if (!ok) break;
           tc_fence_after();
-          mma_kk_nd(nd, d0 + 64 * x, a0, bq + x * (kChunk / 2 >> 4), id);
+          mma_kk_nd<kChunk / 2>(nd, d0 + 64 * x, a0, b0 + s * (2 * kChunk >> 4), id);
           umma_commit(&sd_full[x]);
         }
       }
@@ -1439,20 +1450,21 @@ __global__ void __launch_bounds__(kDkvThreads<CAP>, 1) masked_dkv_kernel(const _
       mbar_wait(&drain[w], 0, nullptr, p.err, DEV_TIMEOUT_DRAIN);
     } else if (warp == 3 && lane == 0) {
       const uint32_t id = idesc_bf16(128, 64 * nd, 0, 1);  // P^T, dS^T in TMEM; dO, Q MN-major
-      const uint64_t dqm0 = mnmajor_desc(smem_u32(sqd), 0);
+      const uint64_t dqm0 = smem_desc_sw128(smem_u32(sqd), kChunk / 2, 1024);  // 64-column pieces 8 KB apart
       bool ok = true;
       for (int it = 0; ok && it < n_it; ++it) {
-        const uint64_t bq = dqm0 + (it & 1) * (4 * kChunk >> 4);
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           // the step's queries have come: its S^T and dP^T have read them
           ok = mbar_wait_soon(&pd_full[x], it & 1, abort_flag, p.err, DEV_TIMEOUT_MMA);
           if (!ok) break;
           tc_fence_after();
-          mma_tm<4, 32>(tmem + 256, tmem + 64 * x, bq + (2 * kChunk >> 4) + x * 512, id, it > 0 || x > 0);
-          mma_tm<4, 32>(tmem + 384, tmem + 128 + 64 * x, bq + x * 512, id, it > 0 || x > 0);
+          const int s = (2 * it + x) % kQdStages;
+          const uint64_t bq = dqm0 + s * (2 * kChunk >> 4);
+          mma_tm<4, 32>(tmem + 256, tmem + 64 * x, bq + (kChunk >> 4), id, it > 0 || x > 0);
+          mma_tm<4, 32>(tmem + 384, tmem + 128 + 64 * x, bq, id, it > 0 || x > 0);
           umma_commit(&pd_done[x]);
-          if (x == 1) umma_commit(&qd_empty[it & 1]);
+          umma_commit(&qd_empty[s]);
         }
       }
       umma_commit(&drain[2]);
@@ -1468,12 +1480,12 @@ __global__ void __launch_bounds__(kDkvThreads<CAP>, 1) masked_dkv_kernel(const _
     const uint32_t s_tm = tmem + lane_off + 64 * x, dp_tm = s_tm + 128;
     bool ok = plan_ok;
     for (int it = 0; ok && it < n_it; ++it) {
-      const int s = it & 1, qt0 = it_qtile(it) * kTile + 64 * x;
-      ok = __all_sync(0xffffffffu, mbar_wait_soon(&rows_full[s], (it >> 1) & 1, abort_flag, p.err, DEV_TIMEOUT_EPILOGUE) &&
+      const int qt0 = it_qtile(it) * kTile + 64 * x;
+      ok = __all_sync(0xffffffffu, mbar_wait_soon(&rows_full[x], it & 1, abort_flag, p.err, DEV_TIMEOUT_EPILOGUE) &&
                                        mbar_wait_soon(&sd_full[x], it & 1, abort_flag, p.err, DEV_TIMEOUT_EPILOGUE));
       if (!ok) break;
       tc_fence_after();
-      const bool part = !s_whole[s];
+      const bool part = !s_whole[x];
       const float slope = BIAS ? p.slopes[it_head(it)] * kLog2e : 0.f;
       const int side = qt0 >= kt * kTile + 32 * quarter + 31 ? -1 : 0;
 #pragma unroll 1
@@ -1483,7 +1495,7 @@ __global__ void __launch_bounds__(kDkvThreads<CAP>, 1) masked_dkv_kernel(const _
         tmem_ld32(dp_tm + 32 * c, dp);
         tmem_ld_wait_regs(sv);
         regs_after_wait(dp);
-        const int col = s * 128 + 64 * x + 32 * c;
+        const int col = 64 * x + 32 * c;
         uint32_t see = 0xffffffffu;
         if (part) {
           see = 0;
@@ -1501,7 +1513,7 @@ __global__ void __launch_bounds__(kDkvThreads<CAP>, 1) masked_dkv_kernel(const _
       tmem_st_wait();
       tc_fence_before();
       warp_arrive(&pd_full[x], lane);
-      if (lane == 0) mbar_arrive(&rows_empty[s]);
+      if (lane == 0) mbar_arrive(&rows_empty[x]);
     }
     // dV (first group), dK (second) once every product is done
     if (ok) ok = __all_sync(0xffffffffu, mbar_wait_soon(&drain[2], 0, abort_flag, p.err, DEV_TIMEOUT_EPILOGUE));
@@ -1538,7 +1550,7 @@ __global__ void __launch_bounds__(kDkvThreads<CAP>, 1) masked_dkv_kernel(const _
 // one CTA per SM (each CTA allocates all 512 TMEM columns).
 int fwd_smem() { return 1024 + 12 * kChunk + 256; }
 int dq_smem() { return 14 * kChunk + 2048 + 256; }
-int dkv_smem() { return 1024 + 12 * kChunk + 4096 + 16 + 256; }
+int dkv_smem() { return 14 * kChunk + 2048 + 16 + 256; }
 
 // Raises a kernel's shared-memory limit once per device.
 template <typename K>
@@ -1653,7 +1665,9 @@ int attention_masked_bwd(const MaskedArgs& a, cudaStream_t s) {
   MaskedBwdParams p;
   memset(&p, 0, sizeof(p));
   if (!head_map(&p.qmap, a.q, a.ldq, a.n_seq, a.S, a.hq, a.hd) || !head_map(&p.kmap, a.k, a.ldk, a.n_seq, a.S, a.hkv, a.hd) ||
-      !head_map(&p.vmap, a.v, a.ldv, a.n_seq, a.S, a.hkv, a.hd) || !head_map(&p.domap, a.d_o, a.lddo, a.n_seq, a.S, a.hq, a.hd))
+      !head_map(&p.vmap, a.v, a.ldv, a.n_seq, a.S, a.hkv, a.hd) || !head_map(&p.domap, a.d_o, a.lddo, a.n_seq, a.S, a.hq, a.hd) ||
+      !head_map(&p.qmap64, a.q, a.ldq, a.n_seq, a.S, a.hq, a.hd, 64) ||
+      !head_map(&p.domap64, a.d_o, a.lddo, a.n_seq, a.S, a.hq, a.hd, 64))
     return 2;
   carve_plan(const_cast<void*>(a.plan), a.n_seq, a.S, &p.plan);
   p.slopes = a.slopes;
