@@ -92,11 +92,16 @@ __device__ __forceinline__ uint64_t turn_step(float f, bool& ok) {
   return ok ? (uint64_t)__double2ull_rz(t * 18446744073709551616.0) : 0;
 }
 
+// Blocks that an SM holds at once: what is in flight bounds the kernel, so as many as leave no register spilled (rotation
+// alone, 4096 tokens: 18.7 us with 8 against 20.3 with 6; forward with norm, 20011 tokens: 57 with 7 against 60 with 6,
+// 75 with 8; backward: 96 with 4 against 117 with 3, 199 with 5).
+constexpr int rot_blocks_per_sm(bool norm, bool bwd) { return bwd ? 4 : norm ? 7 : 8; }
+
 // V: elements per vector (8, or 4 where half the rotated width is no multiple of 8). PAIRS: pair i
 // is (2 i, 2 i + 1), else (i, i + rot / 2). BWD: the norm's backward (without the norm the backward
 // is the forward kernel with the sign of the sines turned).
 template <int V, bool NORM, bool PAIRS, bool BWD>
-__global__ void __launch_bounds__(kRotThreads, BWD ? 4 : 6) rotary_kernel(const __grid_constant__ RotParams p) {
+__global__ void __launch_bounds__(kRotThreads, rot_blocks_per_sm(NORM, BWD)) rotary_kernel(const __grid_constant__ RotParams p) {
   __shared__ uint64_t s_step[kRotMaxPairs];              // a pair's angle per position; bit 0: not finite
   __shared__ float2 s_turn[kRotWarps][kRotMaxPairs];     // the warp's token: (cos, sin) per pair
   extern __shared__ float s_dg[];                        // at the end the groups' sums of dg
@@ -305,26 +310,26 @@ __global__ void __launch_bounds__(kRotThreads, BWD ? 4 : 6) rotary_kernel(const 
   }
 }
 
-// dg[c] = sum over the blocks' partials: rows [0, n_q) for q, [n_q, n_q + n_k) for k (blockIdx.y), 32 columns per
-// block; 32 interleaved sums per column, then one tree: a fixed order.
+// dg[c] = sum over the blocks' partials: rows [0, n_q) for q, [n_q, n_q + n_k) for k (blockIdx.y), eight columns (32
+// bytes) per block; 128 interleaved sums per column, then one tree: a fixed order.
+constexpr int kGainCols = 8;
 __global__ void __launch_bounds__(1024) rotary_gain_kernel(const float* __restrict__ partial, int n_q, int n_k, int hd,
                                                           float* __restrict__ dgq, float* __restrict__ dgk) {
   pdl_wait();
-  __shared__ float s[32][33];
-  const int c = blockIdx.x * 32 + (threadIdx.x & 31), r = threadIdx.x >> 5;
+  __shared__ float s[32][kGainCols];
+  const int k = threadIdx.x % kGainCols, c = blockIdx.x * kGainCols + k;  // hd is a multiple of eight
   const int row0 = blockIdx.y ? n_q : 0, n = blockIdx.y ? n_k : n_q;
   float v = 0.f;
-  if (c < hd) {
 #pragma unroll 8
-    for (int i = r; i < n; i += 32) v += partial[(int64_t)(row0 + i) * hd + c];
-  }
-  s[r][threadIdx.x & 31] = v;
+  for (int i = threadIdx.x / kGainCols; i < n; i += 1024 / kGainCols) v += partial[(int64_t)(row0 + i) * hd + c];
+  for (int o = 16; o >= kGainCols; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);  // the warp's four rows
+  if ((threadIdx.x & 31) < kGainCols) s[threadIdx.x >> 5][k] = v;
   __syncthreads();
-  v = s[threadIdx.x & 31][r];  // lane = partial sum, warp = column
+  if (threadIdx.x >= 32 * kGainCols) return;
+  v = s[threadIdx.x & 31][threadIdx.x >> 5];  // lane = partial sum, warp = column
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  const int col = blockIdx.x * 32 + r;
   float* out = blockIdx.y ? dgk : dgq;
-  if ((threadIdx.x & 31) == 0 && col < hd && out) out[col] = v;
+  if ((threadIdx.x & 31) == 0 && out) out[blockIdx.x * kGainCols + (threadIdx.x >> 5)] = v;
 }
 
 template <int V, bool NORM, bool BWD>
@@ -333,9 +338,10 @@ auto pick_style(bool pairs) {
 }
 
 // Blocks of a launch: several times what the SMs hold at once, so that those that end early make room (20011 tokens:
-// forward 60 against 66 us, backward 97 against 104 with one load); with gain gradients each leaves one row of partial
-// sums.
-constexpr int kRotBlocks = 148 * 24, kRotBwdBlocks = 148 * 8;
+// forward 60 against 66 us, backward 97 against 104 with one load; rotation alone, 4096 tokens, 18.7 with three loads against
+// 19.2 with two or four); with gain gradients each leaves one row of partial sums.
+constexpr int kRotBwdBlocks = 148 * 8;
+int64_t rot_blocks(bool norm, bool bwd) { return bwd ? kRotBwdBlocks : norm ? 148 * 28 : 148 * 24; }
 
 }  // namespace
 
@@ -363,7 +369,7 @@ int rotary(const RotaryArgs& a, cudaStream_t s) {
     d.heads = k ? a.hkv : a.hq;
     d.trips = (d.heads * group + 31) / 32;
     // the blocks in proportion to the heads; few tokens: a token's trips over several warps
-    const int64_t share = std::max<int64_t>(1, (int64_t)(bwd ? kRotBwdBlocks : kRotBlocks) * d.heads / (a.hq + a.hkv));
+    const int64_t share = std::max<int64_t>(1, rot_blocks(norm, bwd) * d.heads / (a.hq + a.hkv));
     int split = 1;
     while (split < d.trips && a.n_tok * split * 2 <= share * kRotWarps) split *= 2;
     d.split = std::min(split, d.trips);
@@ -388,7 +394,7 @@ int rotary(const RotaryArgs& a, cudaStream_t s) {
   if (launch_failed("sl_qk_norm_rope")) return 5;
   note_launch();
   if (gains) {
-    launch_kernel(rotary_gain_kernel, dim3((unsigned)((a.hd + 31) / 32), 2), 1024, 0, s, (const float*)a.partial,
+    launch_kernel(rotary_gain_kernel, dim3((unsigned)(a.hd / kGainCols), 2), 1024, 0, s, (const float*)a.partial,
                   p.side[0].blocks, p.side[1].blocks, a.hd, a.dgq, a.dgk);
     if (launch_failed("sl_qk_norm_rope")) return 5;
     note_launch();
