@@ -468,6 +468,9 @@ __device__ __forceinline__ bool mbar_wait_idle(uint64_t* bar, uint32_t parity, v
   return mbar_wait(bar, parity, abort, err, code);
 }
 
+// Streams of a forward unit: two heads of a group at one query tile, two neighbouring query tiles of a head, or one alone
+enum : int32_t { kTwoHeads = 0, kTwoTiles = 1, kAlone = 2 };
+
 struct MaskedFwdParams {
   CUtensorMap qmap, kmap, vmap;  // [head_dim, heads, seq_len, n_seq], boxes 64 x 1 x 128 x 1
   Plan plan;
@@ -476,7 +479,7 @@ struct MaskedFwdParams {
   int64_t ldo;
   float* lse;                    // [n_q_heads][n_seq * seq_len]
   int32_t n_seq, S, hq, hkv, hd, nd;
-  int32_t n_units, pair_heads;   // pair_heads: the streams are two heads, else two query tiles
+  int32_t n_units, kind;         // of a unit's streams
   float mul, cap_mul;            // see score() and tanh_n()
   int* err;
 };
@@ -546,17 +549,21 @@ __device__ __forceinline__ int unit_number(int i) {
 // A unit's entry of the plan, read a unit ahead, and what it says (apart, so that nothing waits for the read).
 __device__ __forceinline__ int4 unit_entry(const MaskedFwdParams& p, int u) {
   if (u >= p.n_units) return make_int4(0, 0, 0, 0);
-  return p.pair_heads ? p.plan.q_order[u / (p.hq >> 1)] : p.plan.q2_order[u / p.hq];
+  if (p.kind == kTwoTiles) return p.plan.q2_order[u / p.hq];
+  return p.plan.q_order[u / (p.kind == kTwoHeads ? p.hq >> 1 : p.hq)];
 }
 
 __device__ __forceinline__ Unit unit_of(const MaskedFwdParams& p, int u, const int4& e) {
   Unit r;
-  if (p.pair_heads) {
-    const int n_qt = (p.S + kTile - 1) / kTile, half = p.hq >> 1;
+  if (p.kind != kTwoTiles) {
+    const int n_qt = (p.S + kTile - 1) / kTile, heads = p.kind == kTwoHeads ? p.hq >> 1 : p.hq;
     r.b = e.x / n_qt;
     r.qt0 = r.qt1 = e.x % n_qt;
-    r.h0 = 2 * (u % half);
-    r.h1 = r.h0 + 1;
+    r.h0 = r.h1 = u % heads;
+    if (p.kind == kTwoHeads) {
+      r.h0 *= 2;
+      r.h1 = r.h0 + 1;
+    }
     r.j0 = e.y;
     r.j1 = e.z;
   } else {
@@ -635,13 +642,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1) masked_fwd_kernel(const __grid
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int hpg = p.hq / p.hkv;
+  const int hpg = p.hq / p.hkv, n_streams = p.kind == kAlone ? 1 : 2;
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2; ++s) {
       mbar_init(&q_full[s], 1);
       mbar_init(&q_empty[s], 1);
       mbar_init(&kv_full[s], 1);
-      mbar_init(&kv_empty[s], 2);  // both streams
+      mbar_init(&kv_empty[s], n_streams);
     }
     for (int s = 0; s < 4; ++s) {
       mbar_init(&pv_done[s], 1);
@@ -677,7 +684,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) masked_fwd_kernel(const __grid
         e0 = e1;
         e1 = unit_entry(p, unit_number(i + 2));
         const int g = un.h0 / hpg;
-        for (int x = 0; x < 2 && ok; ++x) {
+        for (int x = 0; x < n_streams && ok; ++x) {
           if (i > 0) ok = mbar_wait_idle(&q_empty[x], (i - 1) & 1, abort_flag, p.err, DEV_TIMEOUT_PRODUCER);
           if (!ok) break;
           mbar_arrive_expect_tx(&q_full[x], nd * kChunk);
@@ -701,7 +708,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) masked_fwd_kernel(const __grid
       if (n_q[1]) mbar_wait(&q_full[1], (n_q[1] - 1) & 1, nullptr, p.err, DEV_TIMEOUT_DRAIN);
       for (int k = max(0, t - 2); k < t; ++k) mbar_wait(&kv_full[k & 1], (k >> 1) & 1, nullptr, p.err, DEV_TIMEOUT_DRAIN);
     }
-  } else if (warp == 1 || warp == 2) {
+  } else if (warp <= n_streams) {
     if (lane == 0) {
       const int x = warp - 1;  // stream
       const uint32_t id_s = idesc_bf16(128, 64, 0, 0);         // S = Q K^T: both K-major over d
@@ -768,7 +775,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) masked_fwd_kernel(const __grid
       umma_commit(&drain[x]);
       mbar_wait(&drain[x], 0, nullptr, p.err, DEV_TIMEOUT_DRAIN);
     }
-  } else if (warp >= 4) {
+  } else if (warp >= 4 && warp < 4 + 4 * n_streams) {
     const int x = warp >= 8;                         // stream
     const int quarter = warp & 3;
     const int r = quarter * 32 + lane;               // query row in the tile = TMEM lane
@@ -1668,9 +1675,11 @@ int attention_masked_fwd(const MaskedArgs& a, cudaStream_t s) {
     return 2;
   p.o = static_cast<__nv_bfloat16*>(a.o);
   p.ldo = a.ldo;
-  p.pair_heads = (a.hq / a.hkv) % 2 == 0;
+  const bool pairs = (a.hq / a.hkv) % 2 == 0;
   const int n_t = (a.S + kTile - 1) / kTile;
-  p.n_units = p.pair_heads ? a.n_seq * n_t * (a.hq / 2) : a.n_seq * ((n_t + 1) / 2) * a.hq;
+  // as few units as SMs: each stream has one to itself (3 x 333 tokens, 6 heads: 16.6 against 20 us)
+  p.kind = (int64_t)a.n_seq * n_t * a.hq <= sm_count() ? kAlone : pairs ? kTwoHeads : kTwoTiles;
+  p.n_units = p.kind == kTwoTiles ? a.n_seq * ((n_t + 1) / 2) * a.hq : a.n_seq * n_t * (p.kind == kTwoHeads ? a.hq / 2 : a.hq);
   carve_plan(const_cast<void*>(a.plan), a.n_seq, a.S, &p.plan);
   p.slopes = a.slopes;
   p.lse = const_cast<float*>(a.lse);

@@ -108,7 +108,11 @@ SHAPES = [  # n_seq, S, hq, hkv, hd, documents, prefix, window, padding, ld padd
     (1, 1, 1, 1, 8, 1, 0, 0, 0, 0), (2, 2, 4, 2, 32, 1, 0, 0, 0, 0), (3, 64, 4, 2, 32, 3, 0, 0, 5, 0),
     (1, 127, 2, 1, 64, 2, 20, 0, 0, 8), (2, 128, 6, 3, 96, 1, 0, 0, 0, 0), (1, 129, 5, 1, 40, 2, 129, 0, 0, 0),
     (2, 300, 4, 1, 128, 4, 0, 0, 37, 16), (1, 257, 2, 2, 120, 1, 0, 1, 0, 0), (2, 513, 3, 3, 128, 3, 70, 90, 130, 0),
-    (1, 1000, 8, 2, 64, 7, 0, 0, 400, 0), (9, 200, 2, 1, 16, 2, 30, 0, 0, 0)]
+    (1, 1000, 8, 2, 64, 7, 0, 0, 400, 0), (9, 200, 2, 1, 16, 2, 30, 0, 0, 0),
+    # more (head, query tile) units than a GPU has SMs, so that each CTA goes through several: three heads per group, four
+    # of them, one tile per sequence, long and short documents
+    (5, 333, 24, 8, 64, 3, 40, 0, 20, 0), (11, 200, 16, 4, 40, 2, 0, 60, 11, 8), (160, 40, 3, 1, 32, 2, 0, 0, 3, 0),
+    (2, 700, 32, 8, 128, 3, 0, 0, 0, 0)]
 
 
 @pytest.mark.parametrize("opt", OPTIONS)
