@@ -587,7 +587,7 @@ def sl_attention_masked_bwd(ws: Workspace, q, k, v, o, d_o, lse, n_seq, n_q_head
 
 
 def _logits(fn, t, shape, dtype, dev):
-    if t.dim() != 2 or dtype not in (torch.bfloat16, torch.float32):
+    if dtype not in (torch.bfloat16, torch.float32):
         _refuse(fn)
     return _rows(fn, t, shape, dtype, dev)
 
@@ -597,6 +597,8 @@ def sl_token_logprobs_fwd(logits, targets, logp, stats, entropy=None, top_ids=No
     the backward, and optionally the rows' entropy [N] and the k most likely tokens top_ids, top_logp [N, k]."""
     fn, f32 = "sl_token_logprobs_fwd", torch.float32
     dev = _device(fn, logits)
+    if logits.dim() != 2 or (top_ids is None) != (top_logp is None) or (top_ids is not None and top_ids.dim() != 2):
+        _refuse(fn)
     N, V = logits.shape
     k = 0 if top_ids is None else top_ids.shape[1]
     _check(fn, lib().sl_token_logprobs_fwd(
@@ -610,6 +612,8 @@ def sl_token_logprobs_bwd(logits, targets, stats, g_logp, dlogits, g_entropy=Non
     """dlogits (the logits' type; may be the logits) from the gradients g_logp [N] at logp and g_entropy [N] at entropy."""
     fn, f32 = "sl_token_logprobs_bwd", torch.float32
     dev = _device(fn, logits)
+    if logits.dim() != 2:
+        _refuse(fn)
     N, V = logits.shape
     _check(fn, lib().sl_token_logprobs_bwd(
         SL_DT_F32 if logits.dtype == f32 else SL_DT_BF16, *_logits(fn, logits, logits.shape, logits.dtype, dev), N, V,

@@ -75,6 +75,8 @@ class DecoderLayer:
         if qk_norm is not None:
             self.q_at, self.k_at = e(T, Dq), e(T, Dkv)
         self.softcap, self.slopes = float(softcap), as_dev(slopes, f32)
+        if not self.softcap >= 0 or (plan is not None and (plan.n_seq, plan.seq_len) != (self.n_seq, self.S)):
+            raise ValueError("softcap is not negative, and a plan is of the layer's sequences")
         if plan is None and (self.softcap > 0 or slopes is not None):
             plan = AttentionPlan(self.n_seq, self.S, dev)
         self.plan = plan

@@ -212,3 +212,20 @@ def test_other_stream_graph_and_identical_runs():
     dw = torch.empty_like(z)
     B.sl_token_logprobs_bwd(z, t, want[1], g, dw)
     assert torch.equal(logp, want[0]) and torch.equal(d, dw)
+
+
+def test_refuses_what_is_not_rows():
+    z, t, g, _ = make(4, 64, BF, 3)
+    logp, stats = torch.empty(4, device=DEV), torch.empty(4, 2, device=DEV)
+    ids, top = torch.empty(4, 5, dtype=torch.int32, device=DEV), torch.empty(4, 5, device=DEV)
+    for call in (lambda: B.sl_token_logprobs_fwd(z[None], t, logp, stats),
+                 lambda: B.sl_token_logprobs_fwd(z, t, logp, stats, None, ids, None),
+                 lambda: B.sl_token_logprobs_fwd(z, t, logp, stats, None, None, top),
+                 lambda: B.sl_token_logprobs_fwd(z, t, logp, stats, None, ids.flatten(), top.flatten()),
+                 lambda: B.sl_token_logprobs_fwd(z.half(), t, logp, stats),
+                 lambda: B.sl_token_logprobs_fwd(z, t.long(), logp, stats),
+                 lambda: B.sl_token_logprobs_bwd(z[0], t[:1], stats[:1], g[:1], z[0]),
+                 lambda: B.sl_token_logprobs_bwd(z, t, stats, g, z.float())):
+        with pytest.raises(B.SparseLoRAError) as e:
+            call()
+        assert e.value.code == B.SL_ERR_INVALID_ARG

@@ -154,3 +154,14 @@ def test_default_layer_is_what_it_was():
     ids, targets = p["ids"][pt].to(torch.int32).to(DEV), p["targets"].to(DEV)
     a, b = p["model"].forward_backward(ids, targets), other.forward_backward(ids, targets)
     assert torch.equal(a, b) and other.layers[0].plan is None and other.layers[0].q_at is other.layers[0].q_nat
+
+
+def test_options_that_do_not_fit_are_refused():
+    keep = [(0.5, 0.5)]
+    p = build(keep, seed=84)
+    S = p["model"].layers[0].S
+    for kw in (dict(softcap=-1.0), dict(softcap=math.nan), dict(plan=AttentionPlan(p["n_seq"], S + 1)),
+               dict(plan=AttentionPlan(p["n_seq"] + 1, S))):
+        with pytest.raises(ValueError):
+            SparseLoRAModel(p["frozen"], p["loras"], p["gammas"], keep, p["perm"], p["C"], p["n_seq"], p["heads"], 8, 2.0,
+                            DEV, **kw)
