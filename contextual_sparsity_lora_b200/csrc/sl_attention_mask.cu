@@ -495,6 +495,7 @@ struct MaskedBwdParams {
   int64_t lddq, lddk, lddv;
   int32_t n_seq, S, hq, hkv, hd, nd;
   int32_t n_units;               // of the dq kernel
+  int32_t split;                 // CTAs (1 or 2, a cluster) that share a unit of the dk, dv kernel
   float scale, mul, cap_mul;
   int* err;
 };
@@ -1329,6 +1330,19 @@ __global__ void __launch_bounds__(kBwdThreads, 1) masked_dq_kernel(const __grid_
 // 384. Measured besides: 8 x 512 tokens 62 us; 4096 causal tokens are 1023 TFLOP/s of four products per tile pair.
 constexpr int kQdStages = 5;
 
+// Both CTAs of a cluster: what each wrote to the other's shared memory before it is there behind it.
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t peer_address(uint32_t smem, uint32_t rank) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ void st_peer(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
 template <bool CAP, bool BIAS>
 __global__ void __launch_bounds__(kDkvThreads<CAP>, 1) masked_dkv_kernel(const __grid_constant__ MaskedBwdParams p) {
   extern __shared__ __align__(1024) uint8_t smem_dkv[];
@@ -1355,7 +1369,7 @@ __global__ void __launch_bounds__(kDkvThreads<CAP>, 1) masked_dkv_kernel(const _
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n_t = (p.S + kTile - 1) / kTile;
-  const int g = blockIdx.x % p.hkv;
+  const int unit = blockIdx.x / p.split, rank = blockIdx.x % p.split, g = unit % p.hkv;
   const int hpg = p.hq / p.hkv;
   const int64_t T = (int64_t)p.n_seq * p.S;
   if (threadIdx.x == 0) {
@@ -1391,11 +1405,13 @@ __global__ void __launch_bounds__(kDkvThreads<CAP>, 1) masked_dkv_kernel(const _
   // (key tile, sequence) in the plan's order, and the query tiles q0 .. q1 - 1 that see any of it (at least
   // one, so that a tile that nobody sees takes the same path and gets zeros)
   const bool plan_ok = plan_fits(p.plan, p.n_seq, p.S, p.err);
-  const int4 entry = plan_ok ? p.plan.k_order[blockIdx.x / p.hkv] : make_int4(0, 0, 0, 0);
+  const int4 entry = plan_ok ? p.plan.k_order[unit / p.hkv] : make_int4(0, 0, 0, 0);
   const int kt = entry.x % n_t, b = entry.x / n_t;
-  const int q0 = entry.y, n_it = hpg * (entry.z - q0);
-  auto it_head = [&](int it) { return g * hpg + it % hpg; };
-  auto it_qtile = [&](int it) { return q0 + it / hpg; };
+  // this CTA's steps: all of the unit's, or the first or second half (which may be none)
+  const int q0 = entry.y, n_unit = hpg * (entry.z - q0), it0 = rank ? (n_unit + 1) / 2 : 0;
+  const int n_it = p.split == 1 ? n_unit : rank ? n_unit / 2 : (n_unit + 1) / 2;
+  auto it_head = [&](int it) { return g * hpg + (it0 + it) % hpg; };
+  auto it_qtile = [&](int it) { return q0 + (it0 + it) / hpg; };
 
   // 640 threads start with 96 registers each; 56 in the first four warps and 104 in the others stay within their sum
   if (warp < 4) {
@@ -1505,6 +1521,11 @@ __global__ void __launch_bounds__(kDkvThreads<CAP>, 1) masked_dkv_kernel(const _
       umma_commit(&drain[2]);
       mbar_wait(&drain[2], 0, nullptr, p.err, DEV_TIMEOUT_DRAIN);
     }
+    if (p.split == 2) {  // see the end of the compute warps
+      __syncwarp();
+      cluster_barrier();
+      cluster_barrier();
+    }
   } else {
     if (kWarps == 16) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
     // x: buffer, half of each query tile; c0: first 32 columns of it
@@ -1552,7 +1573,28 @@ __global__ void __launch_bounds__(kDkvThreads<CAP>, 1) masked_dkv_kernel(const _
     }
     // dV (first group), dK (second) once every product is done
     if (ok) ok = __all_sync(0xffffffffu, mbar_wait_soon(&drain[2], 0, abort_flag, p.err, DEV_TIMEOUT_EPILOGUE));
-    if (ok) {
+    // Two CTAs: the first finishes dV, the second dK; each sends the other one's share, fp32, to the other's stages of Q and dO,
+    // which nothing reads any more.
+    const uint32_t acc_tm = tmem + lane_off + 256 + 128 * x;
+    float* share = reinterpret_cast<float*>(sqd);  // [column][row]
+    if (p.split == 2) {
+      __syncwarp();
+      cluster_barrier();
+      if (x != rank) {
+        const uint32_t to = peer_address(smem_u32(share), rank ^ 1) + 4 * r;
+        tc_fence_after();
+#pragma unroll 1
+        for (int k = c0; k < 2 * nd; k += kCols == 1 ? 2 : 1) {
+          uint32_t v[32];
+          tmem_ld32(acc_tm + 32 * k, v);
+          tmem_ld_wait_regs(v);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) st_peer(to + (32 * k + e) * 512, n_it ? v[e] : 0u);
+        }
+      }
+      cluster_barrier();
+    }
+    if (ok && (p.split == 1 || x == rank)) {
       tc_fence_after();
       const int64_t row0 = (int64_t)b * p.S + kt * kTile + 32 * quarter;
       const int n_rows = p.S - kt * kTile - 32 * quarter;
@@ -1562,8 +1604,15 @@ __global__ void __launch_bounds__(kDkvThreads<CAP>, 1) masked_dkv_kernel(const _
 #pragma unroll 1
       for (int k = c0; k < 2 * nd; k += kCols == 1 ? 2 : 1) {
         uint32_t v[32], w[16];
-        tmem_ld32(tmem + lane_off + 256 + 128 * x + 32 * k, v);
+        tmem_ld32(acc_tm + 32 * k, v);
         tmem_ld_wait_regs(v);
+        if (p.split == 2) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const float other = share[(32 * k + e) * 128 + r];
+            v[e] = __float_as_uint(n_it ? __uint_as_float(v[e]) + other : other);
+          }
+        }
 #pragma unroll
         for (int e = 0; e < 32; e += 2) w[e / 2] = pack2(__uint_as_float(v[e]) * mul, __uint_as_float(v[e + 1]) * mul);
         store_rows32(out + 32 * k, ld, w, n_rows, p.hd - 32 * k);
@@ -1629,7 +1678,20 @@ int bwd_launch(const MaskedBwdParams& p, cudaStream_t s) {
   launch_kernel(masked_dq_kernel<CAP, BIAS>, (unsigned)std::min(p.n_units, n_sm), kBwdThreads, dq_smem(), s, p);
   if (launch_failed("sl_attention_masked")) return 5;
   note_launch();
-  launch_kernel(masked_dkv_kernel<CAP, BIAS>, (unsigned)(plan_tiles(p.n_seq, p.S) * p.hkv), kDkvThreads<CAP>, dkv_smem(), s, p);
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)p.split;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(plan_tiles(p.n_seq, p.S) * p.hkv * p.split));
+  cfg.blockDim = dim3(kDkvThreads<CAP>);
+  cfg.dynamicSmemBytes = dkv_smem();
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl_enabled() ? 2 : 1;
+  cudaLaunchKernelEx(&cfg, masked_dkv_kernel<CAP, BIAS>, p);
   if (launch_failed("sl_attention_masked")) return 5;
   note_launch();
   return 0;
@@ -1723,6 +1785,8 @@ int attention_masked_bwd(const MaskedArgs& a, cudaStream_t s) {
   p.hd = a.hd;
   p.nd = (a.hd + 63) / 64;
   p.n_units = (int)(plan_tiles(a.n_seq, a.S) * a.hq);
+  // units that leave half of the SMs free are shared by two CTAs each (3 x 333 tokens, 27 units: 20.3 against 28.6 us; one key tile, two steps: 9.9 against 10.3)
+  p.split = 2 * plan_tiles(a.n_seq, a.S) * a.hkv <= sm_count() ? 2 : 1;
   score_constants(a, &p.scale, &p.mul, &p.cap_mul);
   p.err = a.err;
   if (a.cap > 0.f) return a.slopes ? bwd_launch<true, true>(p, s) : bwd_launch<true, false>(p, s);
