@@ -1326,16 +1326,16 @@ sl_status sl_attention_masked_fwd(const void* q, int64_t ldq, const void* k, int
 }
 
 sl_status sl_attention_masked_bwd(const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v, int64_t ldv,
-                                  const void* d_o, int64_t lddo, const float* lse, int32_t n_seq, int32_t seq_len, int32_t n_q_heads, int32_t n_kv_heads,
-                                  int32_t head_dim, float scale, float softcap, const float* slopes, const void* plan,
-                                  int64_t plan_bytes, void* dq, int64_t lddq, void* dk, int64_t lddk, void* dv,
-                                  int64_t lddv, sl_workspace* ws, sl_stream stream) {
+                                  const void* d_o, int64_t lddo, const float* lse, int32_t n_seq, int32_t seq_len,
+                                  int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim, float scale, float softcap,
+                                  const float* slopes, const void* plan, int64_t plan_bytes, void* dq, int64_t lddq,
+                                  void* dk, int64_t lddk, void* dv, int64_t lddv, sl_workspace* ws, sl_stream stream) {
   if (!q || !k || !v || !d_o || !lse || !plan || !dq || !dk || !dv) return SL_ERR_INVALID_ARG;
   if (sl_status st = masked_args(n_seq, seq_len, n_q_heads, n_kv_heads, head_dim, scale, softcap, plan, plan_bytes))
     return st;
   const int64_t nq = (int64_t)n_q_heads * head_dim, nk = (int64_t)n_kv_heads * head_dim;
-  if (!rows_ok(q, ldq, nq) || !rows_ok(k, ldk, nk) || !rows_ok(v, ldv, nk) || !rows_ok(d_o, lddo, nq) || !rows_ok(dq, lddq, nq) || !rows_ok(dk, lddk, nk) || !rows_ok(dv, lddv, nk) ||
-      !al16(lse))
+  if (!rows_ok(q, ldq, nq) || !rows_ok(k, ldk, nk) || !rows_ok(v, ldv, nk) || !rows_ok(d_o, lddo, nq) ||
+      !rows_ok(dq, lddq, nq) || !rows_ok(dk, lddk, nk) || !rows_ok(dv, lddv, nk) || !al16(lse))
     return SL_ERR_ALIGNMENT;
   const size_t scratch = attention_masked_scratch(n_seq, seq_len, n_q_heads);
   Carver c(nullptr);

@@ -312,8 +312,8 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 }
 // 2^x of two values on the multiply-add units: x = n + f with a whole n and |f| <= 1/2, 2^f a polynomial of degree 5 (least
 // maximum of the relative error with the constant 1: 9e-8, 1.6e-7 with fp32 arithmetic, about ex2.approx's), n added
-// to its exponent. From -127 down: 0 (the exponent of 1 less 127 leaves no bit). 1.5 * 2^23 + x keeps n in its low bits. A quarter of the forward's exponentials,
-// which otherwise wait for the exponential unit (8192 tokens with a bias 537 against 576 us, 4096 causal 131 against 135;
+// to its exponent. From -127 down: 0 (the exponent of 1 less 127 leaves no bit). 1.5 * 2^23 + x keeps n in its low
+// bits. A quarter of the forward's exponentials, which otherwise wait for the exponential unit (8192 tokens with a bias 537 against 576 us, 4096 causal 131 against 135;
 // an eighth 555, three eighths 543, half 585); with a cap, whose tanh is on the same units, and in the backward it gains nothing.
 __device__ __forceinline__ void ex2_poly(f2 x, float& y0, float& y1) {
   float x0, x1;
@@ -531,10 +531,10 @@ __device__ __forceinline__ bool bar_and_compute(bool ok) {
 // a third one for S alone loses what a stream's order gives (604 against 589). TMEM: S_x / P_x of step h at
 // 128 x + 64 (h & 1), O_x at 256 + 128 x.
 //
-// Measured (32 query, 8 key/value heads of 128, one sequence): 8192 tokens with a prefix and a bias 589 us (947 TFLOP/s
-// over the visible pairs, 0.58 of a library bf16 product's rate), 4096 tokens causal 140 us, with a cap 130 us
-// (its documents see fewer tiles), 8 x 512 tokens 39 us. The tensor pipe is busy 48% of the time; the rest are waits between
-// the products and a softmax whose exponentials, 64 per row and step, take as long as the step's products.
+// Measured (32 query, 8 key/value heads of 128): one sequence of 8192 tokens with a prefix and a bias 537 us (1040 TFLOP/s
+// over the visible pairs, 0.63 of a library bf16 product's rate), 4096 tokens causal 131 us, with a cap 131 us (its
+// documents see fewer tiles), 8 x 512 tokens 38 us. The tensor pipe is busy half of the time; the rest are waits between
+// the products and the softmax, 64 exponentials per row and step.
 struct Unit {
   int qt0, qt1, h0, h1, b, j0, j1;
   __device__ __forceinline__ int qt(int x) const { return x ? qt1 : qt0; }
@@ -936,7 +936,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) masked_fwd_kernel(const __grid
 // the query tiles that see it. Each forms S and dP for itself (nine products of a tile pair where one kernel for
 // all would have five and a sum for D), but no partial sum leaves the chip and every sum has a fixed order. With dQ
 // added up across key tiles in global memory (64 KB of fp32 reductions per tile pair, a kernel for D before it and a pass
-// that rounds after it) the backward took 161 us at 8 x 512 tokens and 631 at 4096 capped ones, against 131 and 618, and
+// that rounds after it) the backward took 161 us at 8 x 512 tokens and 631 at 4096 capped ones, against 115 and 534, and
 // dq's last bits depended on the order.
 //
 // D_i = sum_j P_ij dP_ij (= dO_i . o_i) is formed from P and dP in fp32 and not from the stored o: that one is rounded to
@@ -999,9 +999,10 @@ __device__ __forceinline__ void grad32(uint32_t (&s)[32], uint32_t (&dp)[32], fl
 // 128 and 256, dP at 384 and, in the first pass, every other one at 0, the last tile's among them (of two or more):
 // dQ is added up there once that one has been read. K has three stages, since it stays until dS K is done, V two.
 //
-// Measured (32 query, 8 key/value heads of 128): 4096 causal tokens 349 us (five products of a tile pair, 1015 TFLOP/s),
-// capped documents 318 us, 8 x 512 tokens 69 us. The products read both operands of S and dP from shared memory, at
-// its full rate, so the tensor pipe cannot be busy more than 3/4 of the time; it is for half of it.
+// Measured (32 query, 8 key/value heads of 128): 4096 causal tokens 282 us (1200 TFLOP/s of the products done), capped documents
+// 265 us, 8 x 512 tokens 62 us. S and dP formed twice for every tile: 349, 318 and 69 us; K and V in two common stages: 353,
+// 298, 66 (a stage is held from its load to the end of dS K, and the next load waits); dP without its second place: 299.
+// What is left between the products is the chain from a dS over its product to the S that takes its buffer.
 template <bool CAP, bool BIAS>
 __global__ void __launch_bounds__(kBwdThreads, 1) masked_dq_kernel(const __grid_constant__ MaskedBwdParams p) {
   extern __shared__ __align__(1024) uint8_t smem_dq[];
@@ -1319,15 +1320,18 @@ __global__ void __launch_bounds__(kBwdThreads, 1) masked_dq_kernel(const __grid_
 }
 
 // dk, dv: one CTA per (key tile, key/value head) in the plan's order, over (query head of the group, query tile). K and V
-// stay, Q and dO stream through five stages of half a query tile. A step is half a query tile (64 queries): S^T = K Q^T and dP^T = V dO^T of
-// step t + 1 run while the compute warps work on step t; P^T and dS^T replace them in TMEM (bf16, first
+// stay, Q and dO stream through five stages of half a query tile. A step is such a half (64 queries): S^T = K Q^T and
+// dP^T = V dO^T of step t + 1 run while the compute warps work on step t; P^T and dS^T replace them in TMEM (bf16, first
 // operands of dV += P^T dO and dK += dS^T Q). Warp 0 loads, the query rows' lse, D and intervals too; warps 1, 2 and 3 issue
 // S^T, dP^T, and dV and dK (a thread that issues also waits and commits, and meanwhile the tensor cores, which queue
 // about five products, run dry: 340 us at 4096 causal tokens with one such thread, 320 with two, 277 with three); the
 // others compute, one half for the even and one for the odd steps, a key row and 32 query columns per thread at a time:
-// 16 warps, or 8 where a cap's tanh needs the registers (with 16 it spills: 335 against 318 us at 4096 capped
-// tokens, 300 since; without a cap 16 gain 10%). TMEM: S^T of buffer x at 64 x, dP^T at 128 + 64 x, dV at 256, dK at
-// 384. Measured besides: 8 x 512 tokens 62 us; 4096 causal tokens are 1023 TFLOP/s of four products per tile pair.
+// 16 warps, or 8 where a cap's tanh needs the registers (with 16 it spilled: 335 against 318 us at 4096 capped
+// tokens; without a cap 16 gained 10%). TMEM: S^T of buffer x at 64 x, dP^T at 128 + 64 x, dV at 256, dK at 384.
+//
+// Measured (32 query, 8 key/value heads of 128): 4096 causal tokens 264 us (1070 TFLOP/s of four products per tile pair; 286
+// with two stages of whole query tiles), capped 269 us, 8 x 512 tokens 53 us. The products alone take 2640 of a query
+// tile's 3900 cycles (64 columns cost 50 cycles per 16-element step, 128 cost 65); whole tiles do not fit the TMEM.
 constexpr int kQdStages = 5;
 
 // Both CTAs of a cluster: what each wrote to the other's shared memory before it is there behind it.
@@ -1785,7 +1789,8 @@ int attention_masked_bwd(const MaskedArgs& a, cudaStream_t s) {
   p.hd = a.hd;
   p.nd = (a.hd + 63) / 64;
   p.n_units = (int)(plan_tiles(a.n_seq, a.S) * a.hq);
-  // units that leave half of the SMs free are shared by two CTAs each (3 x 333 tokens, 27 units: 20.3 against 28.6 us; one key tile, two steps: 9.9 against 10.3)
+  // units that leave half of the SMs free are shared by two CTAs each (3 x 333 tokens, 27 units: 20.3 against 28.6 us; one
+  // key tile, two steps: 9.9 against 10.3)
   p.split = 2 * plan_tiles(a.n_seq, a.S) * a.hkv <= sm_count() ? 2 : 1;
   score_constants(a, &p.scale, &p.mul, &p.cap_mul);
   p.err = a.err;

@@ -429,8 +429,7 @@ SL_API sl_status sl_attention_bwd(const void* q, const void* k, const void* v, c
  *   gamma_q, gamma_k: bf16 [head_dim], both or neither (NULL: no norm, rotation only).
  * The backward takes the forward's inputs q and k (not read, may be NULL, without gains) and writes
  *   dq, dk and, where given, dgamma_q, dgamma_k (fp32 [head_dim], sums over tokens and heads in a
- *   fixed order; workspace: 1186 * head_dim floats past the header, ws may be NULL without
- *   them).
+ *   fixed order; workspace: 1186 * head_dim floats past the header, ws may be NULL without them).
  * An output may be its input (same pointer and leading dimension: yq = q, dq = dyq); no other overlap. fp32
  * arithmetic, each output rounded once. head_dim in [8, 256], a multiple of 8; rot_dim a multiple of 8
  * up to head_dim. */
@@ -480,11 +479,11 @@ SL_API sl_status sl_attention_masked_fwd(const void* q, int64_t ldq, const void*
                                          const float* slopes, const void* plan, int64_t plan_bytes, void* o,
                                          int64_t ldo, float* lse, sl_workspace* ws, sl_stream stream);
 SL_API sl_status sl_attention_masked_bwd(const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v,
-                                         int64_t ldv, const void* d_o, int64_t lddo, const float* lse, int32_t n_seq, int32_t seq_len, int32_t n_q_heads,
-                                         int32_t n_kv_heads, int32_t head_dim, float scale, float softcap,
-                                         const float* slopes, const void* plan, int64_t plan_bytes, void* dq,
-                                         int64_t lddq, void* dk, int64_t lddk, void* dv, int64_t lddv,
-                                         sl_workspace* ws, sl_stream stream);
+                                         int64_t ldv, const void* d_o, int64_t lddo, const float* lse, int32_t n_seq,
+                                         int32_t seq_len, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
+                                         float scale, float softcap, const float* slopes, const void* plan,
+                                         int64_t plan_bytes, void* dq, int64_t lddq, void* dk, int64_t lddk, void* dv,
+                                         int64_t lddv, sl_workspace* ws, sl_stream stream);
 
 /* Log probabilities of given tokens, entropy and top alternatives of rows of logits, and their gradient
  * (the loss at the LM head, and the scores of a generation).
@@ -498,9 +497,9 @@ SL_API sl_status sl_attention_masked_bwd(const void* q, int64_t ldq, const void*
  *     the loss whose gradients are g_logp[r] at logp and, optionally, g_entropy[r] at entropy (then entropy is
  *     the forward's): dz_j = g_logp ([j = t] - p_j) - g_entropy p_j (log p_j + entropy). A row whose gradients
  *     are both 0 (or that has no target and no g_entropy) gets zeros. Columns from vocab to ldd are left as they were.
- * Logits below -2^123 (about -1e37) count as -inf (probability 0, no gradient). A row with nothing above that: logp = -inf (0 without
- * a target), entropy 0, top_logp = -inf, no gradient. A row with NaN, +inf or a logit above 2^123: NaN results. Sums in
- * fp32 in a fixed order (run-to-run identical). Errors: SL_ERR_INVALID_ARG, SL_ERR_SHAPE (vocab up to 2^24,
+ * Logits below -2^123 (about -1e37) count as -inf (probability 0, no gradient). A row with nothing above that: logp =
+ * -inf (0 without a target), entropy 0, top_logp = -inf, no gradient. A row with NaN, +inf or a logit above 2^123: NaN
+ * results. Sums in fp32 in a fixed order (run-to-run identical). Errors: SL_ERR_INVALID_ARG, SL_ERR_SHAPE (vocab up to 2^24,
  * with top_k up to 6553600 fp32 or 13107200 bf16 columns), SL_ERR_ALIGNMENT. */
 SL_API sl_status sl_token_logprobs_fwd(sl_dtype dtype, const void* logits, int64_t ld, int64_t n_rows, int64_t vocab,
                                        const int32_t* targets, float* logp, float* stats, float* entropy,
