@@ -944,11 +944,22 @@ __global__ void __launch_bounds__(kFwdThreads, 1) masked_fwd_kernel(const __grid
 // together where a row's weight lies on few keys (relative error of dq over 4e-3 with 8 keys, against 2.3e-3).
 
 // dS = P (dP - D) (1 - tanh^2) of 32 columns: from raw products s and dp; c1: -lse (powers of two), c2: -D, each
-// one per row (ROW) or read per column from shared memory. P as packed bf16 in pw (when wanted), dS in dw.
-template <bool CAP, bool BIAS, bool ROW, bool WANT_P>
+// one per row (ROW) or read per column from shared memory. P as packed bf16 in pw (when wanted), dS in dw; FINE: and behind
+// it what the rounding left of dS, as bf16 again.
+//
+// Rounded once, dS costs dq and dk about as much as their own rounding does (relative error of both together 1.41 times
+// the latter's alone for long rows of 128 elements, up to 1.7 for heads of 8 or documents of a few tokens, where one key takes
+// most of a row and its dS is the others' sum). With the rest as a second first operand of dQ += dS K and dK += dS^T Q
+// nothing of that is left. Those products are half as wide for heads up to 64, and one tile is all there is of short sequences:
+// fine_grads() takes the second operand there, where it costs little, and not where the first alone is as good
+// (4096 causal tokens of 128: dq 324 against 281 us with it, dk and dv 294 against 264).
+bool fine_grads(int hd, int S) { return hd <= 64 || S <= kTile; }
+
+template <bool CAP, bool BIAS, bool ROW, bool WANT_P, bool FINE>
 __device__ __forceinline__ void grad32(uint32_t (&s)[32], uint32_t (&dp)[32], float mul, float cap_mul, float slope,
                                        float away, int side, bool part, uint32_t see, float c1, float c2,
-                                       const float* col1, const float* col2, uint32_t (&pw)[16], uint32_t (&dw)[16]) {
+                                       const float* col1, const float* col2, uint32_t (&pw)[16],
+                                       uint32_t (&dw)[FINE ? 32 : 16]) {
   uint32_t th[CAP ? 32 : 2];
   if (CAP) {
     tanh_n(s, cap_mul);
@@ -985,7 +996,9 @@ __device__ __forceinline__ void grad32(uint32_t (&s)[32], uint32_t (&dp)[32], fl
       float d0, d1;
       un(ds, d0, d1);
       if (WANT_P) pw[i / 2] = pack2(x0, x1);
-      dw[i / 2] = pack2(d0, d1);
+      const uint32_t d = pack2(d0, d1);
+      dw[i / 2] = d;
+      if (FINE) dw[16 + i / 2] = pack2(d0 - __uint_as_float(d << 16), d1 - __uint_as_float(d & 0xffff0000u));
     }
   }
 }
@@ -1003,7 +1016,7 @@ __device__ __forceinline__ void grad32(uint32_t (&s)[32], uint32_t (&dp)[32], fl
 // 265 us, 8 x 512 tokens 62 us. S and dP formed twice for every tile: 349, 318 and 69 us; K and V in two common stages: 353,
 // 298, 66 (a stage is held from its load to the end of dS K, and the next load waits); dP without its second place: 299.
 // What is left between the products is the chain from a dS over its product to the S that takes its buffer.
-template <bool CAP, bool BIAS>
+template <bool CAP, bool BIAS, bool FINE>
 __global__ void __launch_bounds__(kBwdThreads, 1) masked_dq_kernel(const __grid_constant__ MaskedBwdParams p) {
   extern __shared__ __align__(1024) uint8_t smem_dq[];
   const int nd = p.nd;
@@ -1131,6 +1144,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) masked_dq_kernel(const __grid_
             tc_fence_after();
             const int s = (l0 + (k < min(2, n) ? n - 1 - k : n - 2 + k)) % 3;
             mma_tm<8, 32>(tmem, tmem + 128 + 128 * b, dk0 + s * (2 * kChunk >> 4), id, k > 0);
+            if (FINE) mma_tm<8, 32>(tmem, tmem + 144 + 128 * b, dk0 + s * (2 * kChunk >> 4), id, true);
             umma_commit(&ds_done[b]);
             umma_commit(&k_empty[s]);
           }
@@ -1280,10 +1294,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1) masked_dq_kernel(const __grid_
         if (lane == 0 && !in_dq) mbar_arrive(&dp_read[0]);
         const int k0 = (j1 - 1 - k) * kTile + 32 * cq;
         const bool part = __any_sync(0xffffffffu, lo > k0 || hi < k0 + 32);
-        uint32_t pw[16], dw[16];
-        grad32<CAP, BIAS, true, false>(s, dp, p.mul, p.cap_mul, slope, (float)(qt0 + r - k0), qt0 + 32 * quarter >= k0 + 31,
+        uint32_t pw[16], dw[FINE ? 32 : 16];
+        grad32<CAP, BIAS, true, false, FINE>(s, dp, p.mul, p.cap_mul, slope, (float)(qt0 + r - k0), qt0 + 32 * quarter >= k0 + 31,
                                        part, see_bits(lo - k0, hi - k0), nl, -sum, nullptr, nullptr, pw, dw);
-        tmem_st16(s_tm + 128 * bf, dw);  // over the scores that this warp itself has read
+        // over the scores that this warp itself has read
+        if constexpr (FINE) tmem_st32(s_tm + 128 * bf, dw);
+        else tmem_st16(s_tm + 128 * bf, dw);
         tmem_st_wait();
         tc_fence_before();
         warp_arrive(&ds_full[bf], lane);
@@ -1347,7 +1363,7 @@ __device__ __forceinline__ void st_peer(uint32_t addr, uint32_t v) {
   asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
-template <bool CAP, bool BIAS>
+template <bool CAP, bool BIAS, bool FINE>
 __global__ void __launch_bounds__(kDkvThreads<CAP>, 1) masked_dkv_kernel(const __grid_constant__ MaskedBwdParams p) {
   extern __shared__ __align__(1024) uint8_t smem_dkv[];
   const int nd = p.nd;
@@ -1518,6 +1534,7 @@ __global__ void __launch_bounds__(kDkvThreads<CAP>, 1) masked_dkv_kernel(const _
           const uint64_t bq = dqm0 + s * (2 * kChunk >> 4);
           mma_tm<4, 32>(tmem + 256, tmem + 64 * x, bq + (kChunk >> 4), id, it > 0 || x > 0);
           mma_tm<4, 32>(tmem + 384, tmem + 128 + 64 * x, bq, id, it > 0 || x > 0);
+          if (FINE) mma_tm<4, 32>(tmem + 384, tmem + 144 + 64 * x, bq, id, true);
           umma_commit(&pd_done[x]);
           umma_commit(&qd_empty[s]);
         }
@@ -1550,7 +1567,7 @@ __global__ void __launch_bounds__(kDkvThreads<CAP>, 1) masked_dkv_kernel(const _
       const int side = qt0 >= kt * kTile + 32 * quarter + 31 ? -1 : 0;
 #pragma unroll 1
       for (int c = c0; c < c0 + kCols; ++c) {
-        uint32_t sv[32], dp[32], pw[16], dw[16];
+        uint32_t sv[32], dp[32], pw[16], dw[FINE ? 32 : 16];
         tmem_ld32(s_tm + 32 * c, sv);
         tmem_ld32(dp_tm + 32 * c, dp);
         tmem_ld_wait_regs(sv);
@@ -1565,10 +1582,11 @@ __global__ void __launch_bounds__(kDkvThreads<CAP>, 1) masked_dkv_kernel(const _
             see |= (uint32_t)(w.x <= kpos && kpos < w.y) << e;
           }
         }
-        grad32<CAP, BIAS, false, true>(sv, dp, p.mul, p.cap_mul, slope, (float)(kpos - qt0 - 32 * c), side, part, see, 0.f,
+        grad32<CAP, BIAS, false, true, FINE>(sv, dp, p.mul, p.cap_mul, slope, (float)(kpos - qt0 - 32 * c), side, part, see, 0.f,
                                        0.f, s_lse + col, s_del + col, pw, dw);
         tmem_st16(s_tm + 32 * c, pw);  // over the scores and products that this warp itself has read
-        tmem_st16(dp_tm + 32 * c, dw);
+        if constexpr (FINE) tmem_st32(dp_tm + 32 * c, dw);
+        else tmem_st16(dp_tm + 32 * c, dw);
       }
       tmem_st_wait();
       tc_fence_before();
@@ -1671,15 +1689,15 @@ int fwd_launch(const MaskedFwdParams& p, cudaStream_t s) {
   return 0;
 }
 
-template <bool CAP, bool BIAS>
+template <bool CAP, bool BIAS, bool FINE>
 int bwd_launch(const MaskedBwdParams& p, cudaStream_t s) {
   static std::atomic<uint64_t> done_q{0}, done_kv{0};
-  if (!smem_limit(masked_dq_kernel<CAP, BIAS>, dq_smem(), done_q) ||
-      !smem_limit(masked_dkv_kernel<CAP, BIAS>, dkv_smem(), done_kv))
+  if (!smem_limit(masked_dq_kernel<CAP, BIAS, FINE>, dq_smem(), done_q) ||
+      !smem_limit(masked_dkv_kernel<CAP, BIAS, FINE>, dkv_smem(), done_kv))
     return 5;
   const int n_sm = sm_count();
   if (n_sm <= 0) return 5;
-  launch_kernel(masked_dq_kernel<CAP, BIAS>, (unsigned)std::min(p.n_units, n_sm), kBwdThreads, dq_smem(), s, p);
+  launch_kernel(masked_dq_kernel<CAP, BIAS, FINE>, (unsigned)std::min(p.n_units, n_sm), kBwdThreads, dq_smem(), s, p);
   if (launch_failed("sl_attention_masked")) return 5;
   note_launch();
   cudaLaunchAttribute attr[2];
@@ -1695,10 +1713,14 @@ int bwd_launch(const MaskedBwdParams& p, cudaStream_t s) {
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = pdl_enabled() ? 2 : 1;
-  cudaLaunchKernelEx(&cfg, masked_dkv_kernel<CAP, BIAS>, p);
+  cudaLaunchKernelEx(&cfg, masked_dkv_kernel<CAP, BIAS, FINE>, p);
   if (launch_failed("sl_attention_masked")) return 5;
   note_launch();
   return 0;
+}
+template <bool CAP, bool BIAS>
+int bwd_launch(const MaskedBwdParams& p, cudaStream_t s) {
+  return fine_grads(p.hd, p.S) ? bwd_launch<CAP, BIAS, true>(p, s) : bwd_launch<CAP, BIAS, false>(p, s);
 }
 
 // scale, mul of score() and cap_mul of tanh_n()

@@ -132,6 +132,20 @@ def test_intervals_and_scores(shape, opt):
     assert (got["o"][empty] == 0).all() and (got["dq"][empty] == 0).all() and (got["lse"][:, empty] == -math.inf).all()
 
 
+@pytest.mark.parametrize("n_seq,S,hq,hkv,hd", [(3, 517, 16, 4, 8), (2, 300, 4, 2, 64), (1, 4, 4, 2, 128), (8, 128, 6, 2, 120)])
+def test_fine_gradients(n_seq, S, hq, hkv, hd):
+    """Heads of up to 64 and sequences of up to 128 tokens: dq and dk are as exact as their own rounding to bf16. What is
+    left of dS behind two bf16 is 2^-17 of it; were that 20 times as large against the output (sums that cancel), it would add
+    2e-4 to the rounding's 1.7e-3: sqrt(1 + (0.2 / 1.7)^2) < 1.01 times the rounding's error, 1.05 allowed."""
+    lo, hi, _ = packed_rows([[S]] * n_seq, S, None, 0, DEV)
+    q, k, v, do = inputs(n_seq, S, hq, hkv, hd, S + hd, 0, 2.0)
+    got = call(q, k, v, do, plan_of(lo, hi, n_seq, S), n_seq, hq, hkv, hd)
+    want = reference(q, k, v, do, lo, hi, n_seq, hq, hkv, hd, 0.0, None, 0.0)
+    for n in ("dq", "dk"):
+        w = want[n][0]
+        assert (got[n].double() - w).norm() <= 1.05 * (w.to(BF).double() - w).norm(), n
+
+
 @pytest.mark.parametrize("n_seq,S,hq,hkv,hd", [(2, 300, 4, 2, 64), (1, 1500, 3, 1, 128), (40, 70, 2, 2, 32), (70, 130, 1, 1, 8)])
 def test_random_intervals(n_seq, S, hq, hkv, hd):
     """Any intervals, not monotone, some empty, some out of range (clipped), whole tiles that see nothing."""
