@@ -1359,7 +1359,6 @@ sl_status rotary_args(const int32_t* positions, const float* inv_freq, int32_t r
                       int32_t hd) {
   if (rot_dim > 0 && (!positions || !inv_freq)) return SL_ERR_INVALID_ARG;
   if (!gamma_q != !gamma_k || (style != SL_ROPE_HALVES && style != SL_ROPE_PAIRS)) return SL_ERR_INVALID_ARG;
-  if (rot_dim == 0 && !gamma_q) return SL_ERR_INVALID_ARG;  // nothing to do
   if (n_tok < 1 || n_tok > (int64_t)1 << 31 || hq < 1 || hkv < 1 || hq > 4096 || hkv > 4096 || hd < 8 || hd > 256 ||
       hd % 8 || rot_dim < 0 || rot_dim > hd || rot_dim % 8 || !(eps >= 0.f))
     return SL_ERR_SHAPE;

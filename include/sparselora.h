@@ -425,7 +425,7 @@ SL_API sl_status sl_attention_bwd(const void* q, const void* k, const void* v, c
  *   q, yq, dyq, dq: bf16 [n_tok, n_q_heads * head_dim]; k, yk, dyk, dk: bf16 [n_tok, n_kv_heads *
  *     head_dim]; each with its leading dimension (a multiple of 8, 16-byte aligned base).
  *   positions: int32 [n_tok], of any sign; inv_freq: fp32 [rot_dim / 2]; both may be NULL with rot_dim =
- *     0 (norm only). t is reduced exactly (64-bit fractions of a turn), at any position.
+ *     0 (norm only, or, without gains, a copy). t is reduced exactly (64-bit fractions of a turn), at any position.
  *   gamma_q, gamma_k: bf16 [head_dim], both or neither (NULL: no norm, rotation only).
  * The backward takes the forward's inputs q and k (not read, may be NULL, without gains) and writes
  *   dq, dk and, where given, dgamma_q, dgamma_k (fp32 [head_dim], sums over tokens and heads in a

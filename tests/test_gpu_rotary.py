@@ -71,7 +71,9 @@ CASES = [  # T, hq, hkv, hd, rot, norm, style, far, pad
     (37, 6, 3, 96, 48, True, 1, 0, 16), (65, 5, 1, 40, 40, True, 0, 1 << 20, 0), (64, 3, 1, 256, 256, True, 0, 0, 0),
     (33, 2, 2, 248, 24, True, 0, 5, 0), (130, 8, 8, 128, 0, True, 0, 0, 8), (257, 4, 1, 32, 8, False, 0, -70000, 0),
     (5, 2, 1, 120, 8, True, 1, 0, 0), (700, 4, 2, 128, 64, False, 0, 2 ** 31 - 800, 0), (2, 2, 1, 256, 64, False, 1, 0, 0),
-    (301, 40, 8, 16, 16, True, 1, 3, 0)]
+    (301, 40, 8, 16, 16, True, 1, 3, 0),
+    # neither norm nor rotation: copies
+    (9, 5, 1, 8, 0, False, 0, 0, 0), (70, 4, 2, 8, 0, False, 1, 0, 8), (3, 2, 2, 64, 0, False, 0, 9, 0)]
 
 
 @pytest.mark.parametrize("T,hq,hkv,hd,rot,norm,style,far,pad", CASES)

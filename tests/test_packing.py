@@ -61,7 +61,7 @@ def test_rotation_refuses(lib):
         return f(q, ldq, A, 128, pos, freq, rot, style, gq, gk, eps, T, hq, hkv, hd, A, 256, yk, ldyk, None)
 
     assert fwd(q=None) == fwd(yk=None) == fwd(pos=None) == fwd(freq=None) == B.SL_ERR_INVALID_ARG
-    assert fwd(gq=None) == fwd(style=2) == fwd(rot=0, gq=None, gk=None) == B.SL_ERR_INVALID_ARG
+    assert fwd(gq=None) == fwd(style=2) == B.SL_ERR_INVALID_ARG
     assert fwd(T=0) == fwd(hq=0) == fwd(hkv=0) == fwd(hd=60) == fwd(hd=264) == fwd(hd=0) == B.SL_ERR_SHAPE
     assert fwd(rot=72) == fwd(rot=12) == fwd(rot=-8) == fwd(eps=-1.0) == fwd(eps=float("nan")) == B.SL_ERR_SHAPE
     assert fwd(q=ODD) == fwd(ldq=248) == fwd(ldq=260) == fwd(ldyk=100) == fwd(gq=ODD) == fwd(pos=A + 2) == \
