@@ -229,7 +229,7 @@ def test_forward_is_identical_between_runs_and_streams_and_follows_its_plan_in_a
     with torch.cuda.stream(s):
         got = call(q, k, v, do, plan.buf, n_seq, hq, hkv, hd, B.Workspace())
     s.synchronize()
-    assert all(torch.equal(got[n], want[n]) for n in ("o", "lse", "dk", "dv"))
+    assert all(torch.equal(got[n], want[n]) for n in ("o", "lse", "dq", "dk", "dv"))
     r = {n: torch.empty_like(t) for n, t in want.items()}
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
