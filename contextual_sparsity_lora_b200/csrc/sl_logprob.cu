@@ -312,15 +312,18 @@ __global__ void __launch_bounds__(kLpThreads) logprob_fwd_kernel(const __grid_co
   const int64_t c0 = min(p.vocab, (int64_t)rank * p.seg), c1 = min(p.vocab, c0 + p.seg), n = c1 - c0;
   const int k = p.k;
 
-  // the sums of this thread's chunks, the next chunk's logits on their way
+  // The sums of this thread's chunks; of bf16 the next chunk's logits are on their way (32 bits: the 16 registers are worth
+  // a third block per SM, 301 rows of 32003 15.8 against 19.4 us, 1000 rows of 64000 66 against 68).
+  constexpr bool kAhead = sizeof(T) == 2;
   Sums a = {-3e38f, 0.f, 0.f};
   const int n_chunk = (int)((n + kLpChunk - 1) / kLpChunk);
   KeyOf<T> top_key = 0;  // of this thread's chunks
   Chunk<T> q, q_next;
-  if ((int)threadIdx.x < n_chunk) load16(row, c0 + (int64_t)threadIdx.x * kLpChunk, c1, q_next);
+  if (kAhead && (int)threadIdx.x < n_chunk) load16(row, c0 + (int64_t)threadIdx.x * kLpChunk, c1, q_next);
   for (int c = threadIdx.x; c < n_chunk; c += kLpThreads) {
-    q = q_next;
-    if (c + kLpThreads < n_chunk) load16(row, c0 + (int64_t)(c + kLpThreads) * kLpChunk, c1, q_next);
+    if (kAhead) q = q_next;
+    else load16(row, c0 + (int64_t)c * kLpChunk, c1, q);
+    if (kAhead && c + kLpThreads < n_chunk) load16(row, c0 + (int64_t)(c + kLpThreads) * kLpChunk, c1, q_next);
     const float top = clamp_max(q), m = fmaxf(top, -kHuge);
     if (k > 0) {
       const KeyOf<T> key = chunk_key<T>(top);
