@@ -8,6 +8,14 @@
 // r multiplies the sums by exact powers of two; logp = ln 2 (x_t - log2 s), H = ln 2 (log2 s - w / s).
 // (r, log2 s) of each row go to the backward, which needs nothing else: p_j = 2^(x_j - log2 s).
 //
+// r is a whole number only as far as fp32 holds one next to it: z log2(e) rounds to r by up to half a unit u of r, and
+// the largest x is then not in (-1, 0] but that rest (64 at most where |r| < 2^31: sums below 2^89, nothing lost, log2 s
+// contains it). From |r| >= 2^31 on it would overflow the sums, or empty them; but there two different logits are at
+// least 128 apart, and e^-128 is 0 in fp32 beside 1: the distribution is the maximum's ties alone. A row whose maximum
+// is such a far logit m (masked by -1e10 or -1e30 throughout, or 1e10 itself) keeps r = 4 m, an exact number that
+// stands beyond every near r and in the order of m, with s = w = 0 until the ties are counted at the end, in a second
+// pass over the row. Others pay nothing: one comparison stands for the two with the ends of the range.
+//
 // The top k (k <= 32): while the sums are taken, the maximum of every 16 consecutive logits goes to
 // shared memory. The k largest logits lie in k of these chunks: those whose maximum exceeds the k-th
 // largest maximum, and the first of those that equal it. Their 16 k logits are read again and
@@ -42,6 +50,9 @@ constexpr int kLpFewChunks = 128;
 constexpr float kLog2e = 1.44269504f;
 constexpr float kLn2 = 0.693147181f;
 constexpr float kHuge = 10633823966279326983230456482242756608.f;  // 2^123: logits below -kHuge count as -infinity; one above kHuge makes its row NaN
+constexpr float kNothing = -3e38f;  // reference of sums that hold nothing
+constexpr float kFar = 2147483648.f;  // 2^31, of |z log2(e)|: see above
+constexpr float kFarLogit = 1488522240.f;  // the smallest z whose z log2(e) rounds to 2^31
 
 struct LpParams {
   const void* z;
@@ -56,8 +67,18 @@ struct LpParams {
 };
 
 struct Sums {
-  float r, s, w;  // reference (whole, in powers of two), sum of 2^x, sum of 2^x x
+  float r, s, w;  // reference (whole, in powers of two; of far logits 4 m), sum of 2^x, sum of 2^x x
 };
+
+// z log2(e) rounded to fp32, for itself (not contracted into a multiply-add).
+__device__ __forceinline__ float in_twos(float z) { return __fmul_rn(z, kLog2e); }
+__device__ __forceinline__ bool is_far(float r) { return fabsf(r) >= kFar; }
+// Two neighbouring far logits may round to the same z log2(e) (the factor is below 2), never three. Whether the next
+// larger fp32 number than z does as z:
+__device__ __forceinline__ bool next_same(float z) {
+  const int b = __float_as_int(z);
+  return in_twos(__int_as_float(b + (b < 0 ? -1 : 1))) == in_twos(z);
+}
 
 __device__ __forceinline__ float lp_ex2(float x) {
   float y;
@@ -315,35 +336,40 @@ __global__ void __launch_bounds__(kLpThreads) logprob_fwd_kernel(const __grid_co
   // The sums of this thread's chunks; of bf16 the next chunk's logits are on their way (32 bits: the 16 registers are worth
   // a third block per SM, 301 rows of 32003 15.8 against 19.4 us, 1000 rows of 64000 66 against 68).
   constexpr bool kAhead = sizeof(T) == 2;
-  Sums a = {-3e38f, 0.f, 0.f};
+  Sums a = {kNothing, 0.f, 0.f};
   const int n_chunk = (int)((n + kLpChunk - 1) / kLpChunk);
   KeyOf<T> top_key = 0;  // of this thread's chunks
+  float z_max = -kHuge;  // the largest logit so far; a.r follows from it
   Chunk<T> q, q_next;
   if (kAhead && (int)threadIdx.x < n_chunk) load16(row, c0 + (int64_t)threadIdx.x * kLpChunk, c1, q_next);
   for (int c = threadIdx.x; c < n_chunk; c += kLpThreads) {
     if (kAhead) q = q_next;
     else load16(row, c0 + (int64_t)c * kLpChunk, c1, q);
     if (kAhead && c + kLpThreads < n_chunk) load16(row, c0 + (int64_t)(c + kLpThreads) * kLpChunk, c1, q_next);
-    const float top = clamp_max(q), m = fmaxf(top, -kHuge);
+    const float top = clamp_max(q), m = fmaxf(top, -kHuge), z_new = fmaxf(z_max, m);
     if (k > 0) {
       const KeyOf<T> key = chunk_key<T>(top);
       keys[c] = key;
       top_key = max(top_key, key);
     }
-    if (m == -kHuge) {  // nothing here, or NaN
+    if (fabsf(m) >= kFarLogit) {  // a far maximum, nothing here (all raised to -kHuge), or NaN
 #pragma unroll
       for (int i = 0; i < kLpChunk / 2; ++i) {
         float z0, z1;
         pair_of(q, i, z0, z1);
         if (z0 != z0 || z1 != z1) a.s = __int_as_float(0x7fffffff);
       }
+      z_max = z_new;
       continue;
     }
-    if (m > kHuge) a.s = __int_as_float(0x7fffffff);
-    const float mr = ceilf(m * kLog2e);
-    if (mr > a.r) move_ref(a, mr);
+    const float ref_new = ceilf(in_twos(z_new));
+    if (z_new > z_max) {
+      a.r = ceilf(in_twos(z_max));
+      move_ref(a, ref_new);
+    }
+    z_max = z_new;
     f2 s[2] = {0, 0}, w[2] = {0, 0};
-    const f2 l2e = pk(kLog2e, kLog2e), ref = pk(-a.r, -a.r);
+    const f2 l2e = pk(kLog2e, kLog2e), ref = pk(-ref_new, -ref_new);
 #pragma unroll
     for (int i = 0; i < kLpChunk / 2; ++i) {
       float z0, z1;
@@ -361,6 +387,13 @@ __global__ void __launch_bounds__(kLpThreads) logprob_fwd_kernel(const __grid_co
       un(add2(w[0], w[1]), s0, s1);
       a.w += s0 + s1;
     }
+  }
+  if (fabsf(z_max) >= kFarLogit) {  // what was summed is 0 beside a far logit (NaN stays)
+    a.r = z_max > -kHuge ? 4.f * z_max : kNothing;
+    a.s *= z_max > kHuge ? __int_as_float(0x7fffffff) : 0.f;
+    a.w *= 0.f;
+  } else {
+    a.r = ceilf(in_twos(z_max));
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -407,22 +440,33 @@ __global__ void __launch_bounds__(kLpThreads) logprob_fwd_kernel(const __grid_co
     cluster.sync();  // the others' shared memory has been read
     if (rank != 0) return;
   }
-  const Sums t = sh.mine;
+  Sums t = sh.mine;
+  if (t.s == 0.f && t.r > kNothing) {  // a far row: the maximum's ties
+    int ties = 0;
+    for (int64_t c = threadIdx.x; c < p.vocab; c += kLpThreads) ties += (float)row[c] == 0.25f * t.r;
+    t.s = (float)block_count(sh, 0, ties);
+  }
   const bool none = t.s == 0.f;  // the row has no logit above -infinity
-  const float l2s = none ? 0.f : log2f(t.s);
+  const bool far = t.s >= 1.f && is_far(t.r);  // neither empty nor NaN
+  const float l2s = none ? 0.f : log2f(t.s), m = 0.25f * t.r;  // m: of a far row
+  auto log_p = [&](float z) {
+    return none ? -INFINITY : far ? fmaf(-kLn2, l2s, z - m) : (fmaf(z, kLog2e, -t.r) - l2s) * kLn2;
+  };
   if (threadIdx.x == 0) {
     const int32_t tg = p.target[r];
     float lp = 0.f;
-    if (tg >= 0 && tg < p.vocab) lp = none ? -INFINITY : (fmaf((float)row[tg], kLog2e, -t.r) - l2s) * kLn2;
+    if (tg >= 0 && tg < p.vocab) lp = log_p((float)row[tg]);
     p.logp[r] = lp;
-    p.stats[r] = make_float2(none ? -INFINITY : t.r, l2s);
+    // of a far row m log2(e); log2 s, which is not negative there, has the sign bit when m is the smaller one of two
+    // logits with this value (what that takes from the log sum is below its rounding)
+    p.stats[r] = far ? make_float2(in_twos(m), next_same(m) ? -l2s : l2s) : make_float2(none ? -INFINITY : t.r, l2s);
     if (ENT) p.entropy[r] = none ? 0.f : (l2s - t.w / t.s) * kLn2;
   }
   if (threadIdx.x < k) {
     const unsigned long long b = sh.best[threadIdx.x];
     const float z = from_order_key((uint32_t)(b >> 32));
     p.top_ids[r * k + threadIdx.x] = (int32_t)~(uint32_t)b;
-    p.top_logp[r * k + threadIdx.x] = none ? -INFINITY : (fmaf(z, kLog2e, -t.r) - l2s) * kLn2;
+    p.top_logp[r * k + threadIdx.x] = log_p(z);
   }
 }
 
@@ -452,15 +496,26 @@ __global__ void __launch_bounds__(256) logprob_bwd_kernel(const __grid_constant_
   const float g = has ? p.g_logp[r] : 0.f;
   const float gh = p.g_entropy ? p.g_entropy[r] : 0.f;
   const bool none = st.x == -INFINITY || (g == 0.f && gh == 0.f);
-  const float inv = lp_ex2(-st.y);
+  const bool far = !none && is_far(st.x) && st.y == st.y;  // see logprob_fwd_kernel's stats
+  const float l2s = far ? fabsf(st.y) : st.y;
+  const float inv = lp_ex2(-l2s);
   const float h = gh != 0.f ? p.entropy[r] : 0.f;
-  const float A = inv * (g + gh * (h - st.y * kLn2)), B = inv * gh * kLn2;
+  const float A = inv * (g + gh * (h - l2s * kLn2)), B = inv * gh * kLn2;
   auto grad = [&](float z, int64_t c) {
     const float x = fmaf(z, kLog2e, -st.x);
     const float e = lp_ex2(x);
     const float d = -e * fmaf(B, fmaxf(x, -1000.f), A);
     return c == t ? d + g : d;
   };
+  if (far) {
+    const bool lower = signbit(st.y);
+    for (int64_t c = c0 + threadIdx.x; c < c1; c += 256) {
+      const float z = (float)row[c];
+      const float d = in_twos(z) == st.x && (lower || !next_same(z)) ? -A : 0.f;
+      out[c] = (T)(c == t ? d + g : d);
+    }
+    return;
+  }
   for (int64_t c = c0 + (int64_t)threadIdx.x * kVec; c < c1; c += 256 * kVec) {
     if (c + kVec <= c1) {
       uint4 w = make_uint4(0u, 0u, 0u, 0u);

@@ -490,14 +490,15 @@ SL_API sl_status sl_attention_masked_bwd(const void* q, int64_t ldq, const void*
  *   logits: bf16 or fp32 [n_rows, vocab] (ld elements, 16-byte aligned rows); targets: int32 [n_rows]; a target
  *     outside [0, vocab) names no token: its logp is 0 and has no gradient.
  *   sl_token_logprobs_fwd: logp[r] = z_t - log sum_j e^(z_j); stats[r] = two floats for the backward, with
- *     log sum_j e^(z_j) = ln 2 (stats[r][0] + stats[r][1]); entropy[r] (optional) = -sum_j p_j log p_j;
+ *     log sum_j e^(z_j) = ln 2 (stats[r][0] + stats[r][1]) to fp32; entropy[r] (optional) = -sum_j p_j log p_j;
  *     with top_k > 0 (<= 32, <= vocab): top_ids[r], top_logp[r] ([n_rows, top_k], dense): the tokens of the largest
  *     logits, largest first, equal ones by the lower index, NaN below every number.
  *   sl_token_logprobs_bwd: dlogits (the logits' type, leading dimension ldd; may be the logits themselves) of
  *     the loss whose gradients are g_logp[r] at logp and, optionally, g_entropy[r] at entropy (then entropy is
  *     the forward's): dz_j = g_logp ([j = t] - p_j) - g_entropy p_j (log p_j + entropy). A row whose gradients
  *     are both 0 (or that has no target and no g_entropy) gets zeros. Columns from vocab to ldd are left as they were.
- * Logits below -2^123 (about -1e37) count as -inf (probability 0, no gradient). A row with nothing above that: logp =
+ * Logits of any finite value (masks of -1e9 or -1e30 too, and rows of nothing else), but those below -2^123 (about
+ * -1e37) count as -inf (probability 0, no gradient). A row with nothing above that: logp =
  * -inf (0 without a target), entropy 0, top_logp = -inf, no gradient. A row with NaN, +inf or a logit above 2^123: NaN
  * results. Sums in fp32 in a fixed order (run-to-run identical). Errors: SL_ERR_INVALID_ARG, SL_ERR_SHAPE (vocab up to 2^24,
  * with top_k up to 6553600 fp32 or 13107200 bf16 columns), SL_ERR_ALIGNMENT. */

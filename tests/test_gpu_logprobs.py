@@ -229,3 +229,76 @@ def test_refuses_what_is_not_rows():
         with pytest.raises(B.SparseLoRAError) as e:
             call()
         assert e.value.code == B.SL_ERR_INVALID_ARG
+
+
+FILLS = (-1e4, -1e9, -1e10, -1e20, -1e30, -1e36)
+
+
+@pytest.mark.parametrize("V", [100, 9000, 131072])
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "fp32"])
+def test_finite_masks(dtype, V):
+    """Rows masked by ordinary large numbers: whole chunks of them before, behind and between what is left, a whole
+    CTA's part of a row that a cluster shares, and a target that is masked."""
+    z, t, g, gh = make(5 * len(FILLS), V, dtype, V + 1, 2.0)
+    for i, fill in enumerate(FILLS):
+        a, b, c, d, e = range(5 * i, 5 * i + 5)
+        z[a, : V // 3] = fill
+        z[b, : V - 7] = fill
+        z[c, V // 2:] = fill
+        z[d, 5: V - 2] = fill
+        z[e, 1:] = fill                         # one token has all
+        t[a], t[e] = V // 3 - 1, 0
+    check(z, t, 8, g, gh)
+    check(z[:2], t[:2], 8, g[:2], gh[:2])       # few rows: clusters
+    check(z[20:22], t[20:22], 8, g[20:22], gh[20:22])
+
+
+def shifted_reference(z, t, plain=reference):
+    """reference() about each row's maximum: beside 1e20 a 64-bit log-sum has lost log(V) (its unit is 2^14)."""
+    top = z.double().amax(1, keepdim=True)
+    lse, logs, p, plogp, H, logp, has, at = plain(z.double() - top, t)
+    return lse + top[:, 0], logs, p, plogp, H, logp, has, at
+
+
+@pytest.mark.parametrize("V", [1, 100, 9000, 131072])
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "fp32"])
+def test_rows_of_far_logits(monkeypatch, dtype, V):
+    """Rows whose maximum itself is large: all equal, masks of several kinds and nothing else, one above the rest, a
+    maximum that comes in many places, neighbouring numbers (which fp32 cannot tell apart times log2 e)."""
+    monkeypatch.setitem(globals(), "reference", shifted_reference)
+    far = [s * v for v in (1e9, 1.4e9, 1.6e9, 1e10, 3e15, 1e20, 1e30, 1e36) for s in (1.0, -1.0)]
+    z, t, g, gh = make(len(far) + 8, V, dtype, V + 2, 2.0)
+    for i, v in enumerate(far):
+        z[i] = v
+    n = len(far)
+    z[n] = -1e30
+    z[n, V // 2:] = -1e10
+    z[n + 1] = -1e10
+    z[n + 1, ::3] = -1e20
+    z[n + 2, V // 2] = 1e10                     # one far logit over ordinary ones
+    z[n + 3, ::5] = 1e20
+    for i, v in ((4, 3e9), (5, -3e9), (6, 2.2e9), (7, -1.2e10)):
+        x = torch.full((V,), v, dtype=dtype)
+        bits = x.view(torch.int16 if dtype == BF else torch.int32)
+        bits += torch.arange(V, dtype=bits.dtype) % 7
+        z[n + i] = x.to(DEV)
+    t[: n] = torch.arange(n, dtype=torch.int32).to(DEV) % V
+    t[n + 4:] = torch.arange(4, dtype=torch.int32).to(DEV) % V
+    check(z, t, min(8, V), g, gh)
+    check(z[2:4], t[2:4], min(8, V), g[2:4], gh[2:4])
+    check(z[n + 5: n + 6], t[n + 5: n + 6], min(8, V), g[n + 5: n + 6], gh[n + 5: n + 6])
+
+
+def test_far_logits_beside_nan_and_infinity():
+    z, t, g, gh = make(4, 600, F32, 5)
+    z[0], z[1], z[2], z[3] = -1e30, 1e20, -1e20, -1e30
+    z[0, 300], z[1, 301] = math.nan, math.inf
+    z[2, 302], z[3, 303] = 2e37, -math.inf      # above 2^123; -inf counts as nothing
+    t[3] = 303
+    logp, stats, ent, ids, top = run_fwd(z, t, 3)
+    d = torch.empty_strided(z.shape, z.stride(), dtype=z.dtype, device=DEV)
+    B.sl_token_logprobs_bwd(z, t, stats, g, d, gh, ent)
+    assert logp[:3].isnan().all() and ent[:3].isnan().all() and d[:3].isnan().all()
+    assert logp[3] == -math.inf and abs(ent[3] - math.log(599)) <= 2.0 ** -12 and d[3].isfinite().all()
+    assert torch.equal(ids[3], torch.tensor([0, 1, 2], dtype=torch.int32, device=DEV))
+    assert (top[3] + math.log(599)).abs().max() <= 2.0 ** -16
