@@ -305,22 +305,26 @@ __device__ __forceinline__ f2 add2(f2 a, f2 b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
+// Maxima that are NaN where one of the values is
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float max2(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
 // 2^x of two values on the multiply-add units: x = n + f with a whole n and |f| <= 1/2, 2^f a polynomial of degree 5 (least
-// maximum of the relative error with the constant 1: 9e-8, 1.6e-7 with fp32 arithmetic, about ex2.approx's), n added
+// maximum of the relative error with the constant 1: 1.1e-7, 1.6e-7 with fp32 arithmetic, about ex2.approx's), n added
 // to its exponent. From -127 down: 0 (the exponent of 1 less 127 leaves no bit). 1.5 * 2^23 + x keeps n in its low
-// bits. A quarter of the forward's exponentials, which otherwise wait for the exponential unit (8192 tokens with a bias 537 against 576 us, 4096 causal 131 against 135;
+// bits. NaN gives some number: the row's maximum keeps it. A quarter of the forward's exponentials, which otherwise wait for the exponential unit (8192 tokens with a bias 537 against 576 us, 4096 causal 131 against 135;
 // an eighth 555, three eighths 543, half 585); with a cap, whose tanh is on the same units, and in the backward it gains nothing.
 __device__ __forceinline__ void ex2_poly(f2 x, float& y0, float& y1) {
   float x0, x1;
   un(x, x0, x1);
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(x0) : "f"(x0), "f"(-127.f));
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(x1) : "f"(x1), "f"(-127.f));
-  x = pk(x0, x1);
+  x = pk(fmaxf(x0, -127.f), fmaxf(x1, -127.f));
   const f2 t = add2(x, both(12582912.f)), f = fma2(add2(t, both(-12582912.f)), both(-1.f), x);
   f2 r = fma2(f, both(0.0013264727f), both(0.009671513f));
   r = fma2(f, r, both(0.055507336f));
@@ -368,7 +372,7 @@ __device__ __forceinline__ float max32(const uint32_t (&v)[32]) {
 #pragma unroll
   for (int e = 0; e < 32; e += 2)
     mx[(e >> 1) & 3] = max3(mx[(e >> 1) & 3], __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
-  return fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
+  return max2(max3(mx[0], mx[1], mx[2]), mx[3]);
 }
 
 // The score in powers of two from a raw product (with a cap: its tanh) v: mul = log2(e) scale, or log2(e) cap. away:
@@ -837,11 +841,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1) masked_fwd_kernel(const __grid
           mask32(s[0], see_bits(lo - k0, hi - k0));
           mask32(s[1], see_bits(lo - k0 - 32, hi - k0 - 32));
         }
-        const float mj = fmaxf(max32(s[0]), max32(s[1])) * mul;
+        // A NaN or +inf score makes its row's maximum NaN, and with it o and lse, whatever ex2_poly makes of it.
+        float mj = max2(max32(s[0]), max32(s[1])) * mul;
+        if (mj == INFINITY) mj = NAN;
         // The running maximum moves only when a row's maximum grows by more than 2^8: the exponentials then
         // stay below 256 and O and l keep one common reference, so O is rescaled rarely.
-        const float m_cand = fmaxf(m, mj);
-        const bool grow = m == -INFINITY || m_cand - m > 8.0f;
+        const float m_cand = max2(m, mj);
+        const bool grow = !(m_cand - m <= 8.0f);  // also from a row that has seen nothing, and to NaN
         const float m_new = grow ? m_cand : m;
         const float mb = m_new == -INFINITY ? 0.f : m_new;  // a row that has seen nothing yet
         const float corr = grow && m != -INFINITY ? ex2(m - mb) : 1.f;  // O and l of a row that saw nothing are 0

@@ -296,3 +296,53 @@ def test_formula_gradient_against_differences():
     diff = (f(*up) - f(*down)) / (2 * h)
     want = sum((r[n][0] * d).sum() for n, d in zip(("dq", "dk", "dv"), e))
     assert abs(diff - want) <= 1e-7 * sum((r[n][0] * d).abs().sum() for n, d in zip(("dq", "dk", "dv"), e))
+
+
+@pytest.mark.parametrize("kw", [{}, dict(slopes=True), dict(softcap=5.0)], ids=["plain", "bias", "cap"])
+def test_nan_and_infinite_scores_show_in_their_rows(kw):
+    """A NaN in a key (at each place of a tile) or in a query: o and lse of the rows that see it are NaN throughout, the
+    others are what they were. A score of +inf too (without a cap, whose tanh is 1 there). With a cap a warp's largest
+    score chooses the form of its tanh, so the others' scores may change by both forms' errors, 5 x 2 x 2^-22 < 2^-18 (lse
+    by that, P by a step of 2^-8 in the rows' sum of at most max |v|, o's own rounding by another)."""
+    n_seq, S, hq, hkv, hd = 1, 300, 2, 1, 64
+    if kw.get("slopes"):
+        kw = dict(slopes=torch.tensor([0.5, 0.25], device=DEV))
+    q, k, v, do = inputs(n_seq, S, hq, hkv, hd, 11)
+    at = torch.arange(S, dtype=torch.int32, device=DEV)
+    plan, ws = plan_of((at - 150).clamp(min=0), at + 1, n_seq, S), B.Workspace()
+
+    def forward(q, k):
+        o, lse = torch.empty_like(q), torch.empty(hq, S, device=DEV)
+        B.sl_attention_masked_fwd(ws, q, k, v, n_seq, hq, hkv, hd, plan, o, lse, **kw)
+        assert ws.read_device_flag() == 0
+        return o, lse
+
+    def same(got, want):
+        if not kw.get("softcap"):
+            return torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        return ((got[0] - want[0]).abs() <= 2.0 ** -7 * v.abs().max()).all() and \
+            ((got[1] - want[1]).abs() <= 2.0 ** -18).all()
+
+    o, lse = forward(q, k)
+    for j in (*range(72), 127, 128, 190, 255, 299):
+        bad = k.clone()
+        bad[j, j % hd] = math.nan
+        sees = (at >= j) & (at - 150 <= j)
+        ob, lseb = forward(q, bad)
+        assert ob[sees].isnan().all() and lseb[:, sees].isnan().all(), j
+        assert same((ob[~sees], lseb[:, ~sees]), (o[~sees], lse[:, ~sees])), j
+        bad = q.clone()
+        bad[j, hd + 3] = math.nan               # of the second head
+        ob, lseb = forward(bad, k)
+        assert ob[j, hd:].isnan().all() and lseb[1, j].isnan()
+        ob[j, hd:], lseb[1, j] = o[j, hd:], lse[1, j]
+        assert same((ob, lseb), (o, lse)), j
+        if not kw.get("softcap"):
+            bad, one = k.clone(), q.clone()
+            bad[j], one[:, :hd] = 0.0, q[:, :hd].abs()
+            bad[j, 5] = math.inf
+            one[j, 5] = 1.0
+            want, (ob, lseb) = forward(one, k), forward(one, bad)
+            hit = sees & (one[:, 5] > 0)
+            assert hit[j] and ob[hit, :hd].isnan().all() and lseb[0, hit].isnan().all(), j
+            assert same((ob[~sees], lseb[:, ~sees]), (want[0][~sees], want[1][:, ~sees])), j
