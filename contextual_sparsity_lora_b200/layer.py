@@ -35,7 +35,8 @@ class DecoderLayer:
         RMSNorm gains [D]; perm: int64 [n_tok], context-first position p holds sequence-order row
         perm[p] (rows of n_seq sequences of equal length).
         rope: (positions int32 [n_tok] in sequence order, inv_freq fp32 [rot_dim / 2], style
-        SL_ROPE_HALVES or SL_ROPE_PAIRS); qk_norm: frozen gains (gq, gk) [head_dim]; plan: which keys each
+        SL_ROPE_HALVES or SL_ROPE_PAIRS; int32 positions on the layer's device are used in place, so layers
+        share them, others are copied; set_positions changes them); qk_norm: frozen gains (gq, gk) [head_dim]; plan: which keys each
         token sees; softcap, slopes [n_q_heads]: see sl_attention_masked_fwd (without a plan: causal)."""
         dev = attn.device
         self.attn, self.ffn = attn, ffn
@@ -81,6 +82,14 @@ class DecoderLayer:
             plan = AttentionPlan(self.n_seq, self.S, dev)
         self.plan = plan
         self.ws = B.Workspace(dev)  # the attention core's scratch (the dq accumulator) and error word
+
+    def set_positions(self, positions):
+        """The positions of the next batches' tokens (whole numbers [n_tok], sequence order, any device), written into
+        the tensor that this layer and those that share it read; a captured graph follows it."""
+        t = torch.as_tensor(positions)
+        if self.positions is None or t.shape != self.positions.shape or t.is_floating_point():
+            raise ValueError("positions are whole numbers, one per token, of a layer that rotates")
+        self.positions.copy_(t)
 
     def _to_seq(self, src, dst, name):
         """Context-first rows -> sequence order; with the block's sigma layout, the context rows'

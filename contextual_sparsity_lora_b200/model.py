@@ -73,7 +73,8 @@ class SparseLoRAModel:
         every layer or a list of such dicts (one per layer); loras: per layer a dict of (A, B);
         gammas: per layer (g1, g2); keep: per layer (attn_keep, ffn_keep); perm: context-first
         row order of the batch (n_seq sequences); heads: (n_q_heads, n_kv_heads, head_dim).
-        rope, plan, softcap, slopes: DecoderLayer's options, the same for every layer; qk_norms: per
+        rope, plan, softcap, slopes: DecoderLayer's options, the same for every layer (one copy of the
+        positions and one plan for all; set_rows changes both from batch to batch); qk_norms: per
         layer (gq, gk); loss: "library" or "kernels" (see above)."""
         if loss not in ("library", "kernels"):
             raise ValueError('loss is "library" or "kernels"')
@@ -89,6 +90,11 @@ class SparseLoRAModel:
         self.lm_head = frozen["lm_head"].to(device=device, dtype=bf).contiguous()
         self.gamma_f = frozen["gamma_f"].to(device=device, dtype=bf).contiguous()
         self.D = self.embed.shape[1]
+        if rope is not None:
+            rope = (torch.as_tensor(rope[0]).to(device=device, dtype=torch.int32).contiguous(), *rope[1:])
+        if plan is None and (softcap > 0 or slopes is not None):
+            plan = AttentionPlan(n_seq, T // n_seq, device)
+        self.plan = plan
         self.layers = []
         for i in range(self.n_layers):
             w = frozen["layers"][i] if "layers" in frozen else frozen
@@ -111,6 +117,21 @@ class SparseLoRAModel:
         self.rstd_f = e(T, dt=torch.float32)
         self.loss = torch.zeros((), dtype=torch.float32, device=device)
         self.loss_kernels = loss == "kernels"
+
+    def set_rows(self, row_lo, row_hi, positions=None):
+        """What the tokens of the next batches see and where they stand, as packed_rows gives it (whole numbers [T] in
+        sequence order, on any device; row_lo or row_hi None: see AttentionPlan.set). A model that rotates needs the
+        positions with them. Captured steps follow both."""
+        lay = self.layers[0]
+        if self.plan is None or (positions is None) != (lay.positions is None):
+            raise ValueError("set_rows needs a model with a plan, and positions exactly when it rotates")
+        rows = [None if r is None else torch.as_tensor(r).to(device=self.device, dtype=torch.int32).contiguous()
+                for r in (row_lo, row_hi)]
+        if any(r is not None and r.shape != (self.T,) for r in rows):
+            raise ValueError("row_lo and row_hi are one number per token")
+        if positions is not None:
+            lay.set_positions(positions)
+        self.plan.set(*rows)
 
     def set_dense(self, on: bool):
         for lay in self.layers:

@@ -165,3 +165,63 @@ def test_options_that_do_not_fit_are_refused():
         with pytest.raises(ValueError):
             SparseLoRAModel(p["frozen"], p["loras"], p["gammas"], keep, p["perm"], p["C"], p["n_seq"], p["heads"], 8, 2.0,
                             DEV, **kw)
+
+
+def test_rows_and_positions_change_from_batch_to_batch():
+    """Two packed batches through one model, positions and rows as packed_rows gives them (on the CPU): the second gives
+    what a model built for it gives; and back."""
+    keep = [(1.0, 1.0), (0.5, 0.5)]
+    p = build(keep, seed=85)
+    hq, hkv, hd = p["heads"]
+    n_seq, S = p["n_seq"], len(p["perm"]) // p["n_seq"]
+    freq = torch.tensor([1000.0 ** (-4 * i / hd) for i in range(hd // 4)])
+    batches = [packed_rows([[S - 21, 12], [9, S - 9]], S, [[5, 0], [0, 11]]), packed_rows([[7, 20, S - 27], [S]], S)]
+
+    def model(batch):
+        plan = AttentionPlan(n_seq, S)
+        plan.set(batch[0].to(DEV), batch[1].to(DEV))
+        return SparseLoRAModel(p["frozen"], p["loras"], p["gammas"], keep, p["perm"], p["C"], n_seq, p["heads"], 8, 2.0,
+                               DEV, rope=(batch[2], freq, B.SL_ROPE_PAIRS), plan=plan, loss="kernels")
+
+    pt = torch.from_numpy(p["perm"])
+    ids, targets = p["ids"][pt].to(torch.int32).to(DEV), p["targets"].to(DEV)
+
+    def step(m):
+        loss = m.forward_backward(ids, targets).clone()
+        return [loss, *(lay.attn.dA[n].clone() for lay in m.layers for n in "qkvo")]
+
+    one = model(batches[0])
+    assert one.layers[0].positions is one.layers[1].positions
+    first, second = step(one), step(model(batches[1]))
+    assert not torch.equal(first[0], second[0])
+    one.set_rows(*batches[1])
+    assert all(torch.equal(a, b) for a, b in zip(step(one), second))
+    one.set_rows(*(t.to(DEV) for t in batches[0]))
+    assert all(torch.equal(a, b) for a, b in zip(step(one), first))
+    lo, hi, pos = batches[0]
+    for args in ((lo, hi), (lo, hi, pos[1:]), (lo[1:], hi, pos), (lo, hi, pos.float())):
+        with pytest.raises(ValueError):
+            one.set_rows(*args)
+    assert all(torch.equal(a, b) for a, b in zip(step(one), first))  # a refused call changes nothing
+    with pytest.raises(ValueError):
+        p["model"].set_rows(lo, hi)
+    with pytest.raises(ValueError):
+        p["model"].layers[0].set_positions(pos)
+
+
+def test_score_options_without_a_plan_share_one():
+    """softcap alone: the layers' causal plan is one, and set_rows changes it."""
+    keep = [(0.5, 0.5), (0.5, 0.5)]
+    p = build(keep, seed=86)
+    m = SparseLoRAModel(p["frozen"], p["loras"], p["gammas"], keep, p["perm"], p["C"], p["n_seq"], p["heads"], 8, 2.0, DEV,
+                        softcap=4.0)
+    assert m.layers[0].plan is m.layers[1].plan is m.plan
+    pt = torch.from_numpy(p["perm"])
+    ids, targets = p["ids"][pt].to(torch.int32).to(DEV), p["targets"].to(DEV)
+    causal = m.forward_backward(ids, targets).clone()
+    S = m.layers[0].S
+    lo, hi, _ = packed_rows([[S - 20, 20]] * p["n_seq"], S)
+    m.set_rows(lo, hi)
+    assert not torch.equal(m.forward_backward(ids, targets), causal)
+    m.set_rows(None, None)
+    assert torch.equal(m.forward_backward(ids, targets), causal)
