@@ -182,10 +182,12 @@ def _check(fn, code):
         raise SparseLoRAError(fn, code)
 
 
-# the current device and the raw handle of its current stream (what torch.cuda.current_device() and
-# torch.cuda.current_stream().cuda_stream give, without the Python objects in between: 3 us of a call)
-_current_device = getattr(torch._C, "_cuda_getDevice", None)
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# The current device and the raw handle of its current stream: what torch.cuda.current_device() and
+# torch.cuda.current_stream().cuda_stream give, without the Python objects in between (3 us of a call), where this
+# torch has the names for it.
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
 def _ptr(t):

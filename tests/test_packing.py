@@ -140,3 +140,18 @@ def test_wrappers_refuse_what_the_library_cannot_see():
         assert e.value.code == B.SL_ERR_INVALID_ARG
     with pytest.raises(B.SparseLoRAError):
         B.attention_plan_buffer(0, 64, "cpu")
+
+
+def test_streams_without_torchs_private_names(monkeypatch):
+    """Where torch has no _cuda_getDevice or _cuda_getCurrentRawStream, its public calls serve."""
+    import importlib.util
+    import types
+
+    for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"):
+        monkeypatch.delattr(torch._C, name, raising=False)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device: types.SimpleNamespace(cuda_stream=100 + device))
+    spec = importlib.util.spec_from_file_location("binding_without_private_names", B.__file__)
+    copy = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(copy)
+    assert copy._current_device() == 3 and copy._raw_stream(3) == 103 and copy._stream().value == 103
