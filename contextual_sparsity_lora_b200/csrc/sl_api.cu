@@ -5,6 +5,7 @@
 #include <cmath>
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 #include <string>
 #include <vector>
@@ -424,6 +425,12 @@ sl_status sl_wanda_scores(const void* x, int64_t n_ctx, int64_t d_in, int64_t ld
 // ------------------------------------------------------------------ decoder layer pieces
 namespace {
 bool rows_ok(const void* p, int64_t ld, int64_t d) { return p && al16(p) && ld >= d && ld % 8 == 0; }
+// 32-bit values that are read and written one by one (null: aligned)
+bool al4(std::initializer_list<const void*> ps) {
+  uintptr_t low = 0;
+  for (const void* p : ps) low |= reinterpret_cast<uintptr_t>(p);
+  return (low & 3) == 0;
+}
 }  // namespace
 
 sl_status sl_rmsnorm_fwd(const void* x, int64_t ldx, const void* res, int64_t ldr, void* sum_out, int64_t lds,
@@ -1300,8 +1307,7 @@ sl_status sl_attention_plan(const int32_t* row_lo, const int32_t* row_hi, int32_
                             int64_t plan_bytes, sl_stream stream) {
   if (!plan) return SL_ERR_INVALID_ARG;
   if (!plan_sizes_ok(n_seq, seq_len) || plan_bytes < attention_plan_bytes(n_seq, seq_len)) return SL_ERR_SHAPE;
-  if (!al16(plan) || (reinterpret_cast<uintptr_t>(row_lo) & 3) || (reinterpret_cast<uintptr_t>(row_hi) & 3))
-    return SL_ERR_ALIGNMENT;
+  if (!al16(plan) || !al4({row_lo, row_hi})) return SL_ERR_ALIGNMENT;
   return from_kernel(attention_plan(row_lo, row_hi, n_seq, seq_len, plan, cs(stream)));
 }
 
@@ -1314,7 +1320,8 @@ sl_status sl_attention_masked_fwd(const void* q, int64_t ldq, const void* k, int
   if (sl_status st = masked_args(n_seq, seq_len, n_q_heads, n_kv_heads, head_dim, scale, softcap, plan, plan_bytes))
     return st;
   const int64_t nq = (int64_t)n_q_heads * head_dim, nk = (int64_t)n_kv_heads * head_dim;
-  if (!rows_ok(q, ldq, nq) || !rows_ok(k, ldk, nk) || !rows_ok(v, ldv, nk) || !rows_ok(o, ldo, nq) || !al16(lse))
+  if (!rows_ok(q, ldq, nq) || !rows_ok(k, ldk, nk) || !rows_ok(v, ldv, nk) || !rows_ok(o, ldo, nq) || !al16(lse) ||
+      !al4({slopes}))
     return SL_ERR_ALIGNMENT;
   if (sl_status st = ws_check(ws, kWorkspaceHeaderBytes)) return st;
   MaskedArgs a = {};
@@ -1335,7 +1342,8 @@ sl_status sl_attention_masked_bwd(const void* q, int64_t ldq, const void* k, int
     return st;
   const int64_t nq = (int64_t)n_q_heads * head_dim, nk = (int64_t)n_kv_heads * head_dim;
   if (!rows_ok(q, ldq, nq) || !rows_ok(k, ldk, nk) || !rows_ok(v, ldv, nk) || !rows_ok(d_o, lddo, nq) ||
-      !rows_ok(dq, lddq, nq) || !rows_ok(dk, lddk, nk) || !rows_ok(dv, lddv, nk) || !al16(lse))
+      !rows_ok(dq, lddq, nq) || !rows_ok(dk, lddk, nk) || !rows_ok(dv, lddv, nk) || !al16(lse) ||
+      !al4({slopes}))
     return SL_ERR_ALIGNMENT;
   const size_t scratch = attention_masked_scratch(n_seq, seq_len, n_q_heads);
   Carver c(nullptr);
@@ -1362,9 +1370,7 @@ sl_status rotary_args(const int32_t* positions, const float* inv_freq, int32_t r
   if (n_tok < 1 || n_tok > (int64_t)1 << 31 || hq < 1 || hkv < 1 || hq > 4096 || hkv > 4096 || hd < 8 || hd > 256 ||
       hd % 8 || rot_dim < 0 || rot_dim > hd || rot_dim % 8 || !(eps >= 0.f))
     return SL_ERR_SHAPE;
-  if ((reinterpret_cast<uintptr_t>(positions) & 3) || (reinterpret_cast<uintptr_t>(inv_freq) & 3) ||
-      !al16(gamma_q) || !al16(gamma_k))
-    return SL_ERR_ALIGNMENT;
+  if (!al4({positions, inv_freq}) || !al16(gamma_q) || !al16(gamma_k)) return SL_ERR_ALIGNMENT;
   return SL_OK;
 }
 }  // namespace
@@ -1400,7 +1406,7 @@ sl_status sl_qk_norm_rope_bwd(const void* dyq, int64_t lddyq, const void* dyk, i
     return st;
   const int64_t nq = (int64_t)n_q_heads * head_dim, nk = (int64_t)n_kv_heads * head_dim;
   if (!rows_ok(dyq, lddyq, nq) || !rows_ok(dyk, lddyk, nk) || !rows_ok(dq, lddq, nq) || !rows_ok(dk, lddk, nk) ||
-      (gamma_q && (!rows_ok(q, ldq, nq) || !rows_ok(k, ldk, nk))))
+      (gamma_q && (!rows_ok(q, ldq, nq) || !rows_ok(k, ldk, nk))) || !al4({dgamma_q, dgamma_k}))
     return SL_ERR_ALIGNMENT;
   RotaryArgs a = {};
   if (dgamma_q || dgamma_k) {
@@ -1435,7 +1441,9 @@ sl_status sl_token_logprobs_fwd(sl_dtype dtype, const void* logits, int64_t ld, 
   if (!logits || !targets || !logp || !stats || (dtype != SL_DT_BF16 && dtype != SL_DT_F32)) return SL_ERR_INVALID_ARG;
   if (top_k > 0 && (!top_ids || !top_logp)) return SL_ERR_INVALID_ARG;
   if (!logprob_sizes_ok(n_rows, vocab) || top_k < 0 || top_k > 32 || top_k > vocab) return SL_ERR_SHAPE;
-  if (!logits_ok(logits, ld, vocab, dtype) || (reinterpret_cast<uintptr_t>(stats) & 7)) return SL_ERR_ALIGNMENT;
+  if (!logits_ok(logits, ld, vocab, dtype) || (reinterpret_cast<uintptr_t>(stats) & 7) ||
+      !al4({targets, logp, entropy, top_ids, top_logp}))
+    return SL_ERR_ALIGNMENT;
   LogprobArgs a = {};
   a.z = logits, a.fp32 = dtype == SL_DT_F32, a.ld = ld, a.rows = n_rows, a.vocab = vocab, a.target = targets;
   a.logp = logp, a.stats = stats, a.entropy = entropy, a.k = top_k, a.top_ids = top_ids, a.top_logp = top_logp;
@@ -1451,7 +1459,7 @@ sl_status sl_token_logprobs_bwd(sl_dtype dtype, const void* logits, int64_t ld, 
     return SL_ERR_INVALID_ARG;
   if (!logprob_sizes_ok(n_rows, vocab)) return SL_ERR_SHAPE;
   if (!logits_ok(logits, ld, vocab, dtype) || !logits_ok(dlogits, ldd, vocab, dtype) ||
-      (reinterpret_cast<uintptr_t>(stats) & 7))
+      (reinterpret_cast<uintptr_t>(stats) & 7) || !al4({targets, g_logp, g_entropy, entropy}))
     return SL_ERR_ALIGNMENT;
   LogprobArgs a = {};
   a.z = logits, a.fp32 = dtype == SL_DT_F32, a.ld = ld, a.rows = n_rows, a.vocab = vocab, a.target = targets;

@@ -432,7 +432,7 @@ SL_API sl_status sl_attention_bwd(const void* q, const void* k, const void* v, c
  *   fixed order; workspace: 1186 * head_dim floats past the header, ws may be NULL without them).
  * An output may be its input (same pointer and leading dimension: yq = q, dq = dyq); no other overlap. fp32
  * arithmetic, each output rounded once. head_dim in [8, 256], a multiple of 8; rot_dim a multiple of 8
- * up to head_dim. */
+ * up to head_dim. Gains start on 16 bytes, 32-bit values on 4. */
 SL_API sl_status sl_qk_norm_rope_fwd(const void* q, int64_t ldq, const void* k, int64_t ldk, const int32_t* positions,
                                      const float* inv_freq, int32_t rot_dim, int32_t style, const void* gamma_q,
                                      const void* gamma_k, float eps, int64_t n_tok, int32_t n_q_heads,
@@ -467,7 +467,7 @@ SL_API sl_status sl_qk_norm_rope_bwd(const void* dyq, int64_t lddyq, const void*
  * row, those that nobody sees too (a product of tiles multiplies them by zero); a row with a NaN score, or one of
  * +inf without a cap, has NaN in o and lse. head_dim in [8, 128], a multiple of 8; seq_len <= 2^20; n_q_heads a
  * multiple of n_kv_heads; at most 2^30 pairs of a query head and a tile of 128 rows (each sequence begins one);
- * pointers 16-byte aligned, leading dimensions multiples of 8. Errors: SL_ERR_INVALID_ARG (null pointer),
+ * pointers 16-byte aligned (slopes 4), leading dimensions multiples of 8. Errors: SL_ERR_INVALID_ARG (null pointer),
  * SL_ERR_SHAPE (a size, scale or cap out of range, a plan buffer too small), SL_ERR_ALIGNMENT, SL_ERR_WORKSPACE. A buffer that holds no plan of the
  * call's sizes is seen on the device: nothing is computed, and the workspace's error word says so. */
 SL_API int64_t sl_attention_plan_bytes(int32_t n_seq, int32_t seq_len);
@@ -487,8 +487,8 @@ SL_API sl_status sl_attention_masked_bwd(const void* q, int64_t ldq, const void*
 
 /* Log probabilities of given tokens, entropy and top alternatives of rows of logits, and their gradient
  * (the loss at the LM head, and the scores of a generation).
- *   logits: bf16 or fp32 [n_rows, vocab] (ld elements, 16-byte aligned rows); targets: int32 [n_rows]; a target
- *     outside [0, vocab) names no token: its logp is 0 and has no gradient.
+ *   logits: bf16 or fp32 [n_rows, vocab] (ld elements, 16-byte aligned rows; stats on 8 bytes, the rest on 4);
+ *     targets: int32 [n_rows]; a target outside [0, vocab) names no token: its logp is 0 and has no gradient.
  *   sl_token_logprobs_fwd: logp[r] = z_t - log sum_j e^(z_j); stats[r] = two floats for the backward, with
  *     log sum_j e^(z_j) = ln 2 (stats[r][0] + stats[r][1]) to fp32; entropy[r] (optional) = -sum_j p_j log p_j;
  *     with top_k > 0 (<= 32, <= vocab): top_ids[r], top_logp[r] ([n_rows, top_k], dense): the tokens of the largest

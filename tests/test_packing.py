@@ -155,3 +155,26 @@ def test_streams_without_torchs_private_names(monkeypatch):
     copy = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(copy)
     assert copy._current_device() == 3 and copy._raw_stream(3) == 103 and copy._stream().value == 103
+
+
+def test_misaligned_32_bit_values_are_refused(lib):
+    """Values that kernels read or write one by one (the others are in the tests above): an address off by two would
+    fault them."""
+    n, off = lib.sl_attention_plan_bytes(2, 300), A + 2
+    bad = []
+    for k in range(2):
+        dg = [A, A]
+        dg[k] = off
+        bad.append(lib.sl_qk_norm_rope_bwd(A, 256, A, 128, A, 256, A, 128, A, A, 64, 0, A, A, 1e-6, 4, 4, 2, 64, A, 256, A, 128,
+                                           *dg, _ws(), None))
+    bad.append(lib.sl_attention_masked_fwd(A, 256, A, 128, A, 128, 2, 300, 4, 2, 64, 0.0, 0.0, off, A, n, A, 256, A, _ws(),
+                                           None))
+    bad.append(lib.sl_attention_masked_bwd(A, 256, A, 128, A, 128, A, 256, A, 2, 300, 4, 2, 64, 0.0, 0.0, off, A, n, A, 256,
+                                           A, 128, A, 128, _ws(), None))
+    for k in range(5):
+        targets, logp, entropy, ids, top = (off if i == k else A for i in range(5))
+        bad.append(lib.sl_token_logprobs_fwd(0, A, 104, 4, 100, targets, logp, A, entropy, 5, ids, top, None))
+    for k in range(4):
+        targets, g, gh, entropy = (off if i == k else A for i in range(4))
+        bad.append(lib.sl_token_logprobs_bwd(0, A, 104, 4, 100, targets, A, g, gh, entropy, A, 104, None))
+    assert bad == [B.SL_ERR_ALIGNMENT] * len(bad)
