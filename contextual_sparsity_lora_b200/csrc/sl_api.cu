@@ -1294,6 +1294,9 @@ sl_status masked_args(int32_t n_seq, int32_t seq_len, int32_t hq, int32_t hkv, i
     return SL_ERR_SHAPE;
   if (((int64_t)seq_len + 127) / 128 * n_seq * hq > 1 << 30) return SL_ERR_SHAPE;  // the kernels' unit numbers are int32
   if (!(scale >= 0.f && scale < INFINITY) || !(cap >= 0.f && cap < INFINITY)) return SL_ERR_SHAPE;
+  float sc, mul, cap_mul;  // the kernels multiply by these: 0 or infinity there would make 0 or NaN of ordinary scores
+  masked_score_constants(scale, cap, hd, &sc, &mul, &cap_mul);
+  if (!std::isnormal(mul) || (cap > 0.f && !std::isnormal(cap_mul))) return SL_ERR_SHAPE;
   if (plan_bytes < attention_plan_bytes(n_seq, seq_len)) return SL_ERR_SHAPE;
   return al16(plan) ? SL_OK : SL_ERR_ALIGNMENT;
 }

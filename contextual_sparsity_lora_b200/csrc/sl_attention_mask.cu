@@ -1729,15 +1729,14 @@ int bwd_launch(const MaskedBwdParams& p, cudaStream_t s) {
   return fine_grads(p.hd, p.S) ? bwd_launch<CAP, BIAS, true>(p, s) : bwd_launch<CAP, BIAS, false>(p, s);
 }
 
-// scale, mul of score() and cap_mul of tanh_n()
-void score_constants(const MaskedArgs& a, float* scale, float* mul, float* cap_mul) {
-  const double sc = a.scale > 0.f ? (double)a.scale : 1.0 / std::sqrt((double)a.hd);
-  *scale = (float)sc;
-  *mul = (float)(1.4426950408889634 * (a.cap > 0.f ? (double)a.cap : sc));
-  *cap_mul = a.cap > 0.f ? (float)(sc / a.cap) : 0.f;
-}
-
 }  // namespace
+
+void masked_score_constants(float scale, float cap, int hd, float* sc, float* mul, float* cap_mul) {
+  const double s = scale > 0.f ? (double)scale : 1.0 / std::sqrt((double)hd);
+  *sc = (float)s;
+  *mul = (float)(1.4426950408889634 * (cap > 0.f ? (double)cap : s));
+  *cap_mul = cap > 0.f ? (float)(s / cap) : 0.f;
+}
 
 int64_t attention_plan_bytes(int n_seq, int S) { return carve_plan(nullptr, n_seq, S, nullptr); }
 
@@ -1784,7 +1783,7 @@ int attention_masked_fwd(const MaskedArgs& a, cudaStream_t s) {
   p.hd = a.hd;
   p.nd = (a.hd + 63) / 64;
   float scale;
-  score_constants(a, &scale, &p.mul, &p.cap_mul);
+  masked_score_constants(a.scale, a.cap, a.hd, &scale, &p.mul, &p.cap_mul);
   p.err = a.err;
   if (a.cap > 0.f) return a.slopes ? fwd_launch<true, true>(p, s) : fwd_launch<true, false>(p, s);
   return a.slopes ? fwd_launch<false, true>(p, s) : fwd_launch<false, false>(p, s);
@@ -1820,7 +1819,7 @@ int attention_masked_bwd(const MaskedArgs& a, cudaStream_t s) {
   // units that leave half of the SMs free are shared by two CTAs each (3 x 333 tokens, 27 units: 20.3 against 28.6 us; one
   // key tile, two steps: 9.9 against 10.3)
   p.split = 2 * plan_tiles(a.n_seq, a.S) * a.hkv <= sm_count() ? 2 : 1;
-  score_constants(a, &p.scale, &p.mul, &p.cap_mul);
+  masked_score_constants(a.scale, a.cap, a.hd, &p.scale, &p.mul, &p.cap_mul);
   p.err = a.err;
   if (a.cap > 0.f) return a.slopes ? bwd_launch<true, true>(p, s) : bwd_launch<true, false>(p, s);
   return a.slopes ? bwd_launch<false, true>(p, s) : bwd_launch<false, false>(p, s);

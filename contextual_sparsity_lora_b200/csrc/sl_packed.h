@@ -68,6 +68,8 @@ struct MaskedArgs {
   int64_t lddq, lddk, lddv;
   void* scratch;              // attention_masked_scratch() bytes: D per query row and head
 };
+// The scale itself (0: 1 / sqrt(hd)), mul of the kernels' score() and cap_mul of their tanh_n()
+void masked_score_constants(float scale, float cap, int hd, float* sc, float* mul, float* cap_mul);
 // Both return 0, 2 (tensor map), 5 (launch).
 int attention_masked_fwd(const MaskedArgs& a, cudaStream_t s);
 int attention_masked_bwd(const MaskedArgs& a, cudaStream_t s);

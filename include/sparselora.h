@@ -468,7 +468,8 @@ SL_API sl_status sl_qk_norm_rope_bwd(const void* dyq, int64_t lddyq, const void*
  * +inf without a cap, has NaN in o and lse. head_dim in [8, 128], a multiple of 8; seq_len <= 2^20; n_q_heads a
  * multiple of n_kv_heads; at most 2^30 pairs of a query head and a tile of 128 rows (each sequence begins one);
  * pointers 16-byte aligned (slopes 4), leading dimensions multiples of 8. Errors: SL_ERR_INVALID_ARG (null pointer),
- * SL_ERR_SHAPE (a size, scale or cap out of range, a plan buffer too small), SL_ERR_ALIGNMENT, SL_ERR_WORKSPACE. A buffer that holds no plan of the
+ * SL_ERR_SHAPE (a size, scale or cap out of range: scale, softcap and scale / softcap, times log2 e, are normal fp32
+ * numbers; a plan buffer too small), SL_ERR_ALIGNMENT, SL_ERR_WORKSPACE. A buffer that holds no plan of the
  * call's sizes is seen on the device: nothing is computed, and the workspace's error word says so. */
 SL_API int64_t sl_attention_plan_bytes(int32_t n_seq, int32_t seq_len);
 SL_API sl_status sl_attention_plan(const int32_t* row_lo, const int32_t* row_hi, int32_t n_seq, int32_t seq_len,

@@ -178,3 +178,20 @@ def test_misaligned_32_bit_values_are_refused(lib):
         targets, g, gh, entropy = (off if i == k else A for i in range(4))
         bad.append(lib.sl_token_logprobs_bwd(0, A, 104, 4, 100, targets, A, g, gh, entropy, A, 104, None))
     assert bad == [B.SL_ERR_ALIGNMENT] * len(bad)
+
+
+def test_scales_and_caps_that_32_bits_do_not_hold_are_refused(lib):
+    """softcap log2(e) or scale / softcap as infinity, zero or a number without all its bits: NaN or 0 for any score. No
+    workspace: a call that passes its checks ends there."""
+    n = lib.sl_attention_plan_bytes(2, 300)
+
+    def both(scale, cap):
+        return (lib.sl_attention_masked_fwd(A, 256, A, 128, A, 128, 2, 300, 4, 2, 64, scale, cap, None, A, n, A, 256, A, None,
+                                            None),
+                lib.sl_attention_masked_bwd(A, 256, A, 128, A, 128, A, 256, A, 2, 300, 4, 2, 64, scale, cap, None, A, n, A, 256,
+                                            A, 128, A, 128, None, None))
+
+    for scale, cap in ((0.0, 3e38), (3e38, 0.0), (0.0, 1e38), (1.0, 1e-39), (1e38, 1e-3), (1e-40, 0.0)):
+        assert both(scale, cap) == (B.SL_ERR_SHAPE,) * 2, (scale, cap)
+    for scale, cap in ((0.0, 0.0), (0.0, 1e6), (1.0, 1e37), (1e-30, 0.0), (0.0, 1e-30)):
+        assert both(scale, cap) == (B.SL_ERR_WORKSPACE,) * 2, (scale, cap)
