@@ -216,6 +216,7 @@ class Workspace:
 
     def _alloc(self, nbytes):
         self.buf = torch.empty(int(nbytes), dtype=torch.uint8, device=self.device)
+        self.index = self.buf.get_device()
         self.c = SlWorkspaceC(self.buf.data_ptr(), self.buf.numel(), 0)
         self.ref = ctypes.byref(self.c)
         _check("sl_workspace_init", lib().sl_workspace_init(ctypes.byref(self.c), _stream()))
@@ -477,10 +478,11 @@ def _flat(fn, t, n, dtype, dev):
     return t.data_ptr()
 
 
-def _device(fn, t):
-    """The index of t's device, which has to be the current one (the calls go to its current stream)."""
+def _device(fn, t, ws=None):
+    """The index of t's device, which has to be the current one (the calls go to its current stream) and the
+    workspace's."""
     dev = t.get_device()
-    if dev < 0 or dev != _current_device():
+    if dev < 0 or dev != _current_device() or (ws is not None and ws.index != dev):
         _refuse(fn)
     return dev
 
@@ -514,7 +516,7 @@ def sl_qk_norm_rope_bwd(ws: Workspace, dyq, dyk, q, k, positions, inv_freq, head
     """Gradients of sl_qk_norm_rope_fwd at its inputs q and k (not read without gains), and at the gains (fp32)
     where dgq, dgk are given."""
     fn, bf = "sl_qk_norm_rope_bwd", torch.bfloat16
-    dev = _device(fn, dyq)
+    dev = _device(fn, dyq, ws)
     rest = _rope_args(fn, dyq, dyk, positions, inv_freq, head_dim, gq, gk, eps, style, dev)
     xs = (None, 0, None, 0)
     if gq is not None:
@@ -566,7 +568,7 @@ def sl_attention_masked_fwd(ws: Workspace, q, k, v, n_seq, n_q_heads, n_kv_heads
     """Attention over the plan's intervals of keys, with scores capped by softcap * tanh(. / softcap) (0: not) and
     lowered by slopes[head] * distance (None: not); o and the rows' log-sum-exp lse [n_q_heads, T]."""
     fn, bf, f32 = "sl_attention_masked_fwd", torch.bfloat16, torch.float32
-    dev = _device(fn, q)
+    dev = _device(fn, q, ws)
     sq, sk = _masked_args(fn, q, k, n_seq, n_q_heads, n_kv_heads, head_dim)
     ws.call(fn, *_rows(fn, q, sq, bf, dev), *_rows(fn, k, sk, bf, dev), *_rows(fn, v, sk, bf, dev), n_seq,
             sq[0] // n_seq, n_q_heads, n_kv_heads, head_dim, scale, softcap, _flat(fn, slopes, n_q_heads, f32, dev),
@@ -579,7 +581,7 @@ def sl_attention_masked_bwd(ws: Workspace, q, k, v, o, d_o, lse, n_seq, n_q_head
     """Gradients of sl_attention_masked_fwd at q, k and v, from its lse and the gradient d_o at o. The call reads like
     sl_attention_bwd's; o itself is not used and may be None."""
     fn, bf, f32 = "sl_attention_masked_bwd", torch.bfloat16, torch.float32
-    dev = _device(fn, q)
+    dev = _device(fn, q, ws)
     sq, sk = _masked_args(fn, q, k, n_seq, n_q_heads, n_kv_heads, head_dim)
     ws.call(fn, *_rows(fn, q, sq, bf, dev), *_rows(fn, k, sk, bf, dev), *_rows(fn, v, sk, bf, dev),
             *_rows(fn, d_o, sq, bf, dev), _flat(fn, lse, n_q_heads * sq[0], f32, dev), n_seq,

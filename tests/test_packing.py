@@ -195,3 +195,27 @@ def test_scales_and_caps_that_32_bits_do_not_hold_are_refused(lib):
         assert both(scale, cap) == (B.SL_ERR_SHAPE,) * 2, (scale, cap)
     for scale, cap in ((0.0, 0.0), (0.0, 1e6), (1.0, 1e37), (1e-30, 0.0), (0.0, 1e-30)):
         assert both(scale, cap) == (B.SL_ERR_WORKSPACE,) * 2, (scale, cap)
+
+
+def test_workspace_of_another_device_is_refused(monkeypatch):
+    """Tensors of the current device 0 (stand-ins on the host) and a workspace of device 1, whose memory the kernels of
+    device 0 may not reach."""
+
+    class OnDevice0(torch.Tensor):
+        def get_device(self):
+            return 0
+
+    here = lambda *s, dt=torch.bfloat16: torch.zeros(*s, dtype=dt).as_subclass(OnDevice0)
+    monkeypatch.setattr(B, "_current_device", lambda: 0)
+    monkeypatch.setattr(B, "_raw_stream", lambda device: 0)
+    ws = object.__new__(B.Workspace)
+    ws.index, ws.device, ws.c = 1, "cuda:1", B.SlWorkspaceC(None, 0, 0)
+    ws.ref = ctypes.byref(ws.c)
+    x, lse, plan = here(4, 64), here(2, 4, dt=torch.float32), here(1 << 16, dt=torch.uint8)
+    for call in (lambda: B.sl_attention_masked_fwd(ws, x, x, x, 1, 2, 2, 32, plan, x, lse),
+                 lambda: B.sl_attention_masked_bwd(ws, x, x, x, x, x, lse, 1, 2, 2, 32, plan, x, x, x),
+                 lambda: B.sl_qk_norm_rope_bwd(ws, x, x, x, x, None, None, 32, x, x, here(32), here(32),
+                                               dgq=here(32, dt=torch.float32))):
+        with pytest.raises(B.SparseLoRAError) as e:
+            call()
+        assert e.value.code == B.SL_ERR_INVALID_ARG
