@@ -346,3 +346,119 @@ def test_nan_and_infinite_scores_show_in_their_rows(kw):
             hit = sees & (one[:, 5] > 0)
             assert hit[j] and ob[hit, :hd].isnan().all() and lseb[0, hit].isnan().all(), j
             assert same((ob[~sees], lseb[:, ~sees]), (want[0][~sees], want[1][:, ~sees])), j
+
+
+def plan_parts(buf, n_seq, S):
+    """What a plan's buffer holds: each part on 16 bytes, in the order in which the kernels' Plan names them."""
+    n_t = (S + 127) // 128
+    words, at, parts = buf.cpu().view(torch.int32), 16, {}
+    for name, n, width in (("lo", n_seq * S, 1), ("hi", n_seq * S, 1), ("q", n_seq * n_t, 4), ("k", n_seq * n_t, 2),
+                           ("q_order", n_seq * n_t, 4), ("k_order", n_seq * n_t, 4), ("q2", n_seq * ((n_t + 1) // 2), 2),
+                           ("q2_order", n_seq * ((n_t + 1) // 2), 4)):
+        parts[name] = words[at: at + n * width].view(n, width).long()
+        at += -(-n * width // 4) * 4
+    assert at == words.numel() and words[1:3].tolist() == [n_seq, S]
+    return parts
+
+
+@pytest.mark.parametrize("n_seq,S", [(1, 131072), (3, 16500), (150, 1), (2, 131071), (1, 16384), (1, 1 << 20)])
+@pytest.mark.parametrize("kind", ["causal", "documents", "random"])
+def test_plans_of_many_tiles(n_seq, S, kind):
+    """Plans of more than 128 tiles (two kernels), up to the longest sequence: rows, ranges and orders."""
+    g = torch.Generator().manual_seed(S)
+    T, n_t = n_seq * S, (S + 127) // 128
+    pos = torch.arange(S).repeat(n_seq)
+    if kind == "causal":
+        lo, hi = torch.zeros(T, dtype=torch.long), pos + 1
+    elif kind == "documents":
+        lens = docs_of(n_seq, S, 7, S // 30, S)
+        lo, hi, _ = (t.long() for t in packed_rows(lens, S, [[90] * len(d) for d in lens], 2000))
+    else:
+        lo = torch.randint(0, S, (T,), generator=g)
+        hi = lo + torch.randint(-40, min(S, 700) + 1, (T,), generator=g)
+        lo[: min(200, S)] = hi[: min(200, S)] = 0
+    rows = (None, None) if kind == "causal" else (lo.int().to(DEV), hi.int().to(DEV))
+    parts = plan_parts(plan_of(*rows, n_seq, S), n_seq, S)
+    empty = lo >= hi
+    lo, hi = torch.where(empty, 0, lo), torch.where(empty, 0, hi.clamp(max=S))
+    assert torch.equal(parts["lo"][:, 0], lo) and torch.equal(parts["hi"][:, 0], hi)
+    pad = n_t * 128 - S
+    tiles = lambda x, fill: torch.nn.functional.pad(x.view(n_seq, S), (0, pad), value=fill).view(n_seq * n_t, 128)
+    full = torch.where(empty, S, lo), torch.where(empty, 0, lo), torch.where(empty, S, hi), hi
+    l_min, l_max, h_min, h_max = (f(tiles(x, v), 1) for x, v, f in zip(full, (S, 0, S, 0), (torch.amin, torch.amax) * 2))
+    nothing, holes = h_max == 0, tiles(empty, False).any(1)
+    want = torch.stack((l_min // 128, (h_max + 127) // 128, (l_max + 127) // 128, h_min // 128), 1)
+    want[holes, 2:] = 0
+    want[nothing] = torch.tensor([0, 1, 0, 0])
+    assert torch.equal(parts["q"], want)
+    # key tiles: the first and the last query tile whose range holds them
+    x, y = want[:, 0].view(n_seq, n_t, 1), want[:, 1].view(n_seq, n_t, 1)
+    at = torch.arange(n_t)
+    first, last = torch.full((n_seq, n_t), n_t), torch.zeros(n_seq, n_t, dtype=torch.long)
+    for t in range(n_t):
+        sees = (at >= x[:, t]) & (at < y[:, t])
+        first, last = torch.where(sees, first.clamp(max=t), first), torch.where(sees, t + 1, last)
+    first, last = torch.where(last == 0, 0, first), torch.where(last == 0, 1, last)
+    assert torch.equal(parts["k"], torch.stack((first, last), 2).view(-1, 2))
+    x, y = (torch.nn.functional.pad(v[..., 0], (0, n_t & 1), value=fill).view(n_seq, -1, 2) for v, fill in ((x, n_t), (y, 0)))
+    assert torch.equal(parts["q2"], torch.stack((x.amin(2), y.amax(2)), 2).view(-1, 2))
+    for name in ("q", "k", "q2"):
+        order, ranges = parts[name + "_order"], parts[name]
+        assert torch.equal(order[:, 0].sort().values, torch.arange(len(ranges)))
+        assert torch.equal(order[:, 1:3], ranges[order[:, 0], :2])
+        length = order[:, 2] - order[:, 1]
+        assert (length[1:] <= length[:-1]).all()
+
+
+@pytest.mark.parametrize("docs,window,prefix,kw", [(1, 0, 0, {}), (5, 900, 70, dict(softcap=9.0)), (2, 0, 0, dict(slopes=True))])
+def test_long_sequences(docs, window, prefix, kw):
+    """A sequence of more than 128 tiles, a head at a time (the reference is S x S in 64 bits)."""
+    S, hq, hkv, hd = 16500, 3, 1, 64
+    if kw.get("slopes"):
+        kw = dict(slopes=torch.tensor([0.5, 0.01, 0.0], device=DEV))
+    lens = docs_of(1, S, docs, S // 40, S)
+    lo, hi, _ = packed_rows(lens, S, [[prefix] * len(d) for d in lens], window, DEV)
+    q, k, v, do = inputs(1, S, hq, hkv, hd, S, 0, 2.0)
+    got = call(q, k, v, do, plan_of(lo, hi, 1, S), 1, hq, hkv, hd, **kw)
+    for h in (0, 2):
+        hs = slice(h * hd, (h + 1) * hd)
+        sl = kw["slopes"][h: h + 1] if "slopes" in kw else None
+        want = reference(q[:, hs], k, v, do[:, hs], lo, hi, 1, 1, 1, hd, kw.get("softcap", 0.0), sl)
+        hold(dict(o=got["o"][:, hs], dq=got["dq"][:, hs], lse=got["lse"][h: h + 1]),
+             {n: want[n] for n in ("o", "dq", "lse")})
+        del want
+    one = {n: got[n].clone() for n in ("dk", "dv")}
+    parts = [call(q[:, h * hd: (h + 1) * hd], k, v, do[:, h * hd: (h + 1) * hd], plan_of(lo, hi, 1, S), 1, 1, 1, hd,
+                  **{**kw, **({"slopes": kw["slopes"][h: h + 1]} if "slopes" in kw else {})}) for h in range(hq)]
+    for n in ("dk", "dv"):  # the group's sum against the heads' own, each rounded to bf16
+        alone = torch.stack([p[n].double() for p in parts])
+        tol = 2.0 ** -8 * (alone.abs().sum(0) + one[n].double().abs()) + 2.0 ** -16 * alone.abs().max()
+        assert ((alone.sum(0) - one[n].double()).abs() <= tol).all(), n
+
+
+@pytest.mark.parametrize("docs,window", [(1, 0), (170, 0), (1, 5), (60, 0)])
+@pytest.mark.parametrize("S,hd", [(512, 128), (512, 96), (129, 72)])
+def test_gradients_of_larger_heads(S, hd, docs, window):
+    """Heads over 64 in sequences over 128 tokens, whose dS is rounded to bf16 once, for long documents, documents and windows
+    of a few tokens: the rounding of dS and that of the result are of the same size and independent, so the error of dq and dk
+    is sqrt(2) of the latter's alone; a tenth more allowed."""
+    n_seq, hq, hkv = 2, 4, 2
+    lens = docs_of(n_seq, S, docs, 0, S)
+    lo, hi, _ = packed_rows(lens, S, None, window, DEV)
+    q, k, v, do = inputs(n_seq, S, hq, hkv, hd, S + hd, 0, 2.0)
+    got = call(q, k, v, do, plan_of(lo, hi, n_seq, S), n_seq, hq, hkv, hd)
+    want = reference(q, k, v, do, lo, hi, n_seq, hq, hkv, hd)
+    for n in ("dq", "dk"):
+        w = want[n][0]
+        assert (got[n].double() - w).norm() <= 1.1 * math.sqrt(2) * (w.to(BF).double() - w).norm(), n
+
+
+def test_wrong_plan_leaves_every_output():
+    """As in the test above of a wrong plan, dq among the outputs."""
+    n_seq, S, hq, hkv, hd = 2, 200, 2, 1, 64
+    q, k, v, do = inputs(n_seq, S, hq, hkv, hd, 3)
+    ws, buf = B.Workspace(), torch.zeros_like(AttentionPlan(n_seq, S).buf)
+    lse = torch.zeros(hq, n_seq * S, device=DEV)
+    dq, dk, dv = (torch.full_like(t, 5.0) for t in (q, k, v))
+    B.sl_attention_masked_bwd(ws, q, k, v, None, do, lse, n_seq, hq, hkv, hd, buf, dq, dk, dv)
+    assert ws.read_device_flag() != 0 and all((t == 5.0).all() for t in (dq, dk, dv))

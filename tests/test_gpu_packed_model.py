@@ -225,3 +225,26 @@ def test_score_options_without_a_plan_share_one():
     assert not torch.equal(m.forward_backward(ids, targets), causal)
     m.set_rows(None, None)
     assert torch.equal(m.forward_backward(ids, targets), causal)
+
+
+def test_default_layer_runs_the_causal_core_and_the_library_loss():
+    """Without the options, against what does not go through them: attention from the layer's own q, k and v by the causal
+    core's entry points, forward and backward, bit for bit; the loss from the logits in 64 bits."""
+    keep = [(0.5, 0.5)]
+    p = build(keep, seed=87)
+    m = p["model"]
+    lay = m.layers[0]
+    pt = torch.from_numpy(p["perm"])
+    ids, targets = p["ids"][pt].to(torch.int32).to(DEV), p["targets"].to(DEV)
+    loss = m.forward_backward(ids, targets).clone()
+    at, ws = lay.attn, B.Workspace()
+    a, lse = torch.empty_like(lay.a_nat), torch.empty_like(lay.lse)
+    B.sl_attention_fwd(ws, lay.q_nat, lay.k_nat, lay.v_nat, lay.n_seq, at.hq, at.hkv, at.hd, a, lse)
+    assert torch.equal(a, lay.a_nat) and torch.equal(lse, lay.lse)
+    dk, dv = torch.empty_like(lay.dk_nat), torch.empty_like(lay.dv_nat)
+    B.sl_attention_bwd(ws, lay.q_nat, lay.k_nat, lay.v_nat, a, lay.da_nat, lse, lay.n_seq, at.hq, at.hkv, at.hd,
+                       torch.empty_like(lay.dq_nat), dk, dv)  # dq: sums of the causal core in no set order
+    assert torch.equal(dk, lay.dk_nat) and torch.equal(dv, lay.dv_nat)
+    logits = torch.matmul(m.hf[m.C:], m.lm_head.t()).double()
+    want = -torch.log_softmax(logits, 1).gather(1, targets.long()[:, None]).mean()
+    assert abs(float(loss) - float(want)) <= 1e-5 * abs(float(want))
