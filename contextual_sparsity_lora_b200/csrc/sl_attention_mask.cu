@@ -164,7 +164,9 @@ __device__ void plan_order(const R* range, int64_t n, int n_t, int4* order, int3
   __syncthreads();
 }
 
-// Key tiles' ranges from the query tiles', and both orders (one block).
+// Key tiles' ranges from the query tiles', and both orders. One block, and two atomics per pair of a query tile and a key
+// tile that it sees: with the rows' kernel 17 us for one causal sequence of 16512 tokens, 76 for 65536, 262 for 131072,
+// 15.7 ms for 2^20 (once per batch, beside attention that grows the same way).
 __device__ void plan_tiles_and_order(const Plan& p, int n_seq, int S, int32_t* hist, int32_t* carry) {
   const int n_t = (S + kTile - 1) / kTile;
   const int64_t n = (int64_t)n_seq * n_t;
@@ -317,7 +319,7 @@ __device__ __forceinline__ float max2(float a, float b) {
   return r;
 }
 // 2^x of two values on the multiply-add units: x = n + f with a whole n and |f| <= 1/2, 2^f a polynomial of degree 5 (least
-// maximum of the relative error with the constant 1: 1.1e-7, 1.6e-7 with fp32 arithmetic, about ex2.approx's), n added
+// maximum of the relative error with the constant 1: 1.1e-7, 1.7e-7 with fp32 arithmetic, about ex2.approx's), n added
 // to its exponent. From -127 down: 0 (the exponent of 1 less 127 leaves no bit). 1.5 * 2^23 + x keeps n in its low
 // bits. NaN gives some number: the row's maximum keeps it. A quarter of the forward's exponentials, which otherwise wait for the exponential unit (8192 tokens with a bias 537 against 576 us, 4096 causal 131 against 135;
 // an eighth 555, three eighths 543, half 585); with a cap, whose tanh is on the same units, and in the backward it gains nothing.
@@ -338,7 +340,7 @@ __device__ __forceinline__ void ex2_poly(f2 x, float& y0, float& y1) {
   y1 = __uint_as_float(r1 + (n1 << 23));
 }
 // tanh of N raw products times mul (= scale / cap), in place. Up to 0.75 an odd polynomial (a least-maximum
-// fit of tanh(u) / u in u^2, relative error 3e-8, 1.6e-7 with fp32 arithmetic): 7 multiply-adds, and small
+// fit of tanh(u) / u in u^2, relative error 6.5e-8, 1.6e-7 with fp32 arithmetic): 7 multiply-adds, and small
 // scores keep their relative exactness. Above, for the whole warp: 1 - 2 / (2^(2 log2(e) u) + 1), error
 // about 1e-7 of 1 (2^x = inf gives 1, 0 gives -1), on the exponential unit, which the softmax needs too.
 // tanh.approx would be off by 5e-4 of the value.
@@ -942,8 +944,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1) masked_fwd_kernel(const __grid
 // the query tiles that see it. Each forms S and dP for itself (nine products of a tile pair where one kernel for
 // all would have five and a sum for D), but no partial sum leaves the chip and every sum has a fixed order. With dQ
 // added up across key tiles in global memory (64 KB of fp32 reductions per tile pair, a kernel for D before it and a pass
-// that rounds after it) the backward took 161 us at 8 x 512 tokens and 631 at 4096 capped ones, against 115 and 534, and
-// dq's last bits depended on the order.
+// that rounds after it) dq's last bits depended on the order. As first built that form took 161 us at 8 x 512 tokens and
+// 631 at 4096 capped ones, this one 129 and 609 (115 and 534 by what came later, which the other form has not had).
 //
 // D_i = sum_j P_ij dP_ij (= dO_i . o_i) is formed from P and dP in fp32 and not from the stored o: that one is rounded to
 // bf16, and its error, the same for all keys of a row, is as large as all other roundings of dq and dk
@@ -953,12 +955,12 @@ __global__ void __launch_bounds__(kFwdThreads, 1) masked_fwd_kernel(const __grid
 // one per row (ROW) or read per column from shared memory. P as packed bf16 in pw (when wanted), dS in dw; FINE: and behind
 // it what the rounding left of dS, as bf16 again.
 //
-// Rounded once, dS costs dq and dk about as much as their own rounding does (relative error of both together 1.41 times
-// the latter's alone for long rows of 128 elements, up to 1.7 for heads of 8 or documents of a few tokens, where one key takes
-// most of a row and its dS is the others' sum). With the rest as a second first operand of dQ += dS K and dK += dS^T Q
-// nothing of that is left. Those products are half as wide for heads up to 64, and one tile is all there is of short sequences:
-// fine_grads() takes the second operand there, where it costs little, and not where the first alone is as good
-// (4096 causal tokens of 128: dq 324 against 281 us with it, dk and dv 294 against 264).
+// Rounded once, dS costs dq and dk about as much as their own rounding does: the error of both together is 1.41 times the
+// latter's alone, 1.35 to 1.47 for heads of 72 to 128 with documents or windows of any length from two tokens on. It grows
+// where few terms make a result: heads of 8 have up to 1.7, and single batches of a few tokens any value up to 2.4
+// (their mean is 1.4 too). With the rest as a second first operand of dQ += dS K and dK += dS^T Q nothing of that is left.
+// fine_grads() takes it for heads up to 64, whose products are half as wide, and for sequences of one tile, where it
+// costs little (4096 causal tokens of 128: dq 324 against 281 us with it, dk and dv 294 against 264).
 bool fine_grads(int hd, int S) { return hd <= 64 || S <= kTile; }
 
 template <bool CAP, bool BIAS, bool ROW, bool WANT_P, bool FINE>
@@ -1009,8 +1011,8 @@ __device__ __forceinline__ void grad32(uint32_t (&s)[32], uint32_t (&dp)[32], fl
   }
 }
 
-// dq: persistent CTAs over units (query tile, head). Q and dO stay, K and V stream through two stages, for D and then, from
-// the last key tile to the first, for dQ. S, dP and K of the last two tiles are kept, so the second pass forms
+// dq: persistent CTAs over units (query tile, head). Q and dO stay, K streams through three stages and V through two, for D
+// and then, from the last key tile to the first, for dQ. S, dP and K of the last two tiles are kept, so the second pass forms
 // them again only from the third on (documents of up to 256 keys: once). Warp 0 loads; warps 1, 2 and 3 issue
 // S = Q K^T, dP = dO V^T and dQ += dS K, S and dP ahead of the compute warps. Warps 4-19 hold a query row and 32 of
 // the 128 key columns per thread. With n key tiles in unit i, step m < n of the first pass has S in buffer (i + m) & 1, the
@@ -1021,7 +1023,9 @@ __device__ __forceinline__ void grad32(uint32_t (&s)[32], uint32_t (&dp)[32], fl
 // Measured (32 query, 8 key/value heads of 128): 4096 causal tokens 282 us (1200 TFLOP/s of the products done), capped documents
 // 265 us, 8 x 512 tokens 62 us. S and dP formed twice for every tile: 349, 318 and 69 us; K and V in two common stages: 353,
 // 298, 66 (a stage is held from its load to the end of dS K, and the next load waits); dP without its second place: 299.
-// What is left between the products is the chain from a dS over its product to the S that takes its buffer.
+// What is left between the products is the chain from a dS over its product to the S that takes its buffer. The 104 registers
+// of a compute thread (96 as compiled) do not hold all: 116 bytes per thread are spilled without a cap, 224 with one, 252
+// with a bias too. (Eight compute warps, which spill nothing, are not measured here.)
 template <bool CAP, bool BIAS, bool FINE>
 __global__ void __launch_bounds__(kBwdThreads, 1) masked_dq_kernel(const __grid_constant__ MaskedBwdParams p) {
   extern __shared__ __align__(1024) uint8_t smem_dq[];
@@ -1348,8 +1352,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) masked_dq_kernel(const __grid_
 // S^T, dP^T, and dV and dK (a thread that issues also waits and commits, and meanwhile the tensor cores, which queue
 // about five products, run dry: 340 us at 4096 causal tokens with one such thread, 320 with two, 277 with three); the
 // others compute, one half for the even and one for the odd steps, a key row and 32 query columns per thread at a time:
-// 16 warps, or 8 where a cap's tanh needs the registers (with 16 it spilled: 335 against 318 us at 4096 capped
-// tokens; without a cap 16 gained 10%). TMEM: S^T of buffer x at 64 x, dP^T at 128 + 64 x, dV at 256, dK at 384.
+// 16 warps (40 to 52 bytes spilled), or 8 where a cap's tanh needs the registers (none; with 16 it spilled: 335 against 318
+// us at 4096 capped tokens; without a cap 16 gained 10%). TMEM: S^T of buffer x at 64 x, dP^T at 128 + 64 x, dV at 256, dK at 384.
 //
 // Measured (32 query, 8 key/value heads of 128): 4096 causal tokens 264 us (1070 TFLOP/s of four products per tile pair; 286
 // with two stages of whole query tiles), capped 269 us, 8 x 512 tokens 53 us. The products alone take 2640 of a query

@@ -24,7 +24,7 @@
 //
 // The forward reads each logit once, the backward reads and writes it once. Measured on 128256 bf16 logits a row: backward,
 // 1024 rows, 88 us (6.0 TB/s, 0.91 of the copy rate); forward with entropy, 1024 rows 61 us, 4096 rows with 20
-// alternatives 211 us (5.0 TB/s, 0.76): its issue slots are four fifths full, with a range check, a maximum, a
+// alternatives 213 us (4.9 TB/s, 0.75): its issue slots are four fifths full, with a range check, a maximum, a
 // conversion, an exponential and two sums per logit (a second maximum that keeps NaN cost 224 us; NaN shows in
 // the sums). Few rows: a cluster of up to 8 CTAs shares a row, each with a contiguous part of the
 // vocabulary, and the first CTA joins sums and candidates through distributed shared memory.

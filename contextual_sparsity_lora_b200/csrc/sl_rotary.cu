@@ -11,6 +11,10 @@
 // computed a pair per lane and serve all its heads through shared memory; the next heads' vectors are on their way
 // meanwhile. (One block per token, each lane one head: 400 of 616 instructions a warp went into set-up, and the
 // forward was bound by issue at 1.8 TB/s.) Blocks of q stand before blocks of k.
+// Measured beside library copies of the same bytes: rotation of 4096 tokens of 40 heads of 128 (84 MB) 18.6 us, a copy 15.0;
+// norm and rotation of 20011 tokens of 30 heads of 96 (231 MB) 57, a copy 41.5; its backward (346 MB) 97, a sum of two tensors
+// 51.5. The vectors in flight are held in registers (64, 72 and 125 to 128 a thread); in the forward with norm the sum and
+// the products with gains stand between a vector's arrival and its store, and issue slots are three quarters full.
 // Angles: p f_i in turns as a 64-bit fraction (f_i / 2 pi scaled by 2^64, times p, wrapping), so
 // far positions lose nothing to the range reduction; one rounding to fp32 before sincospi.
 #include <cuda_bf16.h>

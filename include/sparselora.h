@@ -462,6 +462,9 @@ SL_API sl_status sl_qk_norm_rope_bwd(const void* dyq, int64_t lddyq, const void*
  *     rounded o is not used: the rows' sums of P dP are formed again in fp32; the slopes are constants). Rows
  *     that see nothing give and get zeros. All results are run-to-run identical. Workspace: 4 n_q_heads T bytes
  *     past the header (the forward needs only the header).
+ * Precision: scores, statistics and sums are fp32; P is rounded to bf16 before P v and P^T d_o, dS before its
+ * products, twice (value and rest) for head_dim <= 64 or seq_len <= 128, else once; the results once. The backward
+ * forms P again from lse, so its P is right to |lse| 2^-23 of itself: 2^-9 at scores of 16384.
  * q, o, d_o, dq: bf16 [T, n_q_heads * head_dim]; k, v, dk, dv: bf16 [T, n_kv_heads * head_dim], each with its
  * own leading dimension (slices of one projection's output need no copy). Values have to be finite in every
  * row, those that nobody sees too (a product of tiles multiplies them by zero); a row with a NaN score, or one of
